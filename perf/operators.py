@@ -49,13 +49,13 @@ def listed():
         dict(name="quant_weights", op="quant_weights", E=8, N=4096, K=7168),
         # the down product of a few serving tokens on one expert-parallel share
         dict(name="gemm_decode", op="gemm", M=24, E=16, N=7168, K=2048, active=11, skew=0.0,
-             tail=3, fp32=False),
+             tail=3),
         # the gate/up product of the DeepSeek-V3-shaped batch: about 64 rows an expert
         dict(name="gemm_dsv3", op="gemm", M=16384, E=256, N=4096, K=7168, active=256, skew=0.0,
-             tail=0, fp32=False),
+             tail=0),
         # the gate/up product of the local expert slice: Zipf load, three experts empty
         dict(name="gemm_slice", op="gemm", M=16384, E=8, N=4096, K=7168, active=5, skew=1.2,
-             tail=0, fp32=False),
+             tail=0),
     ]
 
 
@@ -99,7 +99,7 @@ def draw(rng):
     active = rng.randint(1, E)
     return dict(op=op, M=_log_int(rng, active + 8, 16384), E=E, N=128 * _log_int(rng, 1, 32),
                 K=128 * _log_int(rng, 1, 56), active=active, skew=rng.choice([0.0, 0.6, 1.2]),
-                tail=rng.choice([0, 0, 7]), fp32=rng.random() < 0.3)
+                tail=rng.choice([0, 0, 7]))
 
 
 def work(case):
@@ -124,7 +124,7 @@ def work(case):
         return {"bytes": 4 * n + 8 * (n // 16384), "flops": 0}
     M, N, K = case["M"] - case["tail"], case["N"], case["K"]
     return {"bytes": M * K + M * K // 32 + case["active"] * (N * K + N * K // 4096)
-            + M * N * (4 if case["fp32"] else 2), "flops": 2 * M * N * K}
+            + 2 * M * N, "flops": 2 * M * N * K}
 
 
 # ------------------------------------------------------------------------------------------
@@ -215,8 +215,7 @@ def prepare(case, seed):
         for e in range(E):
             s["b"][e], s["sb"][e] = _codes(_randn(g, N, K, std=0.02), 128)
         # the caller's output: rows behind the last expert's stay as they are
-        s["out"] = torch.zeros(M, N, device="cuda",
-                               dtype=torch.float32 if case["fp32"] else torch.bfloat16)
+        s["out"] = torch.zeros(M, N, device="cuda", dtype=torch.bfloat16)
     return s
 
 
@@ -326,7 +325,7 @@ def _gemm_plain(s):
     slot = s["used_at"][e] * cap + pos - s["offsets"][e]
     ap = a.new_zeros(n * cap, K).index_copy_(0, slot, a)
     o = torch.bmm(ap.view(n, cap, K), b.transpose(1, 2)).view(n * cap, N)
-    s["out"][:rows] = o.index_select(0, slot).to(s["out"].dtype)
+    s["out"][:rows] = o.index_select(0, slot).to(torch.bfloat16)
     return {"out": s["out"]}
 
 
@@ -391,7 +390,7 @@ def _run_own(s):
         m.moe_fp8_quantize_weights(s["w"], E, N, K, q, sc, qt, sct)
         return {"codes": q, "scales": sc, "codes_t": qt, "scales_t": sct}
     m.moe_fp8_gemm(s["offsets"], s["M"], s["E"], s["N"], s["K"], s["a"], s["sa"], s["b"], s["sb"],
-                   s["out"], s["fp32"])
+                   s["out"])
     return {"out": s["out"]}
 
 
