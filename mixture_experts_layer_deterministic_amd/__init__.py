@@ -22,12 +22,17 @@ LIB_PATH = os.path.join(_HERE, "libmoe_mi355x.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
 
 MOE_OK = 0
+MOE_ERR_INVALID_ARG = -1
 MOE_PREC_BF16 = 0
 MOE_PREC_MXFP8 = 1
 MOE_PREC_MXFP4 = 2
 MOE_FLAG_PERSISTENT = 1
 MOE_FLAG_MXFP8_WGRAD = 2
 MOE_FLAG_BF16_DW = 4
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2 = 1
 MOE_DEVICE_BAD_EXPERT_INDEX = 1
 MOE_DEVICE_BARRIER_TIMEOUT = 2
 
@@ -52,6 +57,12 @@ class MoeSizes(ctypes.Structure):
                 ("wq", ctypes.c_size_t)]
 
 
+class MoeGate(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -67,6 +78,15 @@ _SIGS = {
     "moe_quantize_weights": [ctypes.POINTER(MoeCfg), _P, _P, _P, _SZ, _P],
     "moe_forward_fused": [ctypes.POINTER(MoeCfg), _P, _P, _P, _P, _P, _P, _SZ, _I32, _P, _P, _P,
                           _P, _P, _P, _P, _P, _SZ, _P, _SZ, _P],
+    "moe_gate_select": [ctypes.POINTER(MoeCfg), ctypes.POINTER(MoeGate), _P, _P, _P, _P, _P],
+    "moe_route_gated": [ctypes.POINTER(MoeCfg), ctypes.POINTER(MoeGate), _P, _P, _P, _P, _P, _P,
+                        _P, _SZ, _P],
+    "moe_gate_backward": [ctypes.POINTER(MoeCfg), ctypes.POINTER(MoeGate), _P, _P, _P, _P, _I32,
+                          _P],
+    "moe_router_backward": [ctypes.POINTER(MoeCfg), _P, _P, _P, _P, _P, _I32, _I32, _P],
+    "moe_fp8_quantize_rows": [_P, _I32, _I32, _P, _P, _P],
+    "moe_fp8_quantize_weights": [_P, _I32, _I32, _I32, _P, _P, _P, _P, _P],
+    "moe_fp8_gemm": [_P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P],
     "moe_permute_static": [ctypes.POINTER(MoeCfg), _P, _P, _P, _SZ, _I32, _P, _P, _P, _P, _P,
                            _P],
 }
@@ -208,3 +228,92 @@ def moe_backward(cfg, ring, slot, offsets, row_src, tk_row, topk_idx, topk_w, w_
                               _ptr(saved), _nbytes(saved), _ptr(dy), _ptr(dx), _ptr(dw1), _ptr(dw2),
                               _ptr(dwr), _ptr(d_topk_w), int(accumulate), _ptr(workspace),
                               _nbytes(workspace), _stream(stream)), "moe_backward")
+
+
+def make_gate(score=MOE_SCORE_SOFTMAX, groups=1, topk_groups=1, group_score=MOE_GROUP_MAX,
+              renorm=True, scale=1.0) -> MoeGate:
+    return MoeGate(score, groups, topk_groups, group_score, int(renorm), scale)
+
+
+_F32, _I32T, _BF16 = torch.float32, torch.int32, torch.bfloat16
+_BYTES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _dev(what, stream, *args):
+    """Device pointers of the tensors in ``args``, (tensor, dtype or dtypes, elements) each, and
+    the stream. The library sees only addresses, so what it cannot check is refused here:
+    another type, fewer elements, strides, host memory, another device than the current one."""
+    cur = torch.cuda.current_device() if stream is None else stream.device_index
+    out = []
+    for t, dtype, n in args:
+        if t is None:
+            out.append(None)
+            continue
+        d = t.dtype
+        if ((d is not dtype and (dtype is not _BYTES or d not in _BYTES)) or t.numel() < n or
+                not t.is_contiguous() or t.get_device() != cur):
+            raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: a tensor of {n} elements of {dtype}, "
+                           f"dense and on device {cur}, expected; got {tuple(t.shape)} of {d} "
+                           f"with strides {t.stride()} on {t.device}")
+        out.append(t.data_ptr())
+    out.append(_stream(stream))
+    return out
+
+
+def moe_gate_select(cfg, gate, logits, bias, topk_idx, topk_w, stream=None):
+    T, E, k = cfg.T, cfg.E, cfg.k
+    _check(lib().moe_gate_select(
+        ctypes.byref(cfg), ctypes.byref(gate),
+        *_dev("moe_gate_select", stream, (logits, _F32, T * E), (bias, _F32, E),
+              (topk_idx, _I32T, T * k), (topk_w, _F32, T * k))), "moe_gate_select")
+
+
+def moe_route_gated(cfg, gate, x, w_router, bias, logits, topk_idx, topk_w, workspace,
+                    stream=None):
+    T, E, k, d = cfg.T, cfg.E, cfg.k, cfg.d
+    *p, st = _dev("moe_route_gated", stream, (x, _BF16, T * d), (w_router, _BF16, E * d),
+                  (bias, _F32, E), (logits, _F32, T * E), (topk_idx, _I32T, T * k),
+                  (topk_w, _F32, T * k), (workspace, torch.uint8, 0))
+    _check(lib().moe_route_gated(ctypes.byref(cfg), ctypes.byref(gate), *p, _nbytes(workspace), st),
+           "moe_route_gated")
+
+
+def moe_gate_backward(cfg, gate, logits, topk_idx, d_topk_w, dlogits, accumulate, stream=None):
+    T, E, k = cfg.T, cfg.E, cfg.k
+    *p, st = _dev("moe_gate_backward", stream, (logits, _F32, T * E), (topk_idx, _I32T, T * k),
+                  (d_topk_w, _F32, T * k), (dlogits, _F32, T * E))
+    _check(lib().moe_gate_backward(ctypes.byref(cfg), ctypes.byref(gate), *p, int(accumulate), st),
+           "moe_gate_backward")
+
+
+def moe_router_backward(cfg, x, w_router, dlogits, dx, dwr, acc_dx, acc_dwr, stream=None):
+    T, E, d = cfg.T, cfg.E, cfg.d
+    *p, st = _dev("moe_router_backward", stream, (x, _BF16, T * d), (w_router, _BF16, E * d),
+                  (dlogits, _F32, T * E), (dx, _BF16, T * d), (dwr, _F32, E * d))
+    _check(lib().moe_router_backward(ctypes.byref(cfg), *p, int(acc_dx), int(acc_dwr), st),
+           "moe_router_backward")
+
+
+def moe_fp8_quantize_rows(src, rows, cols, codes, scales, stream=None):
+    n = rows * cols
+    s, q, sc, st = _dev("moe_fp8_quantize_rows", stream, (src, _BF16, n), (codes, _BYTES, n),
+                        (scales, _F32, n // 128))
+    _check(lib().moe_fp8_quantize_rows(s, rows, cols, q, sc, st), "moe_fp8_quantize_rows")
+
+
+def moe_fp8_quantize_weights(src, E, N, K, codes, scales, codes_t=None, scales_t=None,
+                             stream=None):
+    n = E * N * K
+    s, q, sc, qt, sct, st = _dev("moe_fp8_quantize_weights", stream, (src, _BF16, n),
+                                 (codes, _BYTES, n), (scales, _F32, n // 16384),
+                                 (codes_t, _BYTES, n), (scales_t, _F32, n // 16384))
+    _check(lib().moe_fp8_quantize_weights(s, E, N, K, q, sc, qt, sct, st),
+           "moe_fp8_quantize_weights")
+
+
+def moe_fp8_gemm(offsets, M, E, N, K, a, a_scales, b, b_scales, out, stream=None):
+    o, qa, sa, qb, sb, y, st = _dev("moe_fp8_gemm", stream, (offsets, _I32T, E + 1),
+                                    (a, _BYTES, M * K), (a_scales, _F32, M * K // 128),
+                                    (b, _BYTES, E * N * K), (b_scales, _F32, E * N * K // 16384),
+                                    (out, _BF16, M * N))
+    _check(lib().moe_fp8_gemm(o, M, E, N, K, qa, sa, qb, sb, y, st), "moe_fp8_gemm")

@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
 SOURCES = ["api.cpp", "router.hip", "permute.hip", "gemm.hip", "wgrad.hip", "mx.hip",
-           "elementwise.hip", "fused.hip"]
+           "elementwise.hip", "fused.hip", "gate.hip", "router_grad.hip", "fp8.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 ops are disabled for the device code; the host pass warns that it does not know

@@ -5,11 +5,13 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
 #include "moe.h"
 #include "kernels.h"
+#include "ops.h"
 
 namespace {
 
@@ -201,6 +203,37 @@ int check_wq(const Layout& Y, const void* wq, size_t wq_bytes) {
   if (!aligned16(wq)) return MOE_ERR_INVALID_ARG;
   if (wq_bytes < Y.wq_total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return MOE_OK;
+}
+
+int check_gate(const moe_cfg* c, const moe_gate* g) {
+  if (!g) return MOE_ERR_INVALID_ARG;
+  if (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (g->group_score != MOE_GROUP_MAX && g->group_score != MOE_GROUP_TOP2)
+    return MOE_ERR_INVALID_ARG;
+  if (g->groups < 1 || g->groups > c->E || c->E % g->groups != 0) return MOE_ERR_INVALID_ARG;
+  if (g->topk_groups < 1 || g->topk_groups > g->groups) return MOE_ERR_INVALID_ARG;
+  if (c->k > g->topk_groups * (c->E / g->groups)) return MOE_ERR_INVALID_ARG;
+  if ((g->renorm != 0 && g->renorm != 1) || !std::isfinite(g->scale)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// Weights [E, N, K] of the block-scaled FP8 calls.
+int check_fp8_shape(int32_t E, int32_t N, int32_t K) {
+  if (E < 1 || E > 1024 || N < 128 || N % 128 != 0 || K < 128 || K % 128 != 0 ||
+      (long long)N * K >= (1LL << 31))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+GateParams gate_params(const moe_gate* g) {
+  GateParams p;
+  p.softmax = g->score == MOE_SCORE_SOFTMAX;
+  p.groups = g->groups;
+  p.topk_groups = g->topk_groups;
+  p.top2 = g->group_score == MOE_GROUP_TOP2;
+  p.renorm = g->renorm;
+  p.scale = g->scale;
+  return p;
 }
 
 // Launch tracing (moe_trace_begin / moe_trace_end).
@@ -629,6 +662,119 @@ int moe_backward(const moe_cfg* cfg, const void* ring, size_t ring_bytes, int32_
                        routed ? static_cast<const uint16_t*>(w_router) : nullptr, cfg->T, k, d,
                        static_cast<uint16_t*>(dx), s));
   if (!L.err && routed) L(launch_dwr(dl_pos, xp, xp8, xps, Y.fb, offsets, E, d, dwr, accumulate, s));
+  return L.status();
+}
+
+int moe_gate_select(const moe_cfg* cfg, const moe_gate* gate, const float* logits,
+                    const float* bias, int32_t* topk_idx, float* topk_w, moe_stream_t stream) {
+  int st = check_mode(cfg);
+  if (st) return st;
+  if ((st = check_gate(cfg, gate))) return st;
+  if (!aligned4(logits) || (bias && !aligned4(bias)) || !aligned4(topk_idx) || !aligned4(topk_w))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_device())) return st;
+  Launches L;
+  L(launch_gate_select(gate_params(gate), logits, bias, cfg->T, cfg->E, cfg->k, topk_idx, topk_w,
+                       static_cast<hipStream_t>(stream)));
+  return L.status();
+}
+
+int moe_route_gated(const moe_cfg* cfg, const moe_gate* gate, const void* x, const void* w_router,
+                    const float* bias, float* logits, int32_t* topk_idx, float* topk_w,
+                    void* workspace, size_t ws_bytes, moe_stream_t stream) {
+  int st = check_mode(cfg);
+  if (st) return st;
+  if ((st = check_gate(cfg, gate))) return st;
+  if (!aligned16(x) || !aligned16(w_router) || (bias && !aligned4(bias)) || !aligned4(logits) ||
+      !aligned4(topk_idx) || !aligned4(topk_w) || !aligned16(workspace))
+    return MOE_ERR_INVALID_ARG;
+  const Layout Y = layout(cfg);
+  if (ws_bytes < Y.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if ((st = check_device())) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  Launches L;
+  L(launch_router_logits(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w_router),
+                         at<float>(workspace, Y.wr32), logits, cfg->T, cfg->d, cfg->E, s));
+  if (!L.err)
+    L(launch_gate_select(gate_params(gate), logits, bias, cfg->T, cfg->E, cfg->k, topk_idx, topk_w,
+                         s));
+  return L.status();
+}
+
+int moe_gate_backward(const moe_cfg* cfg, const moe_gate* gate, const float* logits,
+                      const int32_t* topk_idx, const float* d_topk_w, float* dlogits,
+                      int32_t accumulate, moe_stream_t stream) {
+  int st = check_mode(cfg);
+  if (st) return st;
+  if ((st = check_gate(cfg, gate))) return st;
+  if (!aligned4(logits) || !aligned4(topk_idx) || !aligned4(d_topk_w) || !aligned4(dlogits))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_device())) return st;
+  Launches L;
+  L(launch_gate_backward(gate_params(gate), logits, topk_idx, d_topk_w, cfg->T, cfg->E, cfg->k,
+                         dlogits, accumulate, static_cast<hipStream_t>(stream)));
+  return L.status();
+}
+
+int moe_router_backward(const moe_cfg* cfg, const void* x, const void* w_router,
+                        const float* dlogits, void* dx, float* dwr, int32_t acc_dx,
+                        int32_t acc_dwr, moe_stream_t stream) {
+  int st = check_mode(cfg);
+  if (st) return st;
+  if (!aligned16(x) || !aligned16(w_router) || !aligned4(dlogits) || (dx && !aligned16(dx)) ||
+      (dwr && !aligned16(dwr)) || (!dx && !dwr) || dx == x)
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_device())) return st;
+  RouterGradArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w_router),
+                   dlogits, static_cast<uint16_t*>(dx), dwr, cfg->T, cfg->d, cfg->E, acc_dx,
+                   acc_dwr};
+  Launches L;
+  L(launch_router_backward(a, static_cast<hipStream_t>(stream)));
+  return L.status();
+}
+
+int moe_fp8_quantize_rows(const void* src, int32_t rows, int32_t cols, void* codes, float* scales,
+                          moe_stream_t stream) {
+  if (rows < 0 || cols < 128 || cols % 128 != 0) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(src) || !aligned16(codes) || !aligned4(scales)) return MOE_ERR_INVALID_ARG;
+  if ((long long)rows * cols / 2048 >= (1LL << 31)) return MOE_ERR_INVALID_ARG;  // the grid
+  if (rows == 0) return MOE_OK;
+  if (const int st = check_device()) return st;
+  Launches L;
+  L(launch_fp8_quant_rows(static_cast<const uint16_t*>(src), rows, cols,
+                          static_cast<uint8_t*>(codes), scales,
+                          static_cast<hipStream_t>(stream)));
+  return L.status();
+}
+
+int moe_fp8_quantize_weights(const void* src, int32_t E, int32_t N, int32_t K, void* codes,
+                             float* scales, void* codes_t, float* scales_t, moe_stream_t stream) {
+  if (const int st = check_fp8_shape(E, N, K)) return st;
+  if (!aligned16(src) || !aligned16(codes) || !aligned4(scales) || !codes_t != !scales_t ||
+      (codes_t && (!aligned16(codes_t) || !aligned4(scales_t))))
+    return MOE_ERR_INVALID_ARG;
+  if (const int st = check_device()) return st;
+  Launches L;
+  L(launch_fp8_quant_weights(static_cast<const uint16_t*>(src), E, N, K,
+                             static_cast<uint8_t*>(codes), scales, static_cast<uint8_t*>(codes_t),
+                             scales_t, static_cast<hipStream_t>(stream)));
+  return L.status();
+}
+
+int moe_fp8_gemm(const int32_t* offsets, int32_t M, int32_t E, int32_t N, int32_t K, const void* a,
+                 const float* a_scales, const void* b, const float* b_scales, void* out,
+                 moe_stream_t stream) {
+  if (const int st = check_fp8_shape(E, N, K)) return st;
+  if (M < 0 || !aligned4(offsets) || !aligned16(a) || !aligned4(a_scales) || !aligned16(b) ||
+      !aligned4(b_scales) || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  if ((M / 16LL + E) * (N / 128) >= (1LL << 31)) return MOE_ERR_INVALID_ARG;  // the grid
+  if (M == 0) return MOE_OK;
+  if (const int st = check_device()) return st;
+  Fp8GemmArgs g{offsets, static_cast<const uint8_t*>(a), a_scales,
+                static_cast<const uint8_t*>(b), b_scales, static_cast<uint16_t*>(out), M, E, N, K};
+  Launches L;
+  L(launch_fp8_gemm(g, static_cast<hipStream_t>(stream)));
   return L.status();
 }
 

@@ -1,0 +1,216 @@
+"""The block-scaled FP8 quantisers and product on the GPU against 64-bit plain forms
+(tests/_ops.py). Codes and scales must be equal bit for bit. The product's tolerance counts half
+a bf16 step of the output (2^-8), an fp32 step (2^-23) for every addition outside the MFMA, and
+what the FP8 MFMA drops (_bound)."""
+import numpy as np
+import pytest
+import torch
+
+from tests import _ops
+from tests._gpu import DEV, _announce, m
+
+pytestmark = pytest.mark.gpu
+
+F8 = torch.float8_e4m3fn
+
+
+def _values(q):
+    return q.float().cpu().numpy()
+
+
+def _quant_rows(x):
+    R, C = x.shape
+    q = torch.full((R, C), 99, dtype=torch.uint8, device=DEV).view(F8)
+    s = torch.full((C // 128, R), -7.0, device=DEV)
+    m.moe_fp8_quantize_rows(x, R, C, q, s)
+    return q, s
+
+
+def _hard(shape, g):
+    """bf16 values with blocks of zeros, of one value, of tiny and of huge magnitudes."""
+    x = torch.randn(*shape, generator=g) * 2.0 ** torch.randint(-10, 10, shape, generator=g)
+    flat = x.view(-1, shape[-1])
+    flat[0, :128] = 0.0
+    flat[-1, -128:] = 0.0
+    flat[-1, -1] = -3.0
+    flat[flat.shape[0] // 2, :128] *= 1e-30
+    if flat.shape[0] > 3:
+        flat[2] *= 1e30
+    return x.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("R,C", [(1, 128), (1, 7168), (3, 256), (64, 128), (65, 384), (257, 1024),
+                                 (130, 2048), (500, 640)])
+def test_rows_are_quantised_bit_exactly(R, C):
+    _announce(f"[fp8] rows {R} x {C}")
+    x = _hard((R, C), torch.Generator().manual_seed(R + C))
+    q, s = _quant_rows(x.to(DEV))
+    rq, rs = _ops.quantize(x.float().numpy(), 1)
+    np.testing.assert_array_equal(s.cpu().numpy(), rs.T)
+    np.testing.assert_array_equal(_values(q), rq)
+
+
+@pytest.mark.parametrize("E,N,K", [(1, 128, 128), (2, 128, 384), (3, 256, 128), (2, 640, 512)])
+@pytest.mark.parametrize("both", [False, True])
+def test_weights_are_quantised_bit_exactly(E, N, K, both):
+    _announce(f"[fp8] weights {E} x {N} x {K} both={both}")
+    w = _hard((E, N, K), torch.Generator().manual_seed(E + N + K))
+    w[0, :128, :128] = 0.0
+    q = torch.empty(E, N, K, dtype=F8, device=DEV)
+    s = torch.empty(E, N // 128, K // 128, device=DEV)
+    qt = torch.empty(E, K, N, dtype=F8, device=DEV) if both else None
+    st = torch.empty(E, K // 128, N // 128, device=DEV) if both else None
+    m.moe_fp8_quantize_weights(w.to(DEV), E, N, K, q, s, qt, st)
+    rq, rs = _ops.quantize(w.float().numpy(), 128)
+    np.testing.assert_array_equal(s.cpu().numpy(), rs)
+    np.testing.assert_array_equal(_values(q), rq)
+    if both:
+        np.testing.assert_array_equal(st.cpu().numpy(), rs.swapaxes(1, 2))
+        np.testing.assert_array_equal(_values(qt), rq.swapaxes(1, 2))
+
+
+def _codes(shape, g):
+    """Random finite E4M3 codes: every one of the 254 but the two NaNs."""
+    c = torch.randint(0, 254, shape, generator=g)
+    return torch.where(c < 127, c, c + 1).to(torch.uint8).view(F8)
+
+
+# experts' row counts, then rows before the first and behind the last expert
+LOADS = {
+    "one": ([1], 0, 0),
+    "single": ([300], 0, 0),
+    "empty": ([0, 0, 5, 0], 0, 0),
+    "nothing": ([0, 0], 0, 4),
+    "edges": ([127, 128, 129, 0, 1, 255, 256, 257], 0, 0),
+    "small": ([1, 2, 3, 15, 16, 17, 31, 32, 33, 63, 64, 65], 0, 9),
+    "tail": ([40, 0, 90], 3, 21),
+    "big": ([700, 0, 3, 512], 0, 0),
+    "many": ([(7 * e) % 5 for e in range(200)], 0, 1),
+}
+
+
+def _problem(load, N, K, seed):
+    counts, before, behind = LOADS[load]
+    E, M = len(counts), before + sum(counts) + behind
+    g = torch.Generator().manual_seed(seed)
+    off = before + np.concatenate([[0], np.cumsum(counts)])
+    a, b = _codes((M, K), g), _codes((E, N, K), g)
+    sa = torch.rand(K // 128, M, generator=g) * 2.0 ** torch.randint(-6, 6, (K // 128, M), generator=g)
+    sb = torch.rand(E, N // 128, K // 128, generator=g)
+    return off, a, sa, b, sb
+
+
+def _run(off, a, sa, b, sb, out):
+    M, K = a.shape
+    E, N, _ = b.shape
+    m.moe_fp8_gemm(torch.tensor(off, dtype=torch.int32, device=DEV), M, E, N, K, a.to(DEV),
+                   sa.to(DEV), b.to(DEV), sb.to(DEV), out)
+    return out.float().cpu().numpy()
+
+
+def _bound(off, a, sa, b, sb):
+    """What the sums may lose. The FP8 MFMA adds eight consecutive k's products on a grid of 2^-13
+    of the largest of them, so each of the eight loses at most a grid step: 8 2^-13 = 2^-10 of the
+    largest, and summed over the groups at most 2^-10 of the sum of all magnitudes. On top an fp32
+    step (2^-23) of that sum for each of the 16 groups, each block, and the scales' product."""
+    K = a.shape[1]
+    mag = _ops.fp8_gemm(off, np.abs(_values(a)), sa.numpy(), np.abs(_values(b)), sb.numpy())
+    return (2.0 ** -10 + (16 + K // 128 + 4) * 2.0 ** -23) * mag
+
+
+@pytest.mark.parametrize("N,K", [(128, 128), (256, 384), (640, 1024), (384, 256)])
+@pytest.mark.parametrize("load", list(LOADS))
+def test_product(load, N, K):
+    _announce(f"[fp8] product load={load} N={N} K={K}")
+    off, a, sa, b, sb = _problem(load, N, K, N + K)
+    ref = _ops.fp8_gemm(off, _values(a), sa.numpy(), _values(b), sb.numpy())
+    e1 = _bound(off, a, sa, b, sb)
+    out = torch.full((a.shape[0], N), -7.0, dtype=torch.bfloat16, device=DEV)
+    got = _run(off, a, sa, b, sb, out)
+    rows = ~np.isnan(ref[:, 0])
+    assert np.all(got[~rows] == -7.0)  # rows outside the experts' are left as they were
+    worst = float(np.max((np.abs(got - ref) / (2.0 ** -8 * (np.abs(ref) + e1) + e1))[rows],
+                         initial=0.0))
+    assert worst <= 1, worst
+    # the same bits again
+    again = _run(off, a, sa, b, sb, torch.full_like(out, -7.0))
+    np.testing.assert_array_equal(again, got)
+
+
+@pytest.mark.parametrize("N,K", [(128, 128), (384, 640)])
+@pytest.mark.parametrize("load", list(LOADS))
+def test_product_of_small_whole_numbers_is_exact(load, N, K):
+    """Codes 0 and +-1, one in eight of them not 0, scales powers of two: no sum rounds."""
+    off, a, sa, b, sb = _problem(load, N, K, 7)
+    g = torch.Generator().manual_seed(8)
+    few = lambda x: torch.randint(-1, 2, x.shape, generator=g) * (torch.rand(x.shape, generator=g) < 0.19)
+    a, b = few(a).float().to(F8), few(b).float().to(F8)
+    sa = 2.0 ** torch.randint(0, 2, sa.shape, generator=g).float()
+    sb = 2.0 ** torch.randint(0, 2, sb.shape, generator=g).float()
+    ref = _ops.fp8_gemm(off, _values(a), sa.numpy(), _values(b), sb.numpy())
+    assert np.nanmax(np.abs(ref), initial=0.0) <= 256  # whole numbers that bf16 holds
+    out = torch.full((a.shape[0], N), 3.0, dtype=torch.bfloat16, device=DEV)
+    got = _run(off, a, sa, b, sb, out)
+    np.testing.assert_array_equal(got, np.where(np.isnan(ref), 3.0, ref))
+
+
+def test_a_row_does_not_depend_on_its_batch():
+    """One expert's rows alone and among others, first, last and in the middle of a tile."""
+    off, a, sa, b, sb = _problem("big", 256, 512, 3)
+    out = torch.zeros(a.shape[0], 256, dtype=torch.bfloat16, device=DEV)
+    full = _run(off, a, sa, b, sb, out)
+    for r in (0, 1, 127, 128, 500, 699):
+        one = _run(np.array([0, 1, 1, 1, 1]), a[r:r + 1], sa[:, r:r + 1].contiguous(), b, sb,
+                   torch.zeros(1, 256, dtype=torch.bfloat16, device=DEV))
+        np.testing.assert_array_equal(one[0], full[r])
+
+
+def test_offsets_out_of_range_touch_nothing_else():
+    """Offsets past M are clamped; descending ones give no rows."""
+    off, a, sa, b, sb = _problem("single", 128, 128, 5)
+    b, sb = b.repeat(3, 1, 1).contiguous(), sb.repeat(3, 1, 1).contiguous()
+    ref = _run(np.array([0, 300, 300, 300]), a, sa, b, sb, torch.zeros(300, 128, dtype=torch.bfloat16, device=DEV))
+    got = _run(np.array([-5, 300, 900, 2 ** 31 - 1]), a, sa, b, sb,
+               torch.zeros(300, 128, dtype=torch.bfloat16, device=DEV))
+    np.testing.assert_array_equal(got, ref)
+    got = _run(np.array([0, 0, 0, -9]), a, sa, b, sb, torch.full((300, 128), 5.0, dtype=torch.bfloat16, device=DEV))
+    assert np.all(got == 5.0)
+
+
+def test_quantise_and_multiply_and_its_gradient():
+    """The calls as they are used: rows and weights quantised, the product, then the gradient of
+    the rows through the transposed copy; against the products of the quantised values."""
+    _announce("[fp8] a run of the calls")
+    E, N, K, counts = 4, 384, 256, [100, 0, 37, 130]
+    M = sum(counts)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(M, K, generator=g).to(torch.bfloat16)
+    w = (0.05 * torch.randn(E, N, K, generator=g)).to(torch.bfloat16)
+    dy = torch.randn(M, N, generator=g).to(torch.bfloat16)
+    qw = torch.empty(E, N, K, dtype=F8, device=DEV)
+    sw = torch.empty(E, N // 128, K // 128, device=DEV)
+    qt = torch.empty(E, K, N, dtype=F8, device=DEV)
+    st = torch.empty(E, K // 128, N // 128, device=DEV)
+    m.moe_fp8_quantize_weights(w.to(DEV), E, N, K, qw, sw, qt, st)
+    for src, q, s, n in ((x, qw, sw, N), (dy, qt, st, K)):
+        qa, sa = _quant_rows(src.to(DEV))
+        got = _run(off, qa, sa, q, s, torch.empty(M, n, dtype=torch.bfloat16, device=DEV))
+        ref = _ops.fp8_gemm(off, _values(qa), sa.cpu().numpy(), _values(q), s.cpu().numpy())
+        e1 = _bound(off, qa, sa.cpu(), q, s.cpu())
+        assert np.all(np.abs(got - ref) <= 2.0 ** -8 * (np.abs(ref) + e1) + e1)
+        # and near the unquantised product: each code is within 2^-4 of its value
+        full = np.concatenate([src.double().numpy()[off[e]:off[e + 1]]
+                               @ (w[e].double().numpy().T if n == N else w[e].double().numpy())
+                               for e in range(E)])
+        assert np.linalg.norm(got - full) < 2 * 2.0 ** -4 * np.linalg.norm(full)
+
+
+def test_calls_refuse_tensors_the_library_cannot_check():
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device=DEV)
+    q, s = torch.zeros(4, 256, dtype=torch.uint8, device=DEV), torch.zeros(2, 4, device=DEV)
+    for bad in ((x.float(), q, s), (x.cpu(), q, s), (x[:, :128], q, s), (x, q[:2], s),
+                (x, q, s.bfloat16())):
+        with pytest.raises(m.MoeError) as e:
+            m.moe_fp8_quantize_rows(bad[0], 4, 256, bad[1], bad[2])
+        assert e.value.status == -1

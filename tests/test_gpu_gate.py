@@ -1,0 +1,241 @@
+"""The gate and the router gradients on the GPU against 64-bit plain forms (tests/_ops.py).
+
+The choice must be equal, expert for expert. Tolerances count roundings: u = 2^-24 is half an
+fp32 step, the device's expf is within one step (2 u), 2^-8 is half a bf16 step.
+"""
+import itertools
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _ops
+from tests._gpu import DEV, _announce, m
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+inf = math.inf
+
+
+def _logits(T, E, seed, closed=0.0, ties=False):
+    rng = np.random.default_rng(seed)
+    l = rng.normal(scale=1.7, size=(T, E)).astype(np.float32)
+    if ties:  # few distinct values: nearly every choice is between equals
+        l = np.round(l).astype(np.float32)
+    if closed:
+        l[rng.random((T, E)) < closed] = -inf
+    return l
+
+
+def _select(l, k, gate, bias=None):
+    T, E = l.shape
+    idx = torch.full((T, k), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((T, k), -7.0, device=DEV)
+    b = None if bias is None else torch.tensor(bias, dtype=torch.float32, device=DEV)
+    m.moe_gate_select(m.make_cfg(T, 256, E, k, 128), gate, torch.tensor(l, device=DEV), b, idx, w)
+    torch.cuda.synchronize()
+    return idx.cpu().numpy(), w.cpu().numpy()
+
+
+def _check_select(l, k, score, bias=None, groups=1, topk_groups=1, group_score=0, renorm=True,
+                  scale=1.0):
+    g = m.make_gate(score, groups, topk_groups, group_score, renorm, scale)
+    idx, w = _select(l, k, g, bias)
+    ridx, rw = _ops.gate(l, k, score, bias, groups, topk_groups, group_score, renorm,
+                         float(np.float32(scale)))
+    np.testing.assert_array_equal(idx, ridx)
+    # one rounding of a 64-bit value to fp32
+    assert np.all(np.abs(w - rw) <= U * 1.0001 * np.abs(rw) + 2.0 ** -149)
+
+
+SIZES = [(1, 1, 1), (1, 256, 8), (3, 3, 2), (7, 64, 64), (5, 65, 8), (70, 100, 7), (33, 256, 8),
+         (9, 257, 16), (20, 509, 10), (6, 1000, 64), (4, 1024, 40)]
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("T,E,k", SIZES)
+def test_choice_and_weights_without_groups(T, E, k, score):
+    _announce(f"[gate] T={T} E={E} k={k} score={score}")
+    bias = np.random.default_rng(E).normal(scale=0.05, size=E).astype(np.float32)
+    for b, renorm, (closed, ties) in itertools.product(
+            (None, bias), (False, True), ((0, False), (0.3, False), (0.1, True))):
+        _check_select(_logits(T, E, T + E, closed, ties), k, score, b, renorm=renorm, scale=2.5)
+
+
+GROUPS = [(256, 8, 4, 8), (256, 8, 1, 8), (256, 8, 8, 8), (64, 64, 9, 8), (96, 3, 2, 6),
+          (1024, 2, 1, 10), (1024, 512, 100, 12), (130, 65, 33, 20), (1022, 511, 3, 6),
+          (6, 2, 1, 3), (40, 4, 3, 1), (768, 12, 5, 33)]
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E,G,tg,k", GROUPS)
+def test_choice_with_groups(E, G, tg, k, score):
+    _announce(f"[gate] E={E} groups={G} topk_groups={tg} k={k} score={score}")
+    bias = np.random.default_rng(G).normal(scale=0.05, size=E).astype(np.float32)
+    for b, gsc, (closed, ties) in itertools.product(
+            (None, bias), (0, 1), ((0, False), (0.5, False), (0.2, True))):
+        _check_select(_logits(17, E, E + G, closed, ties), k, score, b, G, tg, gsc, True, 1.0)
+
+
+@pytest.mark.parametrize("score", [0, 1])
+def test_closed_rows_nan_and_infinities(score):
+    _announce(f"[gate] closed rows, NaN, infinities, score={score}")
+    l = _logits(12, 96, 5)
+    l[0] = -inf                    # nothing open
+    l[1, 1:] = -inf                # one open expert
+    l[2, ::2] = np.nan             # NaN closes
+    l[3] = np.nan
+    l[4, 10:60] = -np.finfo(np.float32).max  # masked with the type's lowest value
+    l[5] = -np.finfo(np.float32).max
+    l[6, 7] = np.finfo(np.float32).max
+    l[7, [3, 50]] = inf            # two share the row
+    l[8] = 0.0
+    l[8, 40] = -0.0                # equal to 0: index order
+    l[9] = 60.0 + np.arange(96, dtype=np.float32)  # sigmoids that are 1 in 64 bits: by logit
+    l[10] = -200.0 - np.arange(96, dtype=np.float32)[::-1]
+    for renorm, (G, tg, gsc) in itertools.product(
+            (False, True), ((1, 1, 0), (8, 3, 0), (8, 3, 1), (96, 20, 1))):
+        rows = l if not (score == 1 and gsc == 1) else np.delete(l, [9], axis=0)
+        _check_select(rows, 8, score, None, G, tg, gsc, renorm, 1.0)
+    bias = np.linspace(0.2, -0.2, 96).astype(np.float32)
+    _check_select(l, 8, score, bias, 8, 3, 1, True, 1.0)
+
+
+def test_choice_between_scores_that_fp32_cannot_tell_apart():
+    """Two experts whose choice scores differ by less than an fp32 step of them."""
+    l = np.zeros((64, 32), np.float32)
+    rng = np.random.default_rng(0)
+    bias = np.full(32, -1.0, np.float32)
+    a = rng.permuted(np.tile(np.arange(32), (64, 1)), axis=1)[:, :2]
+    bias[:] = np.float32(0.75)
+    for t in range(64):
+        l[t] = -9.0
+        l[t, a[t, 0]] = 12.0
+        l[t, a[t, 1]] = np.nextafter(np.float32(12.0), np.float32(13.0))
+    _check_select(l, 2, 1, bias)
+
+
+def test_a_row_does_not_depend_on_its_batch():
+    _announce("[gate] T=5000 against its rows one at a time")
+    l = _logits(5000, 256, 9)
+    g = m.make_gate(1, 8, 4, 1, True, 2.5)
+    b = np.random.default_rng(1).normal(scale=0.05, size=256).astype(np.float32)
+    idx, w = _select(l, 8, g, b)
+    for t in (0, 1, 77, 2048, 4999):
+        i1, w1 = _select(l[t:t + 1], 8, g, b)
+        np.testing.assert_array_equal(i1[0], idx[t])
+        np.testing.assert_array_equal(w1[0], w[t])
+
+
+def _grad_bound(l, idx, dw, score, renorm, scale):
+    """Roundings of moe_gate_backward's fp32 steps, per logit, times u (see the comments)."""
+    T, E = l.shape
+    k = idx.shape[1]
+    s = _ops.scores(l, score)
+    ok = (idx >= 0) & (idx < E)
+    p = np.where(ok, np.take_along_axis(s, np.where(ok, idx, 0), 1), 0.0)
+    g = np.where(ok, np.abs(scale * np.asarray(dw, np.float64)), 0.0)
+    ga = np.zeros((T, E))
+    for t, j in itertools.product(range(T), range(k)):
+        if ok[t, j]:
+            ga[t, idx[t, j]] += g[t, j]
+    fin = np.where(np.isfinite(l), l, 0.0)
+    A = np.abs(fin).max() * 2  # the largest |l - max|: each exp carries |l - max| u more
+    if score == 1 and not renorm:
+        return s * (1 - s) * ga * (12 + k)  # s, 1 - s: 4 each; the products and slots' sums
+    S = p.sum(1, keepdims=True)
+    if score == 1:
+        # s 4, S 10, q 15, sum of g q 23, difference and division 12, s (1 - s) 10, slots k
+        return np.divide(s * (1 - s) * (ga + (g * p).sum(1, keepdims=True) / np.where(S > 0, S, 1)),
+                         np.where(S > 0, S, 1)) * (48 + k)
+    if renorm:
+        q = np.divide(s, np.where(S > 0, S, 1))
+        gq = (g * p).sum(1, keepdims=True) / np.where(S > 0, S, 1)
+        # and the reference's own sum, whose terms cancel only to 2^-52 of them off the choice
+        ref64 = s * 2 * gq * (k + 8) * 2.0 ** -52
+        return q * (ga + gq * (ga > 0) * k) * (4 * A + 36 + k) + ref64 / U
+    # p: 2 A + E / 64 + 12; the sum of p g 8 more; the last product 2; slots k
+    return s * (ga + (g * p).sum(1, keepdims=True)) * (4 * A + E / 32 + 34 + k)
+
+
+@pytest.mark.parametrize("score,renorm", [(0, True), (0, False), (1, True), (1, False)])
+@pytest.mark.parametrize("T,E,k", SIZES)
+def test_gate_gradient(T, E, k, score, renorm):
+    _announce(f"[gate bwd] T={T} E={E} k={k} score={score} renorm={renorm}")
+    rng = np.random.default_rng(T * 3 + E)
+    for closed in (0.0, 0.2):
+        l = _logits(T, E, T + E, closed)
+        idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+        if k > 1:
+            idx[0, 1] = idx[0, 0]    # one expert twice
+        if T > 2:
+            idx[1, k - 1] = -1       # slots that name none
+            idx[2, 0] = E
+        dw = rng.normal(size=(T, k)).astype(np.float32)
+        ref = _ops.gate_backward(l, idx, dw, score, renorm, 2.5)
+        tol = _grad_bound(l, idx, dw, score, renorm, 2.5) * U + 1e-37
+        cfg, g = m.make_cfg(T, 256, E, k, 128), m.make_gate(score, 1, 1, 0, renorm, 2.5)
+        args = [torch.tensor(v, device=DEV) for v in (l, idx, dw)]
+        dl = torch.full((T, E), -7.0, device=DEV)
+        m.moe_gate_backward(cfg, g, *args, dl, False)
+        got = dl.cpu().numpy()
+        worst = float(np.max(np.abs(got - ref) / tol))
+        assert worst <= 1, worst
+        # added to what is there: one rounding of the sum more
+        base = torch.randn(T, E, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+        acc = base.clone()
+        m.moe_gate_backward(cfg, g, *args, acc, True)
+        assert torch.equal(acc, base + dl)
+
+
+ROUTER = [(1, 256, 1), (1, 256, 256), (5, 512, 3), (64, 256, 8), (127, 256, 129), (128, 512, 128),
+          (200, 768, 509), (1000, 256, 64), (333, 1024, 1024)]
+
+
+@pytest.mark.parametrize("T,d,E", ROUTER)
+def test_router_gradients(T, d, E):
+    _announce(f"[router bwd] T={T} d={d} E={E}")
+    g = torch.Generator().manual_seed(T + d + E)
+    x = torch.randn(T, d, generator=g).to(torch.bfloat16)
+    wr = (0.02 * torch.randn(E, d, generator=g)).to(torch.bfloat16)
+    # magnitudes over several binades, and whole rows without a gradient
+    dl = torch.randn(T, E, generator=g) * 2.0 ** torch.randint(-12, 4, (T, E), generator=g)
+    if T > 2:
+        dl[1] = 0.0
+    dx0 = torch.randn(T, d, generator=g).to(torch.bfloat16)
+    dw0 = torch.randn(E, d, generator=g)
+    cfg = m.make_cfg(T, d, E, 1, 128)
+    X, W, D = x.to(DEV), wr.to(DEV), dl.to(DEV)
+    x64, w64, d64 = x.double(), wr.double(), dl.double()
+    # fp32 sums of three exact products a term: an fp32 step (2^-23) for each addition
+    e_dx = (3 * E + 4) * 2.0 ** -23 * (d64.abs() @ w64.abs())
+    e_dw = (3 * T + 4) * 2.0 ** -23 * (d64.abs().t() @ x64.abs())
+    for acc in (False, True):
+        dx, dw = dx0.clone().to(DEV), dw0.clone().to(DEV)
+        m.moe_router_backward(cfg, X, W, D, dx, dw, acc, acc)
+        rx, rw = d64 @ w64, d64.t() @ x64
+        if acc:
+            rx, rw = rx + dx0.double(), rw + dw0.double()
+        ex = (dx.cpu().double() - rx).abs()
+        ew = (dw.cpu().double() - rw).abs()
+        assert (ex <= 2.0 ** -8 * (rx.abs() + e_dx) + e_dx + 2.0 ** -23 * rx.abs()).all()
+        assert (ew <= e_dw + 2.0 ** -23 * rw.abs()).all()
+        # one gradient at a time, the other's buffer not there
+        dx1, dw1 = dx0.clone().to(DEV), dw0.clone().to(DEV)
+        m.moe_router_backward(cfg, X, W, D, dx1, None, acc, acc)
+        m.moe_router_backward(cfg, X, W, D, None, dw1, acc, acc)
+        assert torch.equal(dx1, dx) and torch.equal(dw1, dw)
+
+
+def test_gate_and_router_calls_refuse_tensors_the_library_cannot_check():
+    cfg, g = m.make_cfg(8, 256, 16, 2, 128), m.make_gate()
+    l = torch.zeros(8, 16, device=DEV)
+    idx, w = torch.zeros(8, 2, dtype=torch.int32, device=DEV), torch.zeros(8, 2, device=DEV)
+    bad = [(l.double(), None, idx, w), (l.t(), None, idx, w), (l[:4], None, idx, w),
+           (l.cpu(), None, idx, w), (l, None, idx.long(), w), (l, w[0], idx, w)]
+    for args in bad:
+        with pytest.raises(m.MoeError) as e:
+            m.moe_gate_select(cfg, g, *args)
+        assert e.value.status == -1
