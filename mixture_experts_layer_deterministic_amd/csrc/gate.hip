@@ -11,6 +11,8 @@
 // The choice is discontinuous, so it is made on 64-bit values: in 32 bits two rounded scores
 // meet or swap where the definition keeps them apart. Where c orders as the logits do (no bias
 // and no sums of scores) the logits themselves are compared, which is exact.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 #include "ops.h"
@@ -18,207 +20,381 @@
 namespace moe {
 namespace {
 
-constexpr int kGateMaxE = 1024;
-constexpr int kGateQ = kGateMaxE / kWave;
 constexpr int kGateWaves = 4;
+constexpr double kClosed = -1.7e308;  // below every open choice score, above what is taken
 
-MOE_DEV float wave_max(float v) {
-#pragma unroll
-  for (int o = kWave / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+// x with lanes moved by a DPP control word; lanes without a source keep their own.
+template <int CTRL, int ROWS>
+MOE_DEV uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+MOE_DEV uint64_t dpp(uint64_t x) {
+  return (uint64_t)dpp<CTRL, ROWS>((uint32_t)x) |
+         ((uint64_t)dpp<CTRL, ROWS>((uint32_t)(x >> 32)) << 32);
+}
+template <int CTRL, int ROWS>
+MOE_DEV float dpp(float x) {
+  return __builtin_bit_cast(float, dpp<CTRL, ROWS>(__builtin_bit_cast(uint32_t, x)));
+}
+template <int CTRL, int ROWS>
+MOE_DEV double dpp(double x) {
+  return __builtin_bit_cast(double, dpp<CTRL, ROWS>(__builtin_bit_cast(uint64_t, x)));
+}
+MOE_DEV uint32_t read_lane(uint32_t x, int l) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, l);
+}
+MOE_DEV float read_lane(float x, int l) {
+  return __builtin_bit_cast(float, read_lane(__builtin_bit_cast(uint32_t, x), l));
+}
+MOE_DEV double read_lane(double x, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  return __builtin_bit_cast(double, (uint64_t)read_lane((uint32_t)u, l) |
+                                        ((uint64_t)read_lane((uint32_t)(u >> 32), l) << 32));
+}
+MOE_DEV uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+MOE_DEV float larger(float a, float b) { return fmaxf(a, b); }
+MOE_DEV double larger(double a, double b) { return __builtin_fmax(a, b); }
+struct Add {
+  template <class F>
+  MOE_DEV F operator()(F a, F b) const { return a + b; }
+};
+struct Larger {
+  template <class F>
+  MOE_DEV F operator()(F a, F b) const { return larger(a, b); }
+};
+// Over the wave, the same in every lane: within rows of 16 lanes by shifts, then lane 15's and
+// lane 31's totals move on. Lanes that a shift gives nothing add `none`.
+template <class Op, class F>
+MOE_DEV F wave_reduce(F v, F none) {
+  Op op;
+  const int lane = threadIdx.x % kWave;
+  F o;
+  o = dpp<0x111, 0xf>(v);
+  v = op(v, lane % 16 >= 1 ? o : none);
+  o = dpp<0x112, 0xf>(v);
+  v = op(v, lane % 16 >= 2 ? o : none);
+  o = dpp<0x114, 0xf>(v);
+  v = op(v, lane % 16 >= 4 ? o : none);
+  o = dpp<0x118, 0xf>(v);
+  v = op(v, lane % 16 >= 8 ? o : none);
+  o = dpp<0x142, 0xa>(v);
+  v = op(v, lane & 16 ? o : none);
+  o = dpp<0x143, 0xc>(v);
+  v = op(v, lane & 32 ? o : none);
+  return read_lane(v, 63);
+}
+// A maximum may meet a lane's own value again, so nothing has to be masked.
+template <class F>
+MOE_DEV F wave_max(F v) {
+  v = larger(v, dpp<0x111, 0xf>(v));
+  v = larger(v, dpp<0x112, 0xf>(v));
+  v = larger(v, dpp<0x114, 0xf>(v));
+  v = larger(v, dpp<0x118, 0xf>(v));
+  v = larger(v, dpp<0x142, 0xa>(v));
+  v = larger(v, dpp<0x143, 0xc>(v));
+  return read_lane(v, 63);
 }
 template <class F>
 MOE_DEV F wave_sum(F v) {
-#pragma unroll
-  for (int o = kWave / 2; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  return wave_reduce<Add>(v, F(0));
+}
+
+// exp(x) for the scores, x <= 709: e^x = 2^n e^r with n = rint(x / ln 2) and |r| <= ln(2) / 2,
+// e^r by its Taylor polynomial of degree 12 (the next term is below 1.8e-16), about 1e-15 in
+// all. 18 instructions; the library's exp also covers what does not occur here.
+MOE_DEV double exp64(double x) {
+  x = x > -745.0 ? x : -745.0;
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  double r = __builtin_fma(n, -6.93147180369123816490e-01, x);
+  r = __builtin_fma(n, -1.90821492927058770002e-10, r);
+  double p = 1.0 / 479001600.0;
+  p = __builtin_fma(p, r, 1.0 / 39916800.0);
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_ldexp(p, (int)n);
+}
+// 1 / y for normal y, to about one step: two Newton steps on the hardware's estimate.
+MOE_DEV double rcp64(double y) {
+  double r = __builtin_amdgcn_rcp(y);
+  r = __builtin_fma(__builtin_fma(-y, r, 1.0), r, r);
+  return __builtin_fma(__builtin_fma(-y, r, 1.0), r, r);
 }
 
 // Softmax numerator of logit l under the row's largest m: 1 at the largest (so +inf entries
 // share the row), 0 for a closed expert and in a row that holds nothing else.
-template <class F>
-MOE_DEV F soft_num(float l, float m) {
-  if (l == -INFINITY) return F(0);
-  if (l == m) return F(1);
-  return exp(F(l) - F(m));
+MOE_DEV double soft_num64(float l, float m) {
+  return l == -INFINITY ? 0.0 : l == m ? 1.0 : exp64((double)l - (double)m);
+}
+MOE_DEV float soft_num(float l, float m) {
+  return l == -INFINITY ? 0.f : l == m ? 1.f : expf(l - m);
+}
+MOE_DEV double sigmoid64(float l) {
+  // below -709 the sum leaves 64 bits' range and the score is 0
+  return l < -709.f ? 0.0 : rcp64(1.0 + exp64(-(double)l));
 }
 
-// One wave per token; choice scores and group scores in LDS.
+// a + b with b as it is stored otherwise: not fused with the product that made it.
+MOE_DEV float add_rounded(float a, float b) {
+#pragma clang fp contract(off)
+  return a + b;
+}
+
+// fp32 in an order that unsigned integers compare, and back; 0 lies below every value's.
+MOE_DEV uint32_t order32(float l) {
+  const uint32_t u = __float_as_uint(l + 0.f);  // -0 as +0
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+MOE_DEV float unorder32(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// One wave per token: lane l holds the V experts from V l on, so that the lowest lane and then
+// its lowest slot that hold a value hold the lowest index. k rounds each take the wave's largest
+// choice score (DPP shifts, no LDS) and the lowest expert that has it.
+// LOGIT: the scores order as the logits do; 32-bit keys, and 64-bit scores only of the chosen.
+// Groups that are whole, aligned runs of 2^i lanes are scored by lane exchanges, others in LDS.
+// Measured on 2048 x 256 (8 groups, sigmoid, bias) and 18944 x 512 (softmax): see the launch.
+template <int V, bool LOGIT>
 __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
     GateParams p, const float* __restrict__ logits, const float* __restrict__ bias, int T, int E,
-    int k, int32_t* __restrict__ idx, float* __restrict__ w) {
+    int k, int vec, int32_t* __restrict__ idx, float* __restrict__ w) {
+  using C = std::conditional_t<LOGIT, uint32_t, double>;
+  constexpr C kTaken = LOGIT ? C(0) : C(-INFINITY);
   extern __shared__ double gate_lds[];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int t = blockIdx.x * kGateWaves + wave;
   const bool live = t < T;
-  const int G = p.groups, gs = E / G;
-  double* cs = gate_lds + (size_t)wave * (E + G);
-  double* gsc = cs + E;
+  const int e0 = lane * V;
   const float* row = logits + (size_t)(live ? t : 0) * E;
-  const bool by_logit = !bias && (G == 1 || !p.top2);
-  float l[kGateQ];
+  float l[V];
+  if (V >= 4 && vec) {  // rows of whole 16-byte pieces
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+      const f32x4 x = e0 + v < E ? *reinterpret_cast<const f32x4*>(row + e0 + v)
+                                 : f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < 4 && v + i < V; ++i) l[v + i] = x[i];
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = e0 + v < E ? row[e0 + v] : -INFINITY;
+  }
   float m = -INFINITY;
 #pragma unroll
-  for (int q = 0; q < kGateQ; ++q) {
-    const int e = lane + kWave * q;
-    float v = e < E ? row[e] : -INFINITY;
-    l[q] = v == v ? v : -INFINITY;
-    m = fmaxf(m, l[q]);
+  for (int v = 0; v < V; ++v) {
+    l[v] = l[v] == l[v] ? l[v] : -INFINITY;
+    m = fmaxf(m, l[v]);
   }
-  m = wave_max(m);
-  double sc[kGateQ], z = 0;
-#pragma unroll
-  for (int q = 0; q < kGateQ; ++q) {
-    if (p.softmax) {
-      sc[q] = soft_num<double>(l[q], m);
-      z += sc[q];
-    } else {
-      sc[q] = l[q] == -INFINITY ? 0.0 : 1.0 / (1.0 + exp(-(double)l[q]));
-    }
-  }
+  double zi = 0;  // 1 / sum of the softmax numerators (0 for a row of closed experts)
   if (p.softmax) {
-    z = wave_sum(z);
+    m = wave_max(m);
+    if (!LOGIT || !p.renorm) {  // renormalised weights need no sum over the row
+      double z = 0;
 #pragma unroll
-    for (int q = 0; q < kGateQ; ++q) sc[q] = z > 0 ? sc[q] / z : 0.0;
-  }
-  double c[kGateQ];
-#pragma unroll
-  for (int q = 0; q < kGateQ; ++q) {
-    const int e = lane + kWave * q;
-    c[q] = l[q] == -INFINITY ? -INFINITY
-           : by_logit        ? (double)l[q]
-                             : sc[q] + (bias ? (double)bias[e < E ? e : 0] : 0.0);
-    if (e < E) cs[e] = c[q];
-  }
-  __syncthreads();
-  for (int g = lane; g < G; g += kWave) {
-    double a = -INFINITY, b = -INFINITY;
-    for (int i = 0; i < gs; ++i) {
-      const double v = cs[g * gs + i];
-      if (v > a) {
-        b = a;
-        a = v;
-      } else if (v > b) {
-        b = v;
-      }
+      for (int v = 0; v < V; ++v) z += soft_num64(l[v], m);
+      z = wave_sum(z);
+      zi = z > 0 ? rcp64(z) : 0.0;
     }
-    gsc[g] = p.top2 && b != -INFINITY ? a + b : a;
   }
-  __syncthreads();
-  // rounds of an argmax over the wave, the lower index first among equals
-  auto best = [&](double bv, int be) {
+  C c[V];
 #pragma unroll
-    for (int o = kWave / 2; o; o >>= 1) {
-      const double ov = __shfl_xor(bv, o);
-      const int oe = __shfl_xor(be, o);
-      if (oe >= 0 && (be < 0 || ov > bv || (ov == bv && oe < be))) {
-        bv = ov;
-        be = oe;
-      }
+  for (int v = 0; v < V; ++v) {
+    if constexpr (LOGIT) {
+      c[v] = e0 + v < E ? order32(l[v]) : kTaken;
+    } else {
+      const double s = p.softmax ? soft_num64(l[v], m) * zi : sigmoid64(l[v]);
+      const double x = s + (bias ? (double)bias[min(e0 + v, E - 1)] : 0.0);
+      c[v] = e0 + v >= E ? kTaken : l[v] > -INFINITY && x > kClosed ? x : kClosed;
     }
-    return be;
-  };
-  uint32_t taken = 0;  // bit q: expert lane + 64 q selected or out of reach
-  if (G > 1 && p.topk_groups < G) {
-    uint32_t gt = 0;  // bit i: group lane + 64 i selected
-    for (int r = 0; r < p.topk_groups; ++r) {
-      double bv = -INFINITY;
-      int be = -1;
-      for (int i = 0; lane + kWave * i < G; ++i) {
-        const double v = gsc[lane + kWave * i];
-        if (!((gt >> i) & 1u) && (be < 0 || v > bv)) {
-          bv = v;
-          be = lane + kWave * i;
+  }
+  // groups
+  const int G = p.groups, gs = E / G;
+  if (G > 1 && p.topk_groups < G) {  // the same for the whole grid
+    const int lpg = gs / V;
+    if (gs % V == 0 && (lpg & (lpg - 1)) == 0) {
+      C a = c[0], b = kTaken;  // the lane's two largest, then its group's
+#pragma unroll
+      for (int v = 1; v < V; ++v) {
+        const C lo = c[v] > a ? a : c[v];
+        a = larger(a, c[v]);
+        b = larger(b, lo);
+      }
+      for (int o = 1; o < lpg; o <<= 1) {
+        const C a1 = __shfl_xor(a, o), b1 = __shfl_xor(b, o);
+        const C lo = a1 > a ? a : a1;
+        a = larger(a, a1);
+        b = larger(larger(b, b1), lo);
+      }
+      if constexpr (!LOGIT)
+        if (p.top2 && b > kClosed) a += b;
+      const int mine = lane / lpg;
+      int rank = 0;  // groups that go before this lane's
+      for (int g = 0; g < G; ++g) {
+        const C o = read_lane(a, g * lpg);
+        rank += o > a || (o == a && g < mine);
+      }
+      if (mine >= G || rank >= p.topk_groups) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] = kTaken;
+      }
+    } else {
+      double* cs = gate_lds + (size_t)wave * (E + G);
+      double* gsc = cs + E;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (e0 + v < E) cs[e0 + v] = (double)c[v];
+      __syncthreads();
+      for (int g = lane; g < G; g += kWave) {
+        double a = -INFINITY, b = -INFINITY;
+        for (int i = 0; i < gs; ++i) {
+          const double x = cs[g * gs + i];
+          const double lo = x > a ? a : x;
+          a = larger(a, x);
+          b = larger(b, lo);
         }
+        if constexpr (!LOGIT)
+          if (p.top2 && b > kClosed) a += b;
+        gsc[g] = a;
       }
-      be = best(bv, be);
-      if (be % kWave == lane) gt |= 1u << (be / kWave);
-    }
-    __syncthreads();
-    for (int i = 0; lane + kWave * i < G; ++i) gsc[lane + kWave * i] = (gt >> i) & 1u ? 1.0 : 0.0;
-    __syncthreads();
+      __syncthreads();
+      uint32_t stay = 0;  // bit i: group lane + 64 i
+      for (int i = 0; lane + kWave * i < G; ++i) {
+        const int g = lane + kWave * i;
+        const double a = gsc[g];
+        int rank = 0;
+        for (int h = 0; h < G; ++h) {
+          const double o = gsc[h];
+          rank += o > a || (o == a && h < g);
+        }
+        if (rank < p.topk_groups) stay |= 1u << i;
+      }
+      __syncthreads();
+      for (int i = 0; lane + kWave * i < G; ++i) gsc[lane + kWave * i] = (stay >> i) & 1u;
+      __syncthreads();
 #pragma unroll
-    for (int q = 0; q < kGateQ; ++q) {
-      const int e = lane + kWave * q;
-      if (e < E && gsc[e / gs] == 0.0) taken |= 1u << q;
+      for (int v = 0; v < V; ++v)
+        if (e0 + v < E && gsc[(e0 + v) / gs] == 0.0) c[v] = kTaken;
     }
   }
-  double mine = 0;
+  float my_l = -INFINITY;
   int my_e = 0;
   for (int j = 0; j < k; ++j) {
-    double bv = -INFINITY;
-    int be = -1;
+    C best = c[0];
 #pragma unroll
-    for (int q = 0; q < kGateQ; ++q) {
-      const int e = lane + kWave * q;
-      if (e < E && !((taken >> q) & 1u) && (be < 0 || c[q] > bv)) {
-        bv = c[q];
-        be = e;
-      }
-    }
-    be = best(bv, be);
-    double s = 0;
+    for (int v = 1; v < V; ++v) best = larger(best, c[v]);
+    const C top = wave_max(best);
+    const int owner = __builtin_ctzll(__ballot(best == top));
+    int at = 0;
+    float lv = l[0];
 #pragma unroll
-    for (int q = 0; q < kGateQ; ++q)
-      if (lane + kWave * q == be) {
-        s = sc[q];
-        taken |= 1u << q;
-      }
-    s = __shfl(s, be % kWave);
-    if (lane == j) {
-      mine = s;
-      my_e = be;
+    for (int v = V - 1; v >= 0; --v) {
+      const bool hit = c[v] == top;
+      at = hit ? v : at;
+      lv = hit ? l[v] : lv;
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = lane == owner && at == v ? kTaken : c[v];
+    const float lj = read_lane(lv, owner);
+    const int ej = owner * V + __builtin_amdgcn_readlane(at, owner);
+    my_l = lane == j ? lj : my_l;
+    my_e = lane == j ? ej : my_e;
   }
-  double sum = 0;
-  for (int j = 0; j < k; ++j) sum += __shfl(mine, j);
+  double s = 0;  // lane j: the score of choice j
+  if (lane < k) {
+    s = !p.softmax ? sigmoid64(my_l) : soft_num64(my_l, m);
+    if (p.softmax && zi > 0) s *= zi;
+  }
+  if (p.renorm) {
+    const double sum = wave_sum(s);
+    s = sum > 0 ? s / sum : 0.0;
+  } else if (p.softmax && !(zi > 0)) {
+    s = 0;
+  }
   if (live && lane < k) {
-    double v = mine;
-    if (p.renorm) v = sum > 0 ? v / sum : 0.0;
     idx[(size_t)t * k + lane] = my_e;
-    w[(size_t)t * k + lane] = (float)(v * (double)p.scale);
+    w[(size_t)t * k + lane] = (float)(s * (double)p.scale);
   }
 }
 
-// One wave per token. Lane j < k takes slot j, then every lane writes its logits' gradients.
+// One wave per token. Lane j < k takes slot j:
 //   g_j = scale dw_j
 //   sigmoid:                 dl_j = g_j s_j (1 - s_j)
 //   sigmoid, renormalised:   dl_j = (g_j - sum_i g_i q_i) / S  s_j (1 - s_j),  q = s / S
 //   softmax, renormalised:   dl_j = q_j (g_j - sum_i q_i g_i)
 //   softmax:                 dl_e = p_e ([e selected] g_e - sum_i p_i g_i), for every e
-// Slots that name one expert twice add up, in ascending j; a slot outside [0, E) counts nothing.
+// The slots' values are scattered over a row of zeros in LDS and the row leaves in 16-byte
+// pieces. Slots that name one expert twice (found by each slot writing its number to its
+// expert's place and reading it back) are added one after the other, in ascending j; a slot
+// outside [0, E) counts nothing. DENSE, softmax without renorm, also reads the row of logits.
+template <int V, bool DENSE>
 __global__ void __launch_bounds__(kGateWaves* kWave) gate_backward_kernel(
     GateParams p, const float* __restrict__ logits, const int32_t* __restrict__ idx,
-    const float* __restrict__ dw, int T, int E, int k, float* __restrict__ dl, int accumulate) {
+    const float* __restrict__ dw, int T, int E, int k, int vec, float* __restrict__ dl,
+    int accumulate) {
+  __shared__ __align__(16) float rows[kGateWaves][V * kWave];
   const int lane = threadIdx.x % kWave;
-  const int t = blockIdx.x * kGateWaves + threadIdx.x / kWave;
-  if (t >= T) return;  // whole waves leave; no barrier below
-  const float* row = logits + (size_t)t * E;
-  float* out = dl + (size_t)t * E;
-  int e = lane < k ? idx[(size_t)t * k + lane] : -1;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int t = blockIdx.x * kGateWaves + wave;
+  const bool live = t < T;
+  const size_t tt = live ? t : 0;
+  const float* row = logits + tt * E;
+  float* out = dl + tt * E;
+  const int e0 = lane * V;
+  float l[V];
+  if constexpr (DENSE) {
+    if (V >= 4 && vec) {
+#pragma unroll
+      for (int v = 0; v < V; v += 4) {
+        const f32x4 x = e0 + v < E ? *reinterpret_cast<const f32x4*>(row + e0 + v)
+                                   : f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 4 && v + i < V; ++i) l[v + i] = x[i];
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) l[v] = e0 + v < E ? row[e0 + v] : -INFINITY;
+    }
+  }
+  int e = lane < k ? idx[tt * k + lane] : -1;
   if (e < 0 || e >= E) e = -1;
   float lj = e >= 0 ? row[e] : -INFINITY;
-  if (!(lj == lj)) lj = -INFINITY;
-  const float g = e >= 0 ? p.scale * dw[(size_t)t * k + lane] : 0.f;
-  const bool dense = p.softmax && !p.renorm;
-  float m = -INFINITY, z = 0.f, v = 0.f, cross = 0.f;
-  if (dense) {
-    for (int i = lane; i < E; i += kWave) m = fmaxf(m, row[i]);  // fmaxf drops a NaN
+  lj = lj == lj ? lj : -INFINITY;
+  const float g = e >= 0 ? p.scale * dw[tt * k + lane] : 0.f;
+  float val, zi = 0.f, m = -INFINITY, cross = 0.f;
+  if constexpr (DENSE) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      l[v] = l[v] == l[v] ? l[v] : -INFINITY;
+      m = fmaxf(m, l[v]);
+    }
     m = wave_max(m);
-    for (int i = lane; i < E; i += kWave) {
-      const float x = row[i];
-      if (x == x) z += soft_num<float>(x, m);
+    float z = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      l[v] = soft_num(l[v], m);
+      z += l[v];
     }
     z = wave_sum(z);
-    z = z > 0 ? 1.f / z : 0.f;
-    cross = wave_sum(soft_num<float>(lj, m) * z * g);
-    v = g;
+    zi = z > 0 ? 1.f / z : 0.f;
+    cross = wave_sum(soft_num(lj, m) * zi * g);
+    val = g;
   } else if (p.softmax) {
     m = wave_max(lj);
-    const float n = soft_num<float>(lj, m);
+    const float n = soft_num(lj, m);
     const float S = wave_sum(n);
     const float q = S > 0 ? n / S : 0.f;
-    v = q * (g - wave_sum(q * g));
+    val = q * (g - wave_sum(q * g));
   } else {
     const float s = lj == -INFINITY ? 0.f : 1.f / (1.f + expf(-lj));
     const float s1 = lj == -INFINITY ? 0.f : 1.f / (1.f + expf(lj));  // 1 - s without its loss
@@ -227,32 +403,88 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_backward_kernel(
       const float S = wave_sum(s);
       ds = S > 0 ? (g - wave_sum(g * (s / S))) / S : 0.f;
     }
-    v = ds * s * s1;
+    val = ds * s * s1;
   }
-  for (int i = lane; i < E; i += kWave) {
-    float a = 0.f;
-    for (int j = 0; j < k; ++j) {
-      const int ej = __builtin_amdgcn_readlane(e, j);
-      const float vj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), j));
-      if (ej == i) a += vj;
-    }
-    if (dense) {
-      const float x = row[i];
-      a = x == x ? soft_num<float>(x, m) * z * (a - cross) : 0.f;
-    }
-    out[i] = accumulate ? out[i] + a : a;
+  float* mine = rows[wave];
+  int* marks = reinterpret_cast<int*>(mine);
+  if (e >= 0) marks[e] = lane;
+  __syncthreads();
+  const bool twice = __any(e >= 0 && marks[e] != lane);
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) mine[v * kWave + lane] = 0.f;
+  __syncthreads();
+  if (!twice) {
+    if (e >= 0) mine[e] = val;
+  } else {
+    for (int j = 0; j < k; ++j)
+      if (lane == j && e >= 0) mine[e] += val;
   }
+  __syncthreads();
+  if (!live) return;
+  auto final = [&](int v, float a) { return DENSE ? l[v] * zi * (a - cross) : a; };
+  if (V >= 4 && vec) {
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+      if (e0 + v >= E) break;
+      f32x4 x = *reinterpret_cast<const f32x4*>(mine + e0 + v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = final(v + i < V ? v + i : 0, x[i]);
+      f32x4* o = reinterpret_cast<f32x4*>(out + e0 + v);
+      if (accumulate) {
+        const f32x4 q = *o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = add_rounded(q[i], x[i]);
+      }
+      *o = x;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (e0 + v >= E) break;
+      const float x = final(v, mine[e0 + v]);
+      out[e0 + v] = accumulate ? add_rounded(out[e0 + v], x) : x;
+    }
+  }
+}
+
+// Calls f with the experts a lane holds as a constant: the least power of two that covers E.
+template <class Fn>
+void with_experts(int E, Fn&& f) {
+  if (E <= 64) f(std::integral_constant<int, 1>{});
+  else if (E <= 128) f(std::integral_constant<int, 2>{});
+  else if (E <= 256) f(std::integral_constant<int, 4>{});
+  else if (E <= 512) f(std::integral_constant<int, 8>{});
+  else f(std::integral_constant<int, 16>{});
+}
+// Whether every row of [T, E] fp32 starts on a 16-byte boundary and holds whole pieces.
+int whole_pieces(const void* p, int E) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && E % 4 == 0;
 }
 
 }  // namespace
 
 hipError_t launch_gate_select(const GateParams& p, const float* logits, const float* bias, int T,
                               int E, int k, int32_t* idx, float* w, hipStream_t s) {
+  const bool by_logit = !bias && (p.groups == 1 || p.topk_groups == p.groups || !p.top2);
+  const int vec = whole_pieces(logits, E);
+  const dim3 grid((T + kGateWaves - 1) / kGateWaves), block(kGateWaves * kWave);
   {
     TraceScope trace("gate_select", s);
-    hipLaunchKernelGGL(gate_select_kernel, dim3((T + kGateWaves - 1) / kGateWaves),
-                       dim3(kGateWaves * kWave), kGateWaves * (E + p.groups) * sizeof(double), s,
-                       p, logits, bias, T, E, k, idx, w);
+    with_experts(E, [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      // the groups' LDS, where they are not whole runs of lanes
+      const int gs = E / p.groups, lpg = gs / V;
+      const bool lds = p.groups > 1 && p.topk_groups < p.groups &&
+                       (gs % V != 0 || (lpg & (lpg - 1)) != 0);
+      const size_t bytes = lds ? kGateWaves * (E + p.groups) * sizeof(double) : 0;
+      if (by_logit)
+        hipLaunchKernelGGL((gate_select_kernel<V, true>), grid, block, bytes, s, p, logits, bias,
+                           T, E, k, vec, idx, w);
+      else
+        hipLaunchKernelGGL((gate_select_kernel<V, false>), grid, block, bytes, s, p, logits, bias,
+                           T, E, k, vec, idx, w);
+    });
   }
   return hipGetLastError();
 }
@@ -260,11 +492,19 @@ hipError_t launch_gate_select(const GateParams& p, const float* logits, const fl
 hipError_t launch_gate_backward(const GateParams& p, const float* logits, const int32_t* idx,
                                 const float* dw, int T, int E, int k, float* dlogits,
                                 int accumulate, hipStream_t s) {
+  const int vec = whole_pieces(dlogits, E) && whole_pieces(logits, E);
+  const dim3 grid((T + kGateWaves - 1) / kGateWaves), block(kGateWaves * kWave);
   {
     TraceScope trace("gate_backward", s);
-    hipLaunchKernelGGL(gate_backward_kernel, dim3((T + kGateWaves - 1) / kGateWaves),
-                       dim3(kGateWaves * kWave), 0, s, p, logits, idx, dw, T, E, k, dlogits,
-                       accumulate);
+    with_experts(E, [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      if (p.softmax && !p.renorm)
+        hipLaunchKernelGGL((gate_backward_kernel<V, true>), grid, block, 0, s, p, logits, idx, dw,
+                           T, E, k, vec, dlogits, accumulate);
+      else
+        hipLaunchKernelGGL((gate_backward_kernel<V, false>), grid, block, 0, s, p, logits, idx, dw,
+                           T, E, k, vec, dlogits, accumulate);
+    });
   }
   return hipGetLastError();
 }
