@@ -55,6 +55,8 @@ MOE_DEV double read_lane(double x, int l) {
 MOE_DEV uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
 MOE_DEV float larger(float a, float b) { return fmaxf(a, b); }
 MOE_DEV double larger(double a, double b) { return __builtin_fmax(a, b); }
+MOE_DEV uint32_t smaller(uint32_t a, uint32_t b) { return min(a, b); }
+MOE_DEV double smaller(double a, double b) { return __builtin_fmin(a, b); }
 struct Add {
   template <class F>
   MOE_DEV F operator()(F a, F b) const { return a + b; }
@@ -84,7 +86,21 @@ MOE_DEV F wave_reduce(F v, F none) {
   v = op(v, lane & 32 ? o : none);
   return read_lane(v, 63);
 }
-// A maximum may meet a lane's own value again, so nothing has to be masked.
+// A maximum may meet a lane's own value again, so nothing has to be masked. Of unsigned numbers
+// 0 is neutral: the shift then merges into the maximum, one instruction a step.
+template <int CTRL, int ROWS>
+MOE_DEV uint32_t dpp0(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false);
+}
+MOE_DEV uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp0<0x111, 0xf>(v));
+  v = max(v, dpp0<0x112, 0xf>(v));
+  v = max(v, dpp0<0x114, 0xf>(v));
+  v = max(v, dpp0<0x118, 0xf>(v));
+  v = max(v, dpp0<0x142, 0xa>(v));
+  v = max(v, dpp0<0x143, 0xc>(v));
+  return read_lane(v, 63);
+}
 template <class F>
 MOE_DEV F wave_max(F v) {
   v = larger(v, dpp<0x111, 0xf>(v));
@@ -104,7 +120,7 @@ MOE_DEV F wave_sum(F v) {
 // e^r by its Taylor polynomial of degree 12 (the next term is below 1.8e-16), about 1e-15 in
 // all. 18 instructions; the library's exp also covers what does not occur here.
 MOE_DEV double exp64(double x) {
-  x = x > -745.0 ? x : -745.0;
+  x = __builtin_fmax(x, -745.0);
   const double n = __builtin_rint(x * 1.4426950408889634);
   double r = __builtin_fma(n, -6.93147180369123816490e-01, x);
   r = __builtin_fma(n, -1.90821492927058770002e-10, r);
@@ -133,14 +149,16 @@ MOE_DEV double rcp64(double y) {
 // Softmax numerator of logit l under the row's largest m: 1 at the largest (so +inf entries
 // share the row), 0 for a closed expert and in a row that holds nothing else.
 MOE_DEV double soft_num64(float l, float m) {
-  return l == -INFINITY ? 0.0 : l == m ? 1.0 : exp64((double)l - (double)m);
+  const double x = exp64((double)l - (double)m);  // no branch: the constants stay in registers
+  return l == -INFINITY ? 0.0 : l == m ? 1.0 : x;
 }
 MOE_DEV float soft_num(float l, float m) {
   return l == -INFINITY ? 0.f : l == m ? 1.f : expf(l - m);
 }
 MOE_DEV double sigmoid64(float l) {
   // below -709 the sum leaves 64 bits' range and the score is 0
-  return l < -709.f ? 0.0 : rcp64(1.0 + exp64(-(double)l));
+  const double x = rcp64(1.0 + exp64(-(double)fmaxf(l, -709.f)));
+  return l < -709.f ? 0.0 : x;
 }
 
 // a + b with b as it is stored otherwise: not fused with the product that made it.
@@ -158,9 +176,29 @@ MOE_DEV float unorder32(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// v[0] >= v[1] >= .., by merging sorted halves (odd-even merges: 1, 5, 19, 63 exchanges).
+template <int V, class C>
+MOE_DEV void sort_down(C (&v)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const C a = v[i + j], b = v[i + j + q];
+            v[i + j] = larger(a, b);
+            v[i + j + q] = smaller(a, b);
+          }
+}
+
 // One wave per token: lane l holds the V experts from V l on, so that the lowest lane and then
-// its lowest slot that hold a value hold the lowest index. k rounds each take the wave's largest
-// choice score (DPP shifts, no LDS) and the lowest expert that has it.
+// its lowest slot that hold a value hold the lowest index. Each lane sorts its V choice scores;
+// k rounds then take the wave's largest head (DPP shifts, no LDS) from the lowest lane that has
+// it. A round costs the same for any V but for the lane's V moves; which of its V experts a lane
+// gave is worked out once, for all k choices together.
 // LOGIT: the scores order as the logits do; 32-bit keys, and 64-bit scores only of the chosen.
 // Groups that are whole, aligned runs of 2^i lanes are scored by lane exchanges, others in LDS.
 // Measured on 2048 x 256 (8 groups, sigmoid, bias) and 18944 x 512 (softmax): see the launch.
@@ -287,29 +325,49 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
         if (e0 + v < E && gsc[(e0 + v) / gs] == 0.0) c[v] = kTaken;
     }
   }
-  float my_l = -INFINITY;
-  int my_e = 0;
+  // rounds: the wave's largest head, from the lowest lane that has it
+  C h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = c[v];
+  sort_down(h);
+  C my_c = kTaken, last = kTaken;
+  int my_at = 0, owner = -1, occ = 0;  // lane j: owner | occ << 8 of choice j
   for (int j = 0; j < k; ++j) {
-    C best = c[0];
+    const C top = wave_max(h[0]);
+    const int o = __builtin_ctzll(__ballot(h[0] == top));
+    occ = o == owner && top == last ? occ + 1 : 0;  // the same value again in the same lane
+    owner = o;
+    last = top;
+    my_c = lane == j ? top : my_c;
+    my_at = lane == j ? o | occ << 8 : my_at;
+    const bool pop = lane == o;
 #pragma unroll
-    for (int v = 1; v < V; ++v) best = larger(best, c[v]);
-    const C top = wave_max(best);
-    const int owner = __builtin_ctzll(__ballot(best == top));
-    int at = 0;
-    float lv = l[0];
-#pragma unroll
-    for (int v = V - 1; v >= 0; --v) {
-      const bool hit = c[v] == top;
-      at = hit ? v : at;
-      lv = hit ? l[v] : lv;
+    for (int v = 0; v + 1 < V; ++v) {
+      C n = h[v + 1];
+      asm("" : "+v"(n));  // else the compiler selects among all V by an index, at V times the cost
+      h[v] = pop ? n : h[v];
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) c[v] = lane == owner && at == v ? kTaken : c[v];
-    const float lj = read_lane(lv, owner);
-    const int ej = owner * V + __builtin_amdgcn_readlane(at, owner);
-    my_l = lane == j ? lj : my_l;
-    my_e = lane == j ? ej : my_e;
+    h[V - 1] = pop ? kTaken : h[V - 1];
   }
+  // lane j finds its expert: the occ-th of the owner's values that equal its own
+  int my_e = 0;
+  {
+    const int o = my_at & 0xff;
+    const int skip = my_at >> 8;
+    int at = 0;
+    int seen = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool hit = __shfl(c[v], o) == my_c;
+      at = hit && seen == skip ? v : at;
+      seen += hit;
+    }
+    my_e = o * V + at;
+  }
+  float my_l;
+  if constexpr (LOGIT) my_l = unorder32(my_c);
+  else my_l = lane < k ? row[my_e] : -INFINITY;
+  my_l = my_l == my_l ? my_l : -INFINITY;
   double s = 0;  // lane j: the score of choice j
   if (lane < k) {
     s = !p.softmax ? sigmoid64(my_l) : soft_num64(my_l, m);
