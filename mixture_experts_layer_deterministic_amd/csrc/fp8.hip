@@ -11,6 +11,8 @@
 // largest, the groups' sums then in fp32. On quantised Gaussian operands that is 1.3e-5 of the
 // result in rms, 300 times less than the bf16 rounding of the output; bf16 MFMAs of the widened
 // codes would keep 1e-8 at half the rate.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 #include "ops.h"
@@ -160,88 +162,211 @@ MOE_DEV RowTile find_rows(const int32_t* __restrict__ offsets, int M, int E, int
 }
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
-MOE_DEV int fp8_swz(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
-MOE_DEV i32x8 fp8_frag(const uint8_t* tile, int row, int g) {
-  const i32x4 lo = *reinterpret_cast<const i32x4*>(tile + fp8_swz(row, g));
-  const i32x4 hi = *reinterpret_cast<const i32x4*>(tile + fp8_swz(row, 4 + g));
+// LDS tiles of 128-byte rows (one block of K), 16-byte chunk c of row r at c ^ (r & 7), so that
+// fragment reads spread over the banks. A lane's operand of the 16 x 16 x 128 MFMA: chunks g and
+// 4 + g of row l % 16 of a block of 16 rows, g = l / 16. Rows and columns take the same k in the
+// same place, which is all a sum over the whole block needs. The two byte offsets are the same
+// in every row block, so the blocks differ by constants.
+struct FragAt {
+  int lo, hi;
+};
+MOE_DEV FragAt frag_at(int lane) {
+  const int r = lane % 16, g = lane / 16;
+  return {r * 128 + ((g ^ (r & 7)) << 4), r * 128 + (((4 + g) ^ (r & 7)) << 4)};
+}
+MOE_DEV i32x8 fp8_frag(const uint8_t* rows16, const FragAt& f) {
+  const i32x4 lo = *reinterpret_cast<const i32x4*>(rows16 + f.lo);
+  const i32x4 hi = *reinterpret_cast<const i32x4*>(rows16 + f.hi);
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
+// One block's product of 16 rows and 16 columns; with the columns first, lane l gets row l % 16,
+// columns 4 (l / 16) .. + 3. (Both scale operands 0: the unscaled instruction.)
+MOE_DEV f32x4 fp8_mfma(const i32x8& b, const i32x8& a) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0,
+                                                          0, 0, 0, 0);
+}
+MOE_DEV __amdgpu_buffer_rsrc_t fp8_rsrc(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00020000);
+}
+// 16 bytes a lane straight into LDS, at lds + 16 lane: 8 rows of 128 bytes a wave.
+MOE_DEV void fp8_load_lds(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
+                                           voff, soff, 0, 0);
+}
+// The chunk a lane fetches into its place of those 8 rows.
+MOE_DEV uint32_t fp8_piece(int lane) { return 16u * ((lane % 8) ^ (lane / 8)); }
 
-// 128 x 128 tiles, four waves of 64 x 64, a step per 128-deep block.
-__global__ void __launch_bounds__(256, 2) fp8_gemm_kernel(const Fp8GemmArgs a) {
-  __shared__ __align__(16) uint8_t lds[2 * kQB * 128];
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int wm = wave / 2, wn = wave % 2, r16 = lane % 16, g = lane / 16;
-  const int nN = a.N / kQB, nK = a.K / kQB;
-  const int n0 = blockIdx.x % nN;
-  const RowTile t = find_rows<128>(a.offsets, a.M, a.E, blockIdx.x / nN);
-  if (t.rows <= 0) return;
-  const uint8_t* ap[4];
-  const uint8_t* bp[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int v = tid + 256 * j, r = v / 8;
-    ap[j] = a.a + (size_t)(t.row0 + min(r, t.rows - 1)) * a.K + v % 8 * 16;
-    bp[j] = a.b + ((size_t)t.e * a.N + (size_t)n0 * kQB + r) * a.K + v % 8 * 16;
+constexpr int kVm4Lgkm0 = 0x0074;  // s_waitcnt vmcnt(4) lgkmcnt(0)
+constexpr int kVm0Lgkm0 = 0x0070;
+
+// Few rows an expert: the weights' stream is what takes the time. BM x 128 tiles, four waves of
+// BM x 32; 128 bytes of K a step go from memory straight into LDS, the weights SB - 1 steps ahead
+// and the rows one. The rows' scales ride in registers, one row a lane, and reach the lanes that
+// need them through the LDS crossbar.
+//  * BM = 128, three weight stages: 80 KB, two workgroups a CU to the last byte of its LDS, with
+//    64 KB of weights on their way.
+//  * BM = 32, two weight stages: 40 KB, four workgroups a CU with as much on their way; of use
+//    where there are few tiles (a serving batch), which then all run at once.
+// A tile's K loop is compiled for 2, 4 and 8 blocks of 16 rows and runs the least that hold its
+// rows: no MFMA, LDS read or load for the rest. (A test per block inside the loop made the
+// compiler keep both sides' accumulators, 1 KB a lane of them in memory.)
+// A wave's loads complete in order; a step issues rows, scales, then weights, so at its top the
+// weight loads issued last may be missing if they are a step further ahead. Loads past the last
+// block read it again into a stage nobody reads, so the counts hold.
+template <int SB>
+struct StreamLds {
+  uint8_t *a0, *a1, *b0, *b1, *b2;
+  template <int S>
+  MOE_DEV uint8_t* a() const {
+    if constexpr (S == 0) return a0;
+    else return a1;
   }
-  const float* sb = a.sb + ((size_t)t.e * nN + n0) * nK;
-  int srow[4];
+  template <int S>
+  MOE_DEV uint8_t* b() const {
+    if constexpr (S == 0) return b0;
+    else if constexpr (S == 1) return b1;
+    else return b2;
+  }
+};
+template <int NMB, int SB>
+struct StreamTile {
+  static constexpr int AJ = NMB / 2;          // row loads a wave: 8 rows each
+  static constexpr int SJ = (NMB + 3) / 4;    // scale registers: 64 rows each
+  __amdgpu_buffer_rsrc_t ra, rb;
+  uint32_t ao[AJ], bo[4];
+  const float* sp[SJ];
+  const float* sb;
+  size_t M;
+  float sv[SJ];
+  int nK, wave, r16;
+  FragAt f;
+  f32x4 acc[NMB][2];
+
+  template <int S>
+  MOE_DEV void issue_a(const StreamLds<SB>& L, int kb) {
+    const uint32_t step = (uint32_t)min(kb, nK - 1) * 128;
 #pragma unroll
-  for (int mb = 0; mb < 4; ++mb) srow[mb] = t.row0 + min(wm * 64 + mb * 16 + r16, t.rows - 1);
-  f32x4 acc[4][4];
+    for (int j = 0; j < AJ; ++j)
+      fp8_load_lds(ra, ao[j], step, L.template a<S>() + (wave * AJ + j) * 1024);
+  }
+  template <int S>
+  MOE_DEV void issue_b(const StreamLds<SB>& L, int kb) {
+    const uint32_t step = (uint32_t)min(kb, nK - 1) * 128;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j)
+      fp8_load_lds(rb, bo[j], step, L.template b<S>() + (wave * 4 + j) * 1024);
+  }
+  MOE_DEV void issue_s(int kb) {
+    const size_t at = (size_t)min(kb, nK - 1) * M;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  i32x4 av[4], bv[4];
-  auto load = [&](int kb) {
+    for (int j = 0; j < SJ; ++j) sv[j] = sp[j][at];
+  }
+  template <int S>  // S: the step's number modulo the stages' common cycle
+  MOE_DEV void step(const StreamLds<SB>& L, int kb) {
+    __builtin_amdgcn_s_waitcnt(SB == 3 ? kVm4Lgkm0 : kVm0Lgkm0);
+    __builtin_amdgcn_s_barrier();
+    const float sbk = sb[kb];
+    float s[NMB];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      bv[j] = *reinterpret_cast<const i32x4*>(bp[j] + (size_t)kb * 128);
-      av[j] = *reinterpret_cast<const i32x4*>(ap[j] + (size_t)kb * 128);
-    }
-  };
-  load(0);
-  for (int kb = 0; kb < nK; ++kb) {
-    __syncthreads();
+    for (int mb = 0; mb < NMB; ++mb) s[mb] = __shfl(sv[mb / 4], mb % 4 * 16 + r16) * sbk;
+    issue_a<(S + 1) % 2>(L, kb + 1);
+    issue_s(kb + 1);
+    issue_b<(S + SB - 1) % SB>(L, kb + SB - 1);
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* A = L.template a<S % 2>();
+    const uint8_t* B = L.template b<S % SB>() + wave * 4096;
+    const i32x8 bf0 = fp8_frag(B, f), bf1 = fp8_frag(B + 2048, f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int v = tid + 256 * j;
-      *reinterpret_cast<i32x4*>(lds + fp8_swz(v / 8, v % 8)) = av[j];
-      *reinterpret_cast<i32x4*>(lds + kQB * 128 + fp8_swz(v / 8, v % 8)) = bv[j];
-    }
-    __syncthreads();
-    if (kb + 1 < nK) load(kb + 1);
-    float s[4];
+    for (int mb = 0; mb < NMB; ++mb) {
+      const i32x8 af = fp8_frag(A + mb * 2048, f);
+      const f32x4 p0 = fp8_mfma(bf0, af), p1 = fp8_mfma(bf1, af);
 #pragma unroll
-    for (int mb = 0; mb < 4; ++mb) s[mb] = a.sa[(size_t)kb * a.M + srow[mb]] * sb[kb];
-    i32x8 bf[4];
-#pragma unroll
-    for (int nb = 0; nb < 4; ++nb)
-      bf[nb] = fp8_frag(lds + kQB * 128, wn * 64 + nb * 16 + r16, g);
-#pragma unroll
-    for (int mb = 0; mb < 4; ++mb) {
-      const i32x8 af = fp8_frag(lds, wm * 64 + mb * 16 + r16, g);
-#pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        const f32x4 blk = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            bf[nb], af, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[mb][nb][r] = __builtin_fmaf(s[mb], blk[r], acc[mb][nb][r]);
+      for (int r = 0; r < 4; ++r) {
+        acc[mb][0][r] = __builtin_fmaf(s[mb], p0[r], acc[mb][0][r]);
+        acc[mb][1][r] = __builtin_fmaf(s[mb], p1[r], acc[mb][1][r]);
       }
     }
   }
-#pragma unroll
-  for (int mb = 0; mb < 4; ++mb) {
-    const int m = wm * 64 + mb * 16 + r16;
-    if (m >= t.rows) continue;
-#pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
-      const size_t at = (size_t)(t.row0 + m) * a.N + n0 * kQB + wn * 64 + nb * 16 + 4 * g;
-      const f32x4 v = acc[mb][nb];
-      *reinterpret_cast<uint2*>(a.out + at) =
-          make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
+  template <int S, int C>  // steps kb + S, .. while fewer than C and n
+  MOE_DEV void steps(const StreamLds<SB>& L, int kb, int n) {
+    if constexpr (S < C) {
+      if (S < n) {
+        step<S>(L, kb + S);
+        steps<S + 1, C>(L, kb, n);
+      }
     }
+  }
+  MOE_DEV void run(const Fp8GemmArgs& a, const RowTile& t, int n0, const StreamLds<SB>& L) {
+    const int lane = threadIdx.x % kWave, g = lane / 16;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    r16 = lane % 16;
+    f = frag_at(lane);
+    nK = a.K / kQB;
+    M = a.M;
+    ra = fp8_rsrc(a.a + (size_t)t.row0 * a.K);
+    rb = fp8_rsrc(a.b + ((size_t)t.e * a.N + (size_t)n0 * kQB) * a.K);
+    sb = a.sb + ((size_t)t.e * (a.N / kQB) + n0) * nK;
+#pragma unroll
+    for (int j = 0; j < AJ; ++j)  // rows past the count read the last one again
+      ao[j] = (uint32_t)min(8 * (wave * AJ + j) + lane / 8, t.rows - 1) * a.K + fp8_piece(lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      bo[j] = (uint32_t)(8 * (wave * 4 + j) + lane / 8) * a.K + fp8_piece(lane);
+#pragma unroll
+    for (int j = 0; j < SJ; ++j) sp[j] = a.sa + t.row0 + min(64 * j + lane, t.rows - 1);
+#pragma unroll
+    for (int i = 0; i < NMB; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    issue_b<0>(L, 0);
+    issue_a<0>(L, 0);
+    issue_s(0);
+    if constexpr (SB == 3) issue_b<1>(L, 1);
+    // whole cycles of the stages, then the rest: a loop left from its middle would hold two sets
+    // of accumulators
+    constexpr int C = SB == 3 ? 6 : 2;
+    int kb = 0;
+    for (; kb + C <= nK; kb += C) steps<0, C>(L, kb, C);
+    steps<0, C - 1>(L, kb, nK - kb);
+    // the loads past the end land before the workgroup gives its LDS back
+    __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
+#pragma unroll
+    for (int mb = 0; mb < NMB; ++mb) {
+      const int m = mb * 16 + r16;
+      if (m >= t.rows) continue;
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) {
+        const size_t at =
+            (size_t)(t.row0 + m) * a.N + (size_t)n0 * kQB + wave * 32 + nb * 16 + 4 * g;
+        const f32x4 v = acc[mb][nb];
+        *reinterpret_cast<uint2*>(a.out + at) =
+            make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
+      }
+    }
+  }
+};
+
+template <int BM>
+__global__ void __launch_bounds__(256, BM == 128 ? 2 : 4) fp8_stream_kernel(const Fp8GemmArgs a) {
+  constexpr int SB = BM == 128 ? 3 : 2;
+  __shared__ __align__(1024) uint8_t a0[BM * 128];
+  __shared__ __align__(1024) uint8_t a1[BM * 128];
+  __shared__ __align__(1024) uint8_t b0[kQB * 128];
+  __shared__ __align__(1024) uint8_t b1[kQB * 128];
+  __shared__ __align__(1024) uint8_t b2[SB == 3 ? kQB * 128 : 16];
+  const StreamLds<SB> L{a0, a1, b0, b1, b2};
+  const int nN = a.N / kQB;
+  const int lt = xcd_contiguous(blockIdx.x, gridDim.x);
+  const RowTile t = find_rows<BM>(a.offsets, a.M, a.E, lt / nN);
+  if (t.rows <= 0) return;  // whole workgroup
+  const int n0 = lt % nN;
+  if (BM == 32 || t.rows <= 32) {
+    StreamTile<2, SB> s;
+    s.run(a, t, n0, L);
+  } else if (t.rows <= 64) {
+    StreamTile<4, SB> s;
+    s.run(a, t, n0, L);
+  } else {
+    StreamTile<8, SB> s;
+    s.run(a, t, n0, L);
   }
 }
 
@@ -270,10 +395,16 @@ hipError_t launch_fp8_quant_weights(const uint16_t* src, int E, int N, int K, ui
 }
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s) {
-  const unsigned grid = (unsigned)(a.M / 128 + a.E) * (unsigned)(a.N / kQB);
+  auto grid = [&](int bm, int bn) {
+    const unsigned n = (unsigned)(a.M / bm + a.E) * (unsigned)((a.N + bn - 1) / bn);
+    return dim3((n + kXcds - 1) / kXcds * kXcds);
+  };
   {
     TraceScope trace("fp8_gemm", s);
-    hipLaunchKernelGGL(fp8_gemm_kernel, dim3(grid), dim3(256), 0, s, a);
+    if (a.M <= 16 * a.E)
+      hipLaunchKernelGGL(fp8_stream_kernel<32>, grid(32, kQB), dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL(fp8_stream_kernel<128>, grid(128, kQB), dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }
