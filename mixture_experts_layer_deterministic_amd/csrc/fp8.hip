@@ -198,6 +198,7 @@ MOE_DEV uint32_t fp8_piece(int lane) { return 16u * ((lane % 8) ^ (lane / 8)); }
 
 constexpr int kVm4Lgkm0 = 0x0074;  // s_waitcnt vmcnt(4) lgkmcnt(0)
 constexpr int kVm0Lgkm0 = 0x0070;
+constexpr int kLgkm0 = 0xc07f;     // lgkmcnt(0) alone
 
 // Few rows an expert: the weights' stream is what takes the time. BM x 128 tiles, four waves of
 // BM x 32; 128 bytes of K a step go from memory straight into LDS, the weights SB - 1 steps ahead
@@ -265,7 +266,8 @@ struct StreamTile {
   MOE_DEV void step(const StreamLds<SB>& L, int kb) {
     __builtin_amdgcn_s_waitcnt(SB == 3 ? kVm4Lgkm0 : kVm0Lgkm0);
     __builtin_amdgcn_s_barrier();
-    const float sbk = sb[kb];
+    // the weights' scale does not change under the kernel: a scalar load
+    const float sbk = ((const __attribute__((address_space(4))) float*)sb)[kb];
     float s[NMB];
 #pragma unroll
     for (int mb = 0; mb < NMB; ++mb) s[mb] = __shfl(sv[mb / 4], mb % 4 * 16 + r16) * sbk;
@@ -297,7 +299,7 @@ struct StreamTile {
     }
   }
   MOE_DEV void run(const Fp8GemmArgs& a, const RowTile& t, int n0, const StreamLds<SB>& L) {
-    const int lane = threadIdx.x % kWave, g = lane / 16;
+    const int lane = threadIdx.x % kWave;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     r16 = lane % 16;
     f = frag_at(lane);
@@ -332,14 +334,9 @@ struct StreamTile {
     for (int mb = 0; mb < NMB; ++mb) {
       const int m = mb * 16 + r16;
       if (m >= t.rows) continue;
-#pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        const size_t at =
-            (size_t)(t.row0 + m) * a.N + (size_t)n0 * kQB + wave * 32 + nb * 16 + 4 * g;
-        const f32x4 v = acc[mb][nb];
-        *reinterpret_cast<uint2*>(a.out + at) =
-            make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
-      }
+      store_dw8_bf16<false>(
+          a.out + (size_t)(t.row0 + m) * a.N + (size_t)n0 * kQB + wave * 32, acc[mb][0], acc[mb][1],
+          lane);
     }
   }
 };
@@ -367,6 +364,172 @@ __global__ void __launch_bounds__(256, BM == 128 ? 2 : 4) fp8_stream_kernel(cons
   } else {
     StreamTile<8, SB> s;
     s.run(a, t, n0, L);
+  }
+}
+
+// Many rows an expert: the MFMAs are what takes the time. 256 x 256 tiles, eight waves of 128 x 64,
+// two stages of 64 KB filled straight from memory; one workgroup a CU, two waves a SIMD.
+//
+// The two waves of a SIMD take turns: while the one runs 16 MFMAs (a quarter of its step's rows by
+// its 64 columns, about 515 cycles) with the scaling of their results in the gaps, the other
+// reads its next fragments from LDS. Waves w and w + 4 share a SIMD, so waves 4..7 run one phase
+// behind, and a barrier ends each phase:
+//     phase        4k        4k + 1    4k + 2    4k + 3    4k + 4
+//     waves 0..3   read k.0  mfma k.0  read k.1  mfma k.1  read (k+1).0
+//     waves 4..7   mfma ..   read k.0  mfma k.0  read k.1  mfma k.1
+// Step k - 1's stage is read for the last time in phase 4k - 1 (a read phase ends with its reads
+// returned), so a wave refills it for step k + 1 in its phase read k.0, and waits for its own
+// loads at the end of read k.1, in phase 4k + 2 or 4k + 3; it is read from 4k + 4 on. Every wave
+// runs the same code, the late ones behind one more barrier.
+constexpr int kBigT = 256;
+constexpr int kBigCodes = kBigT * 128;                // one operand's codes of a step
+constexpr int kBigStage = 2 * kBigCodes + kBigT * 4;  // rows, weights, the rows' scales
+__shared__ __align__(1024) uint8_t fp8_big0[kBigStage];
+__shared__ __align__(1024) uint8_t fp8_big1[kBigStage];
+template <int S>
+MOE_DEV uint8_t* fp8_big() {
+  if constexpr (S == 0) return fp8_big0;
+  else return fp8_big1;
+}
+
+struct BigTile {
+  __amdgpu_buffer_rsrc_t ra, rb;
+  uint32_t ao[4], bo[4], so;
+  const float *sa, *sb;
+  size_t M;
+  int nK, wave, wm, wn;
+  FragAt f;
+  f32x4 acc[8][4];
+
+  template <int S>
+  MOE_DEV void issue(int kb) {
+    uint8_t* st = fp8_big<S>();
+    const uint32_t step = (uint32_t)kb * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fp8_load_lds(rb, bo[j], step, st + kBigCodes + wave * 4096 + j * 1024);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fp8_load_lds(ra, ao[j], step, st + wave * 4096 + j * 1024);
+    // 64 rows' scales; waves 4..7 write what waves 0..3 write
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        fp8_rsrc(sa + kb * M),  // K / 128 rows of M may pass 32 bits
+        (__attribute__((address_space(3))) void*)(st + 2 * kBigCodes + wn * 256), 4, so, 0, 0, 0);
+  }
+  MOE_DEV void phase_end() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // row blocks 4 H .. 4 H + 3 of the step
+  template <int S, int H>
+  MOE_DEV void read(i32x8 (&af)[4]) {
+    const uint8_t* A = fp8_big<S>() + wm * 16384 + H * 8192;
+#pragma unroll
+    for (int mb = 0; mb < 4; ++mb) af[mb] = fp8_frag(A + mb * 2048, f);
+  }
+  // Sixteen MFMAs; the four FMAs that scale a result go out while the third MFMA after it runs.
+  // (Left alone, the compiler waits out each pair's latency before its FMAs.)
+  template <int H>
+  MOE_DEV void multiply(const i32x8 (&bf)[4], const i32x8 (&af)[4], const float (&s)[8],
+                        float sbk) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int mb = 0; mb < 4; ++mb) {
+      const float sk = s[4 * H + mb] * sbk;
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb) {
+        const f32x4 p = fp8_mfma(bf[nb], af[mb]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[4 * H + mb][nb][r] = __builtin_fmaf(sk, p[r], acc[4 * H + mb][nb][r]);
+      }
+    }
+    // masks: 0x2 VALU, 0x8 MFMA
+    __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+    __builtin_amdgcn_sched_group_barrier(0x8, 3, 0);
+#pragma unroll
+    for (int i = 0; i < 13; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x2, 12, 0);
+    __builtin_amdgcn_s_setprio(0);
+  }
+  template <int S>
+  MOE_DEV void step(int kb) {
+    i32x8 bf[4], af[4];
+    float s[8];
+    issue<S ^ 1>(min(kb + 1, nK - 1));  // past the end: the last again, into a stage nobody reads
+    // the weights' scale does not change under the kernel: a scalar load
+    const float sbk = ((const __attribute__((address_space(4))) float*)sb)[kb];
+    const uint8_t* B = fp8_big<S>() + kBigCodes + wn * 8192;
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) bf[nb] = fp8_frag(B + nb * 2048, f);
+    const float* sc = reinterpret_cast<const float*>(fp8_big<S>() + 2 * kBigCodes) + wm * 128 +
+                      threadIdx.x % 16;
+#pragma unroll
+    for (int mb = 0; mb < 8; ++mb) s[mb] = sc[mb * 16];
+    read<S, 0>(af);
+    __builtin_amdgcn_s_waitcnt(kLgkm0);
+    phase_end();
+    multiply<0>(bf, af, s, sbk);
+    phase_end();
+    read<S, 1>(af);
+    __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
+    phase_end();
+    multiply<1>(bf, af, s, sbk);
+    phase_end();
+  }
+};
+
+__global__ void __launch_bounds__(512, 2) fp8_big_kernel(const Fp8GemmArgs a) {
+  const int lane = threadIdx.x % kWave;
+  const int nN = (a.N + kBigT - 1) / kBigT;
+  const int lt = xcd_contiguous(blockIdx.x, gridDim.x);
+  const RowTile t = find_rows<kBigT>(a.offsets, a.M, a.E, lt / nN);
+  if (t.rows <= 0) return;  // whole workgroup
+  const int n0 = lt % nN * kBigT;
+  BigTile b;
+  b.wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  b.wm = b.wave / 4;
+  b.wn = b.wave % 4;
+  b.f = frag_at(lane);
+  b.nK = a.K / kQB;
+  b.ra = fp8_rsrc(a.a + (size_t)t.row0 * a.K);
+  b.rb = fp8_rsrc(a.b + ((size_t)t.e * a.N + n0) * a.K);
+  b.sa = a.sa + t.row0;
+  b.M = a.M;
+  const int cols = min(kBigT, a.N - n0);  // 256, or 128 at an odd end
+  b.sb = a.sb + ((size_t)t.e * (a.N / kQB) + n0 / kQB + min(b.wn / 2, cols / kQB - 1)) * b.nK;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // rows past the end read the last one again
+    const int r = 32 * b.wave + 8 * j + lane / 8;
+    b.ao[j] = (uint32_t)min(r, t.rows - 1) * a.K + fp8_piece(lane);
+    b.bo[j] = (uint32_t)min(r, cols - 1) * a.K + fp8_piece(lane);
+  }
+  b.so = (uint32_t)min(64 * b.wn + lane, t.rows - 1) * 4;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b.acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  b.issue<0>(0);
+  __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
+  b.phase_end();
+  if (b.wm) b.phase_end();
+  int kb = 0;
+  for (; kb + 2 <= b.nK; kb += 2) {
+    b.step<0>(kb);
+    b.step<1>(kb + 1);
+  }
+  if (kb < b.nK) b.step<0>(kb);
+  if (!b.wm) b.phase_end();  // as many barriers for the early waves as for the late ones
+  const int c0 = n0 + b.wn * 64;
+#pragma unroll
+  for (int mb = 0; mb < 8; ++mb) {
+    const int m = b.wm * 128 + mb * 16 + lane % 16;
+    if (m >= t.rows || b.wn * 64 >= cols) continue;
+    uint16_t* row = a.out + (size_t)(t.row0 + m) * a.N + c0;
+    store_dw8_bf16<false>(row, b.acc[mb][0], b.acc[mb][1], lane);
+    store_dw8_bf16<false>(row + 32, b.acc[mb][2], b.acc[mb][3], lane);
   }
 }
 
@@ -401,10 +564,12 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s) {
   };
   {
     TraceScope trace("fp8_gemm", s);
-    if (a.M <= 16 * a.E)
+    if (a.M <= 16LL * a.E)
       hipLaunchKernelGGL(fp8_stream_kernel<32>, grid(32, kQB), dim3(256), 0, s, a);
-    else
+    else if (a.M < 192LL * a.E)
       hipLaunchKernelGGL(fp8_stream_kernel<128>, grid(128, kQB), dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL(fp8_big_kernel, grid(kBigT, kBigT), dim3(512), 0, s, a);
   }
   return hipGetLastError();
 }

@@ -85,6 +85,7 @@ LOADS = {
     "small": ([1, 2, 3, 15, 16, 17, 31, 32, 33, 63, 64, 65], 0, 9),
     "tail": ([40, 0, 90], 3, 21),
     "big": ([700, 0, 3, 512], 0, 0),
+    "two": ([900, 255], 0, 5),
     "many": ([(7 * e) % 5 for e in range(200)], 0, 1),
 }
 
