@@ -370,10 +370,10 @@ __global__ void __launch_bounds__(256, BM == 128 ? 2 : 4) fp8_stream_kernel(cons
 // Many rows an expert: the MFMAs are what takes the time. 256 x 256 tiles, eight waves of 128 x 64,
 // two stages of 64 KB filled straight from memory; one workgroup a CU, two waves a SIMD.
 //
-// The two waves of a SIMD take turns: while the one runs 16 MFMAs (a quarter of its step's rows by
-// its 64 columns, about 515 cycles) with the scaling of their results in the gaps, the other
-// reads its next fragments from LDS. Waves w and w + 4 share a SIMD, so waves 4..7 run one phase
-// behind, and a barrier ends each phase:
+// The two waves of a SIMD take turns: while the one runs 16 MFMAs (half its row blocks by its
+// columns, about 515 cycles) with the scaling of their results in the gaps, the other reads its
+// next fragments from LDS. Waves w and w + 4 share a SIMD, so waves 4..7 run one phase behind,
+// and a barrier ends each phase:
 //     phase        4k        4k + 1    4k + 2    4k + 3    4k + 4
 //     waves 0..3   read k.0  mfma k.0  read k.1  mfma k.1  read (k+1).0
 //     waves 4..7   mfma ..   read k.0  mfma k.0  read k.1  mfma k.1
@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(256, BM == 128 ? 2 : 4) fp8_stream_kernel(cons
 // loads at the end of read k.1, in phase 4k + 2 or 4k + 3; it is read from 4k + 4 on. Every wave
 // runs the same code, the late ones behind one more barrier.
 constexpr int kBigT = 256;
+constexpr int kCus = 256;                             // MI355X; tiles that run at once
 constexpr int kBigCodes = kBigT * 128;                // one operand's codes of a step
 constexpr int kBigStage = 2 * kBigCodes + kBigT * 4;  // rows, weights, the rows' scales
 __shared__ __align__(1024) uint8_t fp8_big0[kBigStage];
@@ -392,62 +393,67 @@ MOE_DEV uint8_t* fp8_big() {
   else return fp8_big1;
 }
 
+// MB x NB blocks of 16 x 16 a wave: 8 x 4 (256 x 256 tiles), 8 x 2 (256 x 128), 4 x 2 (128 x 128).
+template <int MB, int NB>
 struct BigTile {
+  static constexpr int BM = 32 * MB, BN = 64 * NB, HB = MB / 2;
   __amdgpu_buffer_rsrc_t ra, rb;
-  uint32_t ao[4], bo[4], so;
+  uint32_t ao[HB], bo[NB], so;
   const float *sa, *sb;
   size_t M;
   int nK, wave, wm, wn;
   FragAt f;
-  f32x4 acc[8][4];
+  f32x4 acc[MB][NB];
 
   template <int S>
   MOE_DEV void issue(int kb) {
     uint8_t* st = fp8_big<S>();
     const uint32_t step = (uint32_t)kb * 128;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fp8_load_lds(rb, bo[j], step, st + kBigCodes + wave * 4096 + j * 1024);
+    for (int j = 0; j < NB; ++j)
+      fp8_load_lds(rb, bo[j], step, st + kBigCodes + (wave * NB + j) * 1024);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fp8_load_lds(ra, ao[j], step, st + wave * 4096 + j * 1024);
-    // 64 rows' scales; waves 4..7 write what waves 0..3 write
+    for (int j = 0; j < HB; ++j) fp8_load_lds(ra, ao[j], step, st + (wave * HB + j) * 1024);
+    // 64 rows' scales a wave; several waves write the same
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         fp8_rsrc(sa + kb * M),  // K / 128 rows of M may pass 32 bits
-        (__attribute__((address_space(3))) void*)(st + 2 * kBigCodes + wn * 256), 4, so, 0, 0, 0);
+        (__attribute__((address_space(3))) void*)(st + 2 * kBigCodes + wave % (BM / 64) * 256), 4,
+        so, 0, 0, 0);
   }
   MOE_DEV void phase_end() {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   }
-  // row blocks 4 H .. 4 H + 3 of the step
+  // row blocks HB H .. of the step
   template <int S, int H>
-  MOE_DEV void read(i32x8 (&af)[4]) {
-    const uint8_t* A = fp8_big<S>() + wm * 16384 + H * 8192;
+  MOE_DEV void read(i32x8 (&af)[HB]) {
+    const uint8_t* A = fp8_big<S>() + (wm * MB + H * HB) * 2048;
 #pragma unroll
-    for (int mb = 0; mb < 4; ++mb) af[mb] = fp8_frag(A + mb * 2048, f);
+    for (int mb = 0; mb < HB; ++mb) af[mb] = fp8_frag(A + mb * 2048, f);
   }
-  // Sixteen MFMAs; the four FMAs that scale a result go out while the third MFMA after it runs.
-  // (Left alone, the compiler waits out each pair's latency before its FMAs.)
+  // The four FMAs that scale an MFMA's result go out while the third MFMA after it runs. (Left
+  // alone, the compiler waits out each pair's latency before its FMAs.)
   template <int H>
-  MOE_DEV void multiply(const i32x8 (&bf)[4], const i32x8 (&af)[4], const float (&s)[8],
+  MOE_DEV void multiply(const i32x8 (&bf)[NB], const i32x8 (&af)[HB], const float (&s)[MB],
                         float sbk) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int mb = 0; mb < 4; ++mb) {
-      const float sk = s[4 * H + mb] * sbk;
+    for (int mb = 0; mb < HB; ++mb) {
+      const float sk = s[HB * H + mb] * sbk;
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
+      for (int nb = 0; nb < NB; ++nb) {
         const f32x4 p = fp8_mfma(bf[nb], af[mb]);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          acc[4 * H + mb][nb][r] = __builtin_fmaf(sk, p[r], acc[4 * H + mb][nb][r]);
+          acc[HB * H + mb][nb][r] = __builtin_fmaf(sk, p[r], acc[HB * H + mb][nb][r]);
       }
     }
     // masks: 0x2 VALU, 0x8 MFMA
-    __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+    __builtin_amdgcn_sched_group_barrier(0x2, HB, 0);
     __builtin_amdgcn_sched_group_barrier(0x8, 3, 0);
 #pragma unroll
-    for (int i = 0; i < 13; ++i) {
+    for (int i = 3; i < HB * NB; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
       __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
     }
@@ -456,18 +462,18 @@ struct BigTile {
   }
   template <int S>
   MOE_DEV void step(int kb) {
-    i32x8 bf[4], af[4];
-    float s[8];
+    i32x8 bf[NB], af[HB];
+    float s[MB];
     issue<S ^ 1>(min(kb + 1, nK - 1));  // past the end: the last again, into a stage nobody reads
     // the weights' scale does not change under the kernel: a scalar load
     const float sbk = ((const __attribute__((address_space(4))) float*)sb)[kb];
-    const uint8_t* B = fp8_big<S>() + kBigCodes + wn * 8192;
+    const uint8_t* B = fp8_big<S>() + kBigCodes + wn * NB * 2048;
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb) bf[nb] = fp8_frag(B + nb * 2048, f);
-    const float* sc = reinterpret_cast<const float*>(fp8_big<S>() + 2 * kBigCodes) + wm * 128 +
+    for (int nb = 0; nb < NB; ++nb) bf[nb] = fp8_frag(B + nb * 2048, f);
+    const float* sc = reinterpret_cast<const float*>(fp8_big<S>() + 2 * kBigCodes) + wm * MB * 16 +
                       threadIdx.x % 16;
 #pragma unroll
-    for (int mb = 0; mb < 8; ++mb) s[mb] = sc[mb * 16];
+    for (int mb = 0; mb < MB; ++mb) s[mb] = sc[mb * 16];
     read<S, 0>(af);
     __builtin_amdgcn_s_waitcnt(kLgkm0);
     phase_end();
@@ -479,57 +485,141 @@ struct BigTile {
     multiply<1>(bf, af, s, sbk);
     phase_end();
   }
+  // rows row0 .. of expert e and columns n0 .. of its weights (n0 a multiple of 128)
+  MOE_DEV void run(const Fp8GemmArgs& a, int e, int row0, int rows, int n0) {
+    const int lane = threadIdx.x % kWave;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    wm = wave / 4;
+    wn = wave % 4;
+    f = frag_at(lane);
+    nK = a.K / kQB;
+    M = a.M;
+    ra = fp8_rsrc(a.a + (size_t)row0 * a.K);
+    rb = fp8_rsrc(a.b + ((size_t)e * a.N + n0) * a.K);
+    sa = a.sa + row0;
+    const int cols = min(BN, a.N - n0);  // BN, or 128 at an odd end
+    sb = a.sb + ((size_t)e * (a.N / kQB) + n0 / kQB + min(wn * NB * 16, cols - 1) / kQB) * nK;
+    // rows past the end read the last one again
+#pragma unroll
+    for (int j = 0; j < HB; ++j)
+      ao[j] = (uint32_t)min((wave * HB + j) * 8 + lane / 8, rows - 1) * a.K + fp8_piece(lane);
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      bo[j] = (uint32_t)min((wave * NB + j) * 8 + lane / 8, cols - 1) * a.K + fp8_piece(lane);
+    so = (uint32_t)min(wave % (BM / 64) * 64 + lane, rows - 1) * 4;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    issue<0>(0);
+    __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
+    phase_end();
+    if (wm) phase_end();
+    int kb = 0;
+    for (; kb + 2 <= nK; kb += 2) {
+      step<0>(kb);
+      step<1>(kb + 1);
+    }
+    if (kb < nK) step<0>(kb);
+    if (!wm) phase_end();  // as many barriers for the early waves as for the late ones
+    const int c0 = wn * NB * 16;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const int m = (wm * MB + mb) * 16 + lane % 16;
+      if (m >= rows || c0 >= cols) continue;
+      uint16_t* row = a.out + (size_t)(row0 + m) * a.N + n0 + c0;
+#pragma unroll
+      for (int nb = 0; nb < NB; nb += 2)
+        store_dw8_bf16<false>(row + nb * 16, acc[mb][nb], acc[mb][nb + 1], lane);
+    }
+  }
 };
 
-__global__ void __launch_bounds__(512, 2) fp8_big_kernel(const Fp8GemmArgs a) {
+// The experts' row tiles counted out: all of them, and the one with a given number.
+MOE_DEV int big_tiles_of(const Fp8GemmArgs& a, int e) {
+  if (e >= a.E) return 0;
+  const int lo = min(max(a.offsets[e], 0), a.M), hi = min(max(a.offsets[e + 1], 0), a.M);
+  return hi > lo ? (hi - lo + kBigT - 1) / kBigT : 0;
+}
+MOE_DEV int wave_scan(int v) {
   const int lane = threadIdx.x % kWave;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int u = __shfl_up(v, o);
+    v += lane >= o ? u : 0;
+  }
+  return v;
+}
+MOE_DEV int big_count(const Fp8GemmArgs& a) {
+  int n = 0;
+  for (int e0 = 0; e0 < a.E; e0 += kWave)
+    n += __builtin_amdgcn_readlane(wave_scan(big_tiles_of(a, e0 + threadIdx.x % kWave)), 63);
+  return n;
+}
+MOE_DEV RowTile big_rows(const Fp8GemmArgs& a, int mt) {
+  RowTile t{0, 0, 0};
+  for (int e0 = 0; e0 < a.E; e0 += kWave) {
+    const int inc = wave_scan(big_tiles_of(a, e0 + threadIdx.x % kWave));
+    const int all = __builtin_amdgcn_readlane(inc, 63);
+    if (mt < all) {
+      const int n = __popcll(__ballot(inc <= mt));  // experts before the tile's
+      t.e = e0 + n;
+      const int i = mt - (n ? __builtin_amdgcn_readlane(inc, n - 1) : 0);
+      const int lo = min(max(a.offsets[t.e], 0), a.M), hi = min(max(a.offsets[t.e + 1], 0), a.M);
+      t.row0 = lo + i * kBigT;
+      t.rows = min(hi - t.row0, kBigT);
+      return t;
+    }
+    mt -= all;
+  }
+  return t;
+}
+// Tile number -> (row tile, column tile): four row tiles take each column tile in turn, so that
+// the tiles an XCD runs at once (32) share few panels of either operand in its L2.
+MOE_DEV int2 big_order(int lt, int nm, int nN) {
+  const int first = lt / (4 * nN) * 4, gm = min(4, nm - first), r = lt - first * nN;
+  return make_int2(first + r % gm, r / gm);
+}
+
+// Whole rounds of one tile a CU, then what is left: its tiles cut in two (256 x 128) or four
+// (128 x 128) where the parts still fit one round, so that the last round takes half or a quarter
+// of a tile's time. A tile's values do not depend on how it is cut.
+__global__ void __launch_bounds__(512, 2) fp8_big_kernel(const Fp8GemmArgs a) {
   const int nN = (a.N + kBigT - 1) / kBigT;
-  const int lt = xcd_contiguous(blockIdx.x, gridDim.x);
-  const RowTile t = find_rows<kBigT>(a.offsets, a.M, a.E, lt / nN);
-  if (t.rows <= 0) return;  // whole workgroup
-  const int n0 = lt % nN * kBigT;
-  BigTile b;
-  b.wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  b.wm = b.wave / 4;
-  b.wn = b.wave % 4;
-  b.f = frag_at(lane);
-  b.nK = a.K / kQB;
-  b.ra = fp8_rsrc(a.a + (size_t)t.row0 * a.K);
-  b.rb = fp8_rsrc(a.b + ((size_t)t.e * a.N + n0) * a.K);
-  b.sa = a.sa + t.row0;
-  b.M = a.M;
-  const int cols = min(kBigT, a.N - n0);  // 256, or 128 at an odd end
-  b.sb = a.sb + ((size_t)t.e * (a.N / kQB) + n0 / kQB + min(b.wn / 2, cols / kQB - 1)) * b.nK;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {  // rows past the end read the last one again
-    const int r = 32 * b.wave + 8 * j + lane / 8;
-    b.ao[j] = (uint32_t)min(r, t.rows - 1) * a.K + fp8_piece(lane);
-    b.bo[j] = (uint32_t)min(r, cols - 1) * a.K + fp8_piece(lane);
+  const int nm = big_count(a), tiles = nm * nN;
+  const int whole = tiles / kCus * kCus, left = tiles - whole;
+  const int cut = left * 4 <= kCus ? 4 : left * 2 <= kCus ? 2 : 1;
+  const int b = blockIdx.x;
+  int lt, part = 0;
+  if (b < whole) {
+    lt = xcd_contiguous(b, whole);
+  } else {
+    const int n8 = (left * cut + kXcds - 1) / kXcds * kXcds;
+    if (b - whole >= n8) return;  // whole workgroups leave
+    const int j = xcd_contiguous(b - whole, n8);
+    if (j >= left * cut) return;
+    lt = whole + j / cut;
+    part = j % cut;
   }
-  b.so = (uint32_t)min(64 * b.wn + lane, t.rows - 1) * 4;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) b.acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  b.issue<0>(0);
-  __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
-  b.phase_end();
-  if (b.wm) b.phase_end();
-  int kb = 0;
-  for (; kb + 2 <= b.nK; kb += 2) {
-    b.step<0>(kb);
-    b.step<1>(kb + 1);
+  const int2 mn = big_order(lt, nm, nN);
+  const RowTile t = big_rows(a, mn.x);
+  const int n0 = mn.y * kBigT;
+  if (t.rows <= 0) return;
+  if (b < whole || cut == 1) {
+    BigTile<8, 4> w;
+    w.run(a, t.e, t.row0, t.rows, n0);
+    return;
   }
-  if (kb < b.nK) b.step<0>(kb);
-  if (!b.wm) b.phase_end();  // as many barriers for the early waves as for the late ones
-  const int c0 = n0 + b.wn * 64;
-#pragma unroll
-  for (int mb = 0; mb < 8; ++mb) {
-    const int m = b.wm * 128 + mb * 16 + lane % 16;
-    if (m >= t.rows || b.wn * 64 >= cols) continue;
-    uint16_t* row = a.out + (size_t)(t.row0 + m) * a.N + c0;
-    store_dw8_bf16<false>(row, b.acc[mb][0], b.acc[mb][1], lane);
-    store_dw8_bf16<false>(row + 32, b.acc[mb][2], b.acc[mb][3], lane);
+  const int c = n0 + part % 2 * 128;
+  if (c >= a.N) return;
+  if (cut == 2) {
+    BigTile<8, 2> w;
+    w.run(a, t.e, t.row0, t.rows, c);
+  } else {
+    const int r = part / 2 * 128;
+    if (r >= t.rows) return;
+    BigTile<4, 2> w;
+    w.run(a, t.e, t.row0 + r, min(t.rows - r, 128), c);
   }
 }
 
@@ -569,7 +659,8 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s) {
     else if (a.M < 192LL * a.E)
       hipLaunchKernelGGL(fp8_stream_kernel<128>, grid(128, kQB), dim3(256), 0, s, a);
     else
-      hipLaunchKernelGGL(fp8_big_kernel, grid(kBigT, kBigT), dim3(512), 0, s, a);
+      // room for every tile, and for a last round's parts
+      hipLaunchKernelGGL(fp8_big_kernel, dim3(grid(kBigT, kBigT).x + kCus), dim3(512), 0, s, a);
   }
   return hipGetLastError();
 }

@@ -155,6 +155,23 @@ def test_product_of_small_whole_numbers_is_exact(load, N, K):
     np.testing.assert_array_equal(got, np.where(np.isnan(ref), 3.0, ref))
 
 
+@pytest.mark.parametrize("counts", [[3000], [5100], [4000, 8400 - 4000], [8400, 3], [1900, 0, 4300]])
+def test_product_in_every_cut_of_the_last_round(counts):
+    """Row tiles x 8 column tiles: fewer than one round of 256, cut in two or whole, and a whole
+    round with a rest cut in four."""
+    _announce(f"[fp8] product of many rows {counts}")
+    E, M, N, K = len(counts), sum(counts), 2048, 256
+    g = torch.Generator().manual_seed(M)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    a, b = _codes((M, K), g), _codes((E, N, K), g)
+    sa, sb = torch.rand(K // 128, M, generator=g), torch.rand(E, N // 128, K // 128, generator=g)
+    ref = _ops.fp8_gemm(off, _values(a), sa.numpy(), _values(b), sb.numpy())
+    e1 = _bound(off, a, sa, b, sb)
+    got = _run(off, a, sa, b, sb, torch.full((M, N), -7.0, dtype=torch.bfloat16, device=DEV))
+    worst = float(np.max(np.abs(got - ref) / (2.0 ** -8 * (np.abs(ref) + e1) + e1)))
+    assert worst <= 1, worst
+
+
 def test_a_row_does_not_depend_on_its_batch():
     """One expert's rows alone and among others, first, last and in the middle of a tile."""
     off, a, sa, b, sb = _problem("big", 256, 512, 3)
