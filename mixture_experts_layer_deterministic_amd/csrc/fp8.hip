@@ -189,9 +189,10 @@ MOE_DEV __amdgpu_buffer_rsrc_t fp8_rsrc(const void* base) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00020000);
 }
 // 16 bytes a lane straight into LDS, at lds + 16 lane: 8 rows of 128 bytes a wave.
+template <int AUX = 0>
 MOE_DEV void fp8_load_lds(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint8_t* lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
-                                           voff, soff, 0, 0);
+                                           voff, soff, 0, AUX);
 }
 // The chunk a lane fetches into its place of those 8 rows.
 MOE_DEV uint32_t fp8_piece(int lane) { return 16u * ((lane % 8) ^ (lane / 8)); }
@@ -255,7 +256,7 @@ struct StreamTile {
     const uint32_t step = (uint32_t)min(kb, nK - 1) * 128;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      fp8_load_lds(rb, bo[j], step, L.template b<S>() + (wave * 4 + j) * 1024);
+      fp8_load_lds<NMB <= 4 ? 2 : 0>(rb, bo[j], step, L.template b<S>() + (wave * 4 + j) * 1024);
   }
   MOE_DEV void issue_s(int kb) {
     const size_t at = (size_t)min(kb, nK - 1) * M;
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(256, BM == 128 ? 2 : 4) fp8_stream_kernel(cons
   __shared__ __align__(1024) uint8_t b2[SB == 3 ? kQB * 128 : 16];
   const StreamLds<SB> L{a0, a1, b0, b1, b2};
   const int nN = a.N / kQB;
-  const int lt = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int lt = blockIdx.x;
   const RowTile t = find_rows<BM>(a.offsets, a.M, a.E, lt / nN);
   if (t.rows <= 0) return;  // whole workgroup
   const int n0 = lt % nN;
@@ -360,6 +361,9 @@ __global__ void __launch_bounds__(256, BM == 128 ? 2 : 4) fp8_stream_kernel(cons
     s.run(a, t, n0, L);
   } else if (t.rows <= 64) {
     StreamTile<4, SB> s;
+    s.run(a, t, n0, L);
+  } else if (t.rows <= 96) {
+    StreamTile<6, SB> s;
     s.run(a, t, n0, L);
   } else {
     StreamTile<8, SB> s;
@@ -404,6 +408,8 @@ struct BigTile {
   int nK, wave, wm, wn;
   FragAt f;
   f32x4 acc[MB][NB];
+  f32x4 last[3];  // the last products of a phase, and their scales
+  float last_s[3];
 
   template <int S>
   MOE_DEV void issue(int kb) {
@@ -432,11 +438,13 @@ struct BigTile {
 #pragma unroll
     for (int mb = 0; mb < HB; ++mb) af[mb] = fp8_frag(A + mb * 2048, f);
   }
-  // The four FMAs that scale an MFMA's result go out while the third MFMA after it runs. (Left
-  // alone, the compiler waits out each pair's latency before its FMAs.)
+  // The four FMAs that scale an MFMA's result go out while the third MFMA after it runs (left
+  // alone, the compiler waits out each pair's latency before its FMAs); those of the last three
+  // go out in the next phase, when the other waves have the MFMAs (finish).
   template <int H>
   MOE_DEV void multiply(const i32x8 (&bf)[NB], const i32x8 (&af)[HB], const float (&s)[MB],
                         float sbk) {
+    constexpr int n = HB * NB;
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int mb = 0; mb < HB; ++mb) {
@@ -444,21 +452,36 @@ struct BigTile {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const f32x4 p = fp8_mfma(bf[nb], af[mb]);
+        const int i = mb * NB + nb - (n - 3);
+        if (i >= 0) {
+          last[i] = p;
+          last_s[i] = sk;
+        } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[HB * H + mb][nb][r] = __builtin_fmaf(sk, p[r], acc[HB * H + mb][nb][r]);
+          for (int r = 0; r < 4; ++r)
+            acc[HB * H + mb][nb][r] = __builtin_fmaf(sk, p[r], acc[HB * H + mb][nb][r]);
+        }
       }
     }
     // masks: 0x2 VALU, 0x8 MFMA
     __builtin_amdgcn_sched_group_barrier(0x2, HB, 0);
     __builtin_amdgcn_sched_group_barrier(0x8, 3, 0);
 #pragma unroll
-    for (int i = 3; i < HB * NB; ++i) {
+    for (int i = 3; i < n; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
       __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x2, 12, 0);
     __builtin_amdgcn_s_setprio(0);
+  }
+  template <int H>
+  MOE_DEV void finish() {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int at = HB * NB - 3 + i, mb = HB * H + at / NB, nb = at % NB;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        acc[mb][nb][r] = __builtin_fmaf(last_s[i], last[i][r], acc[mb][nb][r]);
+    }
   }
   template <int S>
   MOE_DEV void step(int kb) {
@@ -475,11 +498,13 @@ struct BigTile {
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) s[mb] = sc[mb * 16];
     read<S, 0>(af);
+    finish<1>();
     __builtin_amdgcn_s_waitcnt(kLgkm0);
     phase_end();
     multiply<0>(bf, af, s, sbk);
     phase_end();
     read<S, 1>(af);
+    finish<0>();
     __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
     phase_end();
     multiply<1>(bf, af, s, sbk);
@@ -511,6 +536,11 @@ struct BigTile {
     for (int i = 0; i < MB; ++i)
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      last[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      last_s[i] = 0.f;
+    }
     issue<0>(0);
     __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
     phase_end();
@@ -521,6 +551,7 @@ struct BigTile {
       step<1>(kb + 1);
     }
     if (kb < nK) step<0>(kb);
+    finish<1>();
     if (!wm) phase_end();  // as many barriers for the early waves as for the late ones
     const int c0 = wn * NB * 16;
 #pragma unroll
