@@ -2,10 +2,11 @@
 //   dx[t]  (+)= sum_e dl[t, e] Wr[e]      T x d, reduced over the experts
 //   dWr[e] (+)= sum_t dl[t, e] x[t]       E x d, reduced over the tokens
 //
-// dl is fp32 and x, Wr are bf16. Each dl value is split into three bf16 parts, the rounding of
-// what the parts before left over: h + m + l keeps 24 bits, the products of the parts with bf16
-// values are exact in fp32, and three bf16 MFMAs do an fp32 product's work at a rate that
-// fp32 MFMAs (1/16 of bf16's) do not reach.
+// dl is fp32 and x, Wr are bf16. Each dl value is split into bf16 parts whose products with bf16
+// values are exact in fp32, so bf16 MFMAs do an fp32 product's work at a rate that fp32 MFMAs
+// (1/16 of bf16's) do not reach. Cutting a value's upper 8 bits off, then the next 8 of what is
+// left, gives three parts that add up to all its 24 bits: dWr, an fp32 sum, takes the three. dx
+// is rounded to bf16 (2^-9) at the end and takes two, the second rounded: 17 bits, 2^-17.
 #include "common.h"
 #include "kernels.h"
 #include "ops.h"
@@ -13,143 +14,187 @@
 namespace moe {
 namespace {
 
-constexpr int kRgB = 128;     // tile rows and columns
-constexpr int kRgK = 32;      // reduction depth of a step
-constexpr int kRgPlane = kRgB * kRgK;  // uint16 of one part of a step's dl tile
-constexpr int kRgStage = 4 * kRgPlane;  // three parts, then the bf16 operand
+constexpr int kRgN = 128;  // tile columns
+constexpr int kRgK = 64;   // reduction depth of a step
 
-// Element offset of 16-byte chunk c of row r in a tile of 32-value rows, chunks permuted so that
-// the 16 rows a fragment read touches spread over the banks.
-MOE_DEV int rg_row(int r, int c) { return r * kRgK + ((c ^ ((r >> 1) & 3)) << 3); }
+typedef __attribute__((ext_vector_type(4), aligned(4))) float f32x4u;  // rows of any E
+typedef __attribute__((ext_vector_type(2))) float rg_f2;
+typedef __attribute__((ext_vector_type(2))) __bf16 rg_bf2;
 
-MOE_DEV void split3(float x, uint32_t& h, uint32_t& m, uint32_t& l) {
-  h = f2bf(x);
-  const float r = x - bf2f((uint16_t)h);
-  m = f2bf(r);
-  l = f2bf(r - bf2f((uint16_t)m));
+MOE_DEV uint32_t upper2(float lo, float hi) {  // the upper halves of two floats: cut-off bf16
+  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+MOE_DEV uint32_t round2(float lo, float hi) {  // two floats rounded to bf16
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(rg_f2{lo, hi}, rg_bf2));
+}
+MOE_DEV float cut(float x) {  // what is left of x below its upper 8 bits (exact)
+  return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+}
+template <int P>
+MOE_DEV void split4(const f32x4& x, uint2 (&part)[P]) {
+  const float r0 = cut(x[0]), r1 = cut(x[1]), r2 = cut(x[2]), r3 = cut(x[3]);
+  part[0] = make_uint2(upper2(x[0], x[1]), upper2(x[2], x[3]));
+  if constexpr (P == 2) {
+    part[1] = make_uint2(round2(r0, r1), round2(r2, r3));
+  } else {
+    part[1] = make_uint2(upper2(r0, r1), upper2(r2, r3));
+    part[2] = make_uint2(upper2(cut(r0), cut(r1)), upper2(cut(r2), cut(r3)));
+  }
 }
 
-// Workgroup tiles: first the dWr tiles (the longer reductions), then the dx tiles, so that the
-// long ones start first. Four waves of 64 x 64.
-__global__ void __launch_bounds__(256, 2) router_backward_kernel(const RouterGradArgs a) {
-  __shared__ __align__(16) uint16_t lds[kRgStage];
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int wm = wave / 2, wn = wave % 2;
-  const int nc = a.d / kRgB;
-  const int nw = a.dwr ? (a.E + kRgB - 1) / kRgB * nc : 0;
-  const bool dw = (int)blockIdx.x < nw;
-  const int b = dw ? blockIdx.x : blockIdx.x - nw;
-  const int r0 = b / nc * kRgB, c0 = b % nc * kRgB;  // output rows (experts or tokens), columns
-  const int R = dw ? a.E : a.T, K = dw ? a.T : a.E;
-  const uint16_t* bsrc = dw ? a.x : a.wr;
-  f32x4 acc[4][4];
+// kmajor_swz for rows of 64 values: four groups of 16 to permute.
+MOE_DEV int swz64(int k) { return 16 * (k & 3); }
+// kmajor_frag on such rows.
+MOE_DEV uint4 kmajor_frag64(const uint16_t* s, int base, int kb, int lane) {
+  const int g = lane / 16, q = lane % 16, kr = 8 * g + q / 4;
+  const int n = (base ^ swz64(kr)) + 4 * (q % 4);
+  const uint16_t* p = s + (kb + kr) * 64 + n;
+  const uint2 a = __builtin_bit_cast(uint2, lds_read_tr16(p));
+  const uint2 b = __builtin_bit_cast(uint2, lds_read_tr16(p + 4 * 64));
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+
+// One tile: DW, 64 experts x 128 columns of dWr, reduced over the tokens; else 128 tokens x 128
+// columns of dx, reduced over the experts. Four waves, 2 x 2. A step's dl tile is split once
+// for the workgroup, on its way from registers to LDS; the loads of the next step are out by
+// then. The bf16 operand lies in LDS as it does in memory and reaches the MFMAs through the
+// transposing read; so does dl for dWr, whose reduction axis is the slow one of both.
+template <bool DW>
+struct RouterTile {
+  static constexpr int P = DW ? 3 : 2, BM = DW ? 64 : 128, MB = BM / 32, AJ = BM / 16;
+  static constexpr int kPlane = BM * kRgK;  // values of one part
+  f32x4 av[AJ];
+  uint4 bv[4];
+  f32x4 acc[MB][4];
+
+  // dl rows: DW, tokens k0 + i (reduction), experts r0 ..; else tokens r0 + i, experts k0 ..
+  MOE_DEV void load(const RouterGradArgs& a, int r0, int c0, int k0) {
+    const int tid = threadIdx.x;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < AJ; ++j) {
+      const int i = tid / 16 + 16 * j, t = (DW ? k0 : r0) + i, e = (DW ? r0 : k0) + tid % 16 * 4;
+      const float* p = a.dl + (size_t)t * a.E + e;
+      f32x4 v{0.f, 0.f, 0.f, 0.f};
+      if (t < a.T) {
+        if (e + 3 < a.E) {
+          v = *reinterpret_cast<const f32x4u*>(p);
+        } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // this thread's 16 dl values of a step: dx, row tid / 2 and 16 experts; dWr, token tid / 8 and
-  // 16 experts
-  const int ar = dw ? tid / 8 : tid / 2, ac = dw ? tid % 8 * 16 : tid % 2 * 16;
-  float av[16];
-  uint4 bv[2];
-  auto load = [&](int k0) {
-    const int t = dw ? k0 + ar : r0 + ar, e0 = dw ? r0 + ac : k0 + ac;
-    const float* p = a.dl + (size_t)t * a.E + e0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) av[i] = t < a.T && e0 + i < a.E ? p[i] : 0.f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int v = tid + 256 * j, kr = k0 + v / 16;
-      bv[j] = kr < K ? *reinterpret_cast<const uint4*>(bsrc + (size_t)kr * a.d + c0 + v % 16 * 8)
-                     : make_uint4(0, 0, 0, 0);
-    }
-  };
-  auto store = [&] {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t w[3][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t h0, m0, l0, h1, m1, l1;
-        split3(av[8 * q + 2 * i], h0, m0, l0);
-        split3(av[8 * q + 2 * i + 1], h1, m1, l1);
-        w[0][i] = h0 | (h1 << 16);
-        w[1][i] = m0 | (m1 << 16);
-        w[2][i] = l0 | (l1 << 16);
+          for (int q = 0; q < 3; ++q)
+            if (e + q < a.E) v[q] = p[q];
+        }
       }
-      const int at = dw ? ar * kRgB + ((ac + 8 * q) ^ kmajor_swz(ar)) : rg_row(ar, ac / 8 + q);
+      av[j] = v;
+    }
+    const uint16_t* src = DW ? a.x : a.wr;
+    const int K = DW ? a.T : a.E;
 #pragma unroll
-      for (int s = 0; s < 3; ++s)
-        *reinterpret_cast<uint4*>(lds + s * kRgPlane + at) =
-            make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + tid / 16 + 16 * j;
+      bv[j] = k < K ? *reinterpret_cast<const uint4*>(src + (size_t)k * a.d + c0 + tid % 16 * 8)
+                    : make_uint4(0, 0, 0, 0);
+    }
+  }
+  MOE_DEV void store(uint16_t* lds) const {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < AJ; ++j) {
+      const int i = tid / 16 + 16 * j, c = tid % 16 * 4;
+      uint2 part[P];
+      split4<P>(av[j], part);
+      const int at = DW ? i * 64 + (c ^ swz64(i)) : rowswz(i, c / 8) + c % 8;
+#pragma unroll
+      for (int p = 0; p < P; ++p) *reinterpret_cast<uint2*>(lds + p * kPlane + at) = part[p];
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int v = tid + 256 * j, kr = v / 16;
-      *reinterpret_cast<uint4*>(lds + 3 * kRgPlane + kr * kRgB + ((v % 16 * 8) ^ kmajor_swz(kr))) =
+    for (int j = 0; j < 4; ++j) {
+      const int k = tid / 16 + 16 * j;
+      *reinterpret_cast<uint4*>(lds + P * kPlane + k * kRgN + ((tid % 16 * 8) ^ kmajor_swz(k))) =
           bv[j];
     }
-  };
-  load(0);
-  for (int k0 = 0; k0 < K; k0 += kRgK) {
-    __syncthreads();
-    store();
-    __syncthreads();
-    if (k0 + kRgK < K) load(k0 + kRgK);
-    uint4 bf[4];
+  }
+  MOE_DEV void run(const RouterGradArgs& a, int r0, int c0, uint16_t* lds) {
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int wm = wave / 2, wn = wave % 2;
+    const int R = DW ? a.E : a.T, K = DW ? a.T : a.E;
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb)
-      bf[nb] = kmajor_frag<kRgB>(lds + 3 * kRgPlane, wn * 64 + nb * 16, 0, lane);
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int mb = 0; mb < 4; ++mb) {
-      const int m = wm * 64 + mb * 16;
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    load(a, r0, c0, 0);
+    for (int k0 = 0; k0 < K; k0 += kRgK) {
+      __syncthreads();
+      store(lds);
+      __syncthreads();
+      if (k0 + kRgK < K) load(a, r0, c0, k0 + kRgK);
 #pragma unroll
-      for (int s = 2; s >= 0; --s) {  // the small parts first
-        const uint16_t* pl = lds + s * kRgPlane;
-        const uint4 af = dw ? kmajor_frag<kRgB>(pl, m, 0, lane)
-                            : *reinterpret_cast<const uint4*>(pl + rg_row(m + lane % 16, lane / 16));
+      for (int ks = 0; ks < 2; ++ks) {
+        uint4 bf[4];
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) acc[mb][nb] = mfma16(bf[nb], af, acc[mb][nb]);
+        for (int nb = 0; nb < 4; ++nb)
+          bf[nb] = kmajor_frag<kRgN>(lds + P * kPlane, wn * 64 + nb * 16, ks * 32, lane);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          const int m = (wm * MB + mb) * 16;
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p) {  // the small parts first
+            const uint16_t* pl = lds + p * kPlane;
+            const uint4 af = DW ? kmajor_frag64(pl, m, ks * 32, lane)
+                                : *reinterpret_cast<const uint4*>(
+                                      pl + rowswz(m + lane % 16, ks * 4 + lane / 16));
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) acc[mb][nb] = mfma16(bf[nb], af, acc[mb][nb]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const int r = r0 + (wm * MB + mb) * 16 + lane % 16;
+      if (r >= R) continue;
+      if constexpr (DW) {
+        float* p = a.dwr + (size_t)r * a.d + c0 + wn * 64 + 4 * (lane / 16);
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) {
+          if (a.acc_dwr) store_dw4<true>(p + nb * 16, acc[mb][nb]);
+          else store_dw4<false>(p + nb * 16, acc[mb][nb]);
+        }
+      } else {
+        // one rounding to bf16, of the fp32 sum with what dx held
+        uint16_t* p = a.dx + (size_t)r * a.d + c0 + wn * 64;
+#pragma unroll
+        for (int nb = 0; nb < 4; nb += 2) {
+          if (a.acc_dx) store_dw8_bf16<true>(p + nb * 16, acc[mb][nb], acc[mb][nb + 1], lane);
+          else store_dw8_bf16<false>(p + nb * 16, acc[mb][nb], acc[mb][nb + 1], lane);
+        }
       }
     }
   }
-#pragma unroll
-  for (int mb = 0; mb < 4; ++mb) {
-    const int r = r0 + wm * 64 + mb * 16 + lane % 16;
-    if (r >= R) continue;
-#pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
-      const int c = c0 + wn * 64 + nb * 16 + 4 * (lane / 16);
-      f32x4 v = acc[mb][nb];
-      if (dw) {
-        float* p = a.dwr + (size_t)r * a.d + c;
-        if (a.acc_dwr) store_dw4<true>(p, v);
-        else store_dw4<false>(p, v);
-      } else {
-        // one rounding to bf16, of the fp32 sum with what dx held
-        uint2* p = reinterpret_cast<uint2*>(a.dx + (size_t)r * a.d + c);
-        if (a.acc_dx) {
-          const uint2 o = *p;
-          v[0] += bf2f_lo(o.x);
-          v[1] += bf2f_hi(o.x);
-          v[2] += bf2f_lo(o.y);
-          v[3] += bf2f_hi(o.y);
-        }
-        *p = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
-      }
-    }
+};
+
+// The dWr tiles come first: their reductions are the long ones.
+__global__ void __launch_bounds__(256, 2) router_backward_kernel(const RouterGradArgs a, int nw) {
+  __shared__ __align__(16) uint16_t lds[2 * 128 * kRgK + kRgK * kRgN];
+  static_assert(3 * 64 * kRgK <= 2 * 128 * kRgK, "either tile's parts fit");
+  const int nc = a.d / kRgN;
+  const int b = blockIdx.x;
+  if (b < nw) {
+    RouterTile<true> t;
+    t.run(a, b / nc * 64, b % nc * kRgN, lds);
+  } else {
+    RouterTile<false> t;
+    t.run(a, (b - nw) / nc * 128, (b - nw) % nc * kRgN, lds);
   }
 }
 
 }  // namespace
 
 hipError_t launch_router_backward(const RouterGradArgs& a, hipStream_t s) {
-  const int nc = a.d / kRgB;
-  const int grid = ((a.dwr ? (a.E + kRgB - 1) / kRgB : 0) +
-                    (a.dx ? (a.T + kRgB - 1) / kRgB : 0)) * nc;
+  const int nc = a.d / kRgN;
+  const int nw = a.dwr ? (a.E + 63) / 64 * nc : 0, nx = a.dx ? (a.T + 127) / 128 * nc : 0;
   {
     TraceScope trace("router_backward", s);
-    hipLaunchKernelGGL(router_backward_kernel, dim3(grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(router_backward_kernel, dim3(nw + nx), dim3(256), 0, s, a, nw);
   }
   return hipGetLastError();
 }
