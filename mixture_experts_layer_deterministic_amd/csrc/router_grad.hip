@@ -17,7 +17,6 @@ namespace {
 constexpr int kRgN = 128;  // tile columns
 constexpr int kRgK = 64;   // reduction depth of a step
 
-typedef __attribute__((ext_vector_type(4), aligned(4))) float f32x4u;  // rows of any E
 typedef __attribute__((ext_vector_type(2))) float rg_f2;
 typedef __attribute__((ext_vector_type(2))) __bf16 rg_bf2;
 
@@ -40,6 +39,12 @@ MOE_DEV void split4(const f32x4& x, uint2 (&part)[P]) {
     part[1] = make_uint2(upper2(r0, r1), upper2(r2, r3));
     part[2] = make_uint2(upper2(cut(r0), cut(r1)), upper2(cut(r2), cut(r3)));
   }
+}
+
+MOE_DEV __amdgpu_buffer_rsrc_t rg_rsrc(const void* base, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
+                                           (int)(bytes < 0xffffffffu ? bytes : 0xffffffffu),
+                                           0x00020000);
 }
 
 // kmajor_swz for rows of 64 values: four groups of 16 to permute.
@@ -68,32 +73,25 @@ struct RouterTile {
   f32x4 acc[MB][4];
 
   // dl rows: DW, tokens k0 + i (reduction), experts r0 ..; else tokens r0 + i, experts k0 ..
+  // Buffer loads that end with their tensor, so rows past its end read as zeros without a branch.
+  // A dl row's columns past E belong to the next row: for dx the weight rows they meet are
+  // zeros, for dWr they lead to rows that are not stored.
   MOE_DEV void load(const RouterGradArgs& a, int r0, int c0, int k0) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, i = tid / 16, c = tid % 16;
+    const size_t t0 = DW ? k0 : r0, e0 = DW ? r0 : k0;
+    const __amdgpu_buffer_rsrc_t ra = rg_rsrc(a.dl + t0 * a.E + e0, ((a.T - t0) * a.E - e0) * 4);
 #pragma unroll
-    for (int j = 0; j < AJ; ++j) {
-      const int i = tid / 16 + 16 * j, t = (DW ? k0 : r0) + i, e = (DW ? r0 : k0) + tid % 16 * 4;
-      const float* p = a.dl + (size_t)t * a.E + e;
-      f32x4 v{0.f, 0.f, 0.f, 0.f};
-      if (t < a.T) {
-        if (e + 3 < a.E) {
-          v = *reinterpret_cast<const f32x4u*>(p);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 3; ++q)
-            if (e + q < a.E) v[q] = p[q];
-        }
-      }
-      av[j] = v;
-    }
+    for (int j = 0; j < AJ; ++j)
+      av[j] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                            ra, ((i + 16 * j) * a.E + c * 4) * 4, 0, 0));
     const uint16_t* src = DW ? a.x : a.wr;
-    const int K = DW ? a.T : a.E;
+    const size_t K = DW ? a.T : a.E;
+    const __amdgpu_buffer_rsrc_t rb =
+        rg_rsrc(src + (size_t)k0 * a.d + c0, ((K - k0) * a.d - c0) * 2);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = k0 + tid / 16 + 16 * j;
-      bv[j] = k < K ? *reinterpret_cast<const uint4*>(src + (size_t)k * a.d + c0 + tid % 16 * 8)
-                    : make_uint4(0, 0, 0, 0);
-    }
+    for (int j = 0; j < 4; ++j)
+      bv[j] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                                            rb, ((i + 16 * j) * a.d + c * 8) * 2, 0, 0));
   }
   MOE_DEV void store(uint16_t* lds) const {
     const int tid = threadIdx.x;
