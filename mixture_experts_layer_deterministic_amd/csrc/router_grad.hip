@@ -59,17 +59,30 @@ MOE_DEV uint4 kmajor_frag64(const uint16_t* s, int base, int kb, int lane) {
   return make_uint4(a.x, a.y, b.x, b.y);
 }
 
-// One tile: DW, 64 experts x 128 columns of dWr, reduced over the tokens; else 128 tokens x 128
-// columns of dx, reduced over the experts. Four waves, 2 x 2. A step's dl tile is split once
-// for the workgroup, on its way from registers to LDS; the loads of the next step are out by
-// then. The bf16 operand lies in LDS as it does in memory and reaches the MFMAs through the
-// transposing read; so does dl for dWr, whose reduction axis is the slow one of both.
+// One tile a workgroup of eight waves. DW: 64 experts x 128 columns of dWr, reduced over the
+// tokens; waves 0..3 take the even steps of 64 tokens and waves 4..7 the odd ones, and the second
+// sum is added to the first at the end: the tokens are many and these tiles few, and two chains
+// of steps fill a CU better than one (57 -> 54 us at 2048 x 7168 x 256). Else 128 tokens x 128
+// columns of dx, reduced over the experts by all eight waves. A wave holds 32 x 64 outputs.
+// A step's dl tile is split once for its waves, on its way from registers to LDS; the loads of
+// the next step are out by then. The bf16 operand lies in LDS as it does in memory and reaches
+// the MFMAs through the transposing read; so does dl for dWr, whose reduction axis is the slow
+// one of both.
+constexpr int kRgLdsW = 3 * 64 * kRgK + kRgK * kRgN;   // values of one half's stage
+constexpr int kRgLdsX = 2 * 128 * kRgK + kRgK * kRgN;
+constexpr int kRgLds = 2 * kRgLdsW;
+static_assert(kRgLdsX <= kRgLds && 64 * kRgN * 2 <= kRgLds, "dx's stage and a half's sums fit");
+
 template <bool DW>
 struct RouterTile {
-  static constexpr int P = DW ? 3 : 2, BM = DW ? 64 : 128, MB = BM / 32, AJ = BM / 16;
-  static constexpr int kPlane = BM * kRgK;  // values of one part
+  static constexpr int P = DW ? 3 : 2, BM = DW ? 64 : 128, MB = 2, AJ = 4;
+  static constexpr int kThr = DW ? 256 : 512;   // threads that share a stage
+  static constexpr int kRows = kThr / 16, BJ = kRgK / kRows;
+  static constexpr int kPlane = BM * kRgK;      // values of one part
+  static constexpr int kStride = DW ? 2 * kRgK : kRgK;
+  int tid, wm, wn, lane;
   f32x4 av[AJ];
-  uint4 bv[4];
+  uint4 bv[BJ];
   f32x4 acc[MB][4];
 
   // dl rows: DW, tokens k0 + i (reduction), experts r0 ..; else tokens r0 + i, experts k0 ..
@@ -77,27 +90,27 @@ struct RouterTile {
   // A dl row's columns past E belong to the next row: for dx the weight rows they meet are
   // zeros, for dWr they lead to rows that are not stored.
   MOE_DEV void load(const RouterGradArgs& a, int r0, int c0, int k0) {
-    const int tid = threadIdx.x, i = tid / 16, c = tid % 16;
+    const int i = tid / 16, c = tid % 16, K = DW ? a.T : a.E;
     const size_t t0 = DW ? k0 : r0, e0 = DW ? r0 : k0;
-    const __amdgpu_buffer_rsrc_t ra = rg_rsrc(a.dl + t0 * a.E + e0, ((a.T - t0) * a.E - e0) * 4);
+    const size_t left = k0 < K ? 1 : 0;  // a half may have no step where the other has one
+    const __amdgpu_buffer_rsrc_t ra =
+        rg_rsrc(a.dl + t0 * a.E + e0, left * ((a.T - t0) * a.E - e0) * 4);
 #pragma unroll
     for (int j = 0; j < AJ; ++j)
       av[j] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                            ra, ((i + 16 * j) * a.E + c * 4) * 4, 0, 0));
+                                            ra, ((i + kRows * j) * a.E + c * 4) * 4, 0, 0));
     const uint16_t* src = DW ? a.x : a.wr;
-    const size_t K = DW ? a.T : a.E;
     const __amdgpu_buffer_rsrc_t rb =
-        rg_rsrc(src + (size_t)k0 * a.d + c0, ((K - k0) * a.d - c0) * 2);
+        rg_rsrc(src + (size_t)k0 * a.d + c0, left * ((size_t)(K - k0) * a.d - c0) * 2);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < BJ; ++j)
       bv[j] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                                            rb, ((i + 16 * j) * a.d + c * 8) * 2, 0, 0));
+                                            rb, ((i + kRows * j) * a.d + c * 8) * 2, 0, 0));
   }
   MOE_DEV void store(uint16_t* lds) const {
-    const int tid = threadIdx.x;
 #pragma unroll
     for (int j = 0; j < AJ; ++j) {
-      const int i = tid / 16 + 16 * j, c = tid % 16 * 4;
+      const int i = tid / 16 + kRows * j, c = tid % 16 * 4;
       uint2 part[P];
       split4<P>(av[j], part);
       const int at = DW ? i * 64 + (c ^ swz64(i)) : rowswz(i, c / 8) + c % 8;
@@ -105,26 +118,31 @@ struct RouterTile {
       for (int p = 0; p < P; ++p) *reinterpret_cast<uint2*>(lds + p * kPlane + at) = part[p];
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = tid / 16 + 16 * j;
+    for (int j = 0; j < BJ; ++j) {
+      const int k = tid / 16 + kRows * j;
       *reinterpret_cast<uint4*>(lds + P * kPlane + k * kRgN + ((tid % 16 * 8) ^ kmajor_swz(k))) =
           bv[j];
     }
   }
-  MOE_DEV void run(const RouterGradArgs& a, int r0, int c0, uint16_t* lds) {
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int wm = wave / 2, wn = wave % 2;
+  MOE_DEV void run(const RouterGradArgs& a, int r0, int c0, uint16_t* all) {
+    const int wave = threadIdx.x / kWave, half = DW ? wave / 4 : 0;
+    lane = threadIdx.x % kWave;
+    tid = threadIdx.x % kThr;
+    wm = wave % (kThr / kWave) / 2;
+    wn = wave % 2;
+    uint16_t* lds = all + half * kRgLdsW;
     const int R = DW ? a.E : a.T, K = DW ? a.T : a.E;
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    load(a, r0, c0, 0);
-    for (int k0 = 0; k0 < K; k0 += kRgK) {
+    const int first = __builtin_amdgcn_readfirstlane(half) * kRgK;
+    load(a, r0, c0, first);
+    for (int k0 = 0; k0 < K; k0 += kStride) {
       __syncthreads();
       store(lds);
       __syncthreads();
-      if (k0 + kRgK < K) load(a, r0, c0, k0 + kRgK);
+      if (k0 + kStride < K) load(a, r0, c0, k0 + kStride + first);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         uint4 bf[4];
@@ -145,6 +163,18 @@ struct RouterTile {
           }
         }
       }
+    }
+    if constexpr (DW) {  // the odd steps' sums, lane by lane
+      f32x4* sum = reinterpret_cast<f32x4*>(all) + tid;
+      __syncthreads();
+      if (half == 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i * 256] = acc[i / 4][i % 4];
+      }
+      __syncthreads();
+      if (half == 1) return;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i / 4][i % 4] += sum[i * 256];
     }
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -171,9 +201,8 @@ struct RouterTile {
 };
 
 // The dWr tiles come first: their reductions are the long ones.
-__global__ void __launch_bounds__(256, 2) router_backward_kernel(const RouterGradArgs a, int nw) {
-  __shared__ __align__(16) uint16_t lds[2 * 128 * kRgK + kRgK * kRgN];
-  static_assert(3 * 64 * kRgK <= 2 * 128 * kRgK, "either tile's parts fit");
+__global__ void __launch_bounds__(512, 4) router_backward_kernel(const RouterGradArgs a, int nw) {
+  __shared__ __align__(16) uint16_t lds[kRgLds];
   const int nc = a.d / kRgN;
   const int b = blockIdx.x;
   if (b < nw) {
@@ -192,7 +221,7 @@ hipError_t launch_router_backward(const RouterGradArgs& a, hipStream_t s) {
   const int nw = a.dwr ? (a.E + 63) / 64 * nc : 0, nx = a.dx ? (a.T + 127) / 128 * nc : 0;
   {
     TraceScope trace("router_backward", s);
-    hipLaunchKernelGGL(router_backward_kernel, dim3(nw + nx), dim3(256), 0, s, a, nw);
+    hipLaunchKernelGGL(router_backward_kernel, dim3(nw + nx), dim3(512), 0, s, a, nw);
   }
   return hipGetLastError();
 }
