@@ -49,7 +49,8 @@ typedef enum moe_status {
     MOE_ERR_WORKSPACE_TOO_SMALL = -5
 } moe_status;
 
-enum { MOE_PREC_BF16 = 0, MOE_PREC_MXFP8 = 1, MOE_PREC_MXFP4 = 2 };
+/* 3 is not in use. */
+enum { MOE_PREC_BF16 = 0, MOE_PREC_MXFP8 = 1, MOE_PREC_MXFP4 = 2, MOE_PREC_FP8 = 4 };
 
 /* cfg.flags bits */
 enum {
@@ -71,7 +72,7 @@ enum {
  * I % 128 == 0 (128-wide tiles along I); T * k < 2^31; T * E < 2^31; and, because the kernels
  * address rows with 32-bit offsets: T * d < 2^31, T * k * d < 2^31, T * k * 2I < 2^31 (an
  * expert may receive all T * k rows) and 4 * I * d < 2^31 (the bytes of one expert's W1).
- * precision MOE_PREC_BF16, MOE_PREC_MXFP8 or MOE_PREC_MXFP4 (MXFP4 also needs I % 256 == 0: its
+ * precision MOE_PREC_BF16, MOE_PREC_MXFP8, MOE_PREC_FP8 or MOE_PREC_MXFP4 (MXFP4 also needs I % 256 == 0: its
  * K steps along I are 256 deep).
  * Every entry point that enqueues work also checks that the current HIP device is a gfx950
  * (MOE_ERR_UNSUPPORTED otherwise, MOE_ERR_HIP when no device can be queried).
@@ -100,6 +101,14 @@ enum {
  * MOE_FLAG_MXFP8_WGRAD is not accepted. Buffers: a ring slot holds Xp's codes [T*k, d/2 bytes]
  * then its scales; moe_quantize_weights writes the four weight copies in E2M1.
  *
+ * FP8 mode takes the block-scaled FP8 format of the moe_fp8_ calls below: E4M3 with one fp32 scale
+ * per 1 x 128 of the rows and per 128 x 128 of the weights, on the axes of the MX modes. The
+ * forward products read Xp and W1 quantised along d, and A and W2 along I; the dgrad products dY
+ * and W2 along d, and dH and W1 along 2I. The ring slot holds bf16 Xp as in BF16 mode, and the
+ * weight gradients and dWr read bf16 operands. A is computed from the stored H, and dw and dH from
+ * dA' rounded to bf16, each product's output. moe_quantize_weights is needed as in the MX modes.
+ * MOE_FLAG_PERSISTENT and MOE_FLAG_MXFP8_WGRAD are not accepted, moe_forward_fused not provided.
+ *
  * Weight-gradient precision. The pages do not say in which precision the weight gradients are
  * kept. By default dw1 and dw2 are fp32 (the caller's main gradient, which microbatches
  * accumulate into). With MOE_FLAG_BF16_DW (any precision) they are bf16: each element is
@@ -125,7 +134,7 @@ typedef struct moe_sizes {
     size_t ws_O;           /* offset of the expert outputs O, bf16 [T*k, d], valid after forward */
     size_t ws_dH;          /* offset of dH, bf16 [T*k, 2I], valid after backward */
     size_t ws_dXp;         /* offset of dXp, bf16 [T*k, d], valid after backward */
-    size_t wq;             /* MX modes: bytes of the quantised-weight buffer (0 in BF16 mode) */
+    size_t wq;             /* MX and FP8 modes: bytes of the quantised-weight buffer (else 0) */
 } moe_sizes;
 
 /* Sizes of every caller buffer for `cfg`. Host only; enqueues nothing. (Plumbing of this
@@ -137,13 +146,13 @@ typedef struct moe_sizes {
 int moe_query(const moe_cfg* cfg, moe_sizes* out);
 
 /*
- * moe_quantize_weights - MX modes only: the quantised expert weights every MXFP8 or MXFP4 forward
- * and backward reads. Call it once per weight update; the result serves any number of batches.
+ * moe_quantize_weights - MX and FP8 modes: the quantised expert weights every such forward and
+ * backward reads. Call it once per weight update; the result serves any number of batches.
  *
  *   w1  bf16 [E, 2I, d]   in
  *   w2  bf16 [E, d, I]    in
  *   wq  bytes [wq_bytes]  out, wq_bytes >= moe_sizes.wq. It receives four quantised tensors, each
- *       with its per-32 scales: W1 along d [E, 2I, d] and W2 along I [E, d, I] (forward), and W2
+ *       with its scales (per 32 in the MX modes): W1 along d [E, 2I, d] and W2 along I [E, d, I] (forward), and W2
  *       along d stored transposed [E, I, d] and W1 along 2I stored transposed [E, d, 2I]
  *       (dgrad), in the mode's element format. The layout inside wq is private to the library.
  * Errors: MOE_ERR_INVALID_ARG in BF16 mode; MOE_ERR_WORKSPACE_TOO_SMALL for a short wq.
@@ -242,8 +251,8 @@ int moe_permute_static(const moe_cfg* cfg, const int32_t* topk_idx, const void* 
  *   topk_w   fp32 [T, k]     in
  *   w1       bf16 [E, 2I, d] in
  *   w2       bf16 [E, d, I]  in
- *   wq, wq_bytes             in: MX modes, the buffer moe_quantize_weights filled (ignored in
- *                                BF16 mode, may be NULL)
+ *   wq, wq_bytes             in: MX and FP8 modes, the buffer moe_quantize_weights filled
+ *                                (ignored in BF16 mode, may be NULL)
  *   y        bf16 [T, d]     out
  *   saved    bytes [saved_bytes]   out: H and A at the offsets moe_query reports
  *   workspace bytes [ws_bytes]     scratch
@@ -268,7 +277,7 @@ int moe_forward(const moe_cfg* cfg, const void* ring, size_t ring_bytes, int32_t
  * receives 256 rows or more; otherwise the down projection of those experts' rows sums its K
  * chunks from another start (the separate path gives such blocks a 256 x 256 tile), which
  * changes their O and y in the last bits only. Arguments and errors are those of the three
- * calls; the MX modes return MOE_ERR_UNSUPPORTED. The grid barriers keep their state in a
+ * calls; the other modes return MOE_ERR_UNSUPPORTED. The grid barriers keep their state in a
  * device variable of the library, one per GPU: fused calls that overlap on one GPU race.
  */
 int moe_forward_fused(const moe_cfg* cfg, const void* x, const void* w_router, float* logits,

@@ -22,7 +22,7 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct Layout {
-  bool mx;
+  bool mx, f8;  // the MX modes; the block-scaled FP8 mode
   int fb;  // MX code bits: 8 (MXFP8) or 4 (MXFP4); 0 in BF16 mode
   // workspace
   size_t status, sched, blk_cnt, blk_flag, rank, O, dH, dXp, dyw, dwpart, dl_pos, wg_count,
@@ -33,6 +33,8 @@ struct Layout {
   // operands of one weight gradient quantised along the positions, [rows][P] with scales
   size_t poff, lq, lqs, rq, rqs;
   int P;
+  // workspace, FP8 mode only: the rows of one product quantised (Xp, A, dY or dH), and dA'
+  size_t f8q, f8s, dAp;
   // saved
   size_t H, A, saved_total;
   // ring slot: bf16 Xp, or MX Xp codes at 0 and scales at slot_sc
@@ -130,6 +132,11 @@ Layout layout(const moe_cfg* c) {
   L.lqs = take(lrows * P / 32);
   L.rq = take(rrows * P);
   L.rqs = take(rrows * P / 32);
+  L.f8 = c->precision == MOE_PREC_FP8;
+  const size_t f8 = L.f8 ? 1 : 0, fcols = std::max(d, 2 * I);
+  L.f8q = take(f8 * Tk * fcols);
+  L.f8s = take(f8 * sizeof(float) * Tk * (fcols / 128));
+  L.dAp = take(f8 * 2 * Tk * I);
   L.total = o;
   o = 0;
   L.H = take(2 * Tk * 2 * I);
@@ -153,6 +160,19 @@ Layout layout(const moe_cfg* c) {
     L.wq_total = o;
   } else {
     L.slot = 2 * Tk * d;
+  }
+  if (L.f8) {  // both orientations of both weights, a scale per 128 x 128
+    const size_t n1 = E * 2 * I * d, n2 = E * d * I;
+    o = 0;
+    L.w1f = take(n1);
+    L.w1fs = take(sizeof(float) * (n1 / 16384));
+    L.w2f = take(n2);
+    L.w2fs = take(sizeof(float) * (n2 / 16384));
+    L.w2b = take(n2);
+    L.w2bs = take(sizeof(float) * (n2 / 16384));
+    L.w1b = take(n1);
+    L.w1bs = take(sizeof(float) * (n1 / 16384));
+    L.wq_total = o;
   }
   return L;
 }
@@ -181,8 +201,9 @@ struct Launches {
 int check_mode(const moe_cfg* c) {
   if (!cfg_ok(c)) return MOE_ERR_INVALID_ARG;
   if (c->precision != MOE_PREC_BF16 && c->precision != MOE_PREC_MXFP8 &&
-      c->precision != MOE_PREC_MXFP4)
+      c->precision != MOE_PREC_MXFP4 && c->precision != MOE_PREC_FP8)
     return MOE_ERR_UNSUPPORTED;
+  if (c->precision == MOE_PREC_FP8 && (c->flags & MOE_FLAG_PERSISTENT)) return MOE_ERR_INVALID_ARG;
   if (c->precision == MOE_PREC_MXFP4 && c->I % 256 != 0) return MOE_ERR_INVALID_ARG;
   if (c->flags & ~(MOE_FLAG_PERSISTENT | MOE_FLAG_MXFP8_WGRAD | MOE_FLAG_BF16_DW))
     return MOE_ERR_INVALID_ARG;
@@ -199,7 +220,7 @@ int check_ring(const Layout& L, const void* ring, size_t ring_bytes, int32_t slo
 
 // The quantised weights of the MX modes, or an error code when they are missing.
 int check_wq(const Layout& Y, const void* wq, size_t wq_bytes) {
-  if (!Y.mx) return MOE_OK;
+  if (!Y.mx && !Y.f8) return MOE_OK;
   if (!aligned16(wq)) return MOE_ERR_INVALID_ARG;
   if (wq_bytes < Y.wq_total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return MOE_OK;
@@ -299,7 +320,7 @@ int moe_query(const moe_cfg* cfg, moe_sizes* out) {
   out->ws_O = L.O;
   out->ws_dH = L.dH;
   out->ws_dXp = L.dXp;
-  out->wq = L.mx ? L.wq_total : 0;
+  out->wq = L.mx || L.f8 ? L.wq_total : 0;
   return MOE_OK;
 }
 
@@ -308,7 +329,7 @@ int moe_quantize_weights(const moe_cfg* cfg, const void* w1, const void* w2, voi
   int st = check_mode(cfg);
   if (st) return st;
   const Layout Y = layout(cfg);
-  if (!Y.mx) return MOE_ERR_INVALID_ARG;
+  if (!Y.mx && !Y.f8) return MOE_ERR_INVALID_ARG;
   if (!aligned16(w1) || !aligned16(w2) || !aligned16(wq)) return MOE_ERR_INVALID_ARG;
   if (wq_bytes < Y.wq_total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if ((st = check_device())) return st;
@@ -317,6 +338,14 @@ int moe_quantize_weights(const moe_cfg* cfg, const void* w1, const void* w2, voi
   const uint16_t* a1 = static_cast<const uint16_t*>(w1);
   const uint16_t* a2 = static_cast<const uint16_t*>(w2);
   Launches L;
+  if (Y.f8) {
+    L(launch_fp8_quant_weights(a1, E, 2 * I, d, at<uint8_t>(wq, Y.w1f), at<float>(wq, Y.w1fs),
+                               at<uint8_t>(wq, Y.w1b), at<float>(wq, Y.w1bs), s));
+    if (!L.err)
+      L(launch_fp8_quant_weights(a2, E, d, I, at<uint8_t>(wq, Y.w2f), at<float>(wq, Y.w2fs),
+                                 at<uint8_t>(wq, Y.w2b), at<float>(wq, Y.w2bs), s));
+    return L.status();
+  }
   L(launch_quant_weight(a1, E, 2 * I, d, at<uint8_t>(wq, Y.w1f), at<uint8_t>(wq, Y.w1fs),
                         at<uint8_t>(wq, Y.w1b), at<uint8_t>(wq, Y.w1bs), Y.fb, "quant_w1", s));
   if (!L.err)
@@ -444,6 +473,24 @@ int moe_forward(const moe_cfg* cfg, const void* ring, size_t ring_bytes, int32_t
   uint16_t* A = at<uint16_t>(saved, Y.A);
   uint16_t* O = at<uint16_t>(workspace, Y.O);
   Launches L;
+  if (Y.f8) {
+    // the products find their row tiles from the offsets: no schedule table
+    uint8_t* q = at<uint8_t>(workspace, Y.f8q);
+    float* qs = at<float>(workspace, Y.f8s);
+    L(launch_fp8_quant_rows(reinterpret_cast<const uint16_t*>(slot_base), Tk, d, q, qs, s));
+    if (!L.err)
+      L(launch_fp8_gemm({offsets, q, qs, at<uint8_t>(wq, Y.w1f), at<float>(wq, Y.w1fs), H, Tk, E,
+                         2 * I, d},
+                        s));
+    if (!L.err) L(launch_fp8_swiglu(H, offsets + E, Tk, I, A, q, qs, s));
+    if (!L.err)
+      L(launch_fp8_gemm({offsets, q, qs, at<uint8_t>(wq, Y.w2f), at<float>(wq, Y.w2fs), O, Tk, E,
+                         d, I},
+                        s));
+    if (!L.err)
+      L(launch_combine(O, tk_row, topk_w, cfg->T, cfg->k, d, static_cast<uint16_t*>(y), s));
+    return L.status();
+  }
   L(launch_sched_build(offsets, E, Tk, sched, s));
   if (Y.mx) {
     uint8_t* aq = at<uint8_t>(workspace, Y.aq);
@@ -571,8 +618,37 @@ int moe_backward(const moe_cfg* cfg, const void* ring, size_t ring_bytes, int32_
   const uint16_t* w1p = static_cast<const uint16_t*>(w1);
   const uint16_t* w2p = static_cast<const uint16_t*>(w2);
   Launches L;
-  L(launch_sched_build(offsets, E, Tk, sched, s));
-  if (Y.mx) {
+  if (!Y.f8) L(launch_sched_build(offsets, E, Tk, sched, s));
+  if (Y.f8) {
+    uint8_t* q = at<uint8_t>(workspace, Y.f8q);
+    float* qs = at<float>(workspace, Y.f8s);
+    uint16_t* dAp = at<uint16_t>(workspace, Y.dAp);
+    L(launch_scale_gather(dyp, tk_row, topk_w, cfg->T, k, d, dyw, s));
+    if (!L.err) L(launch_fp8_quant_gather(dyp, row_src, k, offsets + E, Tk, d, q, qs, s));
+    if (!L.err)
+      L(launch_fp8_gemm({offsets, q, qs, at<uint8_t>(wq, Y.w2b), at<float>(wq, Y.w2bs), dAp, Tk, E,
+                         I, d},
+                        s));
+    if (!L.err)
+      L(launch_fp8_swiglu_bwd({dAp, H, A, row_src, topk_w, offsets + E, Tk, I, dH, q, qs, dwpart},
+                              s));
+    if (!L.err)
+      L(launch_dw_router(dwpart, Y.nIt, tk_row, topk_w, cfg->T, k, d_topk_w, dl_pos, routed, s));
+    if (!L.err)
+      L(launch_wgrad({dyw, A, nullptr, nullptr, dw2, offsets, at<int4>(workspace, Y.wg_table2),
+                      wg_count + 1, E, d, I, accumulate, bdw, false, "bwd_down_wgrad",
+                      "wgrad_sched_down"},
+                     s));
+    if (!L.err)
+      L(launch_fp8_gemm({offsets, q, qs, at<uint8_t>(wq, Y.w1b), at<float>(wq, Y.w1bs), dXp, Tk, E,
+                         d, 2 * I},
+                        s));
+    if (!L.err)
+      L(launch_wgrad({dH, xp, nullptr, nullptr, dw1, offsets, at<int4>(workspace, Y.wg_table1),
+                      wg_count, E, 2 * I, d, accumulate, bdw, true, "bwd_gate_wgrad",
+                      "wgrad_sched_gate"},
+                     s));
+  } else if (Y.mx) {
     uint8_t* dyq = at<uint8_t>(workspace, Y.dyq);
     uint8_t* dys = at<uint8_t>(workspace, Y.dys);
     uint8_t* dhq = at<uint8_t>(workspace, Y.dhq);

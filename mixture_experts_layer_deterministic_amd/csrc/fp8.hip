@@ -71,6 +71,109 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const uint16_t* __r
   }
 }
 
+// The layer's own operands, in position order: rows at and past offsets[E] (skipped bad-index
+// rows leave some) are neither read nor written.
+//
+// Row pos of dY in position order: dy[row_src[pos] / k].
+__global__ void __launch_bounds__(256) fp8_quant_gather_kernel(
+    const uint16_t* __restrict__ src, const int32_t* __restrict__ row_src, int k,
+    const int32_t* __restrict__ placed, int M, int cols, uint8_t* __restrict__ codes,
+    float* __restrict__ scales) {
+  const long long v = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int vpr = cols / 8;
+  const long long pos = v / vpr;  // the same for the sixteen lanes of a block
+  if (pos >= min(*placed, M)) return;
+  const int c = (int)(v - pos * vpr);
+  float f[8];
+  widen8(*reinterpret_cast<const uint4*>(src + (size_t)(row_src[pos] / k) * cols + c * 8), f);
+  float amax = amax8(f);
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+  const BlockScale b = block_scale(amax);
+  reinterpret_cast<uint2*>(codes)[v] = codes8(f, b.inv);
+  if (c % 16 == 0) scales[(size_t)(c / 16) * M + pos] = b.scale;
+}
+
+// A = silu(g) u from the stored H = [g | u], rounded to bf16 and quantised from that.
+__global__ void __launch_bounds__(256) fp8_swiglu_kernel(const uint16_t* __restrict__ H,
+                                                         const int32_t* __restrict__ placed, int M,
+                                                         int I, uint16_t* __restrict__ A,
+                                                         uint8_t* __restrict__ codes,
+                                                         float* __restrict__ scales) {
+  const long long v = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int vpr = I / 8;
+  const long long pos = v / vpr;
+  if (pos >= min(*placed, M)) return;
+  const int c = (int)(v - pos * vpr);
+  const uint16_t* h = H + pos * 2 * I + c * 8;
+  float g[8], u[8], f[8];
+  widen8(*reinterpret_cast<const uint4*>(h), g);
+  widen8(*reinterpret_cast<const uint4*>(h + I), u);
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    w[q] = pack_bf2(silu(g[2 * q]) * u[2 * q], silu(g[2 * q + 1]) * u[2 * q + 1]);
+  const uint4 a = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(A)[v] = a;
+  widen8(a, f);
+  float amax = amax8(f);
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+  const BlockScale b = block_scale(amax);
+  reinterpret_cast<uint2*>(codes)[v] = codes8(f, b.inv);
+  if (c % 16 == 0) scales[(size_t)(c / 16) * M + pos] = b.scale;
+}
+
+// The SwiGLU backward: dH = [dg | du] from dA' (bf16), H, A and the row's weight, rounded to bf16
+// and quantised from that; and the router-weight gradient's partial <dA', A> of each 128 columns.
+__global__ void __launch_bounds__(256) fp8_swiglu_bwd_kernel(
+    const uint16_t* __restrict__ dAp, const uint16_t* __restrict__ H,
+    const uint16_t* __restrict__ A, const int32_t* __restrict__ row_src,
+    const float* __restrict__ topk_w, const int32_t* __restrict__ placed, int M, int I,
+    uint16_t* __restrict__ dH, uint8_t* __restrict__ codes, float* __restrict__ scales,
+    float* __restrict__ dwpart) {
+  const long long v = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int vpr = I / 8;
+  const long long pos = v / vpr;
+  if (pos >= min(*placed, M)) return;
+  const int c = (int)(v - pos * vpr);
+  const float wt = topk_w[row_src[pos]];
+  const uint16_t* h = H + pos * 2 * I + c * 8;
+  float dap[8], a[8], g[8], u[8];
+  widen8(reinterpret_cast<const uint4*>(dAp)[v], dap);
+  widen8(reinterpret_cast<const uint4*>(A)[v], a);
+  widen8(*reinterpret_cast<const uint4*>(h), g);
+  widen8(*reinterpret_cast<const uint4*>(h + I), u);
+  float dg[8], du[8], part = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    part = __builtin_fmaf(dap[i], a[i], part);
+    const float da = wt * dap[i], s = sigmoid(g[i]);
+    dg[i] = da * u[i] * s * (1.0f + g[i] * (1.0f - s));
+    du[i] = da * (g[i] * s);
+  }
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) part += __shfl_xor(part, o);
+  const int blk = c / 16, nb = I / kQB;
+  if (c % 16 == 0) dwpart[pos * nb + blk] = part;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const float* d = half ? du : dg;
+    const uint4 o = make_uint4(pack_bf2(d[0], d[1]), pack_bf2(d[2], d[3]), pack_bf2(d[4], d[5]),
+                               pack_bf2(d[6], d[7]));
+    const size_t at = pos * 2 * I + half * I + c * 8;
+    *reinterpret_cast<uint4*>(dH + at) = o;
+    float f[8];
+    widen8(o, f);
+    float amax = amax8(f);
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) amax = fmaxf(amax, __shfl_xor(amax, x));
+    const BlockScale b = block_scale(amax);
+    *reinterpret_cast<uint2*>(codes + at) = codes8(f, b.inv);
+    if (c % 16 == 0) scales[(size_t)(half * nb + blk) * M + pos] = b.scale;
+  }
+}
+
 // One workgroup per 128 x 128 block, which it reads once; the transposed copy goes through LDS.
 __global__ void __launch_bounds__(256) fp8_quant_weights_kernel(
     const uint16_t* __restrict__ src, int N, int K, uint8_t* __restrict__ codes,
@@ -663,6 +766,37 @@ hipError_t launch_fp8_quant_rows(const uint16_t* src, int rows, int cols, uint8_
     TraceScope trace("fp8_quant_rows", s);
     hipLaunchKernelGGL(fp8_quant_rows_kernel, dim3((unsigned)((nv + 255) / 256)), dim3(256), 0, s,
                        src, rows, cols, codes, scales);
+  }
+  return hipGetLastError();
+}
+
+static dim3 grid8(long long rows, int cols) {  // a thread for eight values
+  return dim3((unsigned)((rows * cols / 8 + 255) / 256));
+}
+hipError_t launch_fp8_quant_gather(const uint16_t* src, const int32_t* row_src, int k,
+                                   const int32_t* placed, int M, int cols, uint8_t* codes,
+                                   float* scales, hipStream_t s) {
+  {
+    TraceScope trace("fp8_quant_dy", s);
+    hipLaunchKernelGGL(fp8_quant_gather_kernel, grid8(M, cols), dim3(256), 0, s, src, row_src, k,
+                       placed, M, cols, codes, scales);
+  }
+  return hipGetLastError();
+}
+hipError_t launch_fp8_swiglu(const uint16_t* H, const int32_t* placed, int M, int I, uint16_t* A,
+                             uint8_t* codes, float* scales, hipStream_t s) {
+  {
+    TraceScope trace("fp8_swiglu", s);
+    hipLaunchKernelGGL(fp8_swiglu_kernel, grid8(M, I), dim3(256), 0, s, H, placed, M, I, A, codes,
+                       scales);
+  }
+  return hipGetLastError();
+}
+hipError_t launch_fp8_swiglu_bwd(const Fp8SwigluBwdArgs& a, hipStream_t s) {
+  {
+    TraceScope trace("fp8_swiglu_bwd", s);
+    hipLaunchKernelGGL(fp8_swiglu_bwd_kernel, grid8(a.M, a.I), dim3(256), 0, s, a.dAp, a.H, a.A,
+                       a.row_src, a.topk_w, a.placed, a.M, a.I, a.dH, a.codes, a.scales, a.dwpart);
   }
   return hipGetLastError();
 }

@@ -40,6 +40,28 @@ hipError_t launch_fp8_quant_rows(const uint16_t* src, int rows, int cols, uint8_
 hipError_t launch_fp8_quant_weights(const uint16_t* src, int E, int N, int K, uint8_t* codes,
                                     float* scales, uint8_t* codes_t, float* scales_t,
                                     hipStream_t s);
+// The FP8 mode's steps around its products; M rows in position order, `placed` (device) of them
+// in use. Scales are [columns / 128, M].
+hipError_t launch_fp8_quant_gather(const uint16_t* src, const int32_t* row_src, int k,
+                                   const int32_t* placed, int M, int cols, uint8_t* codes,
+                                   float* scales, hipStream_t s);
+hipError_t launch_fp8_swiglu(const uint16_t* H, const int32_t* placed, int M, int I, uint16_t* A,
+                             uint8_t* codes, float* scales, hipStream_t s);
+struct Fp8SwigluBwdArgs {
+  const uint16_t* dAp;     // bf16 [M, I]
+  const uint16_t* H;       // bf16 [M, 2I]
+  const uint16_t* A;       // bf16 [M, I]
+  const int32_t* row_src;  // [M]
+  const float* topk_w;     // [M] flat
+  const int32_t* placed;
+  int M, I;
+  uint16_t* dH;            // bf16 [M, 2I]
+  uint8_t* codes;          // dH's codes [M, 2I]
+  float* scales;
+  float* dwpart;           // [M, I / 128]
+};
+hipError_t launch_fp8_swiglu_bwd(const Fp8SwigluBwdArgs& a, hipStream_t s);
+
 struct Fp8GemmArgs {
   const int32_t* offsets;  // [E + 1]
   const uint8_t* a;        // [M, K] codes

@@ -7,8 +7,9 @@ from __future__ import annotations
 import torch
 
 from . import (MOE_FLAG_BF16_DW, MOE_FLAG_MXFP8_WGRAD, MOE_FLAG_PERSISTENT, MOE_PREC_BF16,
-               MOE_PREC_MXFP4, MOE_PREC_MXFP8, make_cfg, moe_backward, moe_forward, moe_forward_fused, moe_permute,
-               moe_query, moe_quantize_weights, moe_route)
+               MOE_PREC_MXFP4, MOE_PREC_MXFP8, make_cfg, moe_backward, moe_forward, moe_forward_fused,
+               moe_gate_backward, moe_permute, moe_query, moe_quantize_weights, moe_route,
+               moe_route_gated, moe_router_backward)
 
 
 class MoeLayer:
@@ -18,11 +19,16 @@ class MoeLayer:
     and backward reads the slot its batch was permuted into. With ``precision=MOE_PREC_MXFP8``
     or ``MOE_PREC_MXFP4`` the layer also owns the quantised-weight buffer ``wq``;
     ``quantize_weights`` fills it, and ``mx_wgrad`` (MXFP8 only) makes the weight gradients
-    MXFP8 too. ``bf16_dw`` keeps dw1 and dw2 in bf16.
+    MXFP8 too. ``MOE_PREC_FP8`` owns and fills ``wq`` likewise; its ring slots hold bf16 tokens.
+    ``bf16_dw`` keeps dw1 and dw2 in bf16.
+
+    With ``gate`` (from ``make_gate``) the layer routes by that gate instead of the renormalised
+    top-k softmax, with ``gate_bias`` (fp32 [E], or None) in its choice, and backward takes the
+    router's gradients through it; ``dlogits`` holds the logits' gradient.
     """
 
     def __init__(self, T, d, E, k, I, device="cuda", ring_slots=1, persistent=False,
-                 precision=MOE_PREC_BF16, mx_wgrad=False, bf16_dw=False):
+                 precision=MOE_PREC_BF16, mx_wgrad=False, bf16_dw=False, gate=None, gate_bias=None):
         self.T, self.d, self.E, self.k, self.I = T, d, E, k, I
         flags = ((MOE_FLAG_PERSISTENT if persistent else 0) |
                  (MOE_FLAG_MXFP8_WGRAD if mx_wgrad else 0) | (MOE_FLAG_BF16_DW if bf16_dw else 0))
@@ -51,7 +57,9 @@ class MoeLayer:
         self.dwr = torch.zeros(E, d, dtype=f32, device=dev)
         self.mx = precision in (MOE_PREC_MXFP8, MOE_PREC_MXFP4)
         self.fbits = 8 if precision == MOE_PREC_MXFP8 else 4 if precision == MOE_PREC_MXFP4 else 16
-        self.wq = torch.empty(s.wq, dtype=u8, device=dev) if self.mx else None
+        self.wq = torch.empty(s.wq, dtype=u8, device=dev) if s.wq else None
+        self.gate, self.gate_bias = gate, gate_bias
+        self.dlogits = torch.empty(T, E, dtype=f32, device=dev) if gate is not None else None
 
     # views of intermediates -----------------------------------------------------------------
     def _view(self, buf, off, rows, cols):
@@ -91,6 +99,10 @@ class MoeLayer:
 
     # steps ----------------------------------------------------------------------------------
     def route(self, x, w_router, stream=None):
+        if self.gate is not None:
+            moe_route_gated(self.cfg, self.gate, x, w_router, self.gate_bias, self.logits,
+                            self.topk_idx, self.topk_w, self.workspace, stream)
+            return
         moe_route(self.cfg, x, w_router, self.logits, self.topk_idx, self.topk_w, self.workspace,
                   stream)
 
@@ -117,7 +129,19 @@ class MoeLayer:
                           w1, w2, self.y, self.saved if saved is None else saved, self.workspace,
                           stream)
 
-    def backward(self, w_router, w1, w2, dy, slot=0, accumulate=False, saved=None, stream=None):
+    def backward(self, w_router, w1, w2, dy, slot=0, accumulate=False, saved=None, stream=None,
+                 x=None):
+        """With a gate and a ``w_router``, ``x`` (the tokens) is needed too: the experts' backward
+        runs as for a given routing, then the gate's and the router's add theirs to dx and dwr."""
+        if self.gate is not None and w_router is not None:
+            if x is None:
+                raise ValueError("a gated layer's router gradients need x")
+            self.backward(None, w1, w2, dy, slot, accumulate, saved, stream)
+            moe_gate_backward(self.cfg, self.gate, self.logits, self.topk_idx, self.d_topk_w,
+                              self.dlogits, False, stream)
+            moe_router_backward(self.cfg, x, w_router, self.dlogits, self.dx, self.dwr, True,
+                                accumulate, stream)
+            return
         moe_backward(self.cfg, self.ring, slot, self.offsets, self.row_src, self.tk_row,
                      self.topk_idx, self.topk_w, w_router, w1, w2, self.wq,
                      self.saved if saved is None else saved, dy, self.dx, self.dw1, self.dw2,
@@ -128,6 +152,8 @@ class MoeLayer:
         """One fwd+bwd pass: route (when w_router is given), permute, forward, backward. With
         ``fused`` the first three run as one launch (moe_forward_fused)."""
         if fused:
+            if self.gate is not None:
+                raise ValueError("the single-launch forward routes by the top-k softmax only")
             self.forward_fused(x, w_router, w1, w2, slot, stream=stream)
             self.backward(w_router, w1, w2, dy, slot, stream=stream)
             return
@@ -135,7 +161,7 @@ class MoeLayer:
             self.route(x, w_router, stream)
         self.permute(x, slot, stream)
         self.forward(w1, w2, slot, stream=stream)
-        self.backward(w_router, w1, w2, dy, slot, stream=stream)
+        self.backward(w_router, w1, w2, dy, slot, stream=stream, x=x)
 
 
 class Macrobatch:

@@ -129,3 +129,52 @@ def fp8_gemm(offsets, a, sa, b, sb):
             w = b[e] * np.repeat(np.repeat(np.asarray(sb[e], np.float64), 128, 0), 128, 1)
             out[lo:hi] = av[lo:hi] @ w.T
     return out
+
+
+# the layer in FP8 mode -----------------------------------------------------------------------
+
+
+def bf16(x):
+    """Rounded to bfloat16, nearest, ties to even."""
+    u = np.asarray(x, np.float32).view(np.uint32).astype(np.uint64)
+    return ((u + 0x7FFF + ((u >> 16) & 1)) & 0xFFFF0000).astype(np.uint32).view(np.float32).astype(
+        np.float64)
+
+
+def _image(x, block_rows):
+    """The values the quantised x stands for."""
+    q, s = quantize(x, block_rows)
+    *b, R, K = x.shape
+    return (q.reshape(*b, R // block_rows, block_rows, K // 128, 128)
+            * np.asarray(s, np.float64)[..., :, None, :, None]).reshape(x.shape)
+
+
+def fp8_layer(X, W1, W2, dY, idx, w):
+    """Forward and backward of the FP8 mode with a given routing, in 64 bits, rounded and quantised
+    where the library stores: rows of experts in turn, each token's slots at the end."""
+    T, k = idx.shape
+    E, twoI, d = W1.shape
+    I = twoI // 2
+    out = dict(Y=np.zeros((T, d)), dX=np.zeros((T, d)), dW1=np.zeros(W1.shape),
+               dW2=np.zeros(W2.shape), dw=np.zeros((T, k)))
+    for e in range(E):
+        t, j = np.nonzero(idx == e)
+        if not len(t):
+            continue
+        x, wt = X[t], w[t, j][:, None].astype(np.float64)
+        q1, q2 = _image(W1[e], 128), _image(W2[e], 128)
+        H = bf16(_image(x, 1) @ q1.T)
+        g, u = H[:, :I], H[:, I:]
+        s = 1.0 / (1.0 + np.exp(-g))
+        A = bf16(g * s * u)
+        O = bf16(_image(A, 1) @ q2.T)
+        dap = bf16(_image(dY[t], 1) @ q2)
+        out["dw"][t, j] = (dap * A).sum(1)
+        da = wt * dap
+        dH = bf16(np.concatenate([da * u * s * (1 + g * (1 - s)), da * g * s], axis=1))
+        dXp = bf16(_image(dH, 1) @ q1)
+        out["dW1"][e] = dH.T @ x
+        out["dW2"][e] = bf16(wt * dY[t]).T @ A
+        np.add.at(out["Y"], t, wt * O)
+        np.add.at(out["dX"], t, dXp)
+    return out

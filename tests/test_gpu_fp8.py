@@ -14,6 +14,16 @@ pytestmark = pytest.mark.gpu
 F8 = torch.float8_e4m3fn
 
 
+@pytest.fixture(autouse=True)
+def _float32():
+    """The inputs below are fp32 where no type is named, whatever another test file set."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
+
 def _values(q):
     return q.float().cpu().numpy()
 

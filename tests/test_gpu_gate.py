@@ -19,6 +19,16 @@ U = 2.0 ** -24
 inf = math.inf
 
 
+@pytest.fixture(autouse=True)
+def _float32():
+    """The inputs below are fp32 where no type is named, whatever another test file set."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
+
 def _logits(T, E, seed, closed=0.0, ties=False):
     rng = np.random.default_rng(seed)
     l = rng.normal(scale=1.7, size=(T, E)).astype(np.float32)

@@ -16,6 +16,16 @@ P = ctypes.c_void_p(1 << 20)
 CFG = m.make_cfg(64, 256, 8, 2, 128)
 
 
+@pytest.fixture(autouse=True)
+def _float32():
+    """The inputs below are fp32 where no type is named, whatever another test file set."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
+
 def _ref(x):
     return ctypes.byref(x)
 
@@ -170,3 +180,28 @@ def test_e4m3_form_against_torch():
     v = torch.cat([torch.linspace(-460, 460, 4001), torch.linspace(-0.05, 0.05, 4001)])
     want = v.clamp(-448, 448).to(torch.float8_e4m3fn).float().numpy()
     np.testing.assert_array_equal(_ops.e4m3(v.numpy()), want)
+
+
+def test_fp8_mode_sizes_and_refusals():
+    T, d, E, k, I = 300, 512, 16, 3, 256
+    s8 = m.moe_query(m.make_cfg(T, d, E, k, I, m.MOE_PREC_FP8))
+    s = m.moe_query(m.make_cfg(T, d, E, k, I))
+    up = lambda v: (v + 255) // 256 * 256
+    Tk = T * k
+    assert s8.ring_slot == s.ring_slot and s8.saved == s.saved  # bf16 tokens and activations
+    n1, n2 = E * 2 * I * d, E * d * I
+    assert s8.wq == 2 * (up(n1) + up(4 * n1 // 16384) + up(n2) + up(4 * n2 // 16384))
+    f = max(d, 2 * I)
+    assert s8.workspace - s.workspace == up(Tk * f) + up(4 * Tk * f // 128) + up(2 * Tk * I)
+    assert m.moe_query(m.make_cfg(T, d, E, k, I, m.MOE_PREC_FP8, m.MOE_FLAG_BF16_DW)).wq == s8.wq
+    for flag in (m.MOE_FLAG_PERSISTENT, m.MOE_FLAG_MXFP8_WGRAD):
+        with pytest.raises(m.MoeError) as ei:
+            m.moe_query(m.make_cfg(T, d, E, k, I, m.MOE_PREC_FP8, flag))
+        assert ei.value.status == -1
+    L = m.lib()
+    c = m.make_cfg(T, d, E, k, I, m.MOE_PREC_FP8)
+    assert L.moe_forward_fused(_ref(c), P, P, P, P, P, P, s8.ring_slot, 0, P, P, P, P, P, P, P, P,
+                               s8.saved, P, s8.workspace, None) == -3
+    assert L.moe_quantize_weights(_ref(c), P, P, P, s8.wq - 1, None) == -5
+    assert L.moe_forward(_ref(c), P, s8.ring_slot, 0, P, P, P, P, P, None, 0, P, P, s8.saved, P,
+                         s8.workspace, None) == -1
