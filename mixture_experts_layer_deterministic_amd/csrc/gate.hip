@@ -52,46 +52,52 @@ MOE_DEV double read_lane(double x, int l) {
   return __builtin_bit_cast(double, (uint64_t)read_lane((uint32_t)u, l) |
                                         ((uint64_t)read_lane((uint32_t)(u >> 32), l) << 32));
 }
+// a in the lanes of the mask, b in the others. In assembly, since a chain of selects between
+// neighbours of an array is otherwise turned into selects by an index, among all of them.
+MOE_DEV uint32_t select_lanes(uint64_t mask, uint32_t a, uint32_t b) {
+  asm("v_cndmask_b32_e64 %0, %1, %2, %3" : "=v"(b) : "0"(b), "v"(a), "s"(mask));
+  return b;
+}
+MOE_DEV double select_lanes(uint64_t mask, double a, double b) {
+  const uint64_t x = __builtin_bit_cast(uint64_t, a), y = __builtin_bit_cast(uint64_t, b);
+  return __builtin_bit_cast(
+      double, (uint64_t)select_lanes(mask, (uint32_t)x, (uint32_t)y) |
+                  ((uint64_t)select_lanes(mask, (uint32_t)(x >> 32), (uint32_t)(y >> 32)) << 32));
+}
 MOE_DEV uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
 MOE_DEV float larger(float a, float b) { return fmaxf(a, b); }
 MOE_DEV double larger(double a, double b) { return __builtin_fmax(a, b); }
 MOE_DEV uint32_t smaller(uint32_t a, uint32_t b) { return min(a, b); }
 MOE_DEV double smaller(double a, double b) { return __builtin_fmin(a, b); }
-struct Add {
-  template <class F>
-  MOE_DEV F operator()(F a, F b) const { return a + b; }
-};
-struct Larger {
-  template <class F>
-  MOE_DEV F operator()(F a, F b) const { return larger(a, b); }
-};
+// x moved likewise; lanes without a source get 0.
+template <int CTRL, int ROWS>
+MOE_DEV uint32_t dpp0(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, ROWS == 0xf);
+}
+template <int CTRL, int ROWS>
+MOE_DEV float dpp0(float x) {
+  return __builtin_bit_cast(float, dpp0<CTRL, ROWS>(__builtin_bit_cast(uint32_t, x)));
+}
+template <int CTRL, int ROWS>
+MOE_DEV double dpp0(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  return __builtin_bit_cast(double, (uint64_t)dpp0<CTRL, ROWS>((uint32_t)u) |
+                                        ((uint64_t)dpp0<CTRL, ROWS>((uint32_t)(u >> 32)) << 32));
+}
 // Over the wave, the same in every lane: within rows of 16 lanes by shifts, then lane 15's and
-// lane 31's totals move on. Lanes that a shift gives nothing add `none`.
-template <class Op, class F>
-MOE_DEV F wave_reduce(F v, F none) {
-  Op op;
-  const int lane = threadIdx.x % kWave;
-  F o;
-  o = dpp<0x111, 0xf>(v);
-  v = op(v, lane % 16 >= 1 ? o : none);
-  o = dpp<0x112, 0xf>(v);
-  v = op(v, lane % 16 >= 2 ? o : none);
-  o = dpp<0x114, 0xf>(v);
-  v = op(v, lane % 16 >= 4 ? o : none);
-  o = dpp<0x118, 0xf>(v);
-  v = op(v, lane % 16 >= 8 ? o : none);
-  o = dpp<0x142, 0xa>(v);
-  v = op(v, lane & 16 ? o : none);
-  o = dpp<0x143, 0xc>(v);
-  v = op(v, lane & 32 ? o : none);
+// lane 31's totals move on to the rows behind them.
+template <class F>
+MOE_DEV F wave_sum(F v) {
+  v += dpp0<0x111, 0xf>(v);
+  v += dpp0<0x112, 0xf>(v);
+  v += dpp0<0x114, 0xf>(v);
+  v += dpp0<0x118, 0xf>(v);
+  v += dpp0<0x142, 0xa>(v);
+  v += dpp0<0x143, 0xc>(v);
   return read_lane(v, 63);
 }
 // A maximum may meet a lane's own value again, so nothing has to be masked. Of unsigned numbers
 // 0 is neutral: the shift then merges into the maximum, one instruction a step.
-template <int CTRL, int ROWS>
-MOE_DEV uint32_t dpp0(uint32_t x) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false);
-}
 MOE_DEV uint32_t wave_max(uint32_t v) {
   v = max(v, dpp0<0x111, 0xf>(v));
   v = max(v, dpp0<0x112, 0xf>(v));
@@ -111,17 +117,14 @@ MOE_DEV F wave_max(F v) {
   v = larger(v, dpp<0x143, 0xc>(v));
   return read_lane(v, 63);
 }
-template <class F>
-MOE_DEV F wave_sum(F v) {
-  return wave_reduce<Add>(v, F(0));
-}
-
 // exp(x) for the scores, x <= 709: e^x = 2^n e^r with n = rint(x / ln 2) and |r| <= ln(2) / 2,
 // e^r by its Taylor polynomial of degree 12 (the next term is below 1.8e-16), about 1e-15 in
-// all. 18 instructions; the library's exp also covers what does not occur here.
+// all. 20 instructions; the library's exp also covers what does not occur here.
 MOE_DEV double exp64(double x) {
   x = __builtin_fmax(x, -745.0);
-  const double n = __builtin_rint(x * 1.4426950408889634);
+  // adding 1.5 2^52 rounds to a whole number, which the sum's low word then holds
+  const double t = __builtin_fma(x, 1.4426950408889634, 6755399441055744.0);
+  const double n = t - 6755399441055744.0;
   double r = __builtin_fma(n, -6.93147180369123816490e-01, x);
   r = __builtin_fma(n, -1.90821492927058770002e-10, r);
   double p = 1.0 / 479001600.0;
@@ -137,7 +140,7 @@ MOE_DEV double exp64(double x) {
   p = __builtin_fma(p, r, 0.5);
   p = __builtin_fma(p, r, 1.0);
   p = __builtin_fma(p, r, 1.0);
-  return __builtin_ldexp(p, (int)n);
+  return __builtin_ldexp(p, (int)__builtin_bit_cast(uint64_t, t));
 }
 // 1 / y for normal y, to about one step: two Newton steps on the hardware's estimate.
 MOE_DEV double rcp64(double y) {
@@ -239,10 +242,15 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
     m = wave_max(m);
     if (!LOGIT || !p.renorm) {  // renormalised weights need no sum over the row
       double z = 0;
+      if (m == INFINITY) {  // for the whole wave: the +inf entries share the row
 #pragma unroll
-      for (int v = 0; v < V; ++v) z += soft_num64(l[v], m);
+        for (int v = 0; v < V; ++v) z += l[v] == INFINITY ? 1.0 : 0.0;
+      } else {  // a closed expert's 5e-324 does not change a sum that holds a 1
+#pragma unroll
+        for (int v = 0; v < V; ++v) z += exp64((double)l[v] - (double)m);
+      }
       z = wave_sum(z);
-      zi = z > 0 ? rcp64(z) : 0.0;
+      zi = m > -INFINITY ? rcp64(z) : 0.0;
     }
   }
   C c[V];
@@ -251,7 +259,9 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
     if constexpr (LOGIT) {
       c[v] = e0 + v < E ? order32(l[v]) : kTaken;
     } else {
-      const double s = p.softmax ? soft_num64(l[v], m) * zi : sigmoid64(l[v]);
+      const double s = !p.softmax      ? sigmoid64(l[v])
+                       : m == INFINITY ? (l[v] == INFINITY ? zi : 0.0)
+                                       : exp64((double)l[v] - (double)m) * zi;
       const double x = s + (bias ? (double)bias[min(e0 + v, E - 1)] : 0.0);
       c[v] = e0 + v >= E ? kTaken : l[v] > -INFINITY && x > kClosed ? x : kClosed;
     }
@@ -338,16 +348,12 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
     occ = o == owner && top == last ? occ + 1 : 0;  // the same value again in the same lane
     owner = o;
     last = top;
-    my_c = lane == j ? top : my_c;
-    my_at = lane == j ? o | occ << 8 : my_at;
-    const bool pop = lane == o;
+    const uint64_t pop = 1ull << o, mine = 1ull << j;
+    my_c = select_lanes(mine, top, my_c);
+    my_at = (int)select_lanes(mine, (uint32_t)(o | occ << 8), (uint32_t)my_at);
 #pragma unroll
-    for (int v = 0; v + 1 < V; ++v) {
-      C n = h[v + 1];
-      asm("" : "+v"(n));  // else the compiler selects among all V by an index, at V times the cost
-      h[v] = pop ? n : h[v];
-    }
-    h[V - 1] = pop ? kTaken : h[V - 1];
+    for (int v = 0; v + 1 < V; ++v) h[v] = select_lanes(pop, h[v + 1], h[v]);
+    h[V - 1] = lane == o ? kTaken : h[V - 1];
   }
   // lane j finds its expert: the occ-th of the owner's values that equal its own
   int my_e = 0;
