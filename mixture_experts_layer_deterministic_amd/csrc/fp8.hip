@@ -11,6 +11,7 @@
 // largest, the groups' sums then in fp32. On quantised Gaussian operands that is 1.3e-5 of the
 // result in rms, 300 times less than the bf16 rounding of the output; bf16 MFMAs of the widened
 // codes would keep 1e-8 at half the rate.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -317,9 +318,12 @@ constexpr int kLgkm0 = 0xc07f;     // lgkmcnt(0) alone
 // need them through the LDS crossbar.
 //  * BM = 128, three weight stages: 80 KB, two workgroups a CU to the last byte of its LDS, with
 //    64 KB of weights on their way.
-//  * BM = 32, two weight stages: 40 KB, four workgroups a CU with as much on their way; of use
-//    where there are few tiles (a serving batch), which then all run at once.
-// A tile's K loop is compiled for 2, 4 and 8 blocks of 16 rows and runs the least that hold its
+//  * BM = 32, two weight stages: 40 KB, four workgroups a CU with as much on their way.
+// Tiles are dealt to the XCDs one by one: the column tiles of one expert run side by side on
+// different XCDs (one XCD's consecutive tiles at a time: 1483 us against 1453 at 256 experts of 64
+// rows). Weights that one row tile reads go past the caches (nt) up to 64 rows, where it pays
+// (32 rows an expert 1274 -> 1207 us; 96 rows 1503 -> 1556).
+// A tile's K loop is compiled for 2, 4, 6 and 8 blocks of 16 rows and runs the least that hold its
 // rows: no MFMA, LDS read or load for the rest. (A test per block inside the loop made the
 // compiler keep both sides' accumulators, 1 KB a lane of them in memory.)
 // A wave's loads complete in order; a step issues rows, scales, then weights, so at its top the
@@ -478,6 +482,136 @@ __global__ void __launch_bounds__(256, BM == 128 ? 2 : 4) fp8_stream_kernel(cons
   } else {
     StreamTile<8, SB> s;
     s.run(a, t, n0, L);
+  }
+}
+
+// Few column tiles: with a handful of experts the 128-column tiles leave most CUs without work,
+// and a step's latency is what takes the time. One wave a workgroup takes 32 columns of 32 rows
+// (eight stages) or 64 (five), about 64 KB on their way, two workgroups a CU, and no barrier: its
+// loads complete in order and only it reads them. Every value is summed in the other kernels'
+// order. Loads past the last block read it again into a stage that is not read.
+template <int NMB, int NS>
+struct NarrowTile {
+  static constexpr int AJ = 2 * NMB, G = AJ + 5;    // row loads, all loads of a step
+  static constexpr int kA = NMB * 2048, kB = 4096, kStage = kA + kB + 256;
+  static constexpr int kAhead = (NS - 1) * G;       // loads that may be missing at a step's top
+  static_assert(kAhead < 64, "a wait counts 63 loads");
+  static constexpr int kWait = 0x0f70 | (kAhead & 15) | (kAhead >> 4 << 14);  // vmcnt alone
+  __amdgpu_buffer_rsrc_t ra, rb;
+  uint32_t ao[AJ], bo[4], so;
+  const float *sa, *sb;
+  size_t M;
+  int nK, lane;
+  FragAt f;
+  f32x4 acc[NMB][2];
+
+  MOE_DEV void issue(uint8_t* st, int kb) {
+    kb = min(kb, nK - 1);
+    const uint32_t step = (uint32_t)kb * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fp8_load_lds<2>(rb, bo[j], step, st + kA + j * 1024);
+#pragma unroll
+    for (int j = 0; j < AJ; ++j) fp8_load_lds(ra, ao[j], step, st + j * 1024);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        fp8_rsrc(sa + kb * M), (__attribute__((address_space(3))) void*)(st + kA + kB), 4, so, 0, 0,
+        0);
+  }
+  MOE_DEV void step(uint8_t* st, int kb) {
+    __builtin_amdgcn_s_waitcnt(kWait);
+    __builtin_amdgcn_sched_barrier(0);
+    const float sbk = ((const __attribute__((address_space(4))) float*)sb)[kb];
+    const float* sc = reinterpret_cast<const float*>(st + kA + kB) + lane % 16;
+    const i32x8 bf0 = fp8_frag(st + kA, f), bf1 = fp8_frag(st + kA + 2048, f);
+    i32x8 af[NMB];
+    float s[NMB];
+#pragma unroll
+    for (int mb = 0; mb < NMB; ++mb) {
+      af[mb] = fp8_frag(st + mb * 2048, f);
+      s[mb] = sc[mb * 16] * sbk;
+    }
+    __builtin_amdgcn_s_waitcnt(kLgkm0);  // read, so that the stage may be filled again
+    __builtin_amdgcn_sched_barrier(0);
+    issue(st, kb + NS);
+#pragma unroll
+    for (int mb = 0; mb < NMB; ++mb) {
+      const f32x4 p0 = fp8_mfma(bf0, af[mb]), p1 = fp8_mfma(bf1, af[mb]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        acc[mb][0][r] = __builtin_fmaf(s[mb], p0[r], acc[mb][0][r]);
+        acc[mb][1][r] = __builtin_fmaf(s[mb], p1[r], acc[mb][1][r]);
+      }
+    }
+  }
+  template <int S, int C>
+  MOE_DEV void steps(uint8_t* const (&st)[NS], int kb, int n) {
+    if constexpr (S < C) {
+      if (S < n) {
+        step(st[S], kb + S);
+        steps<S + 1, C>(st, kb, n);
+      }
+    }
+  }
+  MOE_DEV void run(const Fp8GemmArgs& a, const RowTile& t, int n0,
+                   uint8_t* const (&st)[NS]) {
+    lane = threadIdx.x;
+    f = frag_at(lane);
+    nK = a.K / kQB;
+    M = a.M;
+    ra = fp8_rsrc(a.a + (size_t)t.row0 * a.K);
+    rb = fp8_rsrc(a.b + ((size_t)t.e * a.N + n0) * a.K);
+    sa = a.sa + t.row0;
+    sb = a.sb + ((size_t)t.e * (a.N / kQB) + n0 / kQB) * nK;
+#pragma unroll
+    for (int j = 0; j < AJ; ++j)  // rows past the count read the last one again
+      ao[j] = (uint32_t)min(8 * j + lane / 8, t.rows - 1) * a.K + fp8_piece(lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bo[j] = (uint32_t)(8 * j + lane / 8) * a.K + fp8_piece(lane);
+    so = (uint32_t)min(lane, t.rows - 1) * 4;
+#pragma unroll
+    for (int i = 0; i < NMB; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NS; ++i) issue(st[i], i);
+    int kb = 0;
+    for (; kb + NS <= nK; kb += NS) steps<0, NS>(st, kb, NS);
+    steps<0, NS - 1>(st, kb, nK - kb);
+    __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);  // before the workgroup gives its LDS back
+#pragma unroll
+    for (int mb = 0; mb < NMB; ++mb) {
+      const int m = mb * 16 + lane % 16;
+      if (m >= t.rows) continue;
+      store_dw8_bf16<false>(a.out + (size_t)(t.row0 + m) * a.N + n0, acc[mb][0], acc[mb][1], lane);
+    }
+  }
+};
+
+template <int NMB>
+__global__ void __launch_bounds__(64, 1) fp8_narrow_kernel(const Fp8GemmArgs a) {
+  constexpr int kStage = NarrowTile<NMB, 5>::kStage, kMore = NMB == 2 ? kStage : 16;
+  __shared__ __align__(1024) uint8_t s0[kStage];
+  __shared__ __align__(1024) uint8_t s1[kStage];
+  __shared__ __align__(1024) uint8_t s2[kStage];
+  __shared__ __align__(1024) uint8_t s3[kStage];
+  __shared__ __align__(1024) uint8_t s4[kStage];
+  __shared__ __align__(1024) uint8_t s5[kMore];
+  __shared__ __align__(1024) uint8_t s6[kMore];
+  __shared__ __align__(1024) uint8_t s7[kMore];
+  const int nN = a.N / 32;
+  const RowTile t = find_rows<16 * NMB>(a.offsets, a.M, a.E, blockIdx.x / nN);
+  if (t.rows <= 0) return;
+  const int n0 = blockIdx.x % nN * 32;
+  if constexpr (NMB == 2) {
+    uint8_t* const st[8] = {s0, s1, s2, s3, s4, s5, s6, s7};
+    NarrowTile<2, 8> w;
+    w.run(a, t, n0, st);
+  } else {
+    uint8_t* const st[5] = {s0, s1, s2, s3, s4};
+    if (t.rows <= 32) {
+      NarrowTile<2, 5> w;
+      w.run(a, t, n0, st);
+    } else {
+      NarrowTile<4, 5> w;
+      w.run(a, t, n0, st);
+    }
   }
 }
 
@@ -820,21 +954,33 @@ hipError_t launch_fp8_quant_weights(const uint16_t* src, int E, int N, int K, ui
   return hipGetLastError();
 }
 
+// Which kernel, by the rows an expert has on average and the 128-column tiles there may be (M, E
+// and N are all the host knows of the load; every kernel is right for every load). Measured in us,
+// rows spread evenly, N x K = 4096 x 7168 where not said:
+//  * up to 128 tiles, rows few: narrow. E = 1, 32 rows 17 (128-row tiles 34); E = 4, 16 rows an
+//    expert 20 (36). At 256 tiles level: E = 8, 16 rows 39 (42), 64 rows 66 (62).
+//  * 513 to 1024 tiles, up to 16 rows an expert: 32-row tiles, which then all run at once. 7168 x
+//    2048, 11 of 16 experts with 24 rows 30.7 (128-row tiles 33.5). Fewer tiles: E = 8, 16 rows 53
+//    (42); more: E = 256, 16 rows 1163 (1155).
+//  * up to 112 rows an expert: 128-row tiles. E = 64, 96 rows 369 (256 x 256 tiles 463). Above, an
+//    expert's rows begin to need a second tile and its weights a second read: 160 rows 710 (482).
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s) {
   auto grid = [&](int bm, int bn) {
     const unsigned n = (unsigned)(a.M / bm + a.E) * (unsigned)((a.N + bn - 1) / bn);
     return dim3((n + kXcds - 1) / kXcds * kXcds);
   };
-  {
-    TraceScope trace("fp8_gemm", s);
-    if (a.M <= 16LL * a.E)
-      hipLaunchKernelGGL(fp8_stream_kernel<32>, grid(32, kQB), dim3(256), 0, s, a);
-    else if (a.M < 192LL * a.E)
-      hipLaunchKernelGGL(fp8_stream_kernel<128>, grid(128, kQB), dim3(256), 0, s, a);
-    else
-      // room for every tile, and for a last round's parts
-      hipLaunchKernelGGL(fp8_big_kernel, dim3(grid(kBigT, kBigT).x + kCus), dim3(512), 0, s, a);
-  }
+  const long long M = a.M, E = a.E, tiles = E * (a.N / kQB);
+  TraceScope trace("fp8_gemm", s);
+  if (tiles <= kCus / 2 && M <= 32)
+    hipLaunchKernelGGL(fp8_narrow_kernel<2>, grid(32, 32), dim3(64), 0, s, a);
+  else if (tiles <= kCus / 2 && M <= 64 * E)
+    hipLaunchKernelGGL(fp8_narrow_kernel<4>, grid(64, 32), dim3(64), 0, s, a);
+  else if (tiles > 2 * kCus && tiles <= 4 * kCus && M <= 16 * E)
+    hipLaunchKernelGGL(fp8_stream_kernel<32>, grid(32, kQB), dim3(256), 0, s, a);
+  else if (M <= 112 * E)
+    hipLaunchKernelGGL(fp8_stream_kernel<128>, grid(128, kQB), dim3(256), 0, s, a);
+  else  // room for every tile, and for a last round's parts
+    hipLaunchKernelGGL(fp8_big_kernel, dim3(grid(kBigT, kBigT).x + kCus), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 

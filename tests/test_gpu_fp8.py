@@ -182,6 +182,26 @@ def test_product_in_every_cut_of_the_last_round(counts):
     assert worst <= 1, worst
 
 
+@pytest.mark.parametrize("counts,N,K", [
+    ([3, 0, 33, 1, 0, 20] + [0] * 10, 5120, 256),    # 32-row tiles, one expert over a tile
+    ([5, 8], 1024, 1280), ([31], 4096, 128),         # narrow, 32 rows
+    ([40, 3, 70, 0], 512, 640), ([64], 256, 1152),   # narrow, 64 rows, one expert over a tile
+    ([100] * 6, 512, 256), ([130, 90, 0, 128], 256, 384)])
+def test_product_on_each_side_of_the_choice_of_kernel(counts, N, K):
+    _announce(f"[fp8] product {counts} N={N} K={K}")
+    E, M = len(counts), sum(counts) + 2
+    g = torch.Generator().manual_seed(N + K)
+    off = 1 + np.concatenate([[0], np.cumsum(counts)])
+    a, b = _codes((M, K), g), _codes((E, N, K), g)
+    sa, sb = torch.rand(K // 128, M, generator=g), torch.rand(E, N // 128, K // 128, generator=g)
+    ref = _ops.fp8_gemm(off, _values(a), sa.numpy(), _values(b), sb.numpy())
+    e1 = _bound(off, a, sa, b, sb)
+    got = _run(off, a, sa, b, sb, torch.full((M, N), -7.0, dtype=torch.bfloat16, device=DEV))
+    assert np.all(got[[0, -1]] == -7.0)
+    worst = float(np.max((np.abs(got - ref) / (2.0 ** -8 * (np.abs(ref) + e1) + e1))[1:-1]))
+    assert worst <= 1, worst
+
+
 def test_a_row_does_not_depend_on_its_batch():
     """One expert's rows alone and among others, first, last and in the middle of a tile."""
     off, a, sa, b, sb = _problem("big", 256, 512, 3)
