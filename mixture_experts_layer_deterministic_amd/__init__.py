@@ -244,11 +244,14 @@ def _dev(what, stream, *args):
     """Device pointers of the tensors in ``args``, (tensor, dtype or dtypes, elements) each, and
     the stream. The library sees only addresses, so what it cannot check is refused here:
     another type, fewer elements, strides, host memory, another device than the current one."""
+    cur = torch.cuda.current_device()
     if stream is None:
-        cur = torch.cuda.current_device()
         st = torch._C._cuda_getCurrentRawStream(cur)  # without making a Stream object: 1 us less
     else:
-        cur, st = stream.device_index, stream.cuda_stream
+        st = stream.cuda_stream
+        if stream.device_index != cur:
+            raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: a stream of device {stream.device_index} "
+                           f"while device {cur} is current")
     out = []
     for t, dtype, n in args:
         if t is None:

@@ -2,7 +2,8 @@
 // (activations: 1 x 128; weights: 128 x 128), the quantisers and the expert-grouped product.
 //
 // A block's scale is amax / 448 (1 for a block of zeros) and its codes are the values times
-// 448 / amax, rounded to nearest even: the largest magnitude lands on E4M3's largest, 448.
+// 448 / amax, rounded to nearest even: the largest magnitude lands on E4M3's largest, 448. An
+// amax below 2^-110 counts as 2^-110, so that neither quotient leaves fp32's normal numbers.
 // The product takes each 128-deep block from one MFMA in fp32, then adds it, times the two scales,
 // to the fp32 sum: out[p, n] = sum_kb sa[p, kb] sb[n / 128, kb] sum_k a[p, k] b[n, k].
 //
@@ -27,6 +28,7 @@ struct BlockScale {
   float scale, inv;
 };
 MOE_DEV BlockScale block_scale(float amax) {
+  if (amax > 0.f) amax = fmaxf(amax, 0x1p-110f);
   return amax > 0.f ? BlockScale{amax / 448.f, 448.f / amax} : BlockScale{1.f, 1.f};
 }
 MOE_DEV void widen8(const uint4& x, float (&f)[8]) {

@@ -104,13 +104,14 @@ def e4m3(v):
 
 def quantize(x, block_rows):
     """(values the codes stand for before the scale, scales) in the operators' own arithmetic:
-    fp32 scale amax / 448 and fp32 factor 448 / amax, the product rounded to fp32, then to E4M3."""
+    fp32 scale amax / 448 and fp32 factor 448 / amax (amax at least 2^-110 unless 0), the product
+    rounded to fp32, then to E4M3."""
     x = np.asarray(x, np.float32)
     *b, R, K = x.shape
     v = x.reshape(*b, R // block_rows, block_rows, K // 128, 128)
     amax = np.abs(v).max(axis=(-3, -1), keepdims=True)
     one = np.float32(1)
-    safe = np.where(amax > 0, amax, one)
+    safe = np.where(amax > 0, np.maximum(amax, np.float32(2.0 ** -110)), one)
     inv = np.where(amax > 0, np.float32(448) / safe, one)
     scale = np.where(amax > 0, safe / np.float32(448), one)
     return e4m3(v * inv).reshape(x.shape), scale.reshape(*b, R // block_rows, K // 128)

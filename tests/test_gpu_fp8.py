@@ -60,6 +60,43 @@ def test_rows_are_quantised_bit_exactly(R, C):
     np.testing.assert_array_equal(_values(q), rq)
 
 
+def test_blocks_of_tiny_magnitudes():
+    """Down to bf16's smallest: the factor 448 / amax would leave fp32."""
+    x = torch.randn(9, 512, generator=torch.Generator().manual_seed(0)) * 2.0 ** (
+        -90 - 8 * torch.arange(9.0))[:, None]
+    x[8, 100] = 2.0 ** -133  # the smallest subnormal
+    x[8, 101:128] = 0.0
+    x = x.to(torch.bfloat16)
+    q, s = _quant_rows(x.to(DEV))
+    rq, rs = _ops.quantize(x.float().numpy(), 1)
+    np.testing.assert_array_equal(s.cpu().numpy(), rs.T)
+    np.testing.assert_array_equal(_values(q), rq)
+    assert np.isfinite(_values(q)).all()
+
+
+def test_more_than_two_to_the_31_codes():
+    """Rows whose byte offsets pass 32 bits, against the same rows in a call of their own."""
+    R, C, N = 310_000, 7168, 128
+    assert R * C > 2 ** 31
+    _announce(f"[fp8] {R} x {C} rows quantised and multiplied")
+    g = torch.Generator(DEV).manual_seed(0)
+    x = torch.randn(R, C, device=DEV, generator=g, dtype=torch.bfloat16)
+    q, s = _quant_rows(x)
+    last = slice(R - 40, R)
+    q1, s1 = _quant_rows(x[last].clone())
+    assert torch.equal(q[last].view(torch.uint8), q1.view(torch.uint8))
+    assert torch.equal(s[:, last], s1)
+    del x
+    b = torch.randint(0, 127, (1, N, C), device=DEV, generator=g, dtype=torch.uint8)
+    sb = torch.rand(1, 1, C // 128, device=DEV, generator=g)
+    out = torch.empty(R, N, dtype=torch.bfloat16, device=DEV)
+    off = lambda n: torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    m.moe_fp8_gemm(off(R), R, 1, N, C, q, s, b, sb, out)
+    out1 = torch.empty(40, N, dtype=torch.bfloat16, device=DEV)
+    m.moe_fp8_gemm(off(40), 40, 1, N, C, q1, s1, b, sb, out1)
+    assert torch.equal(out[last], out1)
+
+
 @pytest.mark.parametrize("E,N,K", [(1, 128, 128), (2, 128, 384), (3, 256, 128), (2, 640, 512)])
 @pytest.mark.parametrize("both", [False, True])
 def test_weights_are_quantised_bit_exactly(E, N, K, both):

@@ -76,7 +76,7 @@ def test_choice_and_weights_without_groups(T, E, k, score):
 
 GROUPS = [(256, 8, 4, 8), (256, 8, 1, 8), (256, 8, 8, 8), (64, 64, 9, 8), (96, 3, 2, 6),
           (1024, 2, 1, 10), (1024, 512, 100, 12), (130, 65, 33, 20), (1022, 511, 3, 6),
-          (6, 2, 1, 3), (40, 4, 3, 1), (768, 12, 5, 33)]
+          (6, 2, 1, 3), (40, 4, 3, 1), (768, 12, 5, 33), (1024, 1024, 50, 40)]
 
 
 @pytest.mark.parametrize("score", [0, 1])
@@ -237,6 +237,34 @@ def test_router_gradients(T, d, E):
         m.moe_router_backward(cfg, X, W, D, dx1, None, acc, acc)
         m.moe_router_backward(cfg, X, W, D, None, dw1, acc, acc)
         assert torch.equal(dx1, dx) and torch.equal(dw1, dw)
+
+
+def test_more_than_two_to_the_32_bytes_of_logits():
+    """Tokens whose byte offsets pass 32 bits, against the same tokens in a call of their own."""
+    T, E, k, n = 1_200_000, 1000, 6, 50
+    assert 4 * T * E > 2 ** 32
+    _announce(f"[gate] T={T} E={E}: the last {n} tokens")
+    g = torch.Generator(DEV).manual_seed(0)
+    l = torch.randn(T, E, device=DEV, generator=g)
+    gate = m.make_gate(m.MOE_SCORE_SOFTMAX, 1, 1, 0, False, 1.0)
+
+    def run(l):
+        T = l.shape[0]
+        cfg = m.make_cfg(T, 256, E, k, 128)
+        idx = torch.empty(T, k, dtype=torch.int32, device=DEV)
+        w = torch.empty(T, k, device=DEV)
+        m.moe_gate_select(cfg, gate, l, None, idx, w)
+        dl = torch.empty(T, E, device=DEV)
+        m.moe_gate_backward(cfg, gate, l, idx, w, dl, False)
+        x = torch.ones(T, 256, dtype=torch.bfloat16, device=DEV)
+        wr = torch.ones(E, 256, dtype=torch.bfloat16, device=DEV)
+        wr[::3] = 0.5
+        dx = torch.empty(T, 256, dtype=torch.bfloat16, device=DEV)
+        m.moe_router_backward(m.make_cfg(T, 256, E, 1, 128), x, wr, dl, dx, None, False, False)
+        return [t[-n:].clone() for t in (idx, w, dl, dx)]
+
+    for a, b in zip(run(l), run(l[-n:].clone())):
+        assert torch.equal(a, b)
 
 
 def test_gate_and_router_calls_refuse_tensors_the_library_cannot_check():
