@@ -411,7 +411,8 @@ int moe_gate_backward(const moe_cfg* cfg, const moe_gate* gate, const float* log
  *   dx[t]  = bf16( sum_e dlogits[t,e] w_router[e] )     (with acc_dx: that sum + dx[t], one
  *                                                        rounding of the fp32 total)
  *   dwr[e] = sum_t dlogits[t,e] x[t]                    (with acc_dwr: added to dwr[e])
- * Sums in fp32 (dlogits enters with 24 bits) in a fixed order. dlogits must be finite.
+ * Sums in fp32 (dlogits enters with 24 bits) in a fixed order. A dlogits value that is not finite
+ * makes its token's dx and its expert's dwr NaN, and touches no other.
  *
  *   x        bf16 [T, d]    in
  *   w_router bf16 [E, d]    in

@@ -87,8 +87,9 @@ struct RouterTile {
 
   // dl rows: DW, tokens k0 + i (reduction), experts r0 ..; else tokens r0 + i, experts k0 ..
   // Buffer loads that end with their tensor, so rows past its end read as zeros without a branch.
-  // A dl row's columns past E belong to the next row: for dx the weight rows they meet are
-  // zeros, for dWr they lead to rows that are not stored.
+  // A dl row's columns past E belong to the next row: for dx they are cleared on their way to
+  // LDS (the weight rows they meet are zeros, but NaN times zero is not), for dWr they lead to
+  // rows that are not stored.
   MOE_DEV void load(const RouterGradArgs& a, int r0, int c0, int k0) {
     const int i = tid / 16, c = tid % 16, K = DW ? a.T : a.E;
     const size_t t0 = DW ? k0 : r0, e0 = DW ? r0 : k0;
@@ -107,7 +108,14 @@ struct RouterTile {
       bv[j] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
                                             rb, ((i + kRows * j) * a.d + c * 8) * 2, 0, 0));
   }
-  MOE_DEV void store(uint16_t* lds) const {
+  MOE_DEV void store(uint16_t* lds, int left) {  // left: what remains of the reduction
+    if (!DW && left < kRgK) {
+#pragma unroll
+      for (int j = 0; j < AJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (tid % 16 * 4 + q >= left) av[j][q] = 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < AJ; ++j) {
       const int i = tid / 16 + kRows * j, c = tid % 16 * 4;
@@ -140,7 +148,7 @@ struct RouterTile {
     load(a, r0, c0, first);
     for (int k0 = 0; k0 < K; k0 += kStride) {
       __syncthreads();
-      store(lds);
+      store(lds, K - k0);
       __syncthreads();
       if (k0 + kStride < K) load(a, r0, c0, k0 + kStride + first);
 #pragma unroll

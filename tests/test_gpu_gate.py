@@ -239,6 +239,33 @@ def test_router_gradients(T, d, E):
         assert torch.equal(dx1, dx) and torch.equal(dw1, dw)
 
 
+@pytest.mark.parametrize("T,d,E", [(6, 256, 1), (130, 256, 5), (200, 512, 129), (300, 256, 509)])
+def test_a_value_that_is_not_finite_spoils_its_own_rows_only(T, d, E):
+    """The last step of dx's reduction reads past a row's E logits, into the next token's."""
+    _announce(f"[router bwd, NaN] T={T} d={d} E={E}")
+    g = torch.Generator().manual_seed(T + E)
+    x = torch.randn(T, d, generator=g).to(torch.bfloat16).to(DEV)
+    wr = torch.randn(E, d, generator=g).to(torch.bfloat16).to(DEV)
+    dl = torch.randn(T, E, generator=g).to(DEV)
+    cfg = m.make_cfg(T, d, E, 1, 128)
+
+    def run(dl):
+        dx = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
+        dw = torch.zeros(E, d, device=DEV)
+        m.moe_router_backward(cfg, x, wr, dl, dx, dw, False, False)
+        return dx, dw
+
+    rx, rw = run(dl)
+    t, e = T // 2, 0  # the columns that the token before it reads as well
+    for bad in (math.nan, inf, -inf):
+        spoiled = dl.clone()
+        spoiled[t, e] = bad
+        dx, dw = run(spoiled)
+        assert dx[t].isnan().all() and dw[e].isnan().all()
+        rows, experts = torch.arange(T, device=DEV) != t, torch.arange(E, device=DEV) != e
+        assert torch.equal(dx[rows], rx[rows]) and torch.equal(dw[experts], rw[experts])
+
+
 def test_more_than_two_to_the_32_bytes_of_logits():
     """Tokens whose byte offsets pass 32 bits, against the same tokens in a call of their own."""
     T, E, k, n = 1_200_000, 1000, 6, 50
