@@ -389,11 +389,12 @@ int moe_route_gated(const moe_cfg* cfg, const moe_gate* gate, const void* x, con
  *
  * With g_j = scale * d_topk_w[t,j]:
  *   sigmoid            dl_j = g_j s_j (1 - s_j)
- *   sigmoid, renorm    dl_j = (g_j - sum_i g_i q_i) / S * s_j (1 - s_j),  S = sum_i s_i, q = s / S
+ *   sigmoid, renorm    dl_j = (g_j - sum_i g_i q_i) q_j (1 - s_j),  q_j = s_j / sum_i s_i
  *   softmax, renorm    dl_j = q_j (g_j - sum_i g_i q_i)
  *   softmax            dl_e = s_e ([e chosen] g_e - sum_i s_i g_i), for every expert e
- * and 0 for the experts not chosen in the first three. fp32 throughout; sums in a fixed order. A
- * topk_idx entry outside [0, E) counts nothing; one expert named twice gets both slots' sum.
+ * and 0 for the experts not chosen in the first three. fp32, but for the sigmoids and their sum (64
+ * bits, as in the choice); sums in a fixed order. A topk_idx entry outside [0, E) counts nothing;
+ * one expert named twice gets both slots' sum.
  *
  *   logits   fp32 [T, E]    in   (as given to the forward)
  *   topk_idx int32 [T, k]   in

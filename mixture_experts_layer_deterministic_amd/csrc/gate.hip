@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
 // One wave per token. Lane j < k takes slot j:
 //   g_j = scale dw_j
 //   sigmoid:                 dl_j = g_j s_j (1 - s_j)
-//   sigmoid, renormalised:   dl_j = (g_j - sum_i g_i q_i) / S  s_j (1 - s_j),  q = s / S
+//   sigmoid, renormalised:   dl_j = (g_j - sum_i g_i q_i) q_j (1 - s_j),  q = s / S
 //   softmax, renormalised:   dl_j = q_j (g_j - sum_i q_i g_i)
 //   softmax:                 dl_e = p_e ([e selected] g_e - sum_i p_i g_i), for every e
 // The slots' values are scattered over a row of zeros in LDS and the row leaves in 16-byte
@@ -460,14 +460,16 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_backward_kernel(
     const float q = S > 0 ? n / S : 0.f;
     val = q * (g - wave_sum(q * g));
   } else {
-    const float s = lj == -INFINITY ? 0.f : 1.f / (1.f + expf(-lj));
-    const float s1 = lj == -INFINITY ? 0.f : 1.f / (1.f + expf(lj));  // 1 - s without its loss
-    float ds = g;
+    // in 64 bits, as the forward's: scores that fp32 cannot hold still have their shares
+    const double s = sigmoid64(lj);
+    const float s1 = 1.f / (1.f + expf(lj));  // 1 - s without its loss
     if (p.renorm) {
-      const float S = wave_sum(s);
-      ds = S > 0 ? (g - wave_sum(g * (s / S))) / S : 0.f;
+      const double S = wave_sum(s);
+      const float q = S > 0 ? (float)(s / S) : 0.f;
+      val = q * (g - wave_sum(g * q)) * s1;
+    } else {
+      val = g * (float)s * s1;
     }
-    val = ds * s * s1;
   }
   float* mine = rows[wave];
   int* marks = reinterpret_cast<int*>(mine);

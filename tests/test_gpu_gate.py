@@ -200,6 +200,24 @@ def test_gate_gradient(T, E, k, score, renorm):
         assert torch.equal(acc, base + dl)
 
 
+@pytest.mark.parametrize("shift", [-80.0, -95.0, -300.0, -600.0])
+def test_gradient_of_scores_below_fp32(shift):
+    """Every logit of a row far down: the sigmoids leave fp32, their shares of the sum do not."""
+    T, E, k = 40, 24, 6
+    _announce(f"[gate bwd] logits about {shift}")
+    l = (_logits(T, E, 11) + np.float32(shift)).astype(np.float32)
+    gate = m.make_gate(m.MOE_SCORE_SIGMOID, 1, 1, 0, True, 2.5)
+    idx, w = _select(l, k, gate)
+    assert np.all(np.abs(w.sum(1) - 2.5) < 1e-5)
+    dw = np.random.default_rng(12).normal(size=(T, k)).astype(np.float32)
+    dl = torch.full((T, E), -7.0, device=DEV)
+    m.moe_gate_backward(m.make_cfg(T, 256, E, k, 128), gate,
+                        *[torch.tensor(v, device=DEV) for v in (l, idx, dw)], dl, False)
+    ref = _ops.gate_backward(l, idx, dw, 1, True, 2.5)
+    tol = _grad_bound(l, idx, dw, 1, True, 2.5) * U + 1e-37
+    assert np.all(np.abs(dl.cpu().numpy() - ref) <= tol)
+
+
 ROUTER = [(1, 256, 1), (1, 256, 256), (5, 512, 3), (64, 256, 8), (127, 256, 129), (128, 512, 128),
           (200, 768, 509), (1000, 256, 64), (333, 1024, 1024)]
 
