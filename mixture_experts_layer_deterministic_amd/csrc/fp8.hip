@@ -192,8 +192,9 @@ __global__ void __launch_bounds__(256) fp8_quant_weights_kernel(
   __shared__ __align__(16) uint8_t tile[kQB * P];
   __shared__ float red[4];
   const int t = threadIdx.x, cv = t % 16;
-  const int kb = blockIdx.x, nb = blockIdx.y;
-  const size_t e = blockIdx.z;
+  const int nN = N / kQB, nK = K / kQB;
+  const int kb = blockIdx.x % nK, nb = blockIdx.x / nK;  // N / 128 may pass a grid's 65535 in y
+  const size_t e = blockIdx.y;
   const uint16_t* s = src + (e * N + (size_t)nb * kQB) * K + (size_t)kb * kQB;
   uint4 x[8];
 #pragma unroll
@@ -211,7 +212,6 @@ __global__ void __launch_bounds__(256) fp8_quant_weights_kernel(
   if (t % 64 == 0) red[t / 64] = amax;
   __syncthreads();
   const BlockScale b = block_scale(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-  const int nN = N / kQB, nK = K / kQB;
   if (t == 0) {
     scales[(e * nN + nb) * nK + kb] = b.scale;
     if (scales_t) scales_t[(e * nK + kb) * nN + nb] = b.scale;
@@ -950,7 +950,7 @@ hipError_t launch_fp8_quant_weights(const uint16_t* src, int E, int N, int K, ui
                                     hipStream_t s) {
   {
     TraceScope trace("fp8_quant_weights", s);
-    hipLaunchKernelGGL(fp8_quant_weights_kernel, dim3(K / kQB, N / kQB, E), dim3(256), 0, s, src,
+    hipLaunchKernelGGL(fp8_quant_weights_kernel, dim3((unsigned)(K / kQB) * (N / kQB), E), dim3(256), 0, s, src,
                        N, K, codes, scales, codes_t, scales_t);
   }
   return hipGetLastError();

@@ -116,6 +116,32 @@ def test_weights_are_quantised_bit_exactly(E, N, K, both):
         np.testing.assert_array_equal(_values(qt), rq.swapaxes(1, 2))
 
 
+def test_more_blocks_of_weights_than_65535_along_an_axis():
+    """The same 257 blocks of rows 256 times over: every copy's codes and products are the same."""
+    n, times, K = 257 * 128, 256, 128
+    N = n * times
+    _announce(f"[fp8] weights 1 x {N} x {K}")
+    g = torch.Generator(DEV).manual_seed(4)
+    w = torch.randn(n, K, device=DEV, generator=g).to(torch.bfloat16)
+
+    def run(w):
+        N = w.shape[0]
+        q, qt = (torch.empty(1, *sh, dtype=torch.uint8, device=DEV) for sh in ((N, K), (K, N)))
+        s, st = (torch.empty(1, *sh, device=DEV) for sh in ((N // 128, 1), (1, N // 128)))
+        m.moe_fp8_quantize_weights(w, 1, N, K, q, s, qt, st)
+        out = torch.empty(2, N, dtype=torch.bfloat16, device=DEV)
+        m.moe_fp8_gemm(torch.tensor([0, 2], dtype=torch.int32, device=DEV), 2, 1, N, K, q[0, :2],
+                       torch.ones(1, 2, device=DEV), q, s, out)
+        return q, s, qt, st, out
+
+    q1, s1, qt1, st1, out1 = run(w)
+    q, s, qt, st, out = run(w.repeat(times, 1))
+    assert (q.view(times, n, K) == q1).all() and (s.view(times, -1) == s1.view(1, -1)).all()
+    assert (qt.view(K, times, n) == qt1.view(K, 1, n)).all()
+    assert (st.view(times, -1) == st1.view(1, -1)).all()
+    assert (out.view(2, times, n) == out1.view(2, 1, n)).all()
+
+
 def _codes(shape, g):
     """Random finite E4M3 codes: every one of the 254 but the two NaNs."""
     c = torch.randint(0, 254, shape, generator=g)
