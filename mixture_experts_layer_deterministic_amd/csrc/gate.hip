@@ -52,23 +52,9 @@ MOE_DEV double read_lane(double x, int l) {
   return __builtin_bit_cast(double, (uint64_t)read_lane((uint32_t)u, l) |
                                         ((uint64_t)read_lane((uint32_t)(u >> 32), l) << 32));
 }
-// a in the lanes of the mask, b in the others. In assembly, since a chain of selects between
-// neighbours of an array is otherwise turned into selects by an index, among all of them.
-MOE_DEV uint32_t select_lanes(uint64_t mask, uint32_t a, uint32_t b) {
-  asm("v_cndmask_b32_e64 %0, %1, %2, %3" : "=v"(b) : "0"(b), "v"(a), "s"(mask));
-  return b;
-}
-MOE_DEV double select_lanes(uint64_t mask, double a, double b) {
-  const uint64_t x = __builtin_bit_cast(uint64_t, a), y = __builtin_bit_cast(uint64_t, b);
-  return __builtin_bit_cast(
-      double, (uint64_t)select_lanes(mask, (uint32_t)x, (uint32_t)y) |
-                  ((uint64_t)select_lanes(mask, (uint32_t)(x >> 32), (uint32_t)(y >> 32)) << 32));
-}
 MOE_DEV uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
 MOE_DEV float larger(float a, float b) { return fmaxf(a, b); }
 MOE_DEV double larger(double a, double b) { return __builtin_fmax(a, b); }
-MOE_DEV uint32_t smaller(uint32_t a, uint32_t b) { return min(a, b); }
-MOE_DEV double smaller(double a, double b) { return __builtin_fmin(a, b); }
 // x moved likewise; lanes without a source get 0.
 template <int CTRL, int ROWS>
 MOE_DEV uint32_t dpp0(uint32_t x) {
@@ -179,29 +165,81 @@ MOE_DEV float unorder32(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// v[0] >= v[1] >= .., by merging sorted halves (odd-even merges: 1, 5, 19, 63 exchanges).
-template <int V, class C>
-MOE_DEV void sort_down(C (&v)[V]) {
-#pragma unroll
-  for (int p = 1; p < V; p *= 2)
-#pragma unroll
-    for (int q = p; q >= 1; q /= 2)
-#pragma unroll
-      for (int j = q % p; j + q < V; j += 2 * q)
-#pragma unroll
-        for (int i = 0; i < q; ++i)
-          if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-            const C a = v[i + j], b = v[i + j + q];
-            v[i + j] = larger(a, b);
-            v[i + j + q] = smaller(a, b);
-          }
+// The same for 64-bit scores.
+MOE_DEV uint64_t order64(double c) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, c);
+  return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+}
+MOE_DEV uint32_t upper(uint32_t x) { return x; }
+MOE_DEV uint32_t upper(uint64_t x) { return (uint32_t)(x >> 32); }
+MOE_DEV int count(uint64_t lanes) { return __popcll(lanes); }
+// What the wave's lanes wrote to LDS is read behind this by the same wave.
+MOE_DEV void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// One wave per token: lane l holds the V experts from V l on, so that the lowest lane and then
-// its lowest slot that hold a value hold the lowest index. Each lane sorts its V choice scores;
-// k rounds then take the wave's largest head (DPP shifts, no LDS) from the lowest lane that has
-// it. A round costs the same for any V but for the lane's V moves; which of its V experts a lane
-// gave is worked out once, for all k choices together.
+// hit[v]: the lanes whose key[v] is a candidate. All k largest keys of the wave (ties to the lower
+// lane, then slot) are among the candidates, which are 64 at most; their number is returned.
+// Keys whose upper half lies below `least` are none. At least k keys are not such.
+//
+// The k-th largest of the lanes' own maxima bounds the k-th largest key from below, and few keys
+// lie above it. A search by halves over the upper 32 bits finds a bound that k to k + 4 maxima
+// reach: a compare and scalar instructions a step. Where that leaves more than 64 keys (equal
+// ones, or all in few lanes), the k-th key and then its index are found exactly, bit by bit.
+template <int V, class U>
+MOE_DEV int pick_candidates(const U (&key)[V], uint32_t least, int k, int lane,
+                            uint64_t (&hit)[V]) {
+  uint32_t head = upper(key[0]);
+#pragma unroll
+  for (int v = 1; v < V; ++v) head = max(head, upper(key[v]));
+  uint32_t lo = least, hi = ~0u;
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const int n = count(__ballot(head >= mid));
+    if (n >= k) {
+      lo = mid;
+      if (n <= k + 4) break;
+    } else {
+      hi = mid;
+    }
+  }
+  int total = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    hit[v] = __ballot(upper(key[v]) >= lo);
+    total += count(hit[v]);
+  }
+  if (total <= kWave) return total;
+  U kth = 0;  // the largest value that k keys reach
+  for (int b = 8 * sizeof(U) - 1; b >= 0; --b) {
+    const U x = kth | U(1) << b;
+    int n = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) n += count(__ballot(key[v] >= x));
+    if (n >= k) kth = x;
+  }
+  int above = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) above += count(__ballot(key[v] > kth));
+  int end = 0;  // the largest index in front of which too few are equal to it
+  for (int b = 9; b >= 0; --b) {
+    const int x = end | 1 << b;
+    int n = above;
+#pragma unroll
+    for (int v = 0; v < V; ++v) n += count(__ballot(key[v] == kth && lane * V + v < x));
+    if (n < k) end = x;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    hit[v] = __ballot(key[v] > kth || (key[v] == kth && lane * V + v <= end));
+  return k;
+}
+
+// One wave per token: lane l holds the V experts from V l on. pick_candidates leaves at most 64,
+// mostly little more than k; each then counts those in front of it, all against all, which is its
+// place among the choices.
 // LOGIT: the scores order as the logits do; 32-bit keys, and 64-bit scores only of the chosen.
 // Groups that are whole, aligned runs of 2^i lanes are scored by lane exchanges, others in LDS.
 // Measured on 2048 x 256 (8 groups, sigmoid, bias) and 18944 x 512 (softmax): see the launch.
@@ -335,47 +373,58 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
         if (e0 + v < E && gsc[(e0 + v) / gs] == 0.0) c[v] = kTaken;
     }
   }
-  // rounds: the wave's largest head, from the lowest lane that has it
-  C h[V];
+  // the candidates side by side in LDS, one a lane, in the order of their slots
+  using U = std::conditional_t<LOGIT, uint32_t, uint64_t>;
+  U key[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = c[v];
-  sort_down(h);
-  C my_c = kTaken, last = kTaken;
-  int my_at = 0, owner = -1, occ = 0;  // lane j: owner | occ << 8 of choice j
-  for (int j = 0; j < k; ++j) {
-    const C top = wave_max(h[0]);
-    const int o = __builtin_ctzll(__ballot(h[0] == top));
-    occ = o == owner && top == last ? occ + 1 : 0;  // the same value again in the same lane
-    owner = o;
-    last = top;
-    const uint64_t pop = 1ull << o, mine = 1ull << j;
-    my_c = select_lanes(mine, top, my_c);
-    my_at = (int)select_lanes(mine, (uint32_t)(o | occ << 8), (uint32_t)my_at);
-#pragma unroll
-    for (int v = 0; v + 1 < V; ++v) h[v] = select_lanes(pop, h[v + 1], h[v]);
-    h[V - 1] = lane == o ? kTaken : h[V - 1];
+  for (int v = 0; v < V; ++v) {
+    if constexpr (LOGIT) key[v] = c[v];
+    else key[v] = order64(c[v]);
   }
-  // lane j finds its expert: the occ-th of the owner's values that equal its own
-  int my_e = 0;
-  {
-    const int o = my_at & 0xff;
-    const int skip = my_at >> 8;
-    int at = 0;
-    int seen = 0;
+  uint64_t hit[V];
+  const int n = pick_candidates(key, LOGIT ? 1u : upper(order64(kClosed)), k, lane, hit);
+  // LOGIT: the key and the index's complement in one number; equal keys then order by index
+  __shared__ __align__(16) uint64_t list[kGateWaves][kWave];
+  __shared__ int list_e[LOGIT ? 1 : kGateWaves][kWave];
+  list[wave][lane] = 0;
+  if constexpr (!LOGIT) list_e[wave][lane] = E;
+  wave_sync();
+  int before = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const bool hit = __shfl(c[v], o) == my_c;
-      at = hit && seen == skip ? v : at;
-      seen += hit;
+  for (int v = 0; v < V; ++v) {
+    const int at = before + (int)__builtin_amdgcn_mbcnt_hi(
+                                (uint32_t)(hit[v] >> 32),
+                                __builtin_amdgcn_mbcnt_lo((uint32_t)hit[v], 0u));
+    if (hit[v] >> lane & 1) {
+      if constexpr (LOGIT) {
+        list[wave][at] = (uint64_t)key[v] << 32 | (uint32_t)~(e0 + v);
+      } else {
+        list[wave][at] = key[v];
+        list_e[wave][at] = e0 + v;
+      }
     }
-    my_e = o * V + at;
+    before += count(hit[v]);
   }
+  wave_sync();
+  // a candidate's place is the number of those in front of it
+  const uint64_t mine = list[wave][lane];
+  const int my_e = LOGIT ? (int)~(uint32_t)mine : list_e[LOGIT ? 0 : wave][lane];
+  int place = 0;
+  for (int j = 0; j < n; j += 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t o = list[wave][j + i];
+      if constexpr (LOGIT) place += o > mine;
+      else place += o > mine || (o == mine && list_e[wave][j + i] < my_e);
+    }
+  }
+  const bool chosen = lane < n && place < k;
   float my_l;
-  if constexpr (LOGIT) my_l = unorder32(my_c);
-  else my_l = lane < k ? row[my_e] : -INFINITY;
-  my_l = my_l == my_l ? my_l : -INFINITY;
-  double s = 0;  // lane j: the score of choice j
-  if (lane < k) {
+  if constexpr (LOGIT) my_l = unorder32(upper(mine));
+  else my_l = chosen ? row[my_e] : -INFINITY;
+  my_l = chosen && my_l == my_l ? my_l : -INFINITY;
+  double s = 0;  // the score, 0 where nothing was chosen
+  if (chosen) {
     s = !p.softmax ? sigmoid64(my_l) : soft_num64(my_l, m);
     if (p.softmax && zi > 0) s *= zi;
   }
@@ -385,9 +434,9 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
   } else if (p.softmax && !(zi > 0)) {
     s = 0;
   }
-  if (live && lane < k) {
-    idx[(size_t)t * k + lane] = my_e;
-    w[(size_t)t * k + lane] = (float)(s * (double)p.scale);
+  if (live && chosen) {
+    idx[(size_t)t * k + place] = my_e;
+    w[(size_t)t * k + place] = (float)(s * (double)p.scale);
   }
 }
 
