@@ -104,8 +104,10 @@ MOE_DEV F wave_max(F v) {
   return read_lane(v, 63);
 }
 // exp(x) for the scores, x <= 709: e^x = 2^n e^r with n = rint(x / ln 2) and |r| <= ln(2) / 2,
-// e^r by its Taylor polynomial of degree 12 (the next term is below 1.8e-16), about 1e-15 in
-// all. 20 instructions; the library's exp also covers what does not occur here.
+// e^r by its Taylor polynomial. Degree 12 (the next term is below 1.8e-16) gives about 1e-15 in
+// all, with 20 instructions; the library's exp also covers what does not occur here. Degree 10
+// (2.2e-13) is for a sum that only divides what is then rounded to fp32.
+template <int DEGREE = 12>
 MOE_DEV double exp64(double x) {
   x = __builtin_fmax(x, -745.0);
   // adding 1.5 2^52 rounds to a whole number, which the sum's low word then holds
@@ -113,9 +115,11 @@ MOE_DEV double exp64(double x) {
   const double n = t - 6755399441055744.0;
   double r = __builtin_fma(n, -6.93147180369123816490e-01, x);
   r = __builtin_fma(n, -1.90821492927058770002e-10, r);
-  double p = 1.0 / 479001600.0;
-  p = __builtin_fma(p, r, 1.0 / 39916800.0);
-  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  double p = DEGREE == 12 ? 1.0 / 479001600.0 : 1.0 / 3628800.0;
+  if constexpr (DEGREE == 12) {
+    p = __builtin_fma(p, r, 1.0 / 39916800.0);
+    p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  }
   p = __builtin_fma(p, r, 1.0 / 362880.0);
   p = __builtin_fma(p, r, 1.0 / 40320.0);
   p = __builtin_fma(p, r, 1.0 / 5040.0);
@@ -185,24 +189,33 @@ MOE_DEV void wave_sync() {
 // Keys whose upper half lies below `least` are none. At least k keys are not such.
 //
 // The k-th largest of the lanes' own maxima bounds the k-th largest key from below, and few keys
-// lie above it. A search by halves over the upper 32 bits finds a bound that k to k + 4 maxima
-// reach: a compare and scalar instructions a step. Where that leaves more than 64 keys (equal
-// ones, or all in few lanes), the k-th key and then its index are found exactly, bit by bit.
+// lie above it. From the largest maximum down by steps that grow, then by halves, over the upper
+// 32 bits, a search finds a bound that k to k + 4 maxima reach: a compare and scalar instructions
+// a step. Where that leaves more than 64 keys (equal ones, or all in few lanes), the k-th key and
+// then its index are found exactly, bit by bit.
 template <int V, class U>
 MOE_DEV int pick_candidates(const U (&key)[V], uint32_t least, int k, int lane,
                             uint64_t (&hit)[V]) {
   uint32_t head = upper(key[0]);
 #pragma unroll
   for (int v = 1; v < V; ++v) head = max(head, upper(key[v]));
-  uint32_t lo = least, hi = ~0u;
-  while (hi - lo > 1) {
+  uint32_t hi = wave_max(head) + 1, lo, step = sizeof(U) == 4 ? 1u << 20 : 1u << 17;
+  int more;     // maxima that reach lo, less k
+  while (true) {  // an eighth of a binade, a half, two, eight, 32, ..
+    lo = hi - least > step ? hi - step : least;
+    more = count(__ballot(head >= lo)) - k;
+    if (more >= 0 || lo == least) break;
+    hi = lo;
+    step = step < 1u << 29 ? step * 4 : step;
+  }
+  while (more > 4 && hi - lo > 1) {
     const uint32_t mid = lo + (hi - lo) / 2;
-    const int n = count(__ballot(head >= mid));
-    if (n >= k) {
-      lo = mid;
-      if (n <= k + 4) break;
-    } else {
+    const int n = count(__ballot(head >= mid)) - k;
+    if (n < 0) {
       hi = mid;
+    } else {
+      lo = mid;
+      more = n;
     }
   }
   int total = 0;
@@ -242,7 +255,11 @@ MOE_DEV int pick_candidates(const U (&key)[V], uint32_t least, int k, int lane,
 // place among the choices.
 // LOGIT: the scores order as the logits do; 32-bit keys, and 64-bit scores only of the chosen.
 // Groups that are whole, aligned runs of 2^i lanes are scored by lane exchanges, others in LDS.
-// Measured on 2048 x 256 (8 groups, sigmoid, bias) and 18944 x 512 (softmax): see the launch.
+//
+// 18944 x 512, softmax, k = 10: 17 us, 2.3 TB/s of logits. Vector issue bounds it (460
+// instructions a token, a third of them the row's 64-bit exponentials; 85 - 90% of the time). k
+// rounds of the wave's maximum over lanes of sorted keys, in place of the list, took 23.6. 16 and
+// 2048 tokens of 256 with 8 groups, sigmoid and bias: 5.0 and 6.6 us, a chain of latencies.
 template <int V, bool LOGIT>
 __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
     GateParams p, const float* __restrict__ logits, const float* __restrict__ bias, int T, int E,
@@ -285,23 +302,24 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
         for (int v = 0; v < V; ++v) z += l[v] == INFINITY ? 1.0 : 0.0;
       } else {  // a closed expert's 5e-324 does not change a sum that holds a 1
 #pragma unroll
-        for (int v = 0; v < V; ++v) z += exp64((double)l[v] - (double)m);
+        for (int v = 0; v < V; ++v) z += exp64<LOGIT ? 10 : 12>((double)l[v] - (double)m);
       }
       z = wave_sum(z);
       zi = m > -INFINITY ? rcp64(z) : 0.0;
     }
   }
+  // Places past the row's end count as closed experts: of equals they come last, and k <= E.
   C c[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if constexpr (LOGIT) {
-      c[v] = e0 + v < E ? order32(l[v]) : kTaken;
+      c[v] = order32(l[v]);
     } else {
       const double s = !p.softmax      ? sigmoid64(l[v])
                        : m == INFINITY ? (l[v] == INFINITY ? zi : 0.0)
                                        : exp64((double)l[v] - (double)m) * zi;
       const double x = s + (bias ? (double)bias[min(e0 + v, E - 1)] : 0.0);
-      c[v] = e0 + v >= E ? kTaken : l[v] > -INFINITY && x > kClosed ? x : kClosed;
+      c[v] = l[v] > -INFINITY && x > kClosed ? x : kClosed;
     }
   }
   // groups
@@ -370,7 +388,7 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
       __syncthreads();
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (e0 + v < E && gsc[(e0 + v) / gs] == 0.0) c[v] = kTaken;
+        if (e0 + v >= E || gsc[(e0 + v) / gs] == 0.0) c[v] = kTaken;
     }
   }
   // the candidates side by side in LDS, one a lane, in the order of their slots
@@ -383,46 +401,53 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
   }
   uint64_t hit[V];
   const int n = pick_candidates(key, LOGIT ? 1u : upper(order64(kClosed)), k, lane, hit);
-  // LOGIT: the key and the index's complement in one number; equal keys then order by index
+  // LOGIT: the key and the index's complement in one number. Else the list is in index order, so
+  // equal keys are in the order of their places.
   __shared__ __align__(16) uint64_t list[kGateWaves][kWave];
-  __shared__ int list_e[LOGIT ? 1 : kGateWaves][kWave];
+  __shared__ uint2 list_el[LOGIT ? 1 : kGateWaves][kWave];
   list[wave][lane] = 0;
-  if constexpr (!LOGIT) list_e[wave][lane] = E;
   wave_sync();
-  int before = 0;
+  int at = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    at = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(hit[v] >> 32),
+                                        __builtin_amdgcn_mbcnt_lo((uint32_t)hit[v], at));
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int at = before + (int)__builtin_amdgcn_mbcnt_hi(
-                                (uint32_t)(hit[v] >> 32),
-                                __builtin_amdgcn_mbcnt_lo((uint32_t)hit[v], 0u));
-    if (hit[v] >> lane & 1) {
+    if (__builtin_amdgcn_inverse_ballot_w64(hit[v])) {
       if constexpr (LOGIT) {
         list[wave][at] = (uint64_t)key[v] << 32 | (uint32_t)~(e0 + v);
       } else {
         list[wave][at] = key[v];
-        list_e[wave][at] = e0 + v;
+        list_el[wave][at] = make_uint2(e0 + v, __float_as_uint(l[v]));
       }
+      ++at;
     }
-    before += count(hit[v]);
   }
   wave_sync();
   // a candidate's place is the number of those in front of it
   const uint64_t mine = list[wave][lane];
-  const int my_e = LOGIT ? (int)~(uint32_t)mine : list_e[LOGIT ? 0 : wave][lane];
   int place = 0;
-  for (int j = 0; j < n; j += 4) {
+  for (int j = 0; j < n; j += 8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const uint64_t o = list[wave][j + i];
       if constexpr (LOGIT) place += o > mine;
-      else place += o > mine || (o == mine && list_e[wave][j + i] < my_e);
+      else place += o > mine || (o == mine && j + i < lane);
     }
   }
   const bool chosen = lane < n && place < k;
+  int my_e;
   float my_l;
-  if constexpr (LOGIT) my_l = unorder32(upper(mine));
-  else my_l = chosen ? row[my_e] : -INFINITY;
-  my_l = chosen && my_l == my_l ? my_l : -INFINITY;
+  if constexpr (LOGIT) {
+    my_e = (int)~(uint32_t)mine;
+    my_l = unorder32(upper(mine));
+  } else {
+    const uint2 el = list_el[wave][lane];
+    my_e = (int)el.x;
+    my_l = __uint_as_float(el.y);
+  }
+  my_l = chosen ? my_l : -INFINITY;
   double s = 0;  // the score, 0 where nothing was chosen
   if (chosen) {
     s = !p.softmax ? sigmoid64(my_l) : soft_num64(my_l, m);
@@ -450,6 +475,8 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
 // pieces. Slots that name one expert twice (found by each slot writing its number to its
 // expert's place and reading it back) are added one after the other, in ascending j; a slot
 // outside [0, E) counts nothing. DENSE, softmax without renorm, also reads the row of logits.
+// 18944 x 512, every logit: 16 us, 4.9 TB/s, HBM's rate for as much read as written (a large copy
+// does 4.65). 2048 x 256, sigmoid: 3.6 us, the launch and one chain of loads.
 template <int V, bool DENSE>
 __global__ void __launch_bounds__(kGateWaves* kWave) gate_backward_kernel(
     GateParams p, const float* __restrict__ logits, const int32_t* __restrict__ idx,
