@@ -59,6 +59,7 @@ class MoeLayer:
         self.fbits = 8 if precision == MOE_PREC_MXFP8 else 4 if precision == MOE_PREC_MXFP4 else 16
         self.wq = torch.empty(s.wq, dtype=u8, device=dev) if s.wq else None
         self.gate, self.gate_bias = gate, gate_bias
+        self.given = False  # whether topk_idx came from set_routing, without logits
         self.dlogits = torch.empty(T, E, dtype=f32, device=dev) if gate is not None else None
 
     # views of intermediates -----------------------------------------------------------------
@@ -99,6 +100,7 @@ class MoeLayer:
 
     # steps ----------------------------------------------------------------------------------
     def route(self, x, w_router, stream=None):
+        self.given = False
         if self.gate is not None:
             moe_route_gated(self.cfg, self.gate, x, w_router, self.gate_bias, self.logits,
                             self.topk_idx, self.topk_w, self.workspace, stream)
@@ -107,6 +109,7 @@ class MoeLayer:
                   stream)
 
     def set_routing(self, topk_idx, topk_w):
+        self.given = True
         self.topk_idx.copy_(topk_idx)
         self.topk_w.copy_(topk_w)
 
@@ -134,6 +137,8 @@ class MoeLayer:
         """With a gate and a ``w_router``, ``x`` (the tokens) is needed too: the experts' backward
         runs as for a given routing, then the gate's and the router's add theirs to dx and dwr."""
         if self.gate is not None and w_router is not None:
+            if self.given:
+                raise ValueError("a given routing has no logits to take a gate's gradients at")
             if x is None:
                 raise ValueError("a gated layer's router gradients need x")
             self.backward(None, w1, w2, dy, slot, accumulate, saved, stream)

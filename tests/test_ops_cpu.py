@@ -205,3 +205,12 @@ def test_fp8_mode_sizes_and_refusals():
     assert L.moe_quantize_weights(_ref(c), P, P, P, s8.wq - 1, None) == -5
     assert L.moe_forward(_ref(c), P, s8.ring_slot, 0, P, P, P, P, P, None, 0, P, P, s8.saved, P,
                          s8.workspace, None) == -1
+
+
+def test_gated_layer_refuses_router_gradients_of_a_given_routing():
+    from mixture_experts_layer_deterministic_amd import layer
+    L = layer.MoeLayer(4, 256, 8, 2, 128, device="cpu", gate=m.make_gate())
+    L.set_routing(torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2))
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="no logits"):
+        L.backward(x, x, x, x, x=x)
