@@ -106,15 +106,21 @@ MOE_DEV F wave_max(F v) {
 // exp(x) for the scores, x <= 709: e^x = 2^n e^r with n = rint(x / ln 2) and |r| <= ln(2) / 2,
 // e^r by its Taylor polynomial. Degree 12 (the next term is below 1.8e-16) gives about 1e-15 in
 // all, with 20 instructions; the library's exp also covers what does not occur here. Degree 10
-// (2.2e-13) is for a sum that only divides what is then rounded to fp32.
+// (2.2e-13, and |x| 2^-53 from one rounded ln 2) is for a sum that only divides what is then
+// rounded to fp32.
 template <int DEGREE = 12>
 MOE_DEV double exp64(double x) {
   x = __builtin_fmax(x, -745.0);
   // adding 1.5 2^52 rounds to a whole number, which the sum's low word then holds
   const double t = __builtin_fma(x, 1.4426950408889634, 6755399441055744.0);
   const double n = t - 6755399441055744.0;
-  double r = __builtin_fma(n, -6.93147180369123816490e-01, x);
-  r = __builtin_fma(n, -1.90821492927058770002e-10, r);
+  double r;
+  if constexpr (DEGREE == 12) {  // ln 2 in two parts, n times the first exact
+    r = __builtin_fma(n, -6.93147180369123816490e-01, x);
+    r = __builtin_fma(n, -1.90821492927058770002e-10, r);
+  } else {
+    r = __builtin_fma(n, -6.93147180559945309417e-01, x);
+  }
   double p = DEGREE == 12 ? 1.0 / 479001600.0 : 1.0 / 3628800.0;
   if constexpr (DEGREE == 12) {
     p = __builtin_fma(p, r, 1.0 / 39916800.0);
@@ -256,10 +262,11 @@ MOE_DEV int pick_candidates(const U (&key)[V], uint32_t least, int k, int lane,
 // LOGIT: the scores order as the logits do; 32-bit keys, and 64-bit scores only of the chosen.
 // Groups that are whole, aligned runs of 2^i lanes are scored by lane exchanges, others in LDS.
 //
-// 18944 x 512, softmax, k = 10: 17 us, 2.3 TB/s of logits. Vector issue bounds it (460
+// 18944 x 512, softmax, k = 10: 16.8 us, 2.3 TB/s of logits. Vector issue bounds it (450
 // instructions a token, a third of them the row's 64-bit exponentials; 85 - 90% of the time). k
-// rounds of the wave's maximum over lanes of sorted keys, in place of the list, took 23.6. 16 and
-// 2048 tokens of 256 with 8 groups, sigmoid and bias: 5.0 and 6.6 us, a chain of latencies.
+// rounds of the wave's maximum over lanes of sorted keys, in place of the list, took 23.6. 16,
+// 2048 and 18944 tokens of 256 with 8 groups, sigmoid and bias: 4.9 and 6.3 us, a chain of
+// latencies, and 21.4, vector issue again (rounds: 5.3, 6.8 and 29.4).
 template <int V, bool LOGIT>
 __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
     GateParams p, const float* __restrict__ logits, const float* __restrict__ bias, int T, int E,
@@ -310,6 +317,7 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
   }
   // Places past the row's end count as closed experts: of equals they come last, and k <= E.
   C c[V];
+  double sv[LOGIT ? 1 : V];  // the scores, 0 of closed experts
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if constexpr (LOGIT) {
@@ -320,6 +328,7 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
                                        : exp64((double)l[v] - (double)m) * zi;
       const double x = s + (bias ? (double)bias[min(e0 + v, E - 1)] : 0.0);
       c[v] = l[v] > -INFINITY && x > kClosed ? x : kClosed;
+      sv[v] = l[v] > -INFINITY ? s : 0.0;
     }
   }
   // groups
@@ -334,12 +343,17 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
         a = larger(a, c[v]);
         b = larger(b, lo);
       }
-      for (int o = 1; o < lpg; o <<= 1) {
-        const C a1 = __shfl_xor(a, o), b1 = __shfl_xor(b, o);
+      auto merge = [&](C a1, C b1) {
         const C lo = a1 > a ? a : a1;
         a = larger(a, a1);
         b = larger(larger(b, b1), lo);
-      }
+      };
+      // lane l with l ^ 1, l ^ 2, then mirrored in 8 and in 16 lanes, whose halves agree by then
+      if (lpg > 1) merge(dpp<0xb1, 0xf>(a), dpp<0xb1, 0xf>(b));
+      if (lpg > 2) merge(dpp<0x4e, 0xf>(a), dpp<0x4e, 0xf>(b));
+      if (lpg > 4) merge(dpp<0x141, 0xf>(a), dpp<0x141, 0xf>(b));
+      if (lpg > 8) merge(dpp<0x140, 0xf>(a), dpp<0x140, 0xf>(b));
+      for (int o = 16; o < lpg; o <<= 1) merge(__shfl_xor(a, o), __shfl_xor(b, o));
       if constexpr (!LOGIT)
         if (p.top2 && b > kClosed) a += b;
       const int mine = lane / lpg;
@@ -404,7 +418,8 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
   // LOGIT: the key and the index's complement in one number. Else the list is in index order, so
   // equal keys are in the order of their places.
   __shared__ __align__(16) uint64_t list[kGateWaves][kWave];
-  __shared__ uint2 list_el[LOGIT ? 1 : kGateWaves][kWave];
+  __shared__ double list_s[LOGIT ? 1 : kGateWaves][kWave];
+  __shared__ int list_e[LOGIT ? 1 : kGateWaves][kWave];
   list[wave][lane] = 0;
   wave_sync();
   int at = 0;
@@ -419,7 +434,8 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
         list[wave][at] = (uint64_t)key[v] << 32 | (uint32_t)~(e0 + v);
       } else {
         list[wave][at] = key[v];
-        list_el[wave][at] = make_uint2(e0 + v, __float_as_uint(l[v]));
+        list_s[wave][at] = sv[v];
+        list_e[wave][at] = e0 + v;
       }
       ++at;
     }
@@ -428,30 +444,29 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
   // a candidate's place is the number of those in front of it
   const uint64_t mine = list[wave][lane];
   int place = 0;
-  for (int j = 0; j < n; j += 8) {
+  constexpr int kStep = LOGIT ? 4 : 8;  // fewer compares past n; fewer waits
+#pragma unroll 1
+  for (int j = 0; j < n; j += kStep) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kStep; ++i) {
       const uint64_t o = list[wave][j + i];
       if constexpr (LOGIT) place += o > mine;
       else place += o > mine || (o == mine && j + i < lane);
     }
   }
   const bool chosen = lane < n && place < k;
-  int my_e;
-  float my_l;
-  if constexpr (LOGIT) {
-    my_e = (int)~(uint32_t)mine;
-    my_l = unorder32(upper(mine));
-  } else {
-    const uint2 el = list_el[wave][lane];
-    my_e = (int)el.x;
-    my_l = __uint_as_float(el.y);
-  }
-  my_l = chosen ? my_l : -INFINITY;
+  int my_e = 0;
   double s = 0;  // the score, 0 where nothing was chosen
   if (chosen) {
-    s = !p.softmax ? sigmoid64(my_l) : soft_num64(my_l, m);
-    if (p.softmax && zi > 0) s *= zi;
+    if constexpr (LOGIT) {
+      my_e = (int)~(uint32_t)mine;
+      const float my_l = unorder32(upper(mine));
+      s = !p.softmax ? sigmoid64(my_l) : soft_num64(my_l, m);
+      if (p.softmax && zi > 0) s *= zi;
+    } else {
+      my_e = list_e[wave][lane];
+      s = list_s[wave][lane];
+    }
   }
   if (p.renorm) {
     const double sum = wave_sum(s);
