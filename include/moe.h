@@ -412,8 +412,10 @@ int moe_gate_backward(const moe_cfg* cfg, const moe_gate* gate, const float* log
  *   dx[t]  = bf16( sum_e dlogits[t,e] w_router[e] )     (with acc_dx: that sum + dx[t], one
  *                                                        rounding of the fp32 total)
  *   dwr[e] = sum_t dlogits[t,e] x[t]                    (with acc_dwr: added to dwr[e])
- * Sums in fp32 (dlogits enters with 24 bits) in a fixed order. A dlogits value that is not finite
- * makes its token's dx and its expert's dwr NaN, and touches no other.
+ * Sums in fp32 in a fixed order (dlogits enters dwr with all its 24 bits, and dx, which is rounded
+ * to bf16, with 17: an error of at most 2^-17 of each term). A dlogits value that is not finite
+ * makes its token's dx and its expert's dwr NaN, and touches no other; for dx one that rounds to
+ * an infinite bf16 (3.39e38 and above) counts as not finite.
  *
  *   x        bf16 [T, d]    in
  *   w_router bf16 [E, d]    in

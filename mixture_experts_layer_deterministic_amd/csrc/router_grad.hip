@@ -6,7 +6,8 @@
 // values are exact in fp32, so bf16 MFMAs do an fp32 product's work at a rate that fp32 MFMAs
 // (1/16 of bf16's) do not reach. Cutting a value's upper 8 bits off, then the next 8 of what is
 // left, gives three parts that add up to all its 24 bits: dWr, an fp32 sum, takes the three. dx
-// is rounded to bf16 (2^-9) at the end and takes two, the second rounded: 17 bits, 2^-17.
+// is rounded to bf16 (2^-8) at the end and takes two, both rounded to nearest: of x in [1, 2) the
+// first leaves at most 2^-8 and the second at most 2^-17 of that.
 #include "common.h"
 #include "kernels.h"
 #include "ops.h"
@@ -31,11 +32,13 @@ MOE_DEV float cut(float x) {  // what is left of x below its upper 8 bits (exact
 }
 template <int P>
 MOE_DEV void split4(const f32x4& x, uint2 (&part)[P]) {
-  const float r0 = cut(x[0]), r1 = cut(x[1]), r2 = cut(x[2]), r3 = cut(x[3]);
-  part[0] = make_uint2(upper2(x[0], x[1]), upper2(x[2], x[3]));
   if constexpr (P == 2) {
-    part[1] = make_uint2(round2(r0, r1), round2(r2, r3));
+    part[0] = make_uint2(round2(x[0], x[1]), round2(x[2], x[3]));
+    part[1] = make_uint2(round2(x[0] - bf2f_lo(part[0].x), x[1] - bf2f_hi(part[0].x)),
+                         round2(x[2] - bf2f_lo(part[0].y), x[3] - bf2f_hi(part[0].y)));
   } else {
+    const float r0 = cut(x[0]), r1 = cut(x[1]), r2 = cut(x[2]), r3 = cut(x[3]);
+    part[0] = make_uint2(upper2(x[0], x[1]), upper2(x[2], x[3]));
     part[1] = make_uint2(upper2(r0, r1), upper2(r2, r3));
     part[2] = make_uint2(upper2(cut(r0), cut(r1)), upper2(cut(r2), cut(r3)));
   }
@@ -231,7 +234,8 @@ __global__ void __launch_bounds__(512, 4) router_backward_kernel(const RouterGra
 
 hipError_t launch_router_backward(const RouterGradArgs& a, hipStream_t s) {
   const int nc = a.d / kRgN;
-  const int nw = a.dwr ? (a.E + 63) / 64 * nc : 0, nx = a.dx ? (a.T + 127) / 128 * nc : 0;
+  const int nw = a.dwr ? (a.E + 63) / 64 * nc : 0;
+  const int nx = a.dx ? (a.T + 127) / 128 * nc : 0;
   {
     TraceScope trace("router_backward", s);
     hipLaunchKernelGGL(router_backward_kernel, dim3(nw + nx), dim3(512), 0, s, a, nw);

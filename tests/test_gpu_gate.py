@@ -219,7 +219,7 @@ def test_gradient_of_scores_below_fp32(shift):
 
 
 ROUTER = [(1, 256, 1), (1, 256, 256), (5, 512, 3), (64, 256, 8), (127, 256, 129), (128, 512, 128),
-          (200, 768, 509), (1000, 256, 64), (333, 1024, 1024)]
+          (200, 768, 509), (1000, 256, 64), (333, 1024, 1024), (1500, 2048, 16)]
 
 
 @pytest.mark.parametrize("T,d,E", ROUTER)
@@ -238,7 +238,10 @@ def test_router_gradients(T, d, E):
     X, W, D = x.to(DEV), wr.to(DEV), dl.to(DEV)
     x64, w64, d64 = x.double(), wr.double(), dl.double()
     # fp32 sums of three exact products a term: an fp32 step (2^-23) for each addition
-    e_dx = (3 * E + 4) * 2.0 ** -23 * (d64.abs() @ w64.abs())
+    # dx sums two products a term, of dl as two bf16 parts p + q: of a value in [1, 2) p = bf16(v)
+    # leaves at most 2^-8, which lies in a binade with bf16 half steps of 2^-17 or less, so q leaves
+    # 2^-17 of v. (3 E + 4 steps alone are less than that one error, 64 steps, up to E = 19.)
+    e_dx = ((3 * E + 4) * 2.0 ** -23 + 2.0 ** -17) * (d64.abs() @ w64.abs())
     e_dw = (3 * T + 4) * 2.0 ** -23 * (d64.abs().t() @ x64.abs())
     for acc in (False, True):
         dx, dw = dx0.clone().to(DEV), dw0.clone().to(DEV)
