@@ -230,13 +230,141 @@ __global__ void __launch_bounds__(512, 4) router_backward_kernel(const RouterGra
   }
 }
 
+// dWr where experts x columns are few and tokens many: tiles of 16 MB experts x 16 NB columns, whose
+// 16 waves split the tokens, steps of 32 in turn. Operands go from memory to registers in whole
+// pieces and never through LDS, and no wave waits for another: lane l = 16 g + r loads, i = 0 .. 7,
+//  * of x token 8 g + i, columns NB r .. NB r + NB - 1: those 8 x NB values are the lane's parts of
+//    NB fragments once pairs of tokens are woven (one byte permutation a register), fragment n's
+//    column r standing for column NB r + n of the tile;
+//  * of dl token 8 g + i, experts MB r .. MB r + MB - 1: likewise MB fragments.
+// The waves' sums are added in LDS in a fixed order.
+// 8 experts, 16384 x 4096: 49 us, 2.7 TB/s of x, bound by the latency of a wave's one step ahead;
+// 128 experts, 8192 x 4096: 43 us, 0.6 PFLOP/s in three products, bound by the vector work of
+// splitting and weaving. (The 64 x 128 tiles: 233 and 121, on 32 and 64 CUs.)
+constexpr int kFewWaves = 16;
+// A number the compiler has to take as new: sums with it are made where they are used, since kept
+// over the loop they cost more registers than a wave has.
+MOE_DEV uint32_t here(uint32_t x) {
+  asm volatile("" : "+s"(x));
+  return x;
+}
+template <int WORDS>
+MOE_DEV void get_words(__amdgpu_buffer_rsrc_t rows, uint32_t at, uint32_t (&w)[WORDS]) {
+  if constexpr (WORDS == 1) {
+    w[0] = __builtin_amdgcn_raw_buffer_load_b32(rows, at, 0, 0);
+  } else {
+    static_assert(WORDS == 2, "one or two words");
+    const uint2 v = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rows, at, 0, 0));
+    w[0] = v.x;
+    w[1] = v.y;
+  }
+}
+template <int MB, int NB>
+__global__ void __launch_bounds__(kFewWaves* kWave) router_dw_few_kernel(const RouterGradArgs a) {
+  constexpr int kStep = 32, kStride = kFewWaves * kStep;
+  __shared__ float sums[kFewWaves][MB * NB][4][kWave];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x % kWave, r = lane % 16, g = lane / 16;
+  const int nc = a.d / (16 * NB), r0 = blockIdx.x / nc * 16 * MB, c0 = blockIdx.x % nc * 16 * NB;
+  uint32_t dv[8][MB], xv[8][NB / 2];
+  // buffer loads that end with their step's rows: tokens past the end read as zeros without a
+  // branch. dl's columns past E, the next token's, lead to rows that are not stored.
+  auto load = [&](int k0) {
+    const int left = min(a.T - k0, kStep);
+    const __amdgpu_buffer_rsrc_t dl =
+        rg_rsrc(a.dl + (size_t)k0 * a.E + r0, left > 0 ? 4u * (left * a.E - r0) : 0u);
+    const __amdgpu_buffer_rsrc_t x =
+        rg_rsrc(a.x + (size_t)k0 * a.d + c0, left > 0 ? 2u * (left * a.d - c0) : 0u);
+    const uint32_t dl_row = here(a.E * 4), x_row = here(a.d * 2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      get_words<MB>(dl, (8 * g + i) * dl_row + 4 * MB * r, dv[i]);
+      get_words<NB / 2>(x, (8 * g + i) * x_row + 2 * NB * r, xv[i]);
+    }
+  };
+  f32x4 acc[MB][NB];
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  load(wave * kStep);
+  for (int k0 = wave * kStep; k0 < a.T; k0 += kStride) {
+    uint4 bf[NB], af[MB][3];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        w[q] = __builtin_amdgcn_perm(xv[2 * q + 1][n / 2], xv[2 * q][n / 2],
+                                     n % 2 ? 0x07060302u : 0x05040100u);
+      bf[n] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      f32x4 v[2];
+      uint2 lo[3], hi[3];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i / 4][i % 4] = __uint_as_float(dv[i][m]);
+      split4<3>(v[0], lo);
+      split4<3>(v[1], hi);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) af[m][p] = make_uint4(lo[p].x, lo[p].y, hi[p].x, hi[p].y);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // the next loads go out into the registers just read
+    load(k0 + kStride);
+#pragma unroll
+    for (int p = 2; p >= 0; --p)  // the small parts first
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) acc[m][n] = mfma16(bf[n], af[m][p], acc[m][n]);
+  }
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sums[wave][m * NB + n][j][lane] = acc[m][n][j];
+  __syncthreads();
+  // a thread an output: column c of row e of the tile, tile columns side by side
+  for (int o = threadIdx.x; o < 16 * MB * 16 * NB; o += kFewWaves * kWave) {
+    const int e = o / (16 * NB), c = o % (16 * NB);
+    const int m = e % MB, n = c % NB, j = c / NB % 4, l = c / NB / 4 * 16 + e / MB;
+    float s = sums[0][m * NB + n][j][l];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) s += sums[w][m * NB + n][j][l];
+    if (r0 + e < a.E) {
+      float* p = a.dwr + (size_t)(r0 + e) * a.d + c0 + c;
+      *p = a.acc_dwr ? *p + s : s;
+    }
+  }
+}
+
 }  // namespace
 
 hipError_t launch_router_backward(const RouterGradArgs& a, hipStream_t s) {
   const int nc = a.d / kRgN;
-  const int nw = a.dwr ? (a.E + 63) / 64 * nc : 0;
+  int nw = a.dwr ? (a.E + 63) / 64 * nc : 0;
   const int nx = a.dx ? (a.T + 127) / 128 * nc : 0;
-  {
+  // Which kernel sums dWr (by T, d and E alone, so that asking for dx changes no bit of it). Both
+  // gradients in us, 64 x 128 tiles in dx's launch against small tiles in a launch of their own:
+  //  * up to 64 tiles of 64 x 128 and 32 tokens a tile, 1024 at least: small. 16 tiles (64 experts,
+  //    2048 columns) 1024 tokens 19 against 14, 16384 243 against 83; 64 tiles (128 experts, 4096
+  //    columns) 2048 tokens 36 against 31. Fewer tokens: 16 tiles, 512 tokens 11 against 13; 64
+  //    tiles, 1024 tokens 20 against 22. More tiles: 80, 4096 tokens 68 against 76.
+  //  * of them tiles of 16 experts while they are one a CU at most, else of 32. 256 of 16 (64
+  //    experts, 4096 columns), 4096 tokens: 37 against 42; 512 (128 experts, 4096 columns): 53
+  //    against 47.
+  if (nw && nw <= 64 && a.T >= 1024 && a.T >= 32 * nw) {
+    const int n16 = (a.E + 15) / 16 * (a.d / 64), n32 = (a.E + 31) / 32 * (a.d / 64);
+    TraceScope trace("router_dwr", s);
+    if (n16 <= 256)
+      hipLaunchKernelGGL((router_dw_few_kernel<1, 4>), dim3(n16), dim3(kFewWaves * kWave), 0, s, a);
+    else
+      hipLaunchKernelGGL((router_dw_few_kernel<2, 4>), dim3(n32), dim3(kFewWaves * kWave), 0, s, a);
+    nw = 0;
+  }
+  if (nw + nx) {
     TraceScope trace("router_backward", s);
     hipLaunchKernelGGL(router_backward_kernel, dim3(nw + nx), dim3(512), 0, s, a, nw);
   }

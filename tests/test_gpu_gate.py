@@ -219,7 +219,10 @@ def test_gradient_of_scores_below_fp32(shift):
 
 
 ROUTER = [(1, 256, 1), (1, 256, 256), (5, 512, 3), (64, 256, 8), (127, 256, 129), (128, 512, 128),
-          (200, 768, 509), (1000, 256, 64), (333, 1024, 1024), (1500, 2048, 16)]
+          (200, 768, 509), (1000, 256, 64), (333, 1024, 1024),
+          # few tiles of dWr and many tokens, on each side of the choices between its kernels
+          (1023, 512, 37), (1024, 512, 37), (1025, 256, 1), (1500, 2048, 16), (1611, 2048, 130),
+          (2047, 4096, 101), (2048, 4096, 101), (2500, 4352, 70), (5000, 256, 300)]
 
 
 @pytest.mark.parametrize("T,d,E", ROUTER)
@@ -260,7 +263,8 @@ def test_router_gradients(T, d, E):
         assert torch.equal(dx1, dx) and torch.equal(dw1, dw)
 
 
-@pytest.mark.parametrize("T,d,E", [(6, 256, 1), (130, 256, 5), (200, 512, 129), (300, 256, 509)])
+@pytest.mark.parametrize("T,d,E", [(6, 256, 1), (130, 256, 5), (200, 512, 129), (300, 256, 509),
+                                     (1100, 256, 5), (2050, 4096, 101)])
 def test_a_value_that_is_not_finite_spoils_its_own_rows_only(T, d, E):
     """The last step of dx's reduction reads past a row's E logits, into the next token's."""
     _announce(f"[router bwd, NaN] T={T} d={d} E={E}")
