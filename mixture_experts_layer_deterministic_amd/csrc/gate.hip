@@ -623,7 +623,9 @@ int whole_pieces(const void* p, int E) {
 
 hipError_t launch_gate_select(const GateParams& p, const float* logits, const float* bias, int T,
                               int E, int k, int32_t* idx, float* w, hipStream_t s) {
-  const bool by_logit = !bias && (p.groups == 1 || p.topk_groups == p.groups || !p.top2);
+  // The definition compares scores under sums of two, also where every group stays and no sum is
+  // needed: scores that meet in 64 bits (saturated sigmoids) are ties, their logits are not.
+  const bool by_logit = !bias && (p.groups == 1 || !p.top2);
   const int vec = whole_pieces(logits, E);
   const dim3 grid((T + kGateWaves - 1) / kGateWaves), block(kGateWaves * kWave);
   {

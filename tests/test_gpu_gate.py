@@ -329,3 +329,24 @@ def test_gate_and_router_calls_refuse_tensors_the_library_cannot_check():
         with pytest.raises(m.MoeError) as e:
             m.moe_gate_select(cfg, g, *args)
         assert e.value.status == -1
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("G", [2, 8, 96])
+def test_choice_by_sums_of_two_where_every_group_stays(G, score):
+    """Scores that meet in 64 bits (saturated sigmoids, softmax terms that underflow) go to the
+    lower index, though their logits differ: without a bias only one group, or GROUP_MAX, is
+    chosen by the logits."""
+    _announce(f"[gate] G={G}, all stay, sums of two, score={score}")
+    l = _logits(7, 96, 21)
+    l[0] = 60.0 + np.arange(96, dtype=np.float32)
+    l[1] = -5.0
+    l[1, [3, 9, 12]] = 40.0, 50.0, 45.0
+    l[2] = -2000.0 + np.arange(96, dtype=np.float32)
+    l[2, 5] = 0.0
+    l[3, ::3] = -inf
+    l[4, 10:] = -inf
+    l[4, :10] = 100.0 - np.arange(10, dtype=np.float32)[::-1]
+    for k, renorm in itertools.product((3, 8, 40), (False, True)):
+        for gsc in (0, 1):
+            _check_select(l, k, score, None, G, G, gsc, renorm, 1.0)
