@@ -337,7 +337,7 @@ int moe_backward(const moe_cfg* cfg, const void* ring, size_t ring_bytes, int32_
  *
  * Per token, over its row l of E logits (s, c in 64 bits):
  *   s_e = exp(l_e) / sum_i exp(l_i)  (MOE_SCORE_SOFTMAX)  or  1 / (1 + exp(-l_e))
- *         (MOE_SCORE_SIGMOID);
+ *         (MOE_SCORE_SIGMOID; 0 below l_e = -709);
  *   c_e = s_e + bias_e, the choice score (bias NULL: c_e = s_e). The bias, which a trainer moves
  *         to balance the experts' load, takes no part in the weights and has no gradient.
  *   groups > 1: the experts form `groups` equal runs of E / groups. A group scores its largest c
@@ -393,8 +393,9 @@ int moe_route_gated(const moe_cfg* cfg, const moe_gate* gate, const void* x, con
  *   softmax, renorm    dl_j = q_j (g_j - sum_i g_i q_i)
  *   softmax            dl_e = s_e ([e chosen] g_e - sum_i s_i g_i), for every expert e
  * and 0 for the experts not chosen in the first three. fp32, but for the sigmoids and their sum (64
- * bits, as in the choice); sums in a fixed order. A topk_idx entry outside [0, E) counts nothing;
- * one expert named twice gets both slots' sum.
+ * bits, as in the choice); sums in a fixed order. The q of softmax come from the chosen logits
+ * alone, and are not 0 where every chosen s_j underflows 64 bits (weights 0 in the forward). A
+ * topk_idx entry outside [0, E) counts nothing; one expert named twice gets both slots' sum.
  *
  *   logits   fp32 [T, E]    in   (as given to the forward)
  *   topk_idx int32 [T, k]   in

@@ -110,7 +110,7 @@ MOE_DEV F wave_max(F v) {
 // rounded to fp32.
 template <int DEGREE = 12>
 MOE_DEV double exp64(double x) {
-  x = __builtin_fmax(x, -745.0);
+  x = __builtin_fmax(x, -746.0);  // 2^-1076.2, which rounds to 0
   // adding 1.5 2^52 rounds to a whole number, which the sum's low word then holds
   const double t = __builtin_fma(x, 1.4426950408889634, 6755399441055744.0);
   const double n = t - 6755399441055744.0;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
       if (m == INFINITY) {  // for the whole wave: the +inf entries share the row
 #pragma unroll
         for (int v = 0; v < V; ++v) z += l[v] == INFINITY ? 1.0 : 0.0;
-      } else {  // a closed expert's 5e-324 does not change a sum that holds a 1
+      } else {  // a closed expert's is 0
 #pragma unroll
         for (int v = 0; v < V; ++v) z += exp64<LOGIT ? 10 : 12>((double)l[v] - (double)m);
       }

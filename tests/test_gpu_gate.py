@@ -350,3 +350,25 @@ def test_choice_by_sums_of_two_where_every_group_stays(G, score):
     for k, renorm in itertools.product((3, 8, 40), (False, True)):
         for gsc in (0, 1):
             _check_select(l, k, score, None, G, G, gsc, renorm, 1.0)
+
+
+def test_softmax_scores_that_underflow_weigh_nothing():
+    """A bias may choose experts whose exponentials underflow in 64 bits: their scores are 0, and
+    so is their sum."""
+    _announce("[gate] softmax scores below 64 bits, chosen by the bias")
+    E, k = 40, 5
+    l = _logits(4, E, 3)
+    bias = np.zeros(E, np.float32)
+    bias[10:10 + k] = 2.0
+    l[0] = -800.0
+    l[0, 0] = 0.0
+    l[1] = -1e30
+    l[1, 39] = 7.0
+    # exp of these in steps of 2^-1074: 11.47, 4.22, 1.55, 0.53 and 0.21
+    l[2] = -900.0
+    l[2, 0] = 0.0
+    l[2, 10:10 + k] = -742.0, -743.0, -744.0, -745.078125, -746.0
+    for renorm, (G, tg) in itertools.product((False, True), ((1, 1), (4, 4), (4, 3))):
+        _check_select(l, k, 0, bias, G, tg, 1, renorm, 2.5)
+    idx, w = _select(l, k, m.make_gate(0, 1, 1, 0, True, 1.0), bias)
+    assert sorted(idx[0]) == list(range(10, 15)) and not w[0].any() and not w[1].any()
