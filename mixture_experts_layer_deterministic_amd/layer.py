@@ -126,7 +126,10 @@ class MoeLayer:
                     stream)
 
     def forward_fused(self, x, w_router, w1, w2, slot=0, saved=None, stream=None):
-        """route + permute + forward in one kernel launch (moe_forward_fused)."""
+        """route + permute + forward in one kernel launch (moe_forward_fused), which has no gate."""
+        if self.gate is not None:
+            raise ValueError("the single-launch forward routes by the top-k softmax only")
+        self.given = False
         moe_forward_fused(self.cfg, x, w_router, self.logits, self.topk_idx, self.topk_w,
                           self.ring, slot, self.counts, self.offsets, self.row_src, self.tk_row,
                           w1, w2, self.y, self.saved if saved is None else saved, self.workspace,
@@ -157,8 +160,6 @@ class MoeLayer:
         """One fwd+bwd pass: route (when w_router is given), permute, forward, backward. With
         ``fused`` the first three run as one launch (moe_forward_fused)."""
         if fused:
-            if self.gate is not None:
-                raise ValueError("the single-launch forward routes by the top-k softmax only")
             self.forward_fused(x, w_router, w1, w2, slot, stream=stream)
             self.backward(w_router, w1, w2, dy, slot, stream=stream)
             return

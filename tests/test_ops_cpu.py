@@ -214,3 +214,22 @@ def test_gated_layer_refuses_router_gradients_of_a_given_routing():
     x = torch.zeros(4, 256, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="no logits"):
         L.backward(x, x, x, x, x=x)
+
+
+def test_single_launch_forward_is_refused_by_a_gated_layer(monkeypatch):
+    """It routes by the top-k softmax, so the gate's gradients would be taken at another choice."""
+    from mixture_experts_layer_deterministic_amd import layer
+    launched = []
+    monkeypatch.setattr(layer, "moe_forward_fused", lambda *a: launched.append(a))
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    L = layer.MoeLayer(4, 256, 8, 2, 128, device="cpu", gate=m.make_gate())
+    with pytest.raises(ValueError, match="top-k softmax"):
+        L.forward_fused(x, x, x, x)
+    with pytest.raises(ValueError, match="top-k softmax"):
+        L.step(x, x, x, x, x, fused=True)
+    assert not launched
+    # a layer without a gate routes by it, and then has logits
+    L = layer.MoeLayer(4, 256, 8, 2, 128, device="cpu")
+    L.set_routing(torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2))
+    L.forward_fused(x, x, x, x)
+    assert len(launched) == 1 and not L.given
