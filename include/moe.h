@@ -439,7 +439,7 @@ int moe_router_backward(const moe_cfg* cfg, const void* x, const void* w_router,
  *   codes  bytes [rows, cols]         out
  *   scales fp32 [cols / 128, rows]    out: one row of scales per 128 columns, so that the product
  *                                     reads a step's scales of consecutive rows together
- * rows 0 enqueues nothing.
+ * rows 0 enqueues nothing; the three pointers may then be NULL.
  */
 int moe_fp8_quantize_rows(const void* src, int32_t rows, int32_t cols, void* codes, float* scales,
                           moe_stream_t stream);
@@ -475,8 +475,8 @@ int moe_fp8_quantize_weights(const void* src, int32_t E, int32_t N, int32_t K, v
  *   b        bytes [E, N, K]            in
  *   b_scales fp32 [E, N / 128, K / 128] in
  *   out      bf16 [M, N]                out
- * Shapes: 0 <= M < 2^31 (0 enqueues nothing), 1 <= E <= 1024, N and K multiples of 128,
- * N * K < 2^31. Errors: MOE_ERR_INVALID_ARG.
+ * Shapes: 0 <= M < 2^31 (0 enqueues nothing; a, a_scales and out may then be NULL),
+ * 1 <= E <= 1024, N and K multiples of 128, N * K < 2^31. Errors: MOE_ERR_INVALID_ARG.
  */
 int moe_fp8_gemm(const int32_t* offsets, int32_t M, int32_t E, int32_t N, int32_t K, const void* a,
                  const float* a_scales, const void* b, const float* b_scales, void* out,

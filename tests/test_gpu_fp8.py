@@ -325,3 +325,18 @@ def test_calls_refuse_tensors_the_library_cannot_check():
         with pytest.raises(m.MoeError) as e:
             m.moe_fp8_quantize_rows(bad[0], 4, 256, bad[1], bad[2])
         assert e.value.status == -1
+
+
+def test_no_rows_at_all():
+    """A share that receives no tokens: empty tensors, which have no address."""
+    e = lambda dtype, *shape: torch.empty(*shape, dtype=dtype, device=DEV)
+    m.moe_fp8_quantize_rows(e(torch.bfloat16, 0, 256), 0, 256, e(F8, 0, 256),
+                            e(torch.float32, 2, 0))
+    off = torch.zeros(3, dtype=torch.int32, device=DEV)
+    b, sb = torch.zeros(2, 128, 256, dtype=torch.uint8, device=DEV), torch.ones(2, 1, 2, device=DEV)
+    m.moe_fp8_gemm(off, 0, 2, 128, 256, e(F8, 0, 256), e(torch.float32, 2, 0), b, sb,
+                   e(torch.bfloat16, 0, 128))
+    with pytest.raises(m.MoeError):
+        m.moe_fp8_quantize_rows(e(torch.bfloat16, 0, 100), 0, 100, e(F8, 0, 100),
+                                e(torch.float32, 0))
+    torch.cuda.synchronize()

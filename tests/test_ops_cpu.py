@@ -233,3 +233,19 @@ def test_single_launch_forward_is_refused_by_a_gated_layer(monkeypatch):
     L.set_routing(torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2))
     L.forward_fused(x, x, x, x)
     assert len(launched) == 1 and not L.given
+
+
+def test_fp8_calls_take_empty_rows():
+    """What a share without tokens passes: empty tensors, whose address is 0."""
+    L = m.lib()
+    e = ctypes.c_void_p(torch.empty(0, 128).data_ptr())
+    assert e.value is None
+    assert L.moe_fp8_quantize_rows(e, 0, 128, e, e, None) == 0
+    assert L.moe_fp8_gemm(P, 0, 2, 128, 128, e, e, P, P, e, None) == 0
+    # what is not empty, and the shapes, are checked all the same
+    assert L.moe_fp8_quantize_rows(e, 0, 130, e, e, None) == -1
+    assert L.moe_fp8_gemm(None, 0, 2, 128, 128, e, e, P, P, e, None) == -1
+    assert L.moe_fp8_gemm(P, 0, 2, 128, 128, e, e, None, P, e, None) == -1
+    assert L.moe_fp8_gemm(P, 0, 2, 100, 128, e, e, P, P, e, None) == -1
+    assert L.moe_fp8_quantize_rows(e, 1, 128, e, e, None) == -1
+    assert L.moe_fp8_gemm(P, 1, 2, 128, 128, e, P, P, P, P, None) == -1
