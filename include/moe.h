@@ -106,7 +106,8 @@ enum {
  * forward products read Xp and W1 quantised along d, and A and W2 along I; the dgrad products dY
  * and W2 along d, and dH and W1 along 2I. The ring slot holds bf16 Xp as in BF16 mode, and the
  * weight gradients and dWr read bf16 operands. A is computed from the stored H, and dw and dH from
- * dA' rounded to bf16, each product's output. moe_quantize_weights is needed as in the MX modes.
+ * dA' rounded to bf16, each product's output. What is not finite stays so, as NaN. The call
+ * moe_quantize_weights is needed as in the MX modes.
  * MOE_FLAG_PERSISTENT and MOE_FLAG_MXFP8_WGRAD are not accepted, moe_forward_fused not provided.
  *
  * Weight-gradient precision. The pages do not say in which precision the weight gradients are
@@ -432,7 +433,8 @@ int moe_router_backward(const moe_cfg* cfg, const void* x, const void* w_router,
  * Block-scaled FP8: E4M3 codes with one fp32 scale per block of 128 along the reduction axis.
  * scale = amax / 448 and code = rne_e4m3(v * (448 / amax)), amax the block's largest magnitude
  * (a block of zeros: scale 1, codes 0; an amax below 2^-110 counts as 2^-110); the code stands for
- * code * scale. Inputs must be finite.
+ * code * scale. A value that is not finite gets the NaN code and takes no part in amax, so a product
+ * is NaN exactly where it reads one.
  *
  * moe_fp8_quantize_rows - rows of activations or gradients, a scale per 1 x 128.
  *   src    bf16 [rows, cols]          in, cols a multiple of 128

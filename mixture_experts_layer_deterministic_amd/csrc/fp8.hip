@@ -4,6 +4,8 @@
 // A block's scale is amax / 448 (1 for a block of zeros) and its codes are the values times
 // 448 / amax, rounded to nearest even: the largest magnitude lands on E4M3's largest, 448. An
 // amax below 2^-110 counts as 2^-110, so that neither quotient leaves fp32's normal numbers.
+// A value that is not finite gets the NaN code (E4M3 has no infinity) and takes no part in amax:
+// it spoils the sums it is in, and the codes beside it are as without it.
 // The product takes each 128-deep block from one MFMA in fp32, then adds it, times the two scales,
 // to the fp32 sum: out[p, n] = sum_kb sa[p, kb] sb[n / 128, kb] sum_k a[p, k] b[n, k].
 //
@@ -39,15 +41,28 @@ MOE_DEV void widen8(const uint4& x, float (&f)[8]) {
     f[2 * q + 1] = bf2f_hi(w[q]);
   }
 }
-MOE_DEV float amax8(const float (&f)[8]) {
-  float m = 0.f;
+// The largest finite magnitude of eight bf16 values. Magnitudes order as their bits; with 0x80
+// added those that are not finite (0x7f80 and above) become the negative 16-bit numbers.
+MOE_DEV float amax8(const uint4& x) {
+  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
+  typedef __attribute__((ext_vector_type(2))) short s16x2;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  s16x2 m = {0x80, 0x80};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
-  return m;
+  for (int q = 0; q < 4; ++q)
+    m = __builtin_elementwise_max(
+        m, __builtin_bit_cast(s16x2, __builtin_bit_cast(u16x2, w[q] & 0x7fff7fffu) +
+                                         u16x2{0x80, 0x80}));
+  return __uint_as_float((uint32_t)(max(m[0], m[1]) - 0x80) << 16);
+}
+// Two codes. No finite value of a block leaves E4M3's range: amax times 448 / amax, each rounded,
+// is at most 448 and a step, which rounds to 448. The conversion makes NaN of all that is not finite.
+MOE_DEV uint32_t code2(float a, float b) {
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false)) & 0xffffu;
 }
 MOE_DEV uint2 codes8(const float (&f)[8], float inv) {
-  return make_uint2(e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16),
-                    e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16));
+  return make_uint2(code2(f[0] * inv, f[1] * inv) | (code2(f[2] * inv, f[3] * inv) << 16),
+                    code2(f[4] * inv, f[5] * inv) | (code2(f[6] * inv, f[7] * inv) << 16));
 }
 
 // A workgroup quantises 32 rows x 512 columns: a wave takes a row's 512 columns at a time, eight
@@ -87,7 +102,7 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(
     const int r = r0 + wave * 8 + i;
     float f[8];
     widen8(x[i], f);
-    float amax = amax8(f);
+    float amax = amax8(x[i]);
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
     const BlockScale b = block_scale(amax);
@@ -128,7 +143,7 @@ __global__ void __launch_bounds__(256) fp8_swiglu_kernel(const uint16_t* __restr
   const uint4 a = make_uint4(w[0], w[1], w[2], w[3]);
   reinterpret_cast<uint4*>(A)[v] = a;
   widen8(a, f);
-  float amax = amax8(f);
+  float amax = amax8(a);
 #pragma unroll
   for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
   const BlockScale b = block_scale(amax);
@@ -178,7 +193,7 @@ __global__ void __launch_bounds__(256) fp8_swiglu_bwd_kernel(
     *reinterpret_cast<uint4*>(dH + at) = o;
     float f[8];
     widen8(o, f);
-    float amax = amax8(f);
+    float amax = amax8(o);
 #pragma unroll
     for (int x = 1; x < 16; x <<= 1) amax = fmaxf(amax, __shfl_xor(amax, x));
     const BlockScale b = block_scale(amax);
@@ -207,11 +222,7 @@ __global__ void __launch_bounds__(256) fp8_quant_weights_kernel(
     x[j] = *reinterpret_cast<const uint4*>(s + (size_t)(t / 16 + 16 * j) * K + cv * 8);
   float amax = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float f[8];
-    widen8(x[j], f);
-    amax = fmaxf(amax, amax8(f));
-  }
+  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, amax8(x[j]));
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
   if (t % 64 == 0) red[t / 64] = amax;

@@ -340,3 +340,71 @@ def test_no_rows_at_all():
         m.moe_fp8_quantize_rows(e(torch.bfloat16, 0, 100), 0, 100, e(F8, 0, 100),
                                 e(torch.float32, 0))
     torch.cuda.synchronize()
+
+
+BAD = (float("nan"), float("inf"), -float("inf"), -float("nan"))
+
+
+def _spoil(x, at):
+    """x with values that are not finite at the flat places `at`, and x with zeros there."""
+    bad, none = x.clone(), x.clone()
+    for i, p in enumerate(at):
+        bad.view(-1)[p], none.view(-1)[p] = BAD[i % 4], 0.0
+    return bad, none
+
+
+def _check_spoiled(q, s, rq, rs, at):
+    """Codes and scales are those of the block without its spoiled places, which hold NaN codes."""
+    np.testing.assert_array_equal(s.cpu().numpy(), rs)
+    got = _values(q).reshape(-1)
+    assert np.isnan(got[at]).all()
+    got[at] = 0.0
+    np.testing.assert_array_equal(got, rq.reshape(-1))
+
+
+def test_rows_with_values_that_are_not_finite():
+    R, C = 37, 640
+    _announce(f"[fp8] rows {R} x {C} with NaN and infinities")
+    x = _hard((R, C), torch.Generator().manual_seed(2))
+    at = list(range(5 * C, 5 * C + 128)) + [7 * C + 3, 7 * C + 130, 20 * C + 639, 36 * C + 200]
+    bad, none = _spoil(x, at)
+    q, s = _quant_rows(bad.to(DEV))
+    rq, rs = _ops.quantize(none.float().numpy(), 1)
+    _check_spoiled(q, s, rq, rs.T, at)
+
+
+def test_weights_with_values_that_are_not_finite():
+    E, N, K = 2, 256, 384
+    _announce(f"[fp8] weights {E} x {N} x {K} with NaN and infinities")
+    w = _hard((E, N, K), torch.Generator().manual_seed(3))
+    at = [0, 200 * K + 130, 255 * K + 383, N * K + 5 * K + 127, N * K + 5 * K + 128]
+    bad, none = _spoil(w, at)
+    q = torch.empty(E, N, K, dtype=F8, device=DEV)
+    s = torch.empty(E, N // 128, K // 128, device=DEV)
+    qt = torch.empty(E, K, N, dtype=F8, device=DEV)
+    st = torch.empty(E, K // 128, N // 128, device=DEV)
+    m.moe_fp8_quantize_weights(bad.to(DEV), E, N, K, q, s, qt, st)
+    rq, rs = _ops.quantize(none.float().numpy(), 128)
+    _check_spoiled(q, s, rq, rs, at)
+    _check_spoiled(qt.view(torch.uint8).transpose(1, 2).contiguous().view(F8),
+                   st.transpose(1, 2).contiguous(), rq, rs, at)
+
+
+@pytest.mark.parametrize("load", ["one", "single", "edges", "small", "big", "many"])
+def test_a_code_that_is_nan_spoils_its_own_row_or_column(load):
+    N, K = 256, 384
+    _announce(f"[fp8] product load={load} with NaN codes")
+    off, a, sa, b, sb = _problem(load, N, K, 9)
+    out = lambda: torch.full((a.shape[0], N), -7.0, dtype=torch.bfloat16, device=DEV)
+    e = next(i for i in range(len(off) - 1) if off[i + 1] > off[i])
+    p, n = int(off[-1]) - 1, 130
+    A, B = a.view(torch.uint8).clone(), b.view(torch.uint8).clone()
+    A[p, 200], B[e, n, 383] = 0, 0
+    ref = _run(off, A.view(F8), sa, B.view(F8), sb, out())
+    A[p, 200], B[e, n, 383] = 0xFF, 0x7F
+    got = _run(off, A.view(F8), sa, B.view(F8), sb, out())
+    spoiled = np.zeros(got.shape, bool)
+    spoiled[p] = True
+    spoiled[off[e]:off[e + 1], n] = True
+    assert np.isnan(got[spoiled]).all()
+    np.testing.assert_array_equal(got[~spoiled], ref[~spoiled])

@@ -215,3 +215,41 @@ def test_fp8_mode_skips_bad_expert_indices():
     assert_grad("Y", _np(L.y), ref["Y"], TOL_ACT)
     assert_grad("dX", _np(L.dx), ref["dX"], TOL_ACT)
     assert_grad("dW1", _np(L.dw1), ref["dW1"], TOL_GRAD)
+
+
+def test_fp8_mode_keeps_what_is_not_finite():
+    """A NaN or an infinity of a token, or of a gradient, comes out as NaN at that token (and not
+    finite in its experts' weight gradients), and changes no other; a weight's at its expert."""
+    s = SHAPES["tiny"]
+    inp = _inputs("tiny", seed=9)
+    g = torch.Generator().manual_seed(1)
+    idx = torch.rand(s["T"], s["E"], generator=g).topk(s["k"], dim=1).indices.to(torch.int32)
+
+    def step(X, W1, dY):
+        L = _layer("tiny", precision=m.MOE_PREC_FP8)
+        L.quantize_weights(W1, inp["W2"])
+        L.set_routing(idx.to(DEV), torch.full((s["T"], s["k"]), 0.5, device=DEV))
+        L.step(X, None, W1, inp["W2"], dY)
+        torch.cuda.synchronize()
+        return L
+
+    clean = step(inp["X"], inp["W1"], inp["dY"])
+    X, dY, W1 = inp["X"].clone(), inp["dY"].clone(), inp["W1"].clone()
+    X[5, 17], X[100, 3], dY[30, 200] = float("nan"), float("inf"), -float("inf")
+    L = step(X, inp["W1"], dY)
+    t = torch.arange(s["T"], device=DEV)
+    fwd = (t == 5) | (t == 100)
+    bwd = fwd | (t == 30)
+    for got, ref, bad in ((L.y, clean.y, fwd), (L.dx, clean.dx, bwd),
+                          (L.d_topk_w, clean.d_topk_w, bwd)):
+        assert got[bad].isnan().all() and torch.equal(got[~bad], ref[~bad])
+    for e in range(s["E"]):
+        hit = bool((idx[[5, 100, 30]] == e).any())
+        for got, ref in ((L.dw1, clean.dw1), (L.dw2, clean.dw2)):
+            assert bool(got[e].isfinite().all()) != hit
+            assert hit or torch.equal(got[e], ref[e])
+    W1[2, 40, 9] = float("nan")
+    L = step(inp["X"], W1, inp["dY"])
+    bad = (idx == 2).any(1).to(DEV)
+    for got, ref in ((L.y, clean.y), (L.dx, clean.dx)):
+        assert got[bad].isnan().all() and torch.equal(got[~bad], ref[~bad])
