@@ -15,6 +15,7 @@
 // result in rms, 300 times less than the bf16 rounding of the output; bf16 MFMAs of the widened
 // codes would keep 1e-8 at half the rate.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.h"
@@ -984,9 +985,13 @@ hipError_t launch_fp8_quant_weights(const uint16_t* src, int E, int N, int K, ui
 // rows spread evenly, N x K = 4096 x 7168 where not said:
 //  * up to 128 tiles, rows few: narrow. E = 1, 32 rows 17 (128-row tiles 34); E = 4, 16 rows an
 //    expert 20 (36). At 256 tiles level: E = 8, 16 rows 39 (42), 64 rows 66 (62).
-//  * 513 to 1024 tiles, up to 16 rows an expert: 32-row tiles, which then all run at once. 7168 x
-//    2048, 11 of 16 experts with 24 rows 30.7 (128-row tiles 33.5). Fewer tiles: E = 8, 16 rows 53
-//    (42); more: E = 256, 16 rows 1163 (1155).
+//  * up to 16 rows an expert and 513 to 704 tiles with rows in them: 32-row tiles. 128-row tiles run
+//    two a CU, and their second round is then nearly empty. All with rows, 2 or 16 an expert: 512
+//    tiles level (69 and 70 both), 520 81 (128-row tiles 99 and 100), 640 90 and 93 (107 and 111);
+//    768 102 and 127 (112 and 118), 896 132 and 137 (120 and 131), 1024 141 and 147 (135 and 145).
+//    The host counts the experts that have rows as if M rows were dealt at random: 7168 x 2048, 24
+//    rows on 11 of 16 experts 30.7 (33.5); 6144 x 7168, 32 on 13 of 16 86 (106), 64 on all 16 123 (112).
+//    A load less even than that is not seen: 64 of those rows on 13 experts take 105 (32-row tiles 86).
 //  * up to 112 rows an expert: 128-row tiles. E = 64, 96 rows 369 (256 x 256 tiles 463). Above, an
 //    expert's rows begin to need a second tile and its weights a second read: 160 rows 710 (482).
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s) {
@@ -995,12 +1000,13 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s) {
     return dim3((n + kXcds - 1) / kXcds * kXcds);
   };
   const long long M = a.M, E = a.E, tiles = E * (a.N / kQB);
+  const double busy = (double)tiles * -std::expm1(-(double)M / (double)E);
   TraceScope trace("fp8_gemm", s);
   if (tiles <= kCus / 2 && M <= 32)
     hipLaunchKernelGGL(fp8_narrow_kernel<2>, grid(32, 32), dim3(64), 0, s, a);
   else if (tiles <= kCus / 2 && M <= 64 * E)
     hipLaunchKernelGGL(fp8_narrow_kernel<4>, grid(64, 32), dim3(64), 0, s, a);
-  else if (tiles > 2 * kCus && tiles <= 4 * kCus && M <= 16 * E)
+  else if (busy > 2 * kCus && busy <= 2.75 * kCus && M <= 16 * E)
     hipLaunchKernelGGL(fp8_stream_kernel<32>, grid(32, kQB), dim3(256), 0, s, a);
   else if (M <= 112 * E)
     hipLaunchKernelGGL(fp8_stream_kernel<128>, grid(128, kQB), dim3(256), 0, s, a);
