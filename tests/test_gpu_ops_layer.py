@@ -253,3 +253,34 @@ def test_fp8_mode_keeps_what_is_not_finite():
     bad = (idx == 2).any(1).to(DEV)
     for got, ref in ((L.y, clean.y), (L.dx, clean.dx)):
         assert got[bad].isnan().all() and torch.equal(got[~bad], ref[~bad])
+
+
+# Products that the shapes above leave out: 128-row tiles (256 column tiles and more, few rows an
+# expert), and 32-row tiles (640 of them, nearly all with rows) with 128-row ones in the backward.
+SHAPES["many_experts"] = dict(T=150, d=512, E=64, k=2, I=256)
+SHAPES["wide"] = dict(T=128, d=256, E=64, k=2, I=640)
+
+
+@pytest.mark.parametrize("bf16_dw", [False, True])
+@pytest.mark.parametrize("shape", ["many_experts", "wide", "ragged"])
+def test_fp8_mode_accumulates_in_either_gradient_type(shape, bf16_dw):
+    """Both gradient types, written and then added to: the second backward doubles them (in bf16
+    within a rounding of each, far below the bar)."""
+    _announce(f"[fp8 layer] {shape} {SHAPES[shape]} bf16_dw={bf16_dw}")
+    inp = _inputs(shape, seed=10)
+    L = _layer(shape, precision=m.MOE_PREC_FP8, bf16_dw=bf16_dw)
+    L.quantize_weights(inp["W1"], inp["W2"])
+    L.route(inp["X"], inp["Wr"])
+    L.permute(inp["X"])
+    L.forward(inp["W1"], inp["W2"])
+    ref = _ops.fp8_layer(*(_np(inp[n]).astype(np.float64) for n in ("X", "W1", "W2", "dY")),
+                         _np(L.topk_idx), _np(L.topk_w))
+    for times in (1, 2):
+        L.backward(None, inp["W1"], inp["W2"], inp["dY"], accumulate=times == 2)
+        torch.cuda.synchronize()
+        assert L.dw1.dtype == L.dw2.dtype == (torch.bfloat16 if bf16_dw else torch.float32)
+        assert_grad("dW1", _np(L.dw1), times * ref["dW1"], TOL_GRAD)
+        assert_grad("dW2", _np(L.dw2), times * ref["dW2"], TOL_GRAD)
+    assert_grad("Y", _np(L.y), ref["Y"], TOL_ACT)
+    assert_grad("dX", _np(L.dx), ref["dX"], TOL_ACT)
+    assert_grad("d_topk_w", _np(L.d_topk_w), ref["dw"], TOL_GRAD)
