@@ -442,6 +442,7 @@ int moe_router_backward(const moe_cfg* cfg, const void* x, const void* w_router,
  *   scales fp32 [cols / 128, rows]    out: one row of scales per 128 columns, so that the product
  *                                     reads a step's scales of consecutive rows together
  * rows 0 enqueues nothing; the three pointers may then be NULL.
+ * Errors: MOE_ERR_INVALID_ARG, also where ceil(rows / 32) * ceil(cols / 512) >= 2^24.
  */
 int moe_fp8_quantize_rows(const void* src, int32_t rows, int32_t cols, void* codes, float* scales,
                           moe_stream_t stream);

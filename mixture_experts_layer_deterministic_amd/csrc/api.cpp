@@ -814,7 +814,8 @@ int moe_fp8_quantize_rows(const void* src, int32_t rows, int32_t cols, void* cod
   if (rows < 0 || cols < 128 || cols % 128 != 0) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;  // empty buffers have no address to check
   if (!aligned16(src) || !aligned16(codes) || !aligned4(scales)) return MOE_ERR_INVALID_ARG;
-  if ((long long)rows * cols / 2048 >= (1LL << 31)) return MOE_ERR_INVALID_ARG;  // the grid
+  // the grid: a workgroup for 32 rows x 512 columns, and fewer than 2^32 threads
+  if ((rows + 31LL) / 32 * ((cols + 511LL) / 512) >= (1LL << 24)) return MOE_ERR_INVALID_ARG;
   if (const int st = check_device()) return st;
   Launches L;
   L(launch_fp8_quant_rows(static_cast<const uint16_t*>(src), rows, cols,

@@ -249,3 +249,11 @@ def test_fp8_calls_take_empty_rows():
     assert L.moe_fp8_gemm(P, 0, 2, 100, 128, e, e, P, P, e, None) == -1
     assert L.moe_fp8_quantize_rows(e, 1, 128, e, e, None) == -1
     assert L.moe_fp8_gemm(P, 1, 2, 128, 128, e, P, P, P, P, None) == -1
+
+
+def test_quantize_rows_refuses_a_grid_of_more_threads_than_a_launch_takes():
+    L = m.lib()
+    for rows, cols in ((2 ** 29, 128), (2 ** 29 - 31, 512), (2 ** 28, 640), (2 ** 22, 2 ** 16)):
+        assert L.moe_fp8_quantize_rows(P, rows, cols, P, P, None) == -1
+    if torch.cuda.device_count() == 0:  # a GPU would run it
+        assert L.moe_fp8_quantize_rows(P, 2 ** 29 - 32, 128, P, P, None) == -4
