@@ -57,7 +57,7 @@ MOE_DEV float amax8(const uint4& x) {
   return __uint_as_float((uint32_t)(max(m[0], m[1]) - 0x80) << 16);
 }
 // Two codes. No finite value of a block leaves E4M3's range: amax times 448 / amax, each rounded,
-// is at most 448 and a step, which rounds to 448. The conversion makes NaN of all that is not finite.
+// is at most 448 and a step, which rounds to 448. The conversion makes NaN of what is not finite.
 MOE_DEV uint32_t code2(float a, float b) {
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false)) & 0xffffu;
 }
@@ -70,7 +70,7 @@ MOE_DEV uint2 codes8(const float (&f)[8], float inv) {
 // values a lane and sixteen lanes a block, eight rows one after the other with all their loads
 // out at once. The scales of 32 consecutive rows leave as one 128-byte line: with one row a
 // wave, each scale was a 4-byte store of its own to a line that workgroups on other XCDs wrote
-// too. HBM bounds it: 16384 x 7168 in 57 us, 6.2 TB/s, two thirds of it reads.
+// too. HBM bounds it: 16384 x 7168 in 58 us, 6.1 TB/s, two thirds of it reads.
 // GATHER, in the layer: row pos of dY in position order, dy[row_src[pos] / k], for the rows
 // before `placed` (skipped bad-index rows leave some; those are neither read nor written).
 constexpr int kQRows = 32, kQCols = 512;
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(
     const bool live = on && r < end;
     const size_t at = GATHER ? (size_t)((live ? row_src[r] : 0) / k) : (size_t)r;
     const uint16_t* p = src + at * cols + c;
-    // rows are read once: past the caches (66 -> 57 us); dY's rows k times
+    // rows are read once: past the caches (66 -> 57 us a call); dY's rows k times
     x[i] = !live    ? make_uint4(0, 0, 0, 0)
            : GATHER ? *reinterpret_cast<const uint4*>(p)
                     : nt_load16(p);
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(
 //
 // A = silu(g) u from the stored H = [g | u], rounded to bf16 and quantised from that. A thread
 // takes eight columns and sixteen threads a block, all in registers, so HBM bounds it: 16384 x
-// 2048 (2048 tokens, k = 8) in 41 us, 5.6 TB/s with the codes.
+// 2048 (2048 tokens, k = 8) in 42 us, 5.6 TB/s with the codes.
 __global__ void __launch_bounds__(256) fp8_swiglu_kernel(const uint16_t* __restrict__ H,
                                                          const int32_t* __restrict__ placed, int M,
                                                          int I, uint16_t* __restrict__ A,
@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(256) fp8_swiglu_bwd_kernel(
 }
 
 // One workgroup per 128 x 128 block, which it reads once; the transposed copy goes through LDS.
-// HBM bounds it: 8 x 4096 x 7168 with both copies in 177 us, 5.3 TB/s, half reads. (Transposes
-// of 8 x 8 in registers instead of byte reads: 178.6.)
+// HBM bounds it: 8 x 4096 x 7168 with both copies in 180 us, 5.2 TB/s, half reads. (Transposes
+// of 8 x 8 in registers instead of byte reads: 178.6 a call where these took 177.)
 __global__ void __launch_bounds__(256) fp8_quant_weights_kernel(
     const uint16_t* __restrict__ src, int N, int K, uint8_t* __restrict__ codes,
     float* __restrict__ scales, uint8_t* __restrict__ codes_t, float* __restrict__ scales_t) {
@@ -340,7 +340,7 @@ constexpr int kLgkm0 = 0xc07f;     // lgkmcnt(0) alone
 //  * BM = 32, two weight stages: 40 KB, four workgroups a CU with as much on their way.
 // Tiles are dealt to the XCDs one by one: the column tiles of one expert run side by side on
 // different XCDs (one XCD's consecutive tiles at a time: 1483 us against 1453 at 256 experts of 64
-// rows). HBM bounds it: 256 experts of 64 rows, 4096 x 7168, in 1.40 ms, 5.6 TB/s.
+// rows). HBM bounds it: 256 experts of 64 rows, 4096 x 7168, in 1.39 ms, 5.6 TB/s.
 // Weights that one row tile reads go past the caches (nt) up to 64 rows, where it pays
 // (32 rows an expert 1274 -> 1207 us; 96 rows 1503 -> 1556).
 // A tile's K loop is compiled for 2, 4, 6 and 8 blocks of 16 rows and runs the least that hold its
@@ -651,9 +651,9 @@ __global__ void __launch_bounds__(64, 1) fp8_narrow_kernel(const Fp8GemmArgs a) 
 // loads at the end of read k.1, in phase 4k + 2 or 4k + 3; it is read from 4k + 4 on. Every wave
 // runs the same code, the late ones behind one more barrier.
 //
-// 16384 rows over 5 of 8 experts, 4096 x 7168: 447 us, 2.15 PFLOP/s (128-row tiles above: 682).
+// 16384 rows over 5 of 8 experts, 4096 x 7168: 456 us, 2.11 PFLOP/s (128-row tiles above: 682).
 // A library product of that size with one scale an operand takes 375; without the block scales
-// this kernel takes 422. The MFMAs are busy 59% of the time that tiles run; the rest is the
+// this kernel took 422 a call where it took 445. The MFMAs are busy 59% of the time that tiles run; the rest is the
 // phases' ends, a tile's first loads and its epilogue, and the last round.
 constexpr int kBigT = 256;
 constexpr int kCus = 256;                             // MI355X; tiles that run at once
@@ -974,8 +974,8 @@ hipError_t launch_fp8_quant_weights(const uint16_t* src, int E, int N, int K, ui
                                     hipStream_t s) {
   {
     TraceScope trace("fp8_quant_weights", s);
-    hipLaunchKernelGGL(fp8_quant_weights_kernel, dim3((unsigned)(K / kQB) * (N / kQB), E), dim3(256), 0, s, src,
-                       N, K, codes, scales, codes_t, scales_t);
+    hipLaunchKernelGGL(fp8_quant_weights_kernel, dim3((unsigned)(K / kQB) * (N / kQB), E),
+                       dim3(256), 0, s, src, N, K, codes, scales, codes_t, scales_t);
   }
   return hipGetLastError();
 }
@@ -985,13 +985,14 @@ hipError_t launch_fp8_quant_weights(const uint16_t* src, int E, int N, int K, ui
 // rows spread evenly, N x K = 4096 x 7168 where not said:
 //  * up to 128 tiles, rows few: narrow. E = 1, 32 rows 17 (128-row tiles 34); E = 4, 16 rows an
 //    expert 20 (36). At 256 tiles level: E = 8, 16 rows 39 (42), 64 rows 66 (62).
-//  * up to 16 rows an expert and 513 to 704 tiles with rows in them: 32-row tiles. 128-row tiles run
-//    two a CU, and their second round is then nearly empty. All with rows, 2 or 16 an expert: 512
-//    tiles level (69 and 70 both), 520 81 (128-row tiles 99 and 100), 640 90 and 93 (107 and 111);
-//    768 102 and 127 (112 and 118), 896 132 and 137 (120 and 131), 1024 141 and 147 (135 and 145).
-//    The host counts the experts that have rows as if M rows were dealt at random: 7168 x 2048, 24
-//    rows on 11 of 16 experts 30.7 (33.5); 6144 x 7168, 32 on 13 of 16 86 (106), 64 on all 16 123 (112).
-//    A load less even than that is not seen: 64 of those rows on 13 experts take 105 (32-row tiles 86).
+//  * up to 16 rows an expert and 513 to 704 tiles with rows in them: 32-row tiles. 128-row tiles
+//    run two a CU, and their second round is then nearly empty. All with rows, 2 or 16 an expert:
+//    512 tiles level (69 and 70 both), 520 81 (128-row tiles 99 and 100), 640 90 and 93 (107 and
+//    111); 768 102 and 127 (112 and 118), 896 132 and 137 (120 and 131), 1024 141 and 147 (135 and
+//    145). The host counts the experts that have rows as if M rows were dealt at random: 7168 x
+//    2048, 24 rows on 11 of 16 experts 30.7 (33.5); 6144 x 7168, 32 on 13 of 16 86 (106), 64 on all
+//    16 123 (112). A load less even than that is not seen: 64 of those rows on 13 experts take 105
+//    (32-row tiles 86).
 //  * up to 112 rows an expert: 128-row tiles. E = 64, 96 rows 369 (256 x 256 tiles 463). Above, an
 //    expert's rows begin to need a second tile and its weights a second read: 160 rows 710 (482).
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s) {

@@ -115,7 +115,7 @@ MOE_DEV double exp64(double x) {
   const double t = __builtin_fma(x, 1.4426950408889634, 6755399441055744.0);
   const double n = t - 6755399441055744.0;
   double r;
-  if constexpr (DEGREE == 12) {  // ln 2 in two parts, n times the first exact
+  if constexpr (DEGREE == 12) {  // ln 2 cut to 33 bits, n times which is exact, and the rest
     r = __builtin_fma(n, -6.93147180369123816490e-01, x);
     r = __builtin_fma(n, -1.90821492927058770002e-10, r);
   } else {
@@ -262,11 +262,13 @@ MOE_DEV int pick_candidates(const U (&key)[V], uint32_t least, int k, int lane,
 // LOGIT: the scores order as the logits do; 32-bit keys, and 64-bit scores only of the chosen.
 // Groups that are whole, aligned runs of 2^i lanes are scored by lane exchanges, others in LDS.
 //
-// 18944 x 512, softmax, k = 10: 16.8 us, 2.3 TB/s of logits. Vector issue bounds it (450
-// instructions a token, a third of them the row's 64-bit exponentials; 85 - 90% of the time). k
-// rounds of the wave's maximum over lanes of sorted keys, in place of the list, took 23.6. 16,
-// 2048 and 18944 tokens of 256 with 8 groups, sigmoid and bias: 4.9 and 6.3 us, a chain of
-// latencies, and 21.4, vector issue again (rounds: 5.3, 6.8 and 29.4).
+// 18944 x 512, softmax, k = 10: 19.2 us (the profiler's median; 16.7 a call in a run of calls), 2.0
+// TB/s of logits. Vector issue bounds it (460 instructions a token, a third of them the row's
+// 64-bit exponentials; 85 - 90% of the time). 16, 2048 and 18944 tokens of 256 with 8 groups,
+// sigmoid and bias: 4.9 and 6.1 us, a chain of latencies, and 23.4 (21.9 a call), vector issue
+// again: a 64-bit exponential and reciprocal for every expert. k rounds of the wave's maximum over
+// lanes of sorted keys, in place of the list, took 23.6 a call where this takes 16.7, and 5.3, 6.8
+// and 29.4.
 template <int V, bool LOGIT>
 __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
     GateParams p, const float* __restrict__ logits, const float* __restrict__ bias, int T, int E,
@@ -490,8 +492,8 @@ __global__ void __launch_bounds__(kGateWaves* kWave) gate_select_kernel(
 // pieces. Slots that name one expert twice (found by each slot writing its number to its
 // expert's place and reading it back) are added one after the other, in ascending j; a slot
 // outside [0, E) counts nothing. DENSE, softmax without renorm, also reads the row of logits.
-// 18944 x 512, every logit: 16 us, 4.9 TB/s, HBM's rate for as much read as written (a large copy
-// does 4.65). 2048 x 256, sigmoid: 3.6 us, the launch and one chain of loads.
+// 18944 x 512, every logit: 16.7 us, 4.7 TB/s, HBM's rate for as much read as written (a large copy
+// does 4.65). 2048 x 256, sigmoid: 3.5 us, the launch and one chain of loads.
 template <int V, bool DENSE>
 __global__ void __launch_bounds__(kGateWaves* kWave) gate_backward_kernel(
     GateParams p, const float* __restrict__ logits, const int32_t* __restrict__ idx,

@@ -7,7 +7,12 @@
 // (1/16 of bf16's) do not reach. Cutting a value's upper 8 bits off, then the next 8 of what is
 // left, gives three parts that add up to all its 24 bits: dWr, an fp32 sum, takes the three. dx
 // is rounded to bf16 (2^-8) at the end and takes two, both rounded to nearest: of x in [1, 2) the
-// first leaves at most 2^-8 and the second at most 2^-17 of that.
+// first leaves at most 2^-8 and the second at most 2^-17 of that. Those 2^-17 of a term stay below
+// the output's own rounding unless the terms cancel to 2^-9 of their size, and Wr, itself bf16,
+// does not hold values that agree so far and differ: a dense softmax's gradients, whose rows sum to
+// 0, against weights whose common part is 100 (300) times their spread give dx an error of 1.68e-3
+// (1.81e-3), an fp32 product rounded to bf16 1.66e-3. Three parts for dx, both gradients of 2048 x
+// 7168 x 256 with the copies around them: 57 -> 66 us; of 1777 x 4096 x 509: 41 -> 56.
 #include "common.h"
 #include "kernels.h"
 #include "ops.h"
@@ -73,9 +78,11 @@ MOE_DEV uint4 kmajor_frag64(const uint16_t* s, int base, int kb, int lane) {
 // the MFMAs through the transposing read; so does dl for dWr, whose reduction axis is the slow
 // one of both.
 //
-// Both gradients of 2048 x 7168 x 256, five bf16 products of 7.5 GFLOP: 41 us, 0.9 PFLOP/s, of
-// 1.2 that a large library product reaches. A step's fragment reads (20 KB a wave for 48 MFMAs)
-// and its split tile's writes keep LDS as busy as the MFMAs, and dx's tiles end in a part round.
+// Both gradients of 2048 x 7168 x 256, five bf16 products of 7.5 GFLOP: 44.5 us, 0.84 PFLOP/s, of
+// 1.2 that a large library product reaches. A step's fragment reads (20 KB a wave for 48 MFMAs of
+// dWr, 16 KB for 32 of dx) and its split tile's writes keep LDS as busy as the MFMAs, and dx's
+// tiles end in a part round. 256 x 128 tiles of dx, 64 x 64 outputs a wave, would read less and fit
+// the same LDS, but take 156 registers of the 128 that two workgroups a CU leave a wave.
 constexpr int kRgLdsW = 3 * 64 * kRgK + kRgK * kRgN;   // values of one half's stage
 constexpr int kRgLdsX = 2 * 128 * kRgK + kRgK * kRgN;
 constexpr int kRgLds = 2 * kRgLdsW;
@@ -230,16 +237,17 @@ __global__ void __launch_bounds__(512, 4) router_backward_kernel(const RouterGra
   }
 }
 
-// dWr where experts x columns are few and tokens many: tiles of 16 MB experts x 16 NB columns, whose
-// 16 waves split the tokens, steps of 32 in turn. Operands go from memory to registers in whole
-// pieces and never through LDS, and no wave waits for another: lane l = 16 g + r loads, i = 0 .. 7,
+// dWr where experts x columns are few and tokens many: tiles of 16 MB experts x 16 NB columns,
+// whose 16 waves split the tokens, steps of 32 in turn. Operands go from memory to registers in
+// whole pieces and never through LDS, and no wave waits for another: lane l = 16 g + r loads, i =
+// 0 .. 7,
 //  * of x token 8 g + i, columns NB r .. NB r + NB - 1: those 8 x NB values are the lane's parts of
 //    NB fragments once pairs of tokens are woven (one byte permutation a register), fragment n's
 //    column r standing for column NB r + n of the tile;
 //  * of dl token 8 g + i, experts MB r .. MB r + MB - 1: likewise MB fragments.
 // The waves' sums are added in LDS in a fixed order.
-// 8 experts, 16384 x 4096: 49 us, 2.7 TB/s of x, bound by the latency of a wave's one step ahead;
-// 128 experts, 8192 x 4096: 43 us, 0.6 PFLOP/s in three products, bound by the vector work of
+// 8 experts, 16384 x 4096: 48 us, 2.8 TB/s of x, bound by the latency of a wave's one step ahead;
+// 128 experts, 8192 x 4096: 46 us, 0.56 PFLOP/s in three products, bound by the vector work of
 // splitting and weaving. (The 64 x 128 tiles: 233 and 121, on 32 and 64 CUs.)
 constexpr int kFewWaves = 16;
 // A number the compiler has to take as new: sums with it are made where they are used, since kept

@@ -7,9 +7,9 @@ from __future__ import annotations
 import torch
 
 from . import (MOE_FLAG_BF16_DW, MOE_FLAG_MXFP8_WGRAD, MOE_FLAG_PERSISTENT, MOE_PREC_BF16,
-               MOE_PREC_MXFP4, MOE_PREC_MXFP8, make_cfg, moe_backward, moe_forward, moe_forward_fused,
-               moe_gate_backward, moe_permute, moe_query, moe_quantize_weights, moe_route,
-               moe_route_gated, moe_router_backward)
+               MOE_PREC_MXFP4, MOE_PREC_MXFP8, make_cfg, moe_backward, moe_forward,
+               moe_forward_fused, moe_gate_backward, moe_permute, moe_query, moe_quantize_weights,
+               moe_route, moe_route_gated, moe_router_backward)
 
 
 class MoeLayer:
@@ -24,7 +24,8 @@ class MoeLayer:
 
     With ``gate`` (from ``make_gate``) the layer routes by that gate instead of the renormalised
     top-k softmax, with ``gate_bias`` (fp32 [E], or None) in its choice, and backward takes the
-    router's gradients through it; ``dlogits`` holds the logits' gradient.
+    router's gradients through it; ``dlogits`` holds the logits' gradient. The single-launch
+    forward has no gate, and refuses one.
     """
 
     def __init__(self, T, d, E, k, I, device="cuda", ring_slots=1, persistent=False,
