@@ -327,6 +327,9 @@ MOE_DEV void fp8_load_lds(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff
 // The chunk a lane fetches into its place of those 8 rows.
 MOE_DEV uint32_t fp8_piece(int lane) { return 16u * ((lane % 8) ^ (lane / 8)); }
 
+// Behind it no load goes out before those in front of it: what a counted wait relies on.
+MOE_DEV void loads_in_order() { __builtin_amdgcn_sched_barrier(0x40f); }  // arithmetic may pass
+
 constexpr int kVm4Lgkm0 = 0x0074;  // s_waitcnt vmcnt(4) lgkmcnt(0)
 constexpr int kVm0Lgkm0 = 0x0070;
 constexpr int kLgkm0 = 0xc07f;     // lgkmcnt(0) alone
@@ -408,6 +411,7 @@ struct StreamTile {
     for (int mb = 0; mb < NMB; ++mb) s[mb] = __shfl(sv[mb / 4], mb % 4 * 16 + r16) * sbk;
     issue_a<(S + 1) % 2>(L, kb + 1);
     issue_s(kb + 1);
+    loads_in_order();
     issue_b<(S + SB - 1) % SB>(L, kb + SB - 1);
     __builtin_amdgcn_sched_barrier(0);
     const uint8_t* A = L.template a<S % 2>();
@@ -456,6 +460,7 @@ struct StreamTile {
     issue_b<0>(L, 0);
     issue_a<0>(L, 0);
     issue_s(0);
+    loads_in_order();
     if constexpr (SB == 3) issue_b<1>(L, 1);
     // whole cycles of the stages, then the rest: a loop left from its middle would hold two sets
     // of accumulators
@@ -591,7 +596,10 @@ struct NarrowTile {
 #pragma unroll
     for (int i = 0; i < NMB; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < NS; ++i) issue(st[i], i);
+    for (int i = 0; i < NS; ++i) {
+      issue(st[i], i);
+      loads_in_order();
+    }
     int kb = 0;
     for (; kb + NS <= nK; kb += NS) steps<0, NS>(st, kb, NS);
     steps<0, NS - 1>(st, kb, nK - kb);
