@@ -661,8 +661,8 @@ __global__ void __launch_bounds__(64, 1) fp8_narrow_kernel(const Fp8GemmArgs a) 
 //
 // 16384 rows over 5 of 8 experts, 4096 x 7168: 456 us, 2.11 PFLOP/s (128-row tiles above: 682).
 // A library product of that size with one scale an operand takes 375; without the block scales
-// this kernel took 422 a call where it took 445. The MFMAs are busy 59% of the time that tiles run; the rest is the
-// phases' ends, a tile's first loads and its epilogue, and the last round.
+// this kernel took 422 a call where it took 445. The MFMAs are busy 59% of the time that tiles run;
+// the rest is the phases' ends, a tile's first loads and its epilogue, and the last round.
 constexpr int kBigT = 256;
 constexpr int kCus = 256;                             // MI355X; tiles that run at once
 constexpr int kBigCodes = kBigT * 128;                // one operand's codes of a step

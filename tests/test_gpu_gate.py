@@ -372,3 +372,18 @@ def test_softmax_scores_that_underflow_weigh_nothing():
         _check_select(l, k, 0, bias, G, tg, 1, renorm, 2.5)
     idx, w = _select(l, k, m.make_gate(0, 1, 1, 0, True, 1.0), bias)
     assert sorted(idx[0]) == list(range(10, 15)) and not w[0].any() and not w[1].any()
+
+
+@pytest.mark.parametrize("G,tg", [(8, 3), (48, 30), (96, 40)])
+def test_saturated_sigmoids_between_groups(G, tg):
+    """Sigmoids that are 1 in 64 bits: groups whose sums are equal go by their index, and so do
+    the experts in them, whatever their logits."""
+    _announce(f"[gate] G={G} topk_groups={tg}, saturated sigmoids")
+    l = _logits(3, 96, 22)
+    l[0] = 60.0 + np.arange(96, dtype=np.float32)
+    l[1, ::5] = 38.0 + np.arange(20, dtype=np.float32)
+    l[2] = 60.0 + np.arange(96, dtype=np.float32)
+    l[2, :24] = -inf
+    for gsc, renorm in itertools.product((0, 1), (False, True)):
+        _check_select(l, 8, 1, None, G, tg, gsc, renorm, 1.0)
+        _check_select(l, 8, 1, np.zeros(96, np.float32), G, tg, gsc, renorm, 1.0)
