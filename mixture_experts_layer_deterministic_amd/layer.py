@@ -7,7 +7,7 @@ from __future__ import annotations
 import torch
 
 from . import (MOE_FLAG_BF16_DW, MOE_FLAG_MXFP8_WGRAD, MOE_FLAG_PERSISTENT, MOE_PREC_BF16,
-               MOE_PREC_MXFP4, MOE_PREC_MXFP8, make_cfg, moe_backward, moe_forward,
+               MOE_PREC_MXFP4, MOE_PREC_MXFP8, _dev, make_cfg, moe_backward, moe_forward,
                moe_forward_fused, moe_gate_backward, moe_permute, moe_query, moe_quantize_weights,
                moe_route, moe_route_gated, moe_router_backward)
 
@@ -145,6 +145,9 @@ class MoeLayer:
                 raise ValueError("a given routing has no logits to take a gate's gradients at")
             if x is None:
                 raise ValueError("a gated layer's router gradients need x")
+            # refused before the experts' gradients are written or added to
+            _dev("MoeLayer.backward", stream, (x, torch.bfloat16, self.T * self.d),
+                 (w_router, torch.bfloat16, self.E * self.d))
             self.backward(None, w1, w2, dy, slot, accumulate, saved, stream)
             moe_gate_backward(self.cfg, self.gate, self.logits, self.topk_idx, self.d_topk_w,
                               self.dlogits, False, stream)

@@ -284,3 +284,16 @@ def test_fp8_mode_accumulates_in_either_gradient_type(shape, bf16_dw):
     assert_grad("Y", _np(L.y), ref["Y"], TOL_ACT)
     assert_grad("dX", _np(L.dx), ref["dX"], TOL_ACT)
     assert_grad("d_topk_w", _np(L.d_topk_w), ref["dw"], TOL_GRAD)
+
+
+def test_gated_backward_refuses_tokens_before_it_adds_gradients():
+    inp = _inputs("tiny", seed=11)
+    L = _step(_layer("tiny", gate=m.make_gate(m.MOE_SCORE_SIGMOID)), inp)
+    before = _results(L)
+    for x, wr in ((inp["X"].float(), inp["Wr"]), (inp["X"][:9], inp["Wr"]),
+                  (inp["X"], inp["Wr"].cpu()), (inp["X"], inp["Wr"].t())):
+        with pytest.raises(m.MoeError):
+            L.backward(wr, inp["W1"], inp["W2"], inp["dY"], accumulate=True, x=x)
+    torch.cuda.synchronize()
+    for a, b in zip(_results(L), before):
+        assert torch.equal(a, b)
