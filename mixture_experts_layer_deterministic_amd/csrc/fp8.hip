@@ -21,6 +21,7 @@
 #include "common.h"
 #include "kernels.h"
 #include "ops.h"
+#include "tiles8.h"
 
 namespace moe {
 namespace {
@@ -261,49 +262,6 @@ __global__ void __launch_bounds__(256) fp8_quant_weights_kernel(
 // ------------------------------------------------------------------------------------------
 // The product
 
-// Row tiles without a table. Expert e's tiles take the slots from offsets[e] / BM + e on: the
-// next expert's first slot is at least that plus ceil(rows / BM), since floor((o + c) / BM) + 1
-// >= floor(o / BM) + ceil(c / BM). M / BM + E slots hold every tile, whatever the load; a slot
-// finds its expert from the offsets alone, and the ones between two experts' tiles do nothing.
-struct RowTile {
-  int e, row0, rows;  // rows <= 0: nothing to do
-};
-template <int BM>
-MOE_DEV RowTile find_rows(const int32_t* __restrict__ offsets, int M, int E, int slot) {
-  // the last expert whose first slot is at most this one: starts ascend, so it is a count
-  const int lane = threadIdx.x % kWave;
-  int n = 0;
-  for (int e0 = 0; e0 < E; e0 += kWave) {
-    const int e = e0 + lane;
-    const bool le = e < E && min(max(offsets[e], 0), M) / BM + e <= slot;
-    const int c = __popcll(__ballot(le));
-    n += c;
-    if (c < kWave) break;
-  }
-  RowTile t{0, 0, 0};
-  n = __builtin_amdgcn_readfirstlane(n);
-  if (n == 0) return t;  // offsets[0] > 0, and no expert starts this early
-  t.e = n - 1;
-  const int o = min(max(offsets[t.e], 0), M), end = min(max(offsets[t.e + 1], 0), M);
-  const int i = slot - (o / BM + t.e);
-  t.row0 = o + i * BM;
-  t.rows = i < 0 ? 0 : min(end - t.row0, BM);  // i < 0: the offsets do not ascend
-  return t;
-}
-
-typedef __attribute__((ext_vector_type(4))) int i32x4;
-// LDS tiles of 128-byte rows (one block of K), 16-byte chunk c of row r at c ^ (r & 7), so that
-// fragment reads spread over the banks. A lane's operand of the 16 x 16 x 128 MFMA: chunks g and
-// 4 + g of row l % 16 of a block of 16 rows, g = l / 16. Rows and columns take the same k in the
-// same place, which is all a sum over the whole block needs. The two byte offsets are the same
-// in every row block, so the blocks differ by constants.
-struct FragAt {
-  int lo, hi;
-};
-MOE_DEV FragAt frag_at(int lane) {
-  const int r = lane % 16, g = lane / 16;
-  return {r * 128 + ((g ^ (r & 7)) << 4), r * 128 + (((4 + g) ^ (r & 7)) << 4)};
-}
 MOE_DEV i32x8 fp8_frag(const uint8_t* rows16, const FragAt& f) {
   const i32x4 lo = *reinterpret_cast<const i32x4*>(rows16 + f.lo);
   const i32x4 hi = *reinterpret_cast<const i32x4*>(rows16 + f.hi);
@@ -315,24 +273,7 @@ MOE_DEV f32x4 fp8_mfma(const i32x8& b, const i32x8& a) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0,
                                                           0, 0, 0, 0);
 }
-MOE_DEV __amdgpu_buffer_rsrc_t fp8_rsrc(const void* base) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00020000);
-}
-// 16 bytes a lane straight into LDS, at lds + 16 lane: 8 rows of 128 bytes a wave.
-template <int AUX = 0>
-MOE_DEV void fp8_load_lds(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint8_t* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
-                                           voff, soff, 0, AUX);
-}
-// The chunk a lane fetches into its place of those 8 rows.
-MOE_DEV uint32_t fp8_piece(int lane) { return 16u * ((lane % 8) ^ (lane / 8)); }
-
-// Behind it no load goes out before those in front of it: what a counted wait relies on.
-MOE_DEV void loads_in_order() { __builtin_amdgcn_sched_barrier(0x40f); }  // arithmetic may pass
-
 constexpr int kVm4Lgkm0 = 0x0074;  // s_waitcnt vmcnt(4) lgkmcnt(0)
-constexpr int kVm0Lgkm0 = 0x0070;
-constexpr int kLgkm0 = 0xc07f;     // lgkmcnt(0) alone
 
 // Few rows an expert: the weights' stream is what takes the time. BM x 128 tiles, four waves of
 // BM x 32; 128 bytes of K a step go from memory straight into LDS, the weights SB - 1 steps ahead
@@ -386,14 +327,14 @@ struct StreamTile {
     const uint32_t step = (uint32_t)min(kb, nK - 1) * 128;
 #pragma unroll
     for (int j = 0; j < AJ; ++j)
-      fp8_load_lds(ra, ao[j], step, L.template a<S>() + (wave * AJ + j) * 1024);
+      load_lds16(ra, ao[j], step, L.template a<S>() + (wave * AJ + j) * 1024);
   }
   template <int S>
   MOE_DEV void issue_b(const StreamLds<SB>& L, int kb) {
     const uint32_t step = (uint32_t)min(kb, nK - 1) * 128;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      fp8_load_lds<NMB <= 4 ? 2 : 0>(rb, bo[j], step, L.template b<S>() + (wave * 4 + j) * 1024);
+      load_lds16<NMB <= 4 ? 2 : 0>(rb, bo[j], step, L.template b<S>() + (wave * 4 + j) * 1024);
   }
   MOE_DEV void issue_s(int kb) {
     const size_t at = (size_t)min(kb, nK - 1) * M;
@@ -444,15 +385,15 @@ struct StreamTile {
     f = frag_at(lane);
     nK = a.K / kQB;
     M = a.M;
-    ra = fp8_rsrc(a.a + (size_t)t.row0 * a.K);
-    rb = fp8_rsrc(a.b + ((size_t)t.e * a.N + (size_t)n0 * kQB) * a.K);
+    ra = buf_rsrc(a.a + (size_t)t.row0 * a.K);
+    rb = buf_rsrc(a.b + ((size_t)t.e * a.N + (size_t)n0 * kQB) * a.K);
     sb = a.sb + ((size_t)t.e * (a.N / kQB) + n0) * nK;
 #pragma unroll
     for (int j = 0; j < AJ; ++j)  // rows past the count read the last one again
-      ao[j] = (uint32_t)min(8 * (wave * AJ + j) + lane / 8, t.rows - 1) * a.K + fp8_piece(lane);
+      ao[j] = (uint32_t)min(8 * (wave * AJ + j) + lane / 8, t.rows - 1) * a.K + lds_piece(lane);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      bo[j] = (uint32_t)(8 * (wave * 4 + j) + lane / 8) * a.K + fp8_piece(lane);
+      bo[j] = (uint32_t)(8 * (wave * 4 + j) + lane / 8) * a.K + lds_piece(lane);
 #pragma unroll
     for (int j = 0; j < SJ; ++j) sp[j] = a.sa + t.row0 + min(64 * j + lane, t.rows - 1);
 #pragma unroll
@@ -535,11 +476,11 @@ struct NarrowTile {
     kb = min(kb, nK - 1);
     const uint32_t step = (uint32_t)kb * 128;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fp8_load_lds<2>(rb, bo[j], step, st + kA + j * 1024);
+    for (int j = 0; j < 4; ++j) load_lds16<2>(rb, bo[j], step, st + kA + j * 1024);
 #pragma unroll
-    for (int j = 0; j < AJ; ++j) fp8_load_lds(ra, ao[j], step, st + j * 1024);
+    for (int j = 0; j < AJ; ++j) load_lds16(ra, ao[j], step, st + j * 1024);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        fp8_rsrc(sa + kb * M), (__attribute__((address_space(3))) void*)(st + kA + kB), 4, so, 0, 0,
+        buf_rsrc(sa + kb * M), (__attribute__((address_space(3))) void*)(st + kA + kB), 4, so, 0, 0,
         0);
   }
   MOE_DEV void step(uint8_t* st, int kb) {
@@ -583,15 +524,15 @@ struct NarrowTile {
     f = frag_at(lane);
     nK = a.K / kQB;
     M = a.M;
-    ra = fp8_rsrc(a.a + (size_t)t.row0 * a.K);
-    rb = fp8_rsrc(a.b + ((size_t)t.e * a.N + n0) * a.K);
+    ra = buf_rsrc(a.a + (size_t)t.row0 * a.K);
+    rb = buf_rsrc(a.b + ((size_t)t.e * a.N + n0) * a.K);
     sa = a.sa + t.row0;
     sb = a.sb + ((size_t)t.e * (a.N / kQB) + n0 / kQB) * nK;
 #pragma unroll
     for (int j = 0; j < AJ; ++j)  // rows past the count read the last one again
-      ao[j] = (uint32_t)min(8 * j + lane / 8, t.rows - 1) * a.K + fp8_piece(lane);
+      ao[j] = (uint32_t)min(8 * j + lane / 8, t.rows - 1) * a.K + lds_piece(lane);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) bo[j] = (uint32_t)(8 * j + lane / 8) * a.K + fp8_piece(lane);
+    for (int j = 0; j < 4; ++j) bo[j] = (uint32_t)(8 * j + lane / 8) * a.K + lds_piece(lane);
     so = (uint32_t)min(lane, t.rows - 1) * 4;
 #pragma unroll
     for (int i = 0; i < NMB; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -663,8 +604,6 @@ __global__ void __launch_bounds__(64, 1) fp8_narrow_kernel(const Fp8GemmArgs a) 
 // A library product of that size with one scale an operand takes 375; without the block scales
 // this kernel took 422 a call where it took 445. The MFMAs are busy 59% of the time that tiles run;
 // the rest is the phases' ends, a tile's first loads and its epilogue, and the last round.
-constexpr int kBigT = 256;
-constexpr int kCus = 256;                             // MI355X; tiles that run at once
 constexpr int kBigCodes = kBigT * 128;                // one operand's codes of a step
 constexpr int kBigStage = 2 * kBigCodes + kBigT * 4;  // rows, weights, the rows' scales
 __shared__ __align__(1024) uint8_t fp8_big0[kBigStage];
@@ -695,12 +634,12 @@ struct BigTile {
     const uint32_t step = (uint32_t)kb * 128;
 #pragma unroll
     for (int j = 0; j < NB; ++j)
-      fp8_load_lds(rb, bo[j], step, st + kBigCodes + (wave * NB + j) * 1024);
+      load_lds16(rb, bo[j], step, st + kBigCodes + (wave * NB + j) * 1024);
 #pragma unroll
-    for (int j = 0; j < HB; ++j) fp8_load_lds(ra, ao[j], step, st + (wave * HB + j) * 1024);
+    for (int j = 0; j < HB; ++j) load_lds16(ra, ao[j], step, st + (wave * HB + j) * 1024);
     // 64 rows' scales a wave; several waves write the same
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        fp8_rsrc(sa + kb * M),  // K / 128 rows of M may pass 32 bits
+        buf_rsrc(sa + kb * M),  // K / 128 rows of M may pass 32 bits
         (__attribute__((address_space(3))) void*)(st + 2 * kBigCodes + wave % (BM / 64) * 256), 4,
         so, 0, 0, 0);
   }
@@ -797,18 +736,18 @@ struct BigTile {
     f = frag_at(lane);
     nK = a.K / kQB;
     M = a.M;
-    ra = fp8_rsrc(a.a + (size_t)row0 * a.K);
-    rb = fp8_rsrc(a.b + ((size_t)e * a.N + n0) * a.K);
+    ra = buf_rsrc(a.a + (size_t)row0 * a.K);
+    rb = buf_rsrc(a.b + ((size_t)e * a.N + n0) * a.K);
     sa = a.sa + row0;
     const int cols = min(BN, a.N - n0);  // BN, or 128 at an odd end
     sb = a.sb + ((size_t)e * (a.N / kQB) + n0 / kQB + min(wn * NB * 16, cols - 1) / kQB) * nK;
     // rows past the end read the last one again
 #pragma unroll
     for (int j = 0; j < HB; ++j)
-      ao[j] = (uint32_t)min((wave * HB + j) * 8 + lane / 8, rows - 1) * a.K + fp8_piece(lane);
+      ao[j] = (uint32_t)min((wave * HB + j) * 8 + lane / 8, rows - 1) * a.K + lds_piece(lane);
 #pragma unroll
     for (int j = 0; j < NB; ++j)
-      bo[j] = (uint32_t)min((wave * NB + j) * 8 + lane / 8, cols - 1) * a.K + fp8_piece(lane);
+      bo[j] = (uint32_t)min((wave * NB + j) * 8 + lane / 8, cols - 1) * a.K + lds_piece(lane);
     so = (uint32_t)min(wave % (BM / 64) * 64 + lane, rows - 1) * 4;
 #pragma unroll
     for (int i = 0; i < MB; ++i)
@@ -843,52 +782,6 @@ struct BigTile {
     }
   }
 };
-
-// The experts' row tiles counted out: all of them, and the one with a given number.
-MOE_DEV int big_tiles_of(const Fp8GemmArgs& a, int e) {
-  if (e >= a.E) return 0;
-  const int lo = min(max(a.offsets[e], 0), a.M), hi = min(max(a.offsets[e + 1], 0), a.M);
-  return hi > lo ? (hi - lo + kBigT - 1) / kBigT : 0;
-}
-MOE_DEV int wave_scan(int v) {
-  const int lane = threadIdx.x % kWave;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const int u = __shfl_up(v, o);
-    v += lane >= o ? u : 0;
-  }
-  return v;
-}
-MOE_DEV int big_count(const Fp8GemmArgs& a) {
-  int n = 0;
-  for (int e0 = 0; e0 < a.E; e0 += kWave)
-    n += __builtin_amdgcn_readlane(wave_scan(big_tiles_of(a, e0 + threadIdx.x % kWave)), 63);
-  return n;
-}
-MOE_DEV RowTile big_rows(const Fp8GemmArgs& a, int mt) {
-  RowTile t{0, 0, 0};
-  for (int e0 = 0; e0 < a.E; e0 += kWave) {
-    const int inc = wave_scan(big_tiles_of(a, e0 + threadIdx.x % kWave));
-    const int all = __builtin_amdgcn_readlane(inc, 63);
-    if (mt < all) {
-      const int n = __popcll(__ballot(inc <= mt));  // experts before the tile's
-      t.e = e0 + n;
-      const int i = mt - (n ? __builtin_amdgcn_readlane(inc, n - 1) : 0);
-      const int lo = min(max(a.offsets[t.e], 0), a.M), hi = min(max(a.offsets[t.e + 1], 0), a.M);
-      t.row0 = lo + i * kBigT;
-      t.rows = min(hi - t.row0, kBigT);
-      return t;
-    }
-    mt -= all;
-  }
-  return t;
-}
-// Tile number -> (row tile, column tile): four row tiles take each column tile in turn, so that
-// the tiles an XCD runs at once (32) share few panels of either operand in its L2.
-MOE_DEV int2 big_order(int lt, int nm, int nN) {
-  const int first = lt / (4 * nN) * 4, gm = min(4, nm - first), r = lt - first * nN;
-  return make_int2(first + r % gm, r / gm);
-}
 
 // Whole rounds of one tile a CU, then what is left: its tiles cut in two (256 x 128) or four
 // (128 x 128) where the parts still fit one round, so that the last round takes half or a quarter
