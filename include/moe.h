@@ -487,6 +487,118 @@ int moe_fp8_gemm(const int32_t* offsets, int32_t M, int32_t E, int32_t N, int32_
                  moe_stream_t stream);
 
 /*
+ * 8-bit integers: symmetric int8 codes with one fp32 scale a row - a token of the activations, an
+ * output channel of the weights. scale = amax / 127 and code = rne(127 v / amax), amax the row's
+ * largest magnitude (a row of zeros: scale 1, codes 0; an amax below 2^-110 counts as 2^-110); ties
+ * are exact, so the codes are those of the quotient itself. A row that holds a value that is not
+ * finite gets codes 0 and the scale NaN.
+ *
+ * moe_i8_quantize_rows - rows of activations, or weights [E, N, K] as their E * N rows.
+ *   src    bf16 [rows, cols]   in, cols a multiple of 128
+ *   codes  int8 [rows, cols]   out, -127 .. 127
+ *   scales fp32 [rows]         out
+ * rows 0 enqueues nothing; the three pointers may then be NULL.
+ * Errors: MOE_ERR_INVALID_ARG, also for rows of 2^24 and more (a workgroup takes a row or four).
+ */
+int moe_i8_quantize_rows(const void* src, int32_t rows, int32_t cols, void* codes, float* scales,
+                         moe_stream_t stream);
+
+/*
+ * moe_i8_gemm - expert-grouped product of int8 rows and weights:
+ *   out[p, n] = bf16( a_scales[p] * (sum_k a[p, k] b[e, n, k]) * b_scales[e, n] )
+ *                                                            for offsets[e] <= p < offsets[e + 1]
+ * The sum is exact (32-bit integers), its two products are fp32, and the result is rounded once to
+ * bf16. It does not depend on the other rows. E = 1 with offsets {0, M} is a plain product. Codes may
+ * be -128 too. Needs no workspace.
+ *
+ *   offsets  int32 [E + 1]     in, ascending, within [0, M] (values outside are clamped). Rows of
+ *                              `out` before the first or behind the last expert's are left as they
+ *                              were.
+ *   a        int8 [M, K]       in
+ *   a_scales fp32 [M]          in
+ *   b        int8 [E, N, K]    in
+ *   b_scales fp32 [E, N]       in
+ *   out      bf16 [M, N]       out
+ * Shapes: 0 <= M < 2^31 (0 enqueues nothing; a, a_scales and out may then be NULL),
+ * 1 <= E <= 1024, N and K multiples of 128, K < 2^17, N * K < 2^31. Errors: MOE_ERR_INVALID_ARG.
+ */
+int moe_i8_gemm(const int32_t* offsets, int32_t M, int32_t E, int32_t N, int32_t K, const void* a,
+                const float* a_scales, const void* b, const float* b_scales, void* out,
+                moe_stream_t stream);
+
+/* Activations of the gated products. In fp32; GELU by the error function or its tanh form. */
+enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1, MOE_ACT_GELU_TANH = 2, MOE_ACT_RELU = 3 };
+
+/*
+ * moe_i8_gemm_gated - moe_i8_gemm with the gate in its epilogue: with g and u the fp32 products of
+ * a row and the weights' rows i and I + i,
+ *   out[p, i] = bf16( act(g) * u )
+ * so that neither projection is stored. The result is what moe_i8_quantize_rows takes before the
+ * down product.
+ *   b        int8 [E, 2I, K]   in: rows 0..I-1 gate, I..2I-1 up, as in W1
+ *   b_scales fp32 [E, 2I]      in
+ *   out      bf16 [M, I]       out
+ * The rest, and the shapes with N = 2I (I a multiple of 128), are moe_i8_gemm's.
+ */
+int moe_i8_gemm_gated(const int32_t* offsets, int32_t M, int32_t E, int32_t I, int32_t K,
+                      int32_t act, const void* a, const float* a_scales, const void* b,
+                      const float* b_scales, void* out, moe_stream_t stream);
+
+/*
+ * The dense gated feed-forward block in bf16: the shared expert that every token passes beside its
+ * routed ones, or a layer without experts. Shapes: T >= 1, d and I multiples of 128;
+ * (T + 64) * max(d, 2I) < 2^31 and 4 * I * d < 2^31 (32-bit offsets).
+ */
+typedef struct moe_ffn {
+    int32_t T;     /* tokens */
+    int32_t d;     /* hidden size */
+    int32_t I;     /* intermediate size */
+    int32_t act;   /* MOE_ACT_* */
+    int32_t flags; /* 0, or MOE_FLAG_BF16_DW: dw1 and dw2 are bf16 buffers instead of fp32 */
+} moe_ffn;
+typedef struct moe_ffn_sizes {
+    size_t workspace; /* bytes of scratch that serve both calls (dH, partial sums) */
+} moe_ffn_sizes;
+int moe_ffn_query(const moe_ffn* ffn, moe_ffn_sizes* out);
+
+/*
+ * moe_ffn_forward
+ *   [g | u] = x w1^T    A = act(g) * u    y = A w2^T    (with acc_y: y + A w2^T)
+ * Sums are fp32 and outputs bf16, each rounded once; A is formed from the fp32 g and u, and y from
+ * the rounded A. With acc_y the fp32 total of the stored y and the product is rounded once.
+ *
+ *   x   bf16 [T, d]     in
+ *   w1  bf16 [2I, d]    in: rows 0..I-1 gate, I..2I-1 up
+ *   w2  bf16 [d, I]     in
+ *   H   bf16 [T, 2I]    out: [g | u], which moe_ffn_backward reads; or NULL (not wanted)
+ *   A   bf16 [T, I]     out
+ *   y   bf16 [T, d]     out (or added to); not x
+ *   workspace bytes [ws_bytes]   scratch: calls that share one follow each other
+ */
+int moe_ffn_forward(const moe_ffn* ffn, const void* x, const void* w1, const void* w2, void* H,
+                    void* A, void* y, int32_t acc_y, void* workspace, size_t ws_bytes,
+                    moe_stream_t stream);
+
+/*
+ * moe_ffn_backward - gradients of <y, dy>:
+ *   dA = dy w2    dH = bf16([dA * u * act'(g) | dA * act(g)])   (g, u from the stored H)
+ *   dx  = dH w1      dw1 = dH^T x      dw2 = dy^T A
+ * Sums are fp32. dx is rounded once to bf16, with acc_dx after the stored dx is added in fp32; dw1
+ * and dw2 likewise with acc_dw (fp32, or bf16 with MOE_FLAG_BF16_DW). relu'(0) = 0.
+ *
+ *   x, w1, w2, H, A     in, as in moe_ffn_forward of the same batch
+ *   dy  bf16 [T, d]     in
+ *   dx  bf16 [T, d]     out (or added to); not x and not dy
+ *   dw1 [2I, d]         out (or added to)
+ *   dw2 [d, I]          out (or added to)
+ *   workspace bytes [ws_bytes]   scratch
+ */
+int moe_ffn_backward(const moe_ffn* ffn, const void* x, const void* w1, const void* w2,
+                     const void* H, const void* A, const void* dy, void* dx, void* dw1, void* dw2,
+                     int32_t acc_dx, int32_t acc_dw, void* workspace, size_t ws_bytes,
+                     moe_stream_t stream);
+
+/*
  * Launch tracing, for benchmarks and profilers; the layer never needs it.
  * moe_trace_begin: until moe_trace_end, every kernel the library enqueues is bracketed by two
  * hipEventRecord calls on the kernel's own stream: events[2i] before and events[2i+1] after the

@@ -34,6 +34,10 @@ MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
 MOE_GROUP_MAX = 0
 MOE_GROUP_TOP2 = 1
+MOE_ACT_SILU = 0
+MOE_ACT_GELU = 1
+MOE_ACT_GELU_TANH = 2
+MOE_ACT_RELU = 3
 MOE_DEVICE_BAD_EXPERT_INDEX = 1
 MOE_DEVICE_BARRIER_TIMEOUT = 2
 
@@ -64,6 +68,15 @@ class MoeGate(ctypes.Structure):
                 ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class MoeFfn(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("I", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class MoeFfnSizes(ctypes.Structure):
+    _fields_ = [("workspace", ctypes.c_size_t)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -88,6 +101,13 @@ _SIGS = {
     "moe_fp8_quantize_rows": [_P, _I32, _I32, _P, _P, _P],
     "moe_fp8_quantize_weights": [_P, _I32, _I32, _I32, _P, _P, _P, _P, _P],
     "moe_fp8_gemm": [_P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P],
+    "moe_i8_quantize_rows": [_P, _I32, _I32, _P, _P, _P],
+    "moe_i8_gemm": [_P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P],
+    "moe_i8_gemm_gated": [_P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P],
+    "moe_ffn_query": [ctypes.POINTER(MoeFfn), ctypes.POINTER(MoeFfnSizes)],
+    "moe_ffn_forward": [ctypes.POINTER(MoeFfn), _P, _P, _P, _P, _P, _P, _I32, _P, _SZ, _P],
+    "moe_ffn_backward": [ctypes.POINTER(MoeFfn), _P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32,
+                         _P, _SZ, _P],
     "moe_permute_static": [ctypes.POINTER(MoeCfg), _P, _P, _P, _SZ, _I32, _P, _P, _P, _P, _P,
                            _P],
 }
@@ -237,6 +257,7 @@ def make_gate(score=MOE_SCORE_SOFTMAX, groups=1, topk_groups=1, group_score=MOE_
 
 
 _F32, _I32T, _BF16 = torch.float32, torch.int32, torch.bfloat16
+_I8 = torch.int8
 _BYTES = (torch.uint8, torch.float8_e4m3fn)
 
 
@@ -325,3 +346,57 @@ def moe_fp8_gemm(offsets, M, E, N, K, a, a_scales, b, b_scales, out, stream=None
                                     (b, _BYTES, E * N * K), (b_scales, _F32, E * N * K // 16384),
                                     (out, _BF16, M * N))
     _check(lib().moe_fp8_gemm(o, M, E, N, K, qa, sa, qb, sb, y, st), "moe_fp8_gemm")
+
+
+def moe_i8_quantize_rows(src, rows, cols, codes, scales, stream=None):
+    n = rows * cols
+    s, q, sc, st = _dev("moe_i8_quantize_rows", stream, (src, _BF16, n), (codes, _I8, n),
+                        (scales, _F32, rows))
+    _check(lib().moe_i8_quantize_rows(s, rows, cols, q, sc, st), "moe_i8_quantize_rows")
+
+
+def moe_i8_gemm(offsets, M, E, N, K, a, a_scales, b, b_scales, out, stream=None):
+    o, qa, sa, qb, sb, y, st = _dev("moe_i8_gemm", stream, (offsets, _I32T, E + 1),
+                                    (a, _I8, M * K), (a_scales, _F32, M), (b, _I8, E * N * K),
+                                    (b_scales, _F32, E * N), (out, _BF16, M * N))
+    _check(lib().moe_i8_gemm(o, M, E, N, K, qa, sa, qb, sb, y, st), "moe_i8_gemm")
+
+
+def moe_i8_gemm_gated(offsets, M, E, I, K, act, a, a_scales, b, b_scales, out, stream=None):
+    o, qa, sa, qb, sb, y, st = _dev("moe_i8_gemm_gated", stream, (offsets, _I32T, E + 1),
+                                    (a, _I8, M * K), (a_scales, _F32, M),
+                                    (b, _I8, E * 2 * I * K), (b_scales, _F32, E * 2 * I),
+                                    (out, _BF16, M * I))
+    _check(lib().moe_i8_gemm_gated(o, M, E, I, K, act, qa, sa, qb, sb, y, st),
+           "moe_i8_gemm_gated")
+
+
+def make_ffn(T, d, I, act=MOE_ACT_SILU, flags=0) -> MoeFfn:
+    return MoeFfn(T, d, I, act, flags)
+
+
+def moe_ffn_query(ffn: MoeFfn) -> MoeFfnSizes:
+    out = MoeFfnSizes()
+    _check(lib().moe_ffn_query(ctypes.byref(ffn), ctypes.byref(out)), "moe_ffn_query")
+    return out
+
+
+def moe_ffn_forward(ffn, x, w1, w2, H, A, y, acc_y, workspace, stream=None):
+    T, d, I = ffn.T, ffn.d, ffn.I
+    *p, ws, st = _dev("moe_ffn_forward", stream, (x, _BF16, T * d), (w1, _BF16, 2 * I * d),
+                      (w2, _BF16, d * I), (H, _BF16, T * 2 * I), (A, _BF16, T * I),
+                      (y, _BF16, T * d), (workspace, torch.uint8, 0))
+    _check(lib().moe_ffn_forward(ctypes.byref(ffn), *p, int(acc_y), ws, _nbytes(workspace), st),
+           "moe_ffn_forward")
+
+
+def moe_ffn_backward(ffn, x, w1, w2, H, A, dy, dx, dw1, dw2, acc_dx, acc_dw, workspace,
+                     stream=None):
+    T, d, I = ffn.T, ffn.d, ffn.I
+    dw = _BF16 if ffn.flags & MOE_FLAG_BF16_DW else _F32
+    *p, ws, st = _dev("moe_ffn_backward", stream, (x, _BF16, T * d), (w1, _BF16, 2 * I * d),
+                      (w2, _BF16, d * I), (H, _BF16, T * 2 * I), (A, _BF16, T * I),
+                      (dy, _BF16, T * d), (dx, _BF16, T * d), (dw1, dw, 2 * I * d),
+                      (dw2, dw, d * I), (workspace, torch.uint8, 0))
+    _check(lib().moe_ffn_backward(ctypes.byref(ffn), *p, int(acc_dx), int(acc_dw), ws,
+                                  _nbytes(workspace), st), "moe_ffn_backward")

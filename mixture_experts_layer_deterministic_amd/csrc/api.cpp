@@ -246,6 +246,48 @@ int check_fp8_shape(int32_t E, int32_t N, int32_t K) {
   return MOE_OK;
 }
 
+int check_i8_shape(int32_t E, int32_t N, int32_t K) {
+  if (const int st = check_fp8_shape(E, N, K)) return st;
+  return K < (1 << 17) ? MOE_OK : MOE_ERR_INVALID_ARG;  // 128 * 128 * K stays below 2^31
+}
+
+bool act_ok(int32_t act) { return act >= MOE_ACT_SILU && act <= MOE_ACT_RELU; }
+
+int i8_gemm(const int32_t* offsets, int32_t M, int32_t E, int32_t N, int32_t K, int32_t act,
+            bool gated, const void* a, const float* a_scales, const void* b,
+            const float* b_scales, void* out, moe_stream_t stream) {
+  if (const int st = check_i8_shape(E, N, K)) return st;
+  if (M < 0 || !aligned4(offsets) || !aligned16(b) || !aligned4(b_scales))
+    return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;  // empty buffers have no address to check
+  if (!aligned16(a) || !aligned4(a_scales) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  if ((M / 16LL + E) * (N / 128) >= (1LL << 31)) return MOE_ERR_INVALID_ARG;  // the grid
+  if (const int st = check_device()) return st;
+  I8GemmArgs g{offsets, static_cast<const uint8_t*>(a), a_scales, static_cast<const uint8_t*>(b),
+               b_scales, static_cast<uint16_t*>(out), M, E, N, K, act};
+  Launches L;
+  L(launch_i8_gemm(g, gated, static_cast<hipStream_t>(stream)));
+  return L.status();
+}
+
+int check_ffn(const moe_ffn* f) {
+  if (!f || f->T < 1 || f->d < 128 || f->d % 128 != 0 || f->I < 128 || f->I % 128 != 0 ||
+      !act_ok(f->act) || (f->flags & ~MOE_FLAG_BF16_DW))
+    return MOE_ERR_INVALID_ARG;
+  const long long T = f->T, d = f->d, I = f->I;
+  if ((T + 64) * std::max(d, 2 * I) >= (1LL << 31) || 4 * I * d >= (1LL << 31))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+struct FfnLayout {
+  size_t dH, total;
+};
+FfnLayout ffn_layout(const moe_ffn* f) {
+  FfnLayout L{};
+  L.total = align_up(2 * (size_t)f->T * 2 * f->I);
+  return L;
+}
+
 GateParams gate_params(const moe_gate* g) {
   GateParams p;
   p.softmax = g->score == MOE_SCORE_SOFTMAX;
@@ -852,6 +894,107 @@ int moe_fp8_gemm(const int32_t* offsets, int32_t M, int32_t E, int32_t N, int32_
                 static_cast<const uint8_t*>(b), b_scales, static_cast<uint16_t*>(out), M, E, N, K};
   Launches L;
   L(launch_fp8_gemm(g, static_cast<hipStream_t>(stream)));
+  return L.status();
+}
+
+int moe_i8_quantize_rows(const void* src, int32_t rows, int32_t cols, void* codes, float* scales,
+                         moe_stream_t stream) {
+  if (rows < 0 || rows >= (1 << 24) || cols < 128 || cols % 128 != 0) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;  // empty buffers have no address to check
+  if (!aligned16(src) || !aligned16(codes) || !aligned4(scales)) return MOE_ERR_INVALID_ARG;
+  if (const int st = check_device()) return st;
+  Launches L;
+  L(launch_i8_quant_rows(static_cast<const uint16_t*>(src), rows, cols,
+                         static_cast<uint8_t*>(codes), scales, static_cast<hipStream_t>(stream)));
+  return L.status();
+}
+
+int moe_i8_gemm(const int32_t* offsets, int32_t M, int32_t E, int32_t N, int32_t K, const void* a,
+                const float* a_scales, const void* b, const float* b_scales, void* out,
+                moe_stream_t stream) {
+  return i8_gemm(offsets, M, E, N, K, 0, false, a, a_scales, b, b_scales, out, stream);
+}
+
+int moe_i8_gemm_gated(const int32_t* offsets, int32_t M, int32_t E, int32_t I, int32_t K,
+                      int32_t act, const void* a, const float* a_scales, const void* b,
+                      const float* b_scales, void* out, moe_stream_t stream) {
+  if (I < 128 || I % 128 != 0 || I >= (1 << 30) || !act_ok(act)) return MOE_ERR_INVALID_ARG;
+  return i8_gemm(offsets, M, E, 2 * I, K, act, true, a, a_scales, b, b_scales, out, stream);
+}
+
+int moe_ffn_query(const moe_ffn* ffn, moe_ffn_sizes* out) {
+  if (!out) return MOE_ERR_INVALID_ARG;
+  if (const int st = check_ffn(ffn)) return st;
+  out->workspace = ffn_layout(ffn).total;
+  return MOE_OK;
+}
+
+int moe_ffn_forward(const moe_ffn* ffn, const void* x, const void* w1, const void* w2, void* H,
+                    void* A, void* y, int32_t acc_y, void* workspace, size_t ws_bytes,
+                    moe_stream_t stream) {
+  if (const int st = check_ffn(ffn)) return st;
+  if (!aligned16(x) || !aligned16(w1) || !aligned16(w2) || (H && !aligned16(H)) ||
+      !aligned16(A) || !aligned16(y) || y == x || !aligned16(workspace))
+    return MOE_ERR_INVALID_ARG;
+  const FfnLayout Y = ffn_layout(ffn);
+  if (ws_bytes < Y.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (const int st = check_device()) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  FfnArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.w1 = static_cast<const uint16_t*>(w1);
+  a.w2 = static_cast<const uint16_t*>(w2);
+  a.H = static_cast<uint16_t*>(H);
+  a.A = static_cast<uint16_t*>(A);
+  a.y = static_cast<uint16_t*>(y);
+  a.T = ffn->T;
+  a.d = ffn->d;
+  a.I = ffn->I;
+  a.act = ffn->act;
+  a.acc_y = acc_y != 0;
+  Launches L;
+  L(launch_ffn_gate_up(a, s));
+  if (!L.err) L(launch_ffn_down(a, s));
+  return L.status();
+}
+
+int moe_ffn_backward(const moe_ffn* ffn, const void* x, const void* w1, const void* w2,
+                     const void* H, const void* A, const void* dy, void* dx, void* dw1, void* dw2,
+                     int32_t acc_dx, int32_t acc_dw, void* workspace, size_t ws_bytes,
+                     moe_stream_t stream) {
+  if (const int st = check_ffn(ffn)) return st;
+  if (!aligned16(x) || !aligned16(w1) || !aligned16(w2) || !aligned16(H) || !aligned16(A) ||
+      !aligned16(dy) || !aligned16(dx) || !aligned16(dw1) || !aligned16(dw2) || dx == x ||
+      dx == dy || !aligned16(workspace))
+    return MOE_ERR_INVALID_ARG;
+  const FfnLayout Y = ffn_layout(ffn);
+  if (ws_bytes < Y.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (const int st = check_device()) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int bdw = ffn->flags & MOE_FLAG_BF16_DW ? 1 : 0, acc = acc_dw != 0;
+  FfnArgs a{};
+  a.w1 = static_cast<const uint16_t*>(w1);
+  a.w2 = static_cast<const uint16_t*>(w2);
+  a.H = const_cast<uint16_t*>(static_cast<const uint16_t*>(H));
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.dH = at<uint16_t>(workspace, Y.dH);
+  a.dx = static_cast<uint16_t*>(dx);
+  a.T = ffn->T;
+  a.d = ffn->d;
+  a.I = ffn->I;
+  a.act = ffn->act;
+  a.acc_dx = acc_dx != 0;
+  Launches L;
+  L(launch_ffn_dh(a, s));
+  if (!L.err)
+    L(launch_ffn_dw({a.dy, static_cast<const uint16_t*>(A), dw2, a.T, a.d, a.I, acc, bdw,
+                     "ffn_dw2"},
+                    s));
+  if (!L.err) L(launch_ffn_dx(a, s));
+  if (!L.err)
+    L(launch_ffn_dw({a.dH, static_cast<const uint16_t*>(x), dw1, a.T, 2 * a.I, a.d, acc, bdw,
+                     "ffn_dw1"},
+                    s));
   return L.status();
 }
 

@@ -1,0 +1,268 @@
+// 8-bit integers: symmetric codes with one fp32 scale a row (activations: a token; weights: an
+// output channel), the quantiser and the expert-grouped products.
+//
+// A row's scale is amax / 127 (1 for a row of zeros; an amax below 2^-110 counts as 2^-110, so that
+// no quotient leaves fp32's normal numbers) and its codes are rne(127 v / amax), -127 .. 127. A row
+// that holds a value that is not finite gets codes 0 and the scale NaN: a product is NaN in that
+// row's (or channel's) results and nowhere else.
+// The products add codes exactly, in 32-bit integers (K below 2^17: 128 * 128 * K fits), so their
+// results do not depend on any order of summation, nor on the kernel chosen:
+//   out[p, n] = bf16(sa[p] * sum_k a[p, k] b[e, n, k] * sb[e, n]).
+#include <algorithm>
+#include <cmath>
+
+#include "common.h"
+#include "kernels.h"
+#include "ops.h"
+#include "products.h"
+
+namespace moe {
+namespace {
+
+// 127 v / amax is a tie between two codes or at least 2^-16 of itself away from one: with v = a 2^i
+// and amax = b 2^j (a, b < 256) the distance is a multiple of 2^(i-j) / 2b, and 127 a / b 2^(i-j) is
+// at most 254 a < 2^16 times that. Products with 127 / amax moved by 2^-19 of itself down and up,
+// each error below 2^-22, therefore round to the same code, or are a tie's two neighbours, of which
+// the even one is taken. The sum with 1.5 2^23 rounds to a whole number, whose low byte is the code.
+struct I8Scale {
+  float scale, lo, hi;
+  bool finite;
+};
+MOE_DEV I8Scale i8_scale(uint32_t amax_bits) {  // the largest magnitude's bf16 bits
+  I8Scale s;
+  s.finite = amax_bits < 0x7f80;
+  float amax = __uint_as_float(amax_bits << 16);
+  if (amax > 0.f) amax = fmaxf(amax, 0x1p-110f);
+  const float inv = amax > 0.f && s.finite ? 127.f / amax : 0.f;
+  s.scale = !s.finite ? __uint_as_float(0x7fc00000u) : amax > 0.f ? amax / 127.f : 1.f;
+  s.lo = inv * (1.f - 0x1p-19f);
+  s.hi = inv * (1.f + 0x1p-19f);
+  return s;
+}
+MOE_DEV uint32_t i8_code(float v, const I8Scale& s) {
+  const uint32_t lo = __float_as_uint(__builtin_fmaf(v, s.lo, 12582912.f));
+  const uint32_t hi = __float_as_uint(__builtin_fmaf(v, s.hi, 12582912.f));
+  return lo & 1 ? hi : lo;
+}
+MOE_DEV uint32_t i8_code4(float a, float b, float c, float d, const I8Scale& s) {
+  const uint32_t ab = __builtin_amdgcn_perm(i8_code(b, s), i8_code(a, s), 0x0c0c0400u);
+  const uint32_t cd = __builtin_amdgcn_perm(i8_code(d, s), i8_code(c, s), 0x0c0c0400u);
+  return ab | cd << 16;
+}
+MOE_DEV uint2 i8_codes8(const uint4& x, const I8Scale& s) {
+  if (!s.finite) return make_uint2(0, 0);
+  return make_uint2(i8_code4(bf2f_lo(x.x), bf2f_hi(x.x), bf2f_lo(x.y), bf2f_hi(x.y), s),
+                    i8_code4(bf2f_lo(x.z), bf2f_hi(x.z), bf2f_lo(x.w), bf2f_hi(x.w), s));
+}
+// The largest magnitude bits of eight bf16 values (they order as the magnitudes; NaN last).
+MOE_DEV uint32_t amax_bits8(const uint4& x) {
+  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  u16x2 m = {0, 0};
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[q] & 0x7fff7fffu));
+  return max((uint32_t)m[0], (uint32_t)m[1]);
+}
+
+// W waves take a row, U pieces of eight values a lane, all in registers: one read. U = 0: rows too
+// long for that are read twice.
+template <int W, int U>
+__global__ void __launch_bounds__(256) i8_quant_rows_kernel(const uint16_t* __restrict__ src,
+                                                            long long rows, int cols,
+                                                            uint8_t* __restrict__ codes,
+                                                            float* __restrict__ scales) {
+  constexpr int kPer = 4 / W;  // rows a workgroup
+  __shared__ uint32_t red[4];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const long long r = (long long)blockIdx.x * kPer + wave / W;
+  if (W == 1 && r >= rows) return;  // a whole wave; with W == 4 the grid has the rows
+  const uint16_t* p = src + (size_t)r * cols;
+  uint8_t* q = codes + (size_t)r * cols;
+  const int c0 = (wave % W * kWave + lane) * 8;
+  constexpr int kStep = W * kWave * 8;
+  uint4 x[U ? U : 1];
+  uint32_t amax = 0;
+  if constexpr (U > 0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      x[i] = c0 + i * kStep < cols ? nt_load16(p + c0 + i * kStep) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < U; ++i) amax = max(amax, amax_bits8(x[i]));
+  } else {
+    for (int c = c0; c < cols; c += kStep)
+      amax = max(amax, amax_bits8(*reinterpret_cast<const uint4*>(p + c)));
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, o));
+  if constexpr (W > 1) {
+    if (lane == 0) red[wave] = amax;
+    __syncthreads();
+    amax = max(max(red[0], red[1]), max(red[2], red[3]));
+  }
+  const I8Scale s = i8_scale(amax);
+  if (wave % W == 0 && lane == 0) scales[r] = s.scale;
+  if constexpr (U > 0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (c0 + i * kStep < cols)
+        *reinterpret_cast<uint2*>(q + c0 + i * kStep) = i8_codes8(x[i], s);
+  } else {
+    for (int c = c0; c < cols; c += kStep)
+      *reinterpret_cast<uint2*>(q + c) = i8_codes8(*reinterpret_cast<const uint4*>(p + c), s);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// The products
+
+// The scales of four consecutive columns (any multiple of 4 bytes).
+MOE_DEV f32x4 col_scales(const float* p) {
+  return f32x4{p[0], p[1], p[2], p[3]};
+}
+// Rows row0 .. of the tile and columns n0 .. of its weights; a gated tile's n0 counts gate columns.
+template <bool GATED, class T>
+MOE_DEV void i8_epilogue(const I8GemmArgs& a, const T& w, int e, int row0, int rows, int n0,
+                         int cols) {
+  const float* sb = a.sb + (size_t)e * a.N;
+  const int out_n = GATED ? a.N / 2 : a.N;
+  if constexpr (!GATED) {
+    const int c0 = w.wn * T::NB * 16;
+    if (c0 >= cols) return;  // a whole wave
+    f32x4 sc[T::NB];
+#pragma unroll
+    for (int nb = 0; nb < T::NB; ++nb)
+      sc[nb] = col_scales(sb + n0 + c0 + nb * 16 + 4 * (w.lane / 16));
+#pragma unroll
+    for (int mb = 0; mb < T::MB; ++mb) {
+      const int m = w.row_of(mb);
+      const bool on = m < rows;
+      const float s = a.sa[row0 + min(m, rows - 1)];
+      f32x4 v[T::NB];
+#pragma unroll
+      for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[nb][r] = (float)w.acc[mb][nb][r] * s * sc[nb][r];
+      store_blocks<T::NB>(a.out + (size_t)(row0 + m) * out_n + n0 + c0, v, w.lane, on, false);
+    }
+  } else {
+    constexpr int NG = T::NB / 2;
+    const int c0 = n0 + w.wn * NG * 16;
+    f32x4 sg[NG], su[NG];
+#pragma unroll
+    for (int nb = 0; nb < NG; ++nb) {
+      sg[nb] = col_scales(sb + c0 + nb * 16 + 4 * (w.lane / 16));
+      su[nb] = col_scales(sb + out_n + c0 + nb * 16 + 4 * (w.lane / 16));
+    }
+    with_act(a.act, [&](auto tag) {
+#pragma unroll
+      for (int mb = 0; mb < T::MB; ++mb) {
+        const int m = w.row_of(mb);
+        const bool on = m < rows;
+        const float s = a.sa[row0 + min(m, rows - 1)];
+        f32x4 v[NG];
+#pragma unroll
+        for (int nb = 0; nb < NG; ++nb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float g = (float)w.acc[mb][nb][r] * s * sg[nb][r];
+            const float u = (float)w.acc[mb][nb + NG][r] * s * su[nb][r];
+            v[nb][r] = act_of<decltype(tag)::value>(g) * u;
+          }
+        store_blocks<NG>(a.out + (size_t)(row0 + m) * out_n + c0, v, w.lane, on, false);
+      }
+    });
+  }
+}
+
+template <int BM, int BN, bool GATED>
+MOE_DEV void i8_tile(const I8GemmArgs& a, int e, int row0, int rows, int n0) {
+  Tile8<Int8, BM, BN, false, false, GATED> w;
+  w.begin();
+  w.a_rows(a.a + (size_t)row0 * a.K, a.K, rows);
+  const uint8_t* b = a.b + (size_t)e * a.N * a.K;
+  int cols = BN;
+  if constexpr (GATED) {
+    const int I = a.N / 2;
+    w.b_rows(b, a.K, [&](int i) { return i < BN / 2 ? n0 + i : I + n0 + i - BN / 2; });
+  } else {
+    cols = min(BN, a.N - n0);  // BN, or 128 at an odd end
+    w.b_rows(b + (size_t)n0 * a.K, a.K, [&](int i) { return min(i, cols - 1); });
+  }
+  w.run(a.K / 128);
+  i8_epilogue<GATED>(a, w, e, row0, rows, n0, cols);
+}
+
+// Many rows an expert: 256 x 256 tiles, whole rounds of one a CU and then what is left, cut in two
+// (256 x 128) or four (128 x 128) where the parts still fit one round.
+template <bool GATED>
+__global__ void __launch_bounds__(512, 2) i8_big_kernel(const I8GemmArgs a) {
+  const int nN = (a.N + kBigT - 1) / kBigT;
+  const int nm = big_count(a), tiles = nm * nN;
+  const int whole = tiles / kCus * kCus, left = tiles - whole;
+  const int cut = left * 4 <= kCus ? 4 : left * 2 <= kCus ? 2 : 1;
+  const int b = blockIdx.x;
+  int lt, part = 0;
+  if (b < whole) {
+    lt = xcd_contiguous(b, whole);
+  } else {
+    const int n8 = (left * cut + kXcds - 1) / kXcds * kXcds;
+    if (b - whole >= n8) return;  // whole workgroups leave
+    const int j = xcd_contiguous(b - whole, n8);
+    if (j >= left * cut) return;
+    lt = whole + j / cut;
+    part = j % cut;
+  }
+  const int2 mn = big_order(lt, nm, nN);
+  const RowTile t = big_rows(a, mn.x);
+  if (t.rows <= 0) return;
+  constexpr int kCols = GATED ? kBigT / 2 : kBigT;  // output columns
+  const int n0 = mn.y * kCols;
+  if (b < whole || cut == 1) {
+    i8_tile<256, 256, GATED>(a, t.e, t.row0, t.rows, n0);
+    return;
+  }
+  const int c = n0 + part % 2 * (kCols / 2);
+  if (c >= (GATED ? a.N / 2 : a.N)) return;
+  if (cut == 2) {
+    i8_tile<256, 128, GATED>(a, t.e, t.row0, t.rows, c);
+  } else {
+    const int r = part / 2 * 128;
+    if (r >= t.rows) return;
+    i8_tile<128, 128, GATED>(a, t.e, t.row0 + r, min(t.rows - r, 128), c);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_i8_quant_rows(const uint16_t* src, long long rows, int cols, uint8_t* codes,
+                                float* scales, hipStream_t s) {
+  TraceScope trace("i8_quant_rows", s);
+  const auto go = [&](auto kernel, int per) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, src, rows,
+                       cols, codes, scales);
+  };
+  if (cols <= 512) go(i8_quant_rows_kernel<1, 1>, 4);
+  else if (cols <= 1024) go(i8_quant_rows_kernel<1, 2>, 4);
+  else if (cols <= 2048) go(i8_quant_rows_kernel<1, 4>, 4);
+  else if (cols <= 4096) go(i8_quant_rows_kernel<1, 8>, 4);
+  else if (cols <= 8192) go(i8_quant_rows_kernel<4, 4>, 1);
+  else if (cols <= 16384) go(i8_quant_rows_kernel<4, 8>, 1);
+  else go(i8_quant_rows_kernel<4, 0>, 1);
+  return hipGetLastError();
+}
+
+hipError_t launch_i8_gemm(const I8GemmArgs& a, bool gated, hipStream_t s) {
+  auto grid = [&](int bm, int bn) {
+    const unsigned n = (unsigned)(a.M / bm + a.E) * (unsigned)((a.N + bn - 1) / bn);
+    return dim3((n + kXcds - 1) / kXcds * kXcds);
+  };
+  TraceScope trace(gated ? "i8_gemm_gated" : "i8_gemm", s);
+  // room for every tile, and for a last round's parts
+  const dim3 big(grid(kBigT, kBigT).x + kCus);
+  if (gated) hipLaunchKernelGGL(i8_big_kernel<true>, big, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL(i8_big_kernel<false>, big, dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace moe

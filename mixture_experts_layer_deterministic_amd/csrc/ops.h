@@ -1,4 +1,5 @@
-// Internal launch interface of the gate, the router gradients and the block-scaled FP8 products
+// Internal launch interface of the gate, the router gradients, the block-scaled FP8 and int8
+// products and the dense feed-forward block
 // (kernels.h holds the layer's own). Every function only enqueues on the given stream and
 // returns the launch status.
 #pragma once
@@ -72,5 +73,45 @@ struct Fp8GemmArgs {
   int M, E, N, K;
 };
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s);
+
+// int8.hip: int8 codes with one fp32 scale a row (tokens) or output channel (weights)
+hipError_t launch_i8_quant_rows(const uint16_t* src, long long rows, int cols, uint8_t* codes,
+                                float* scales, hipStream_t s);
+struct I8GemmArgs {
+  const int32_t* offsets;  // [E + 1]
+  const uint8_t* a;        // [M, K] codes
+  const float* sa;         // [M]
+  const uint8_t* b;        // [E, N, K] codes; gated: N = 2I, gate rows then up rows
+  const float* sb;         // [E, N]
+  uint16_t* out;           // [M, N] bf16; gated [M, N / 2]
+  int M, E, N, K, act;
+};
+hipError_t launch_i8_gemm(const I8GemmArgs& a, bool gated, hipStream_t s);
+
+// ffn.hip: the dense gated feed-forward block, bf16
+struct FfnArgs {
+  const uint16_t* x;   // [T, d]
+  const uint16_t* w1;  // [2I, d]
+  const uint16_t* w2;  // [d, I]
+  uint16_t* H;         // [T, 2I]; the forward's may be null
+  uint16_t* A;         // [T, I]
+  uint16_t* y;         // [T, d]
+  const uint16_t* dy;  // [T, d]
+  uint16_t* dH;        // [T, 2I]
+  uint16_t* dx;        // [T, d]
+  int T, d, I, act, acc_y, acc_dx;
+};
+struct FfnDwArgs {
+  const uint16_t* L;  // [T, Md]
+  const uint16_t* R;  // [T, Nd]
+  void* dw;           // [Md, Nd] fp32, or (bf16_dw) bf16
+  int T, Md, Nd, acc, bf16_dw;
+  const char* name;
+};
+hipError_t launch_ffn_gate_up(const FfnArgs& a, hipStream_t s);
+hipError_t launch_ffn_down(const FfnArgs& a, hipStream_t s);
+hipError_t launch_ffn_dh(const FfnArgs& a, hipStream_t s);
+hipError_t launch_ffn_dx(const FfnArgs& a, hipStream_t s);
+hipError_t launch_ffn_dw(const FfnDwArgs& a, hipStream_t s);
 
 }  // namespace moe

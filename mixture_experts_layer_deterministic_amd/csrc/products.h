@@ -1,0 +1,402 @@
+// Products of bf16 or int8 operands for many rows: 256- and 128-wide tiles of eight waves that
+// take turns at the matrix cores, fed straight into LDS (int8.hip, ffn.hip).
+//
+// One step is 128 bytes of K: 64 bf16 values or 128 codes. Both types' MFMAs (16 x 16 x 32 bf16,
+// 16 x 16 x 64 int8) take 16 bytes a lane of either operand, so a step is two of them on each pair
+// of blocks, whatever the type. An operand lies in LDS as
+//  * K-contiguous rows of 128 bytes (frag_at): lane l takes chunks l / 16 and 4 + l / 16 of row
+//    l % 16, the first in the step's first MFMA and the other in the second; or
+//  * K-major (bf16: 64 rows of K as they lie in memory, column groups permuted by kmajor_swz), read
+//    with the transposing LDS read, which gives the same k in the same places.
+//
+// Waves w and w + 4 share a SIMD and run a phase apart: the one multiplies while the other reads its
+// fragments and sends out the next loads, and a barrier ends each phase. With two phases a half
+// step (256 x 256 tiles) the schedule is fp8.hip's:
+//     phase        4k        4k + 1    4k + 2    4k + 3    4k + 4
+//     waves 0..3   read k.0  mfma k.0  read k.1  mfma k.1  read (k+1).0
+//     waves 4..7   mfma ..   read k.0  mfma k.0  read k.1  mfma k.1
+// and smaller tiles take a step at once:
+//     phase        2k        2k + 1    2k + 2
+//     waves 0..3   read k    mfma k    read k+1
+//     waves 4..7   mfma k-1  read k    mfma k
+// Step k - 1's stage is read for the last time in phase 4k - 1 (2k - 1), so a wave fills it with step
+// k + NS - 1 in its phase read k.0 (read k). A wave waits for its own loads of step k + 1 at the end
+// of its last read phase of step k, a phase or more before anyone reads them, and leaves the
+// (NS - 2) steps behind it on their way. Loads past the last step read that one again into a stage
+// that nobody reads.
+//
+// LDS: four arrays of 32 KB and two of 16 KB, which every tile shape divides in its own way, so that
+// one kernel may hold several shapes:
+//     256 x 256   2 stages   rows x0, x1; columns x2, x3
+//     256 x 128   3 stages   rows x0, x1, x2; columns y0, y1, x3    (128 x 256: the reverse)
+//     128 x 128   4 stages   x0 .. x3, rows then columns in each
+// The stages are distinct arrays and the loop is unrolled over them, so that the compiler does not
+// wait for every load before each read.
+#pragma once
+
+#include "dma.h"
+#include "tiles8.h"
+
+namespace moe {
+namespace {
+
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+
+// Two values rounded to nearest even, NaN kept.
+MOE_DEV uint32_t to_bf2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+struct Bf16 {
+  using Acc = f32x4;
+  static constexpr int kStepK = 64;  // values of K a step
+  static MOE_DEV Acc zero() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+  // columns first: lane l gets row l % 16, columns 4 (l / 16) .. + 3
+  static MOE_DEV Acc mma(const i32x4& b, const i32x4& a, const Acc& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b),
+                                                   __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
+  }
+};
+struct Int8 {
+  using Acc = i32x4;
+  static constexpr int kStepK = 128;
+  static MOE_DEV Acc zero() { return i32x4{0, 0, 0, 0}; }
+  static MOE_DEV Acc mma(const i32x4& b, const i32x4& a, const Acc& c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, c, 0, 0, 0);
+  }
+};
+
+__shared__ __align__(1024) uint8_t prod_x0[32768];
+__shared__ __align__(1024) uint8_t prod_x1[32768];
+__shared__ __align__(1024) uint8_t prod_x2[32768];
+__shared__ __align__(1024) uint8_t prod_x3[32768];
+__shared__ __align__(1024) uint8_t prod_y0[16384];
+__shared__ __align__(1024) uint8_t prod_y1[16384];
+template <int I>
+MOE_DEV uint8_t* prod_x() {
+  if constexpr (I == 0) return prod_x0;
+  else if constexpr (I == 1) return prod_x1;
+  else if constexpr (I == 2) return prod_x2;
+  else return prod_x3;
+}
+// the operand 256 wide, and the one 128 wide, of three stages
+template <int S>
+MOE_DEV uint8_t* prod_narrow() {
+  if constexpr (S == 0) return prod_y0;
+  else if constexpr (S == 1) return prod_y1;
+  else return prod_x3;
+}
+
+MOE_DEV i32x4 lds_chunk(const uint8_t* p) { return *reinterpret_cast<const i32x4*>(p); }
+// kmajor_frag_dma for stages W values wide
+template <int W>
+MOE_DEV i32x4 kmajor_chunk(const uint8_t* st, int base, int kb, int lane) {
+  const uint16_t* s = reinterpret_cast<const uint16_t*>(st);
+  const int g = lane / 16, q = lane % 16, kr = 8 * g + q / 4;
+  const int n = (base ^ kmajor_swz(kr)) + 4 * (q % 4);
+  const s16x4 a = lds_read_tr16_scoped(s + (kb + kr) * W + n);
+  const s16x4 b = lds_read_tr16_scoped(s + (kb + kr + 4) * W + n);
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  const s16x8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(i32x4, v);
+}
+
+// AKM, BKM: that operand is K-major. GATED: columns 0 .. BN / 2 - 1 of the tile are the gate's, the
+// rest the matching ones of the up projection, and a wave's blocks half of each.
+template <class El, int BM_, int BN_, bool AKM = false, bool BKM = false, bool GATED = false>
+struct Tile8 {
+  using Acc = typename El::Acc;
+  static constexpr int BM = BM_, BN = BN_;
+  static constexpr int WM = BM == 256 && BN == 128 ? 4 : 2, WN = 8 / WM;  // waves
+  static constexpr int MB = BM / 16 / WM, NB = BN / 16 / WN;              // blocks a wave
+  static constexpr int NS = BM + BN == 512 ? 2 : BM + BN == 384 ? 3 : 4;
+  static constexpr int H = NS == 2 ? 2 : 1, HB = MB / H;                  // halves of a step
+  static constexpr int AJ = BM / 64, BJ = BN / 64;                        // loads a wave and step
+  static constexpr int kBehind = (NS - 2) * (AJ + BJ);                    // loads not waited for
+  static constexpr int kWait = 0x0070 | kBehind;                          // lgkmcnt(0) too
+  static_assert(kBehind < 16, "the low bits of vmcnt");
+  static constexpr bool kGated = GATED;
+  static constexpr bool kBf16 = sizeof(Acc) && El::kStepK == 64;
+  static_assert(kBf16 || (!AKM && !BKM), "transposing reads are 16-bit");
+
+  __amdgpu_buffer_rsrc_t ra, rb;
+  uint32_t ao[AJ], bo[BJ], astep, bstep;
+  int nK, lane, wave, wm, wn;
+  FragAt f;
+  Acc acc[MB][NB];
+
+  template <int S>
+  static MOE_DEV uint8_t* a_stage() {
+    if constexpr (NS == 2) return prod_x<S>();
+    else if constexpr (NS == 4) return prod_x<S>();
+    else if constexpr (BM == 256) return prod_x<S>();
+    else return prod_narrow<S>();
+  }
+  template <int S>
+  static MOE_DEV uint8_t* b_stage() {
+    if constexpr (NS == 2) return prod_x<2 + S>();
+    else if constexpr (NS == 4) return prod_x<S>() + 16384;
+    else if constexpr (BN == 256) return prod_x<S>();
+    else return prod_narrow<S>();
+  }
+
+  MOE_DEV void begin() {
+    lane = threadIdx.x % kWave;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    wm = wave / WN;
+    wn = wave % WN;
+    f = frag_at(lane);
+  }
+  // A's rows 0 .. rows - 1, `pitch` bytes apart; those past the end read the last one again
+  MOE_DEV void a_rows(const void* base, uint32_t pitch, int rows) {
+    ra = buf_rsrc(base);
+    astep = 128;
+#pragma unroll
+    for (int j = 0; j < AJ; ++j)
+      ao[j] = (uint32_t)min((wave * AJ + j) * 8 + lane / 8, rows - 1) * pitch + lds_piece(lane);
+  }
+  // B's rows (columns of the product): row(i) is where the tile's i-th lies
+  template <class Row>
+  MOE_DEV void b_rows(const void* base, uint32_t pitch, Row row) {
+    rb = buf_rsrc(base);
+    bstep = 128;
+#pragma unroll
+    for (int j = 0; j < BJ; ++j)
+      bo[j] = (uint32_t)row((wave * BJ + j) * 8 + lane / 8) * pitch + lds_piece(lane);
+  }
+  // K-major: `bytes` from base on hold every row of K; what lies behind reads as zeros. Of the
+  // tile's W columns `width` are there (W, or 128 of 256); the others read those again.
+  template <int W, int J>
+  MOE_DEV void k_major(uint32_t (&off)[J], uint32_t pitch, int width) {
+    constexpr int R = 512 / W;  // rows of K a load
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int kr = (wave * J + j) * R + lane / (W / 8);
+      int c = (lane % (W / 8) * 8) ^ kmajor_swz(kr);
+      c = c < width ? c : c - 128;
+      off[j] = (uint32_t)kr * pitch + 2u * c;
+    }
+  }
+  MOE_DEV void a_cols(const void* base, uint32_t pitch, uint32_t bytes, int width) {
+    ra = raw_rsrc(base, bytes);
+    astep = 64 * pitch;
+    k_major<BM>(ao, pitch, width);
+  }
+  MOE_DEV void b_cols(const void* base, uint32_t pitch, uint32_t bytes, int width) {
+    rb = raw_rsrc(base, bytes);
+    bstep = 64 * pitch;
+    k_major<BN>(bo, pitch, width);
+  }
+
+  // LDS row of a wave's column block, and the tile's column where it begins (a gated tile's: of its
+  // half)
+  MOE_DEV int b_block(int nb) const {
+    if constexpr (!GATED) return (wn * NB + nb) * 16;
+    else return nb < NB / 2 ? (wn * NB / 2 + nb) * 16 : BN / 2 + (wn * NB / 2 + nb - NB / 2) * 16;
+  }
+
+  template <int S>
+  MOE_DEV void issue(int kb) {
+    kb = min(kb, nK - 1);
+    // the range of a resource is checked against the lane's offset alone
+    const uint32_t sa = AKM ? 0u : (uint32_t)kb * 128, va = AKM ? (uint32_t)kb * astep : 0u;
+    const uint32_t sb = BKM ? 0u : (uint32_t)kb * 128, vb = BKM ? (uint32_t)kb * bstep : 0u;
+#pragma unroll
+    for (int j = 0; j < BJ; ++j)
+      load_lds16(rb, bo[j] + vb, sb, b_stage<S>() + (wave * BJ + j) * 1024);
+#pragma unroll
+    for (int j = 0; j < AJ; ++j)
+      load_lds16(ra, ao[j] + va, sa, a_stage<S>() + (wave * AJ + j) * 1024);
+  }
+  template <int S>
+  MOE_DEV i32x4 a_frag(int mb, int h) const {
+    const int r = (wm * MB + mb) * 16;
+    if constexpr (AKM) return kmajor_chunk<BM>(a_stage<S>(), r, 32 * h, lane);
+    else return lds_chunk(a_stage<S>() + r * 128 + (h ? f.hi : f.lo));
+  }
+  template <int S>
+  MOE_DEV i32x4 b_frag(int nb, int h) const {
+    const int r = b_block(nb);
+    if constexpr (BKM) return kmajor_chunk<BN>(b_stage<S>(), r, 32 * h, lane);
+    else return lds_chunk(b_stage<S>() + r * 128 + (h ? f.hi : f.lo));
+  }
+  MOE_DEV void phase_end() const {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  template <int P>
+  MOE_DEV void multiply(const i32x4 (&bf)[2][NB], const i32x4 (&af)[2][HB]) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int mb = 0; mb < HB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          acc[HB * P + mb][nb] = El::mma(bf[h][nb], af[h][mb], acc[HB * P + mb][nb]);
+    __builtin_amdgcn_s_setprio(0);
+  }
+  template <int S>
+  MOE_DEV void step(int kb) {
+    i32x4 bf[2][NB], af[2][HB];
+    issue<(S + NS - 1) % NS>(kb + NS - 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) bf[h][nb] = b_frag<S>(nb, h);
+#pragma unroll
+      for (int mb = 0; mb < HB; ++mb) af[h][mb] = a_frag<S>(mb, h);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(H == 1 ? kWait : kLgkm0);
+    phase_end();
+    multiply<0>(bf, af);
+    phase_end();
+    if constexpr (H == 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int mb = 0; mb < HB; ++mb) af[h][mb] = a_frag<S>(HB + mb, h);
+      __builtin_amdgcn_s_waitcnt(kWait);
+      phase_end();
+      multiply<1>(bf, af);
+      phase_end();
+    }
+  }
+  template <int S, int C>  // steps kb + S, .. while fewer than C and n
+  MOE_DEV void steps(int kb, int n) {
+    if constexpr (S < C) {
+      if (S < n) {
+        step<S>(kb + S);
+        steps<S + 1, C>(kb, n);
+      }
+    }
+  }
+  template <int S>
+  MOE_DEV void fill() {
+    if constexpr (S < NS - 1) {
+      issue<S>(S);
+      loads_in_order();
+      fill<S + 1>();
+    }
+  }
+  // The sums over `steps_of_k` steps (one at least) of what the operands were set to.
+  MOE_DEV void run(int steps_of_k) {
+    nK = steps_of_k;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = El::zero();
+    fill<0>();
+    __builtin_amdgcn_s_waitcnt(kWait);  // step 0
+    phase_end();
+    const bool late = wave >= 4;
+    if (late) phase_end();
+    int kb = 0;
+    for (; kb + NS <= nK; kb += NS) steps<0, NS>(kb, NS);
+    steps<0, NS - 1>(kb, nK - kb);
+    if (!late) phase_end();  // as many barriers for the early waves as for the late ones
+    // the loads past the end land before the stages are filled again or given back
+    __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
+    phase_end();
+  }
+
+  MOE_DEV int row_of(int mb) const { return (wm * MB + mb) * 16 + lane % 16; }
+};
+
+// Two side-by-side 16 x 16 blocks of bf16 results stored (with add, added in fp32 to what is
+// there): lanes l and l ^ 16 swap halves, so that each stores eight consecutive columns and a row's
+// 64 bytes leave together. row: this lane's row at the blocks' first column.
+MOE_DEV void store_pair(uint16_t* row, const f32x4& lo, const f32x4& hi, int lane, bool on,
+                        bool add) {
+  const int g = lane / 16;
+  const bool even = (g & 1) == 0;
+  float o[8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float r = __shfl_xor(even ? hi[q] : lo[q], 16);
+    o[q] = even ? lo[q] : r;
+    o[4 + q] = even ? r : hi[q];
+  }
+  if (!on) return;
+  uint4* p = reinterpret_cast<uint4*>(row + (even ? 4 * g : 12 + 4 * g));
+  if (add) {
+    const uint4 v = *p;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      o[2 * q] += bf2f_lo(w[q]);
+      o[2 * q + 1] += bf2f_hi(w[q]);
+    }
+  }
+  *p = make_uint4(to_bf2(o[0], o[1]), to_bf2(o[2], o[3]), to_bf2(o[4], o[5]), to_bf2(o[6], o[7]));
+}
+// NB blocks of a row, 16 columns each
+template <int NB>
+MOE_DEV void store_blocks(uint16_t* row, const f32x4 (&v)[NB], int lane, bool on, bool add) {
+  if constexpr (NB == 1) {
+    if (!on) return;
+    uint2* p = reinterpret_cast<uint2*>(row + 4 * (lane / 16));
+    f32x4 o = v[0];
+    if (add) {
+      const uint2 w = *p;
+      o[0] += bf2f_lo(w.x);
+      o[1] += bf2f_hi(w.x);
+      o[2] += bf2f_lo(w.y);
+      o[3] += bf2f_hi(w.y);
+    }
+    *p = make_uint2(to_bf2(o[0], o[1]), to_bf2(o[2], o[3]));
+  } else {
+#pragma unroll
+    for (int nb = 0; nb < NB; nb += 2)
+      store_pair(row + nb * 16, v[nb], v[nb + 1], lane, on, add);
+  }
+}
+
+// The activations of the gated products and their derivatives, in fp32.
+constexpr int kSilu = 0, kGelu = 1, kGeluTanh = 2, kRelu = 3;
+constexpr float kGeluC = 0.7978845608028654f, kGeluK = 0.044715f;  // sqrt(2 / pi), the cubic's
+template <int ACT>
+MOE_DEV float act_of(float g) {
+  if constexpr (ACT == kSilu) return g * sigmoid(g);
+  else if constexpr (ACT == kGelu) return 0.5f * g * erfcf(g * -0.70710678f);
+  else if constexpr (ACT == kGeluTanh)  // 0.5 (1 + tanh z) = sigmoid(2 z)
+    return g * sigmoid(2.f * kGeluC * (g + kGeluK * g * g * g));
+  else return g < 0.f ? 0.f : g;  // NaN stays
+}
+// act(g) and act'(g)
+template <int ACT>
+MOE_DEV float2 act_grad(float g) {
+  if constexpr (ACT == kSilu) {
+    const float s = sigmoid(g);
+    return make_float2(g * s, s * (1.f + g * (1.f - s)));
+  } else if constexpr (ACT == kGelu) {
+    const float p = 0.5f * erfcf(g * -0.70710678f);  // 1 + erf would cancel
+    return make_float2(g * p, p + g * 0.3989422804f * __expf(-0.5f * g * g));
+  } else if constexpr (ACT == kGeluTanh) {
+    const float s = sigmoid(2.f * kGeluC * (g + kGeluK * g * g * g));
+    return make_float2(g * s,
+                       s + g * s * (1.f - s) * (2.f * kGeluC) * (1.f + 3.f * kGeluK * g * g));
+  } else {
+    return g < 0.f ? make_float2(0.f, 0.f) : make_float2(g, g > 0.f ? 1.f : g);
+  }
+}
+template <int A>
+struct ActTag {
+  static constexpr int value = A;
+};
+// fn(ActTag<act>)
+template <class Fn>
+MOE_DEV void with_act(int act, Fn fn) {
+  switch (act) {
+    case kSilu: fn(ActTag<kSilu>()); break;
+    case kGelu: fn(ActTag<kGelu>()); break;
+    case kGeluTanh: fn(ActTag<kGeluTanh>()); break;
+    default: fn(ActTag<kRelu>()); break;
+  }
+}
+
+}  // namespace
+}  // namespace moe

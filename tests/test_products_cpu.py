@@ -1,0 +1,158 @@
+"""Host checks of the 8-bit integer products and the dense gated feed-forward block: every refusal
+happens before anything is enqueued; and the plain forms the GPU tests compare with are pinned
+against differences and exact arithmetic."""
+import ctypes
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _products as P64
+from tests._util import ensure_built
+
+m = ensure_built()
+P = ctypes.c_void_p(1 << 20)
+Q = ctypes.c_void_p(1 << 21)
+ODD = ctypes.c_void_p((1 << 20) + 2)
+ARG = m.MOE_ERR_INVALID_ARG
+
+
+def _refuses(fn, good, at, bad):
+    args = list(good)
+    args[at] = bad
+    assert fn(*args) == ARG, (fn.__name__, at, bad)
+
+
+def test_quantize_rows_refuses():
+    fn = m.lib().moe_i8_quantize_rows
+    good = (P, 4, 256, P, P, None)
+    for at, bads in ((0, (None, ODD)), (1, (-1, 1 << 24)), (2, (0, 64, 200, -128)),
+                     (3, (None, ODD)), (4, (None, ODD))):
+        for bad in bads:
+            _refuses(fn, good, at, bad)
+    assert fn(None, 0, 256, None, None, None) == 0  # no rows, no addresses
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_products_refuse(gated):
+    L = m.lib()
+    if gated:
+        fn, good = L.moe_i8_gemm_gated, [P, 4, 2, 128, 256, 0, P, P, P, P, P, None]
+        for bad in (-1, 4):
+            _refuses(fn, good, 5, bad)
+    else:
+        fn, good = L.moe_i8_gemm, [P, 4, 2, 128, 256, P, P, P, P, P, None]
+    ptr = 6 if gated else 5
+    for at in (0, ptr, ptr + 1, ptr + 2, ptr + 3, ptr + 4):
+        _refuses(fn, good, at, None)
+        _refuses(fn, good, at, ODD)
+    for at, bads in ((1, (-1,)), (2, (0, 1025, -3)), (3, (0, 64, 130, -128, 1 << 30)),
+                     (4, (0, 64, 130, 1 << 17, (1 << 17) + 128))):
+        for bad in bads:
+            _refuses(fn, good, at, bad)
+    big = list(good)
+    big[3], big[4] = 1 << 17, 1 << 14  # N K = 2^31
+    assert fn(*big) == ARG
+    big = list(good)
+    big[1], big[3] = 2 ** 31 - 1, 1 << 21  # more tiles than a grid has
+    big[4] = 128
+    assert fn(*big) == ARG
+    empty = list(good)
+    empty[1] = 0
+    empty[ptr] = empty[ptr + 1] = empty[ptr + 4] = None
+    assert fn(*empty) == 0
+
+
+def test_ffn_refuses_shapes():
+    for bad in (dict(T=0), dict(d=64), dict(d=200), dict(I=0), dict(I=130), dict(act=4),
+                dict(act=-1), dict(flags=1), dict(flags=2), dict(flags=8),
+                dict(T=1 << 20, d=2048), dict(T=1 << 20, I=1024, d=128),
+                dict(T=2 ** 31 - 1), dict(d=1 << 15, I=1 << 14)):
+        c = m.make_ffn(**{**dict(T=4, d=256, I=128), **bad})
+        with pytest.raises(m.MoeError) as e:
+            m.moe_ffn_query(c)
+        assert e.value.status == ARG, bad
+        r = ctypes.byref(c)
+        assert m.lib().moe_ffn_forward(r, P, P, P, P, P, Q, 0, P, 1 << 40, None) == ARG
+        assert m.lib().moe_ffn_backward(r, P, P, P, P, P, Q, ODD, P, P, 0, 0, P, 1 << 40,
+                                        None) == ARG
+    assert m.lib().moe_ffn_query(None, ctypes.byref(m.MoeFfnSizes())) == ARG
+    assert m.lib().moe_ffn_query(ctypes.byref(m.make_ffn(4, 256, 128)), None) == ARG
+
+
+def test_ffn_calls_refuse_pointers_and_short_workspaces():
+    L = m.lib()
+    c = m.make_ffn(4, 256, 128)
+    n = m.moe_ffn_query(c).workspace
+    r = ctypes.byref(c)
+    fwd = [r, P, P, P, P, P, Q, 0, P, n, None]
+    for at in (1, 2, 3, 4, 5, 6, 8):
+        if at != 4:  # H may be NULL
+            _refuses(L.moe_ffn_forward, fwd, at, None)
+        _refuses(L.moe_ffn_forward, fwd, at, ODD)
+    _refuses(L.moe_ffn_forward, fwd, 6, P)  # y is not x
+    short = list(fwd)
+    short[9] = n - 1
+    assert L.moe_ffn_forward(*short) == -5
+    bwd = [r, P, P, P, P, P, P, Q, P, P, 0, 0, P, n, None]
+    for at in (1, 2, 3, 4, 5, 6, 7, 8, 9, 12):
+        _refuses(L.moe_ffn_backward, bwd, at, None)
+        _refuses(L.moe_ffn_backward, bwd, at, ODD)
+    _refuses(L.moe_ffn_backward, bwd, 7, P)  # dx is neither x nor dy
+    short = list(bwd)
+    short[13] = n - 1
+    assert L.moe_ffn_backward(*short) == -5
+
+
+def test_codes_are_those_of_the_exact_quotient():
+    """Every ratio of two bf16 mantissas, and smaller values: the 64-bit form rounds as exact
+    fractions do, ties included."""
+    ties = 0
+    for b in (128, 129, 131, 170, 200, 254, 255):
+        vals = [a * 2.0 ** -s for s in range(0, 9) for a in range(128, b + 1 if s == 0 else 256)]
+        row = np.array([vals + [float(b)]])
+        codes, scales = P64.quantize_rows(row)
+        for v, c in zip(vals, codes[0]):
+            q = Fraction(127) * Fraction(v) / b
+            assert c == round(q)  # Fractions round half to even
+            ties += (q * 2).denominator == 1 and q.denominator == 2
+        assert scales[0] == np.float32(b) / np.float32(127)
+    assert ties > 20
+
+
+@pytest.mark.parametrize("a", P64.ACTS)
+def test_ffn_gradients_against_differences(a):
+    rng = np.random.default_rng(a)
+    T, d, I, h = 5, 6, 4, 1e-5
+    x, dy = rng.standard_normal((T, d)), rng.standard_normal((T, d))
+    w1, w2 = rng.standard_normal((2 * I, d)), rng.standard_normal((d, I))
+    H, A, _ = P64.ffn_forward(x, w1, w2, a)
+    assert np.abs(H).min() > 1e-3  # no ReLU corner within the step
+    _, dx, dw1, dw2 = P64.ffn_backward(x, w1, w2, H, A, dy, a)
+
+    def loss():
+        _, A, _ = P64.ffn_forward(x, w1, w2, a)
+        return float((A @ w2.T * dy).sum())
+
+    for v, g in ((x, dx), (w1, dw1), (w2, dw2)):
+        for i in np.ndindex(*v.shape):
+            keep = v[i]
+            v[i] = keep + h
+            up = loss()
+            v[i] = keep - h
+            down = loss()
+            v[i] = keep
+            # the differences' own error: h^2 times a third derivative of order 10
+            assert abs((up - down) / (2 * h) - g[i]) < 1e-6 * (1 + abs(g[i])), i
+
+
+@pytest.mark.parametrize("a", P64.ACTS)
+def test_activations_are_torchs(a):
+    g = np.linspace(-9, 9, 2001)
+    t = torch.tensor(g, requires_grad=True)
+    F = torch.nn.functional
+    y = [F.silu, F.gelu, lambda v: F.gelu(v, approximate="tanh"), F.relu][a](t)
+    y.sum().backward()
+    np.testing.assert_allclose(P64.act(a, g), y.detach().numpy(), rtol=1e-12, atol=1e-14)
+    np.testing.assert_allclose(P64.act_grad(a, g), t.grad.numpy(), rtol=1e-9, atol=1e-12)
