@@ -273,7 +273,6 @@ MOE_DEV f32x4 fp8_mfma(const i32x8& b, const i32x8& a) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0,
                                                           0, 0, 0, 0);
 }
-constexpr int kVm4Lgkm0 = 0x0074;  // s_waitcnt vmcnt(4) lgkmcnt(0)
 
 // Few rows an expert: the weights' stream is what takes the time. BM x 128 tiles, four waves of
 // BM x 32; 128 bytes of K a step go from memory straight into LDS, the weights SB - 1 steps ahead

@@ -233,6 +233,37 @@ __global__ void __launch_bounds__(512, 2) i8_big_kernel(const I8GemmArgs a) {
   }
 }
 
+template <int NMB, int SB, bool GATED>
+MOE_DEV void i8_stream(const I8GemmArgs& a, const RowTile& t, int n0, const StreamStages<SB>& L) {
+  StreamProduct<Int8, NMB, SB, GATED> w;
+  w.begin();
+  w.a_rows(a.a + (size_t)t.row0 * a.K, a.K, t.rows);
+  const int I = a.N / 2;
+  w.b_rows(a.b + (size_t)t.e * a.N * a.K, a.K, [&](int i) {
+    return !GATED ? n0 + i : i < 64 ? n0 + i : I + n0 + i - 64;
+  });
+  w.run(L, a.K / 128);
+  i8_epilogue<GATED>(a, w, t.e, t.row0, t.rows, n0, 128);
+}
+template <int BM, bool GATED>
+__global__ void __launch_bounds__(256, BM == 128 ? 2 : 4) i8_stream_kernel(const I8GemmArgs a) {
+  constexpr int SB = BM == 128 ? 3 : 2;
+  __shared__ __align__(1024) uint8_t a0[BM * 128];
+  __shared__ __align__(1024) uint8_t a1[BM * 128];
+  __shared__ __align__(1024) uint8_t b0[128 * 128];
+  __shared__ __align__(1024) uint8_t b1[128 * 128];
+  __shared__ __align__(1024) uint8_t b2[SB == 3 ? 128 * 128 : 16];
+  const StreamStages<SB> L{a0, a1, b0, b1, b2};
+  const int nN = a.N / 128, lt = blockIdx.x;
+  const RowTile t = find_rows<BM>(a.offsets, a.M, a.E, lt / nN);
+  if (t.rows <= 0) return;  // whole workgroup
+  const int n0 = lt % nN * (GATED ? 64 : 128);
+  if (BM == 32 || t.rows <= 32) i8_stream<2, SB, GATED>(a, t, n0, L);
+  else if (t.rows <= 64) i8_stream<4, SB, GATED>(a, t, n0, L);
+  else if (t.rows <= 96) i8_stream<6, SB, GATED>(a, t, n0, L);
+  else i8_stream<8, SB, GATED>(a, t, n0, L);
+}
+
 }  // namespace
 
 hipError_t launch_i8_quant_rows(const uint16_t* src, long long rows, int cols, uint8_t* codes,
@@ -258,6 +289,18 @@ hipError_t launch_i8_gemm(const I8GemmArgs& a, bool gated, hipStream_t s) {
     return dim3((n + kXcds - 1) / kXcds * kXcds);
   };
   TraceScope trace(gated ? "i8_gemm_gated" : "i8_gemm", s);
+  const long long M = a.M, E = a.E, tiles = E * (a.N / 128);
+  const double busy = (double)tiles * -std::expm1(-(double)M / (double)E);
+  if (busy > 2 * kCus && busy <= 2.75 * kCus && M <= 16 * E) {
+    if (gated) hipLaunchKernelGGL((i8_stream_kernel<32, true>), grid(32, 128), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((i8_stream_kernel<32, false>), grid(32, 128), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  if (M <= 112 * E) {
+    if (gated) hipLaunchKernelGGL((i8_stream_kernel<128, true>), grid(128, 128), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((i8_stream_kernel<128, false>), grid(128, 128), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
   // room for every tile, and for a last round's parts
   const dim3 big(grid(kBigT, kBigT).x + kCus);
   if (gated) hipLaunchKernelGGL(i8_big_kernel<true>, big, dim3(512), 0, s, a);

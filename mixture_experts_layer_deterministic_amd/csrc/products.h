@@ -306,6 +306,126 @@ struct Tile8 {
   MOE_DEV int row_of(int mb) const { return (wm * MB + mb) * 16 + lane % 16; }
 };
 
+// Few rows a weight: the weights' stream is what takes the time. Tiles of up to 128 rows and 128 of
+// the weights' rows, four waves of 32 of them each; 128 bytes of K a step go straight into LDS, the
+// weights SB - 1 steps ahead and the rows one.
+//  * 128 rows, three weight stages: 80 KB, two workgroups a CU, 64 KB of weights on their way.
+//  * 32 rows, two weight stages: 40 KB, four workgroups a CU with as much on their way.
+// A tile's K loop is compiled for 2, 4, 6 and 8 blocks of 16 rows and runs the least that hold its
+// rows. Weights that one row tile reads go past the caches (nt) up to 64 rows.
+// A wave's loads complete in order; a step issues rows, then weights, so at its top the weight loads
+// issued last may be missing if they are a step further ahead. Loads past the last step read it
+// again into a stage nobody reads, so the counts hold.
+template <int SB>
+struct StreamStages {
+  uint8_t *a0, *a1, *b0, *b1, *b2;
+  template <int S>
+  MOE_DEV uint8_t* a() const {
+    if constexpr (S == 0) return a0;
+    else return a1;
+  }
+  template <int S>
+  MOE_DEV uint8_t* b() const {
+    if constexpr (S == 0) return b0;
+    else if constexpr (S == 1) return b1;
+    else return b2;
+  }
+};
+template <class El, int NMB, int SB, bool GATED>
+struct StreamProduct {
+  static constexpr int MB = NMB, NB = 2, BN = 128;
+  static constexpr int AJ = NMB / 2;  // row loads a wave: 8 rows each
+  __amdgpu_buffer_rsrc_t ra, rb;
+  uint32_t ao[AJ], bo[4];
+  int nK, lane, wn;  // wn: the wave
+  FragAt f;
+  typename El::Acc acc[NMB][2];
+
+  MOE_DEV void begin() {
+    lane = threadIdx.x % kWave;
+    wn = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    f = frag_at(lane);
+  }
+  MOE_DEV void a_rows(const void* base, uint32_t pitch, int rows) {
+    ra = buf_rsrc(base);
+#pragma unroll
+    for (int j = 0; j < AJ; ++j)  // rows past the count read the last one again
+      ao[j] = (uint32_t)min(8 * (wn * AJ + j) + lane / 8, rows - 1) * pitch + lds_piece(lane);
+  }
+  // row(i): where the i-th of the tile's weight rows lies; a gated tile's first half are the gate's
+  template <class Row>
+  MOE_DEV void b_rows(const void* base, uint32_t pitch, Row row) {
+    rb = buf_rsrc(base);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = 8 * (wn * 4 + j) + lane / 8;  // a wave's 32: its own two blocks
+      bo[j] = (uint32_t)row(GATED ? j / 2 * 64 + wn * 16 + i % 16 : i) * pitch + lds_piece(lane);
+    }
+  }
+  template <int S>
+  MOE_DEV void issue_a(const StreamStages<SB>& L, int kb) {
+    const uint32_t step = (uint32_t)min(kb, nK - 1) * 128;
+#pragma unroll
+    for (int j = 0; j < AJ; ++j)
+      load_lds16(ra, ao[j], step, L.template a<S>() + (wn * AJ + j) * 1024);
+  }
+  template <int S>
+  MOE_DEV void issue_b(const StreamStages<SB>& L, int kb) {
+    const uint32_t step = (uint32_t)min(kb, nK - 1) * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      load_lds16<NMB <= 4 ? 2 : 0>(rb, bo[j], step, L.template b<S>() + (wn * 4 + j) * 1024);
+  }
+  template <int S>  // S: the step's number modulo the stages' common cycle
+  MOE_DEV void step(const StreamStages<SB>& L, int kb) {
+    __builtin_amdgcn_s_waitcnt(SB == 3 ? kVm4Lgkm0 : kVm0Lgkm0);
+    __builtin_amdgcn_s_barrier();
+    issue_a<(S + 1) % 2>(L, kb + 1);
+    loads_in_order();
+    issue_b<(S + SB - 1) % SB>(L, kb + SB - 1);
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* A = L.template a<S % 2>();
+    const uint8_t* B = L.template b<S % SB>() + wn * 4096;
+    const i32x4 b0l = lds_chunk(B + f.lo), b0h = lds_chunk(B + f.hi);
+    const i32x4 b1l = lds_chunk(B + 2048 + f.lo), b1h = lds_chunk(B + 2048 + f.hi);
+#pragma unroll
+    for (int mb = 0; mb < NMB; ++mb) {
+      const i32x4 al = lds_chunk(A + mb * 2048 + f.lo), ah = lds_chunk(A + mb * 2048 + f.hi);
+      acc[mb][0] = El::mma(b0l, al, acc[mb][0]);
+      acc[mb][1] = El::mma(b1l, al, acc[mb][1]);
+      acc[mb][0] = El::mma(b0h, ah, acc[mb][0]);
+      acc[mb][1] = El::mma(b1h, ah, acc[mb][1]);
+    }
+  }
+  template <int S, int C>  // steps kb + S, .. while fewer than C and n
+  MOE_DEV void steps(const StreamStages<SB>& L, int kb, int n) {
+    if constexpr (S < C) {
+      if (S < n) {
+        step<S>(L, kb + S);
+        steps<S + 1, C>(L, kb, n);
+      }
+    }
+  }
+  MOE_DEV void run(const StreamStages<SB>& L, int steps_of_k) {
+    nK = steps_of_k;
+#pragma unroll
+    for (int i = 0; i < NMB; ++i) acc[i][0] = acc[i][1] = El::zero();
+    issue_b<0>(L, 0);
+    issue_a<0>(L, 0);
+    loads_in_order();
+    if constexpr (SB == 3) issue_b<1>(L, 1);
+    // whole cycles of the stages, then the rest: a loop left from its middle would hold two sets
+    // of accumulators
+    constexpr int C = SB == 3 ? 6 : 2;
+    int kb = 0;
+    for (; kb + C <= nK; kb += C) steps<0, C>(L, kb, C);
+    steps<0, C - 1>(L, kb, nK - kb);
+    // the loads past the end land before the workgroup gives its LDS back
+    __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
+  }
+  MOE_DEV int row_of(int mb) const { return mb * 16 + lane % 16; }
+};
+
 // Two side-by-side 16 x 16 blocks of bf16 results stored (with add, added in fp32 to what is
 // there): lanes l and l ^ 16 swap halves, so that each stores eight consecutive columns and a row's
 // 64 bytes leave together. row: this lane's row at the blocks' first column.

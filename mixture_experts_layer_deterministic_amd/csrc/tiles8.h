@@ -69,6 +69,7 @@ MOE_DEV uint32_t lds_piece(int lane) { return 16u * ((lane % 8) ^ (lane / 8)); }
 // Behind it no load goes out before those in front of it: what a counted wait relies on.
 MOE_DEV void loads_in_order() { __builtin_amdgcn_sched_barrier(0x40f); }  // arithmetic may pass
 
+constexpr int kVm4Lgkm0 = 0x0074;  // s_waitcnt vmcnt(4) lgkmcnt(0)
 constexpr int kVm0Lgkm0 = 0x0070;  // s_waitcnt vmcnt(0) lgkmcnt(0)
 constexpr int kLgkm0 = 0xc07f;     // lgkmcnt(0) alone
 
