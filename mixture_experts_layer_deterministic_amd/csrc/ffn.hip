@@ -176,6 +176,35 @@ __global__ void __launch_bounds__(512, 2) ffn_dw_kernel(const FfnDwArgs a) {
   }
 }
 
+long long ceil_div(long long n, int t) { return (n + t - 1) / t; }
+
+// The tile shape for a product of m rows and n columns: that of the fewest rounds of one tile a CU,
+// each at what a step of it takes when the card is full, in us: 256 x 256 1.35, 256 x 128 0.95,
+// 128 x 128 0.67 (bytes a step 64, 48 and 32 KB). Measured, the whole call in us, 256 x 256 / 256 x
+// 128 / 128 x 128: [g | u] of 2048 x 7168 x 2048 141 / 107 / 142 (128, 256, 512 tiles), its y
+// 51 / 64 / 88 (224, 448, 896), dH 155 / 107 / 80 (64, 128, 256); [g | u] of 1777 x 4096 x 1408
+// 80 / 53 / 72 (77, 154, 308).
+enum Shape { kBig, kTall, kWide, kSmall };
+Shape tile_shape(long long m, long long n) {
+  static const struct {
+    int bm, bn;
+    float us;
+  } shapes[4] = {{256, 256, 1.35f}, {256, 128, 0.95f}, {128, 256, 0.95f}, {128, 128, 0.67f}};
+  int best = 0;
+  float least = 0.f;
+  long long fewest = 0;
+  for (int i = 0; i < 4; ++i) {
+    const long long tiles = ceil_div(m, shapes[i].bm) * ceil_div(n, shapes[i].bn);
+    const float us = (float)ceil_div(tiles, kCus) * shapes[i].us;
+    if (i == 0 || us < least || (us == least && tiles < fewest)) {
+      best = i;
+      least = us;
+      fewest = tiles;
+    }
+  }
+  return (Shape)best;
+}
+
 template <class K, class A>
 hipError_t launch_tiles(const char* name, K kernel, const A& a, long long tiles, hipStream_t s) {
   {
@@ -185,29 +214,35 @@ hipError_t launch_tiles(const char* name, K kernel, const A& a, long long tiles,
   }
   return hipGetLastError();
 }
-long long ceil_div(long long n, int t) { return (n + t - 1) / t; }
+// Kernel K<BM, BN> of the shape that fits m rows and n columns.
+#define MOE_LAUNCH_SHAPE(name, K, a, m, n, s)                                                   \
+  switch (tile_shape(m, n)) {                                                                   \
+    case kBig:                                                                                  \
+      return launch_tiles(name, K<256, 256>, a, ceil_div(m, 256) * ceil_div(n, 256), s);         \
+    case kTall:                                                                                 \
+      return launch_tiles(name, K<256, 128>, a, ceil_div(m, 256) * ceil_div(n, 128), s);         \
+    case kWide:                                                                                 \
+      return launch_tiles(name, K<128, 256>, a, ceil_div(m, 128) * ceil_div(n, 256), s);         \
+    default:                                                                                    \
+      return launch_tiles(name, K<128, 128>, a, ceil_div(m, 128) * ceil_div(n, 128), s);         \
+  }
 
 }  // namespace
 
 hipError_t launch_ffn_gate_up(const FfnArgs& a, hipStream_t s) {
-  return launch_tiles("ffn_gate_up", ffn_gate_up_kernel<256, 256>, a,
-                      ceil_div(a.T, 256) * (a.I / 128), s);
+  MOE_LAUNCH_SHAPE("ffn_gate_up", ffn_gate_up_kernel, a, a.T, 2LL * a.I, s)
 }
 hipError_t launch_ffn_down(const FfnArgs& a, hipStream_t s) {
-  return launch_tiles("ffn_down", ffn_down_kernel<256, 256>, a,
-                      ceil_div(a.T, 256) * ceil_div(a.d, 256), s);
+  MOE_LAUNCH_SHAPE("ffn_down", ffn_down_kernel, a, a.T, a.d, s)
 }
 hipError_t launch_ffn_dh(const FfnArgs& a, hipStream_t s) {
-  return launch_tiles("ffn_dh", ffn_dh_kernel<256, 256>, a,
-                      ceil_div(a.T, 256) * ceil_div(a.I, 256), s);
+  MOE_LAUNCH_SHAPE("ffn_dh", ffn_dh_kernel, a, a.T, a.I, s)
 }
 hipError_t launch_ffn_dx(const FfnArgs& a, hipStream_t s) {
-  return launch_tiles("ffn_dx", ffn_dx_kernel<256, 256>, a,
-                      ceil_div(a.T, 256) * ceil_div(a.d, 256), s);
+  MOE_LAUNCH_SHAPE("ffn_dx", ffn_dx_kernel, a, a.T, a.d, s)
 }
 hipError_t launch_ffn_dw(const FfnDwArgs& a, hipStream_t s) {
-  return launch_tiles(a.name, ffn_dw_kernel<256, 256>, a,
-                      ceil_div(a.Md, 256) * ceil_div(a.Nd, 256), s);
+  MOE_LAUNCH_SHAPE(a.name, ffn_dw_kernel, a, a.Md, a.Nd, s)
 }
 
 }  // namespace moe

@@ -10,28 +10,28 @@
 //    with the transposing LDS read, which gives the same k in the same places.
 //
 // Waves w and w + 4 share a SIMD and run a phase apart: the one multiplies while the other reads its
-// fragments and sends out the next loads, and a barrier ends each phase. With two phases a half
-// step (256 x 256 tiles) the schedule is fp8.hip's:
+// fragments and sends out loads, and a barrier ends each phase. A step is one turn of reading and one
+// of multiplying (phase 2k reads, 2k + 1 multiplies for waves 0..3, one later for waves 4..7), or in
+// the 256 x 256 tiles two:
 //     phase        4k        4k + 1    4k + 2    4k + 3    4k + 4
 //     waves 0..3   read k.0  mfma k.0  read k.1  mfma k.1  read (k+1).0
 //     waves 4..7   mfma ..   read k.0  mfma k.0  read k.1  mfma k.1
-// and smaller tiles take a step at once:
-//     phase        2k        2k + 1    2k + 2
-//     waves 0..3   read k    mfma k    read k+1
-//     waves 4..7   mfma k-1  read k    mfma k
-// Step k - 1's stage is read for the last time in phase 4k - 1 (2k - 1), so a wave fills it with step
-// k + NS - 1 in its phase read k.0 (read k). A wave waits for its own loads of step k + 1 at the end
-// of its last read phase of step k, a phase or more before anyone reads them, and leaves the
-// (NS - 2) steps behind it on their way. Loads past the last step read that one again into a stage
-// that nobody reads.
+// What a tile waits for is its loads (without the MFMAs, or without the LDS reads, the time is the
+// same; without the loads two thirds), so they go out as early as their place is free:
+//  * With NS = 3 stages and more, step k - 1's stage is read for the last time in phase 2k - 1, and a
+//    wave fills it with step k + NS - 1 in its phase read k.
+//  * The 256 x 256 tiles have two stages, each in two parts. Part 0 is what read k.0 reads: all of the
+//    columns and half of the rows' blocks, or (rows K-major) the first half of K of both. Once
+//    everyone has read it, it takes step k + 2's, in phase read k.1; part 1 takes step k + 1's in
+//    read k.0. So every load has a whole step to arrive, with 64 KB on their way throughout.
+// At the end of a reading phase a wave waits for its own loads of what the next one reads, a barrier
+// or more before anyone reads it; those issued since stay on their way. Loads past the last step
+// read that one again into a place that nobody reads.
 //
-// LDS: four arrays of 32 KB and two of 16 KB, which every tile shape divides in its own way, so that
-// one kernel may hold several shapes:
-//     256 x 256   2 stages   rows x0, x1; columns x2, x3
-//     256 x 128   3 stages   rows x0, x1, x2; columns y0, y1, x3    (128 x 256: the reverse)
-//     128 x 128   4 stages   x0 .. x3, rows then columns in each
-// The stages are distinct arrays and the loop is unrolled over them, so that the compiler does not
-// wait for every load before each read.
+// LDS: ten units of 16 KB, 128 rows of 128 bytes or 32 rows of K of 256 values. A 256-wide operand
+// takes two: K-contiguous, the first half of each wave's blocks and the second; K-major, the halves
+// of the step. The units are distinct arrays and the loop is unrolled over the stages, so that the
+// compiler sees which loads and reads meet, and does not wait for every load before each read.
 #pragma once
 
 #include "dma.h"
@@ -67,25 +67,41 @@ struct Int8 {
   }
 };
 
-__shared__ __align__(1024) uint8_t prod_x0[32768];
-__shared__ __align__(1024) uint8_t prod_x1[32768];
-__shared__ __align__(1024) uint8_t prod_x2[32768];
-__shared__ __align__(1024) uint8_t prod_x3[32768];
-__shared__ __align__(1024) uint8_t prod_y0[16384];
-__shared__ __align__(1024) uint8_t prod_y1[16384];
-template <int I>
-MOE_DEV uint8_t* prod_x() {
-  if constexpr (I == 0) return prod_x0;
-  else if constexpr (I == 1) return prod_x1;
-  else if constexpr (I == 2) return prod_x2;
-  else return prod_x3;
+__shared__ __align__(1024) uint8_t prod_u0[16384];
+__shared__ __align__(1024) uint8_t prod_u1[16384];
+__shared__ __align__(1024) uint8_t prod_u2[16384];
+__shared__ __align__(1024) uint8_t prod_u3[16384];
+__shared__ __align__(1024) uint8_t prod_u4[16384];
+__shared__ __align__(1024) uint8_t prod_u5[16384];
+__shared__ __align__(1024) uint8_t prod_u6[16384];
+__shared__ __align__(1024) uint8_t prod_u7[16384];
+__shared__ __align__(1024) uint8_t prod_u8[16384];
+__shared__ __align__(1024) uint8_t prod_u9[16384];
+template <int U>
+MOE_DEV uint8_t* prod_unit() {
+  if constexpr (U == 0) return prod_u0;
+  else if constexpr (U == 1) return prod_u1;
+  else if constexpr (U == 2) return prod_u2;
+  else if constexpr (U == 3) return prod_u3;
+  else if constexpr (U == 4) return prod_u4;
+  else if constexpr (U == 5) return prod_u5;
+  else if constexpr (U == 6) return prod_u6;
+  else if constexpr (U == 7) return prod_u7;
+  else if constexpr (U == 8) return prod_u8;
+  else return prod_u9;
 }
-// the operand 256 wide, and the one 128 wide, of three stages
-template <int S>
-MOE_DEV uint8_t* prod_narrow() {
-  if constexpr (S == 0) return prod_y0;
-  else if constexpr (S == 1) return prod_y1;
-  else return prod_x3;
+
+template <int I>
+struct Int {
+  static constexpr int value = I;
+};
+// fn(Int<0>) .. fn(Int<N - 1>)
+template <int N, int I = 0, class Fn>
+MOE_DEV void each(Fn fn) {
+  if constexpr (I < N) {
+    fn(Int<I>());
+    each<N, I + 1>(fn);
+  }
 }
 
 MOE_DEV i32x4 lds_chunk(const uint8_t* p) { return *reinterpret_cast<const i32x4*>(p); }
@@ -110,36 +126,21 @@ struct Tile8 {
   static constexpr int BM = BM_, BN = BN_;
   static constexpr int WM = BM == 256 && BN == 128 ? 4 : 2, WN = 8 / WM;  // waves
   static constexpr int MB = BM / 16 / WM, NB = BN / 16 / WN;              // blocks a wave
-  static constexpr int NS = BM + BN == 512 ? 2 : BM + BN == 384 ? 3 : 4;
-  static constexpr int H = NS == 2 ? 2 : 1, HB = MB / H;                  // halves of a step
-  static constexpr int AJ = BM / 64, BJ = BN / 64;                        // loads a wave and step
-  static constexpr int kBehind = (NS - 2) * (AJ + BJ);                    // loads not waited for
-  static constexpr int kWait = 0x0070 | kBehind;                          // lgkmcnt(0) too
+  static constexpr int AU = BM / 128, BU = BN / 128, NS = 10 / (AU + BU);  // units, stages
+  static constexpr bool kTwo = NS == 2;            // two turns a step
+  static constexpr bool kByK = AKM;                // which split K, not the rows
+  static constexpr int AJ = 2 * AU, BJ = 2 * BU;   // loads a wave and step
+  static constexpr int kBehind = kTwo ? AJ + BJ : (NS - 2) * (AJ + BJ);  // loads not waited for
+  static constexpr int kWait = 0x0070 | kBehind;   // lgkmcnt(0) too
   static_assert(kBehind < 16, "the low bits of vmcnt");
-  static constexpr bool kGated = GATED;
-  static constexpr bool kBf16 = sizeof(Acc) && El::kStepK == 64;
-  static_assert(kBf16 || (!AKM && !BKM), "transposing reads are 16-bit");
+  static_assert(El::kStepK == 64 || (!AKM && !BKM), "transposing reads are 16-bit");
+  static_assert(!AKM || BKM, "parts by K need both K-major");
 
   __amdgpu_buffer_rsrc_t ra, rb;
   uint32_t ao[AJ], bo[BJ], astep, bstep;
   int nK, lane, wave, wm, wn;
   FragAt f;
   Acc acc[MB][NB];
-
-  template <int S>
-  static MOE_DEV uint8_t* a_stage() {
-    if constexpr (NS == 2) return prod_x<S>();
-    else if constexpr (NS == 4) return prod_x<S>();
-    else if constexpr (BM == 256) return prod_x<S>();
-    else return prod_narrow<S>();
-  }
-  template <int S>
-  static MOE_DEV uint8_t* b_stage() {
-    if constexpr (NS == 2) return prod_x<2 + S>();
-    else if constexpr (NS == 4) return prod_x<S>() + 16384;
-    else if constexpr (BN == 256) return prod_x<S>();
-    else return prod_narrow<S>();
-  }
 
   MOE_DEV void begin() {
     lane = threadIdx.x % kWave;
@@ -148,13 +149,22 @@ struct Tile8 {
     wn = wave % WN;
     f = frag_at(lane);
   }
+  // The KB of an operand's units that a wave's load j fills: load j goes to unit j / 2.
+  MOE_DEV int kb_of(int j) const { return 16 * (j / 2) + 2 * wave + j % 2; }
+  // Where row L of an operand's units lies in the tile: a unit has the first (second) half of each
+  // wave's B blocks.
+  template <int U, int B>
+  static MOE_DEV int tile_row(int L) {
+    return U == 1 ? L : L % 128 / (B * 8) * (B * 16) + L / 128 * (B * 8) + L % (B * 8);
+  }
   // A's rows 0 .. rows - 1, `pitch` bytes apart; those past the end read the last one again
   MOE_DEV void a_rows(const void* base, uint32_t pitch, int rows) {
     ra = buf_rsrc(base);
     astep = 128;
 #pragma unroll
     for (int j = 0; j < AJ; ++j)
-      ao[j] = (uint32_t)min((wave * AJ + j) * 8 + lane / 8, rows - 1) * pitch + lds_piece(lane);
+      ao[j] = (uint32_t)min(tile_row<AU, MB>(kb_of(j) * 8 + lane / 8), rows - 1) * pitch +
+              lds_piece(lane);
   }
   // B's rows (columns of the product): row(i) is where the tile's i-th lies
   template <class Row>
@@ -162,8 +172,10 @@ struct Tile8 {
     rb = buf_rsrc(base);
     bstep = 128;
 #pragma unroll
-    for (int j = 0; j < BJ; ++j)
-      bo[j] = (uint32_t)row((wave * BJ + j) * 8 + lane / 8) * pitch + lds_piece(lane);
+    for (int j = 0; j < BJ; ++j) {
+      const int L = kb_of(j) * 8 + lane / 8;  // a gated tile's: gate rows, then up rows
+      bo[j] = (uint32_t)row(GATED ? L : tile_row<BU, NB>(L)) * pitch + lds_piece(lane);
+    }
   }
   // K-major: `bytes` from base on hold every row of K; what lies behind reads as zeros. Of the
   // tile's W columns `width` are there (W, or 128 of 256); the others read those again.
@@ -172,7 +184,7 @@ struct Tile8 {
     constexpr int R = 512 / W;  // rows of K a load
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int kr = (wave * J + j) * R + lane / (W / 8);
+      const int kr = kb_of(j) * R + lane / (W / 8);
       int c = (lane % (W / 8) * 8) ^ kmajor_swz(kr);
       c = c < width ? c : c - 128;
       off[j] = (uint32_t)kr * pitch + 2u * c;
@@ -189,80 +201,131 @@ struct Tile8 {
     k_major<BN>(bo, pitch, width);
   }
 
-  // LDS row of a wave's column block, and the tile's column where it begins (a gated tile's: of its
-  // half)
-  MOE_DEV int b_block(int nb) const {
-    if constexpr (!GATED) return (wn * NB + nb) * 16;
-    else return nb < NB / 2 ? (wn * NB / 2 + nb) * 16 : BN / 2 + (wn * NB / 2 + nb - NB / 2) * 16;
-  }
-
-  template <int S>
+  // Part P of step kb into stage S (P = 2: all of it)
+  template <int S, int P>
   MOE_DEV void issue(int kb) {
     kb = min(kb, nK - 1);
     // the range of a resource is checked against the lane's offset alone
     const uint32_t sa = AKM ? 0u : (uint32_t)kb * 128, va = AKM ? (uint32_t)kb * astep : 0u;
     const uint32_t sb = BKM ? 0u : (uint32_t)kb * 128, vb = BKM ? (uint32_t)kb * bstep : 0u;
-#pragma unroll
-    for (int j = 0; j < BJ; ++j)
-      load_lds16(rb, bo[j] + vb, sb, b_stage<S>() + (wave * BJ + j) * 1024);
-#pragma unroll
-    for (int j = 0; j < AJ; ++j)
-      load_lds16(ra, ao[j] + va, sa, a_stage<S>() + (wave * AJ + j) * 1024);
+    constexpr int U = S * (AU + BU);
+    auto load_a = [&](auto j) {
+      constexpr int J = decltype(j)::value;
+      if constexpr (P == 2 || P == J / 2)
+        load_lds16(ra, ao[J] + va, sa, prod_unit<U + J / 2>() + (2 * wave + J % 2) * 1024);
+    };
+    auto load_b = [&](auto j) {
+      constexpr int J = decltype(j)::value;
+      if constexpr (P == 2 || (kByK ? P == J / 2 : P == 0))
+        load_lds16(rb, bo[J] + vb, sb, prod_unit<U + AU + J / 2>() + (2 * wave + J % 2) * 1024);
+    };
+    load_b(Int<0>());
+    load_b(Int<1>());
+    if constexpr (BJ == 4) {
+      load_b(Int<2>());
+      load_b(Int<3>());
+    }
+    load_a(Int<0>());
+    load_a(Int<1>());
+    if constexpr (AJ == 4) {
+      load_a(Int<2>());
+      load_a(Int<3>());
+    }
   }
-  template <int S>
-  MOE_DEV i32x4 a_frag(int mb, int h) const {
-    const int r = (wm * MB + mb) * 16;
-    if constexpr (AKM) return kmajor_chunk<BM>(a_stage<S>(), r, 32 * h, lane);
-    else return lds_chunk(a_stage<S>() + r * 128 + (h ? f.hi : f.lo));
+  // half h of row block mb, of column block nb
+  template <int S, int M, int Hh>
+  MOE_DEV i32x4 a_frag() const {
+    constexpr int U = S * (AU + BU);
+    if constexpr (AKM && AU == 2)
+      return kmajor_chunk<256>(prod_unit<U + Hh>(), (wm * MB + M) * 16, 0, lane);
+    else if constexpr (AKM)
+      return kmajor_chunk<128>(prod_unit<U>(), (wm * MB + M) * 16, 32 * Hh, lane);
+    else if constexpr (AU == 2)
+      return lds_chunk(prod_unit<U + M / (MB / 2)>() + (wm * MB * 8 + M % (MB / 2) * 16) * 128 +
+                       (Hh ? f.hi : f.lo));
+    else
+      return lds_chunk(prod_unit<U>() + (wm * MB + M) * 2048 + (Hh ? f.hi : f.lo));
   }
-  template <int S>
-  MOE_DEV i32x4 b_frag(int nb, int h) const {
-    const int r = b_block(nb);
-    if constexpr (BKM) return kmajor_chunk<BN>(b_stage<S>(), r, 32 * h, lane);
-    else return lds_chunk(b_stage<S>() + r * 128 + (h ? f.hi : f.lo));
+  template <int S, int N, int Hh>
+  MOE_DEV i32x4 b_frag() const {
+    constexpr int U = S * (AU + BU) + AU;
+    if constexpr (BKM && BU == 2)
+      return kmajor_chunk<256>(prod_unit<U + Hh>(), (wn * NB + N) * 16, 0, lane);
+    else if constexpr (BKM)
+      return kmajor_chunk<128>(prod_unit<U>(), (wn * NB + N) * 16, 32 * Hh, lane);
+    else if constexpr (BU == 2)
+      return lds_chunk(prod_unit<U + N / (NB / 2)>() + (wn * NB * 8 + N % (NB / 2) * 16) * 128 +
+                       (Hh ? f.hi : f.lo));
+    else if constexpr (GATED)
+      return lds_chunk(prod_unit<U>() + (N / (NB / 2) * 64 + wn * NB * 8 + N % (NB / 2) * 16) * 128 +
+                       (Hh ? f.hi : f.lo));
+    else
+      return lds_chunk(prod_unit<U>() + (wn * NB + N) * 2048 + (Hh ? f.hi : f.lo));
   }
   MOE_DEV void phase_end() const {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   }
-  template <int P>
-  MOE_DEV void multiply(const i32x4 (&bf)[2][NB], const i32x4 (&af)[2][HB]) {
+  // halves H0 .. H0 + HN - 1 of row blocks M0 .. M0 + MN - 1, and of all column blocks
+  template <int S, int M0, int MN, int H0, int HN>
+  MOE_DEV void read_a(i32x4 (&af)[HN][MN]) const {
+    each<HN * MN>([&](auto i) {
+      constexpr int I = decltype(i)::value;
+      af[I / MN][I % MN] = a_frag<S, M0 + I % MN, H0 + I / MN>();
+    });
+  }
+  template <int S, int H0, int HN>
+  MOE_DEV void read_b(i32x4 (&bf)[HN][NB]) const {
+    each<HN * NB>([&](auto i) {
+      constexpr int I = decltype(i)::value;
+      bf[I / NB][I % NB] = b_frag<S, I % NB, H0 + I / NB>();
+    });
+  }
+  // the end of a reading phase, the multiplication, and its end
+  template <int M0, int MN, int HN>
+  MOE_DEV void multiply(const i32x4 (&bf)[HN][NB], const i32x4 (&af)[HN][MN]) {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(kWait);
+    phase_end();
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < HN; ++h)
 #pragma unroll
-      for (int mb = 0; mb < HB; ++mb)
+      for (int mb = 0; mb < MN; ++mb)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
-          acc[HB * P + mb][nb] = El::mma(bf[h][nb], af[h][mb], acc[HB * P + mb][nb]);
+          acc[M0 + mb][nb] = El::mma(bf[h][nb], af[h][mb], acc[M0 + mb][nb]);
     __builtin_amdgcn_s_setprio(0);
+    phase_end();
   }
   template <int S>
   MOE_DEV void step(int kb) {
-    i32x4 bf[2][NB], af[2][HB];
-    issue<(S + NS - 1) % NS>(kb + NS - 1);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) bf[h][nb] = b_frag<S>(nb, h);
-#pragma unroll
-      for (int mb = 0; mb < HB; ++mb) af[h][mb] = a_frag<S>(mb, h);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(H == 1 ? kWait : kLgkm0);
-    phase_end();
-    multiply<0>(bf, af);
-    phase_end();
-    if constexpr (H == 2) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int mb = 0; mb < HB; ++mb) af[h][mb] = a_frag<S>(HB + mb, h);
-      __builtin_amdgcn_s_waitcnt(kWait);
-      phase_end();
-      multiply<1>(bf, af);
-      phase_end();
+    if constexpr (!kTwo) {
+      i32x4 bf[2][NB], af[2][MB];
+      issue<(S + NS - 1) % NS, 2>(kb + NS - 1);
+      read_b<S, 0, 2>(bf);
+      read_a<S, 0, MB, 0, 2>(af);
+      multiply<0, MB, 2>(bf, af);
+    } else if constexpr (kByK) {
+      i32x4 bf[1][NB], af[1][MB];
+      issue<S ^ 1, 1>(kb + 1);
+      read_b<S, 0, 1>(bf);
+      read_a<S, 0, MB, 0, 1>(af);
+      multiply<0, MB, 1>(bf, af);
+      issue<S, 0>(kb + 2);
+      read_b<S, 1, 1>(bf);
+      read_a<S, 0, MB, 1, 1>(af);
+      multiply<0, MB, 1>(bf, af);
+    } else {
+      i32x4 bf[2][NB], af[2][MB / 2];
+      issue<S ^ 1, 1>(kb + 1);
+      read_b<S, 0, 2>(bf);
+      read_a<S, 0, MB / 2, 0, 2>(af);
+      multiply<0, MB / 2, 2>(bf, af);
+      issue<S, 0>(kb + 2);
+      read_a<S, MB / 2, MB / 2, 0, 2>(af);
+      multiply<MB / 2, MB / 2, 2>(bf, af);
     }
   }
   template <int S, int C>  // steps kb + S, .. while fewer than C and n
@@ -277,7 +340,7 @@ struct Tile8 {
   template <int S>
   MOE_DEV void fill() {
     if constexpr (S < NS - 1) {
-      issue<S>(S);
+      issue<S, 2>(S);
       loads_in_order();
       fill<S + 1>();
     }
@@ -289,8 +352,16 @@ struct Tile8 {
     for (int i = 0; i < MB; ++i)
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = El::zero();
-    fill<0>();
-    __builtin_amdgcn_s_waitcnt(kWait);  // step 0
+    if constexpr (kTwo) {
+      issue<0, 0>(0);
+      loads_in_order();
+      issue<0, 1>(0);
+      loads_in_order();
+      issue<1, 0>(1);
+    } else {
+      fill<0>();
+    }
+    __builtin_amdgcn_s_waitcnt(kWait);  // what step 0 reads first
     phase_end();
     const bool late = wave >= 4;
     if (late) phase_end();
@@ -298,7 +369,7 @@ struct Tile8 {
     for (; kb + NS <= nK; kb += NS) steps<0, NS>(kb, NS);
     steps<0, NS - 1>(kb, nK - kb);
     if (!late) phase_end();  // as many barriers for the early waves as for the late ones
-    // the loads past the end land before the stages are filled again or given back
+    // the loads past the end land before the units are filled again or given back
     __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
     phase_end();
   }
