@@ -280,11 +280,12 @@ int check_ffn(const moe_ffn* f) {
   return MOE_OK;
 }
 struct FfnLayout {
-  size_t dH, total;
+  size_t dH, part, total;
 };
 FfnLayout ffn_layout(const moe_ffn* f) {
   FfnLayout L{};
-  L.total = align_up(2 * (size_t)f->T * 2 * f->I);
+  L.part = align_up(2 * (size_t)f->T * 2 * f->I);
+  L.total = L.part + kFfnPartBytes;
   return L;
 }
 
@@ -951,6 +952,7 @@ int moe_ffn_forward(const moe_ffn* ffn, const void* x, const void* w1, const voi
   a.d = ffn->d;
   a.I = ffn->I;
   a.act = ffn->act;
+  a.part = at<float>(workspace, Y.part);
   a.acc_y = acc_y != 0;
   Launches L;
   L(launch_ffn_gate_up(a, s));
@@ -978,6 +980,7 @@ int moe_ffn_backward(const moe_ffn* ffn, const void* x, const void* w1, const vo
   a.H = const_cast<uint16_t*>(static_cast<const uint16_t*>(H));
   a.dy = static_cast<const uint16_t*>(dy);
   a.dH = at<uint16_t>(workspace, Y.dH);
+  a.part = at<float>(workspace, Y.part);
   a.dx = static_cast<uint16_t*>(dx);
   a.T = ffn->T;
   a.d = ffn->d;

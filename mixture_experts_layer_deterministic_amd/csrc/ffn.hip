@@ -2,8 +2,8 @@
 //   [g | u] = x W1^T    A = act(g) u    y (+)= A W2^T
 //   dA = dy W2    dH = bf16([dA u act'(g) | dA act(g)])
 //   dx (+)= dH W1    dW1 (+)= dH^T x    dW2 (+)= dy^T A
-// Sums are fp32 in ascending order of K. A is formed from the fp32 g and u, dH from the bf16 H that
-// the forward stored, and both are rounded once, as the next product reads them.
+// Sums are fp32 in a fixed order. A is formed from the fp32 g and u, dH from the bf16 H that the
+// forward stored, and both are rounded once, as the next product reads them.
 #include <algorithm>
 
 #include "common.h"
@@ -11,169 +11,322 @@
 #include "ops.h"
 #include "products.h"
 
+#define MOE_BOTH static __host__ __device__ __forceinline__
+
 namespace moe {
 namespace {
 
-// Tile b of a grid of nm x nN tiles, dealt so that an XCD's share is contiguous; x < 0: none.
-MOE_DEV int2 dense_tile(int b, int grid, int nm, int nN) {
-  const int lt = xcd_contiguous(b, grid);
-  return lt < nm * nN ? big_order(lt, nm, nN) : make_int2(-1, 0);
-}
-MOE_DEV int tiles_of(int n, int t) { return (n + t - 1) / t; }
+// The five products. Each has rows m x columns n (a gated one: of its weights) over steps of K, the
+// layouts of its operands, how a tile reads them from step k0 on, and what becomes of its sums:
+// store(w) for the rows row0 .. row0 + rows - 1 and columns n0 .. of the result, `cols` of the tile's
+// columns being there. w.acc holds the sums, for rows w.row_of(mb) and column blocks of wave w.wn.
 
 // A and, if it is wanted, H = [g | u].
-template <int BM, int BN>
-__global__ void __launch_bounds__(512, 2) ffn_gate_up_kernel(const FfnArgs a) {
-  constexpr int kCols = BN / 2;
-  const int2 mn = dense_tile(blockIdx.x, gridDim.x, tiles_of(a.T, BM), a.I / kCols);
-  if (mn.x < 0) return;
-  const int row0 = mn.x * BM, rows = min(a.T - row0, BM), n0 = mn.y * kCols;
-  Tile8<Bf16, BM, BN, false, false, true> w;
-  w.begin();
-  w.a_rows(a.x + (size_t)row0 * a.d, 2 * a.d, rows);
-  const int I = a.I;
-  w.b_rows(a.w1, 2 * a.d, [&](int i) { return i < kCols ? n0 + i : I + n0 + i - kCols; });
-  w.run(a.d / 64);
-  constexpr int NG = w.NB / 2;
-  const int c0 = n0 + w.wn * NG * 16;
-  with_act(a.act, [&](auto tag) {
-#pragma unroll
-    for (int mb = 0; mb < w.MB; ++mb) {
-      const int m = w.row_of(mb);
-      const bool on = m < rows;
-      f32x4 g[NG], u[NG], v[NG];
-#pragma unroll
-      for (int nb = 0; nb < NG; ++nb) {
-        g[nb] = w.acc[mb][nb];
-        u[nb] = w.acc[mb][nb + NG];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[nb][r] = act_of<decltype(tag)::value>(g[nb][r]) * u[nb][r];
-      }
-      const size_t row = row0 + m;
-      store_blocks<NG>(a.A + row * I + c0, v, w.lane, on, false);
-      if (a.H) {
-        store_blocks<NG>(a.H + row * 2 * I + c0, g, w.lane, on, false);
-        store_blocks<NG>(a.H + row * 2 * I + I + c0, u, w.lane, on, false);
-      }
-    }
-  });
-}
-
-// out (+)= L R^T with both K-contiguous: y from A and W2.
-template <int BM, int BN>
-__global__ void __launch_bounds__(512, 2) ffn_down_kernel(const FfnArgs a) {
-  const int2 mn = dense_tile(blockIdx.x, gridDim.x, tiles_of(a.T, BM), tiles_of(a.d, BN));
-  if (mn.x < 0) return;
-  const int row0 = mn.x * BM, rows = min(a.T - row0, BM), n0 = mn.y * BN;
-  const int cols = min(BN, a.d - n0);
-  Tile8<Bf16, BM, BN> w;
-  w.begin();
-  w.a_rows(a.A + (size_t)row0 * a.I, 2 * a.I, rows);
-  w.b_rows(a.w2 + (size_t)n0 * a.I, 2 * a.I, [&](int i) { return min(i, cols - 1); });
-  w.run(a.I / 64);
-  const int c0 = w.wn * w.NB * 16;
-  if (c0 >= cols) return;
-#pragma unroll
-  for (int mb = 0; mb < w.MB; ++mb) {
-    const int m = w.row_of(mb);
-    store_blocks<w.NB>(a.y + (size_t)(row0 + m) * a.d + n0 + c0, w.acc[mb], w.lane, m < rows,
-                       a.acc_y);
+struct GateUp {
+  using Args = FfnArgs;
+  static constexpr bool kAKM = false, kBKM = false, kGated = true;
+  static constexpr const char* kName = "ffn_gate_up";
+  MOE_BOTH long long m(const Args& a) { return a.T; }
+  MOE_BOTH long long n(const Args& a) { return 2LL * a.I; }
+  MOE_BOTH int steps(const Args& a) { return a.d / 64; }
+  template <class W>
+  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int, int k0) {
+    w.a_rows(a.x + (size_t)row0 * a.d + 64 * k0, 2 * a.d, rows);
+    const int I = a.I;
+    w.b_rows(a.w1 + 64 * k0, 2 * a.d,
+             [&](int i) { return i < W::BN / 2 ? n0 + i : I + n0 + i - W::BN / 2; });
   }
-}
-
-// dH from dA = dy W2 and H. W2 is [d, I]: K-major.
-template <int BM, int BN>
-__global__ void __launch_bounds__(512, 2) ffn_dh_kernel(const FfnArgs a) {
-  const int2 mn = dense_tile(blockIdx.x, gridDim.x, tiles_of(a.T, BM), tiles_of(a.I, BN));
-  if (mn.x < 0) return;
-  const int row0 = mn.x * BM, rows = min(a.T - row0, BM), n0 = mn.y * BN;
-  const int cols = min(BN, a.I - n0), I = a.I;
-  Tile8<Bf16, BM, BN, false, true> w;
-  w.begin();
-  w.a_rows(a.dy + (size_t)row0 * a.d, 2 * a.d, rows);
-  w.b_cols(a.w2 + n0, 2 * I, 2u * a.d * I, cols);
-  w.run(a.d / 64);
-  const int c0 = w.wn * w.NB * 16;
-  if (c0 >= cols) return;
-  with_act(a.act, [&](auto tag) {
+  template <class W>
+  static MOE_DEV void store(const Args& a, const W& w, int row0, int rows, int n0, int) {
+    constexpr int NG = W::NB / 2;
+    const int c0 = n0 + w.wn * NG * 16, I = a.I;
+    with_act(a.act, [&](auto tag) {
 #pragma unroll
-    for (int mb = 0; mb < w.MB; ++mb) {
-      const int m = w.row_of(mb);
-      const bool on = m < rows;
-      const size_t at = (size_t)(row0 + min(m, rows - 1)) * 2 * I + n0 + c0;
-      f32x4 dg[w.NB], du[w.NB];
+      for (int mb = 0; mb < W::MB; ++mb) {
+        const int m = w.row_of(mb);
+        const bool on = m < rows;
+        f32x4 g[NG], u[NG], v[NG];
 #pragma unroll
-      for (int nb = 0; nb < w.NB; ++nb) {
-        const int c = nb * 16 + 4 * (w.lane / 16);
-        const uint2 gv = *reinterpret_cast<const uint2*>(a.H + at + c);
-        const uint2 uv = *reinterpret_cast<const uint2*>(a.H + at + I + c);
-        const float g4[4] = {bf2f_lo(gv.x), bf2f_hi(gv.x), bf2f_lo(gv.y), bf2f_hi(gv.y)};
-        const float u4[4] = {bf2f_lo(uv.x), bf2f_hi(uv.x), bf2f_lo(uv.y), bf2f_hi(uv.y)};
+        for (int nb = 0; nb < NG; ++nb) {
+          g[nb] = w.acc[mb][nb];
+          u[nb] = w.acc[mb][nb + NG];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float da = w.acc[mb][nb][r];
-          const float2 f = act_grad<decltype(tag)::value>(g4[r]);
-          dg[nb][r] = da * u4[r] * f.y;
-          du[nb][r] = da * f.x;
+          for (int r = 0; r < 4; ++r) v[nb][r] = act_of<decltype(tag)::value>(g[nb][r]) * u[nb][r];
+        }
+        const size_t row = row0 + m;
+        store_blocks<NG>(a.A + row * I + c0, v, w.lane, on, false);
+        if (a.H) {
+          store_blocks<NG>(a.H + row * 2 * I + c0, g, w.lane, on, false);
+          store_blocks<NG>(a.H + row * 2 * I + I + c0, u, w.lane, on, false);
         }
       }
-      store_blocks<w.NB>(a.dH + at, dg, w.lane, on, false);
-      store_blocks<w.NB>(a.dH + at + I, du, w.lane, on, false);
-    }
-  });
-}
+    });
+  }
+};
 
-// dx (+)= dH W1. W1 is [2I, d]: K-major.
-template <int BM, int BN>
-__global__ void __launch_bounds__(512, 2) ffn_dx_kernel(const FfnArgs a) {
-  const int2 mn = dense_tile(blockIdx.x, gridDim.x, tiles_of(a.T, BM), tiles_of(a.d, BN));
-  if (mn.x < 0) return;
-  const int row0 = mn.x * BM, rows = min(a.T - row0, BM), n0 = mn.y * BN;
-  const int cols = min(BN, a.d - n0);
-  Tile8<Bf16, BM, BN, false, true> w;
-  w.begin();
-  w.a_rows(a.dH + (size_t)row0 * 2 * a.I, 4 * a.I, rows);
-  w.b_cols(a.w1 + n0, 2 * a.d, 4u * a.I * a.d, cols);
-  w.run(2 * a.I / 64);
-  const int c0 = w.wn * w.NB * 16;
+template <class W>
+MOE_DEV void store_rows(uint16_t* out, int ld, bool add, const W& w, int row0, int rows, int n0,
+                        int cols) {
+  const int c0 = w.wn * W::NB * 16;
   if (c0 >= cols) return;
 #pragma unroll
-  for (int mb = 0; mb < w.MB; ++mb) {
+  for (int mb = 0; mb < W::MB; ++mb) {
     const int m = w.row_of(mb);
-    store_blocks<w.NB>(a.dx + (size_t)(row0 + m) * a.d + n0 + c0, w.acc[mb], w.lane, m < rows,
-                       a.acc_dx);
+    store_blocks<W::NB>(out + (size_t)(row0 + m) * ld + n0 + c0, w.acc[mb], w.lane, m < rows, add);
   }
 }
 
+// y (+)= A W2^T
+struct Down {
+  using Args = FfnArgs;
+  static constexpr bool kAKM = false, kBKM = false, kGated = false;
+  static constexpr const char* kName = "ffn_down";
+  MOE_BOTH long long m(const Args& a) { return a.T; }
+  MOE_BOTH long long n(const Args& a) { return a.d; }
+  MOE_BOTH int steps(const Args& a) { return a.I / 64; }
+  template <class W>
+  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int cols, int k0) {
+    w.a_rows(a.A + (size_t)row0 * a.I + 64 * k0, 2 * a.I, rows);
+    w.b_rows(a.w2 + (size_t)n0 * a.I + 64 * k0, 2 * a.I, [&](int i) { return min(i, cols - 1); });
+  }
+  template <class W>
+  static MOE_DEV void store(const Args& a, const W& w, int row0, int rows, int n0, int cols) {
+    store_rows(a.y, a.d, a.acc_y, w, row0, rows, n0, cols);
+  }
+};
+
+// dH from dA = dy W2 and H. W2 is [d, I]: K-major.
+struct Dh {
+  using Args = FfnArgs;
+  static constexpr bool kAKM = false, kBKM = true, kGated = false;
+  static constexpr const char* kName = "ffn_dh";
+  MOE_BOTH long long m(const Args& a) { return a.T; }
+  MOE_BOTH long long n(const Args& a) { return a.I; }
+  MOE_BOTH int steps(const Args& a) { return a.d / 64; }
+  template <class W>
+  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int cols, int k0) {
+    w.a_rows(a.dy + (size_t)row0 * a.d + 64 * k0, 2 * a.d, rows);
+    w.b_cols(a.w2 + (size_t)64 * k0 * a.I + n0, 2 * a.I, 2u * (a.d - 64 * k0) * a.I, cols);
+  }
+  template <class W>
+  static MOE_DEV void store(const Args& a, const W& w, int row0, int rows, int n0, int cols) {
+    const int c0 = w.wn * W::NB * 16, I = a.I;
+    if (c0 >= cols) return;
+    with_act(a.act, [&](auto tag) {
+#pragma unroll
+      for (int mb = 0; mb < W::MB; ++mb) {
+        const int m = w.row_of(mb);
+        const bool on = m < rows;
+        const size_t at = (size_t)(row0 + min(m, rows - 1)) * 2 * I + n0 + c0;
+        f32x4 dg[W::NB], du[W::NB];
+#pragma unroll
+        for (int nb = 0; nb < W::NB; ++nb) {
+          const int c = nb * 16 + 4 * (w.lane / 16);
+          const uint2 gv = *reinterpret_cast<const uint2*>(a.H + at + c);
+          const uint2 uv = *reinterpret_cast<const uint2*>(a.H + at + I + c);
+          const float g4[4] = {bf2f_lo(gv.x), bf2f_hi(gv.x), bf2f_lo(gv.y), bf2f_hi(gv.y)};
+          const float u4[4] = {bf2f_lo(uv.x), bf2f_hi(uv.x), bf2f_lo(uv.y), bf2f_hi(uv.y)};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float da = w.acc[mb][nb][r];
+            const float2 f = act_grad<decltype(tag)::value>(g4[r]);
+            dg[nb][r] = da * u4[r] * f.y;
+            du[nb][r] = da * f.x;
+          }
+        }
+        store_blocks<W::NB>(a.dH + at, dg, w.lane, on, false);
+        store_blocks<W::NB>(a.dH + at + I, du, w.lane, on, false);
+      }
+    });
+  }
+};
+
+// dx (+)= dH W1. W1 is [2I, d]: K-major.
+struct Dx {
+  using Args = FfnArgs;
+  static constexpr bool kAKM = false, kBKM = true, kGated = false;
+  static constexpr const char* kName = "ffn_dx";
+  MOE_BOTH long long m(const Args& a) { return a.T; }
+  MOE_BOTH long long n(const Args& a) { return a.d; }
+  MOE_BOTH int steps(const Args& a) { return 2 * a.I / 64; }
+  template <class W>
+  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int cols, int k0) {
+    w.a_rows(a.dH + (size_t)row0 * 2 * a.I + 64 * k0, 4 * a.I, rows);
+    w.b_cols(a.w1 + (size_t)64 * k0 * a.d + n0, 2 * a.d, 2u * (2 * a.I - 64 * k0) * a.d, cols);
+  }
+  template <class W>
+  static MOE_DEV void store(const Args& a, const W& w, int row0, int rows, int n0, int cols) {
+    store_rows(a.dx, a.d, a.acc_dx, w, row0, rows, n0, cols);
+  }
+};
+
 // dW [Md, Nd] (+)= L^T R over the tokens, both operands K-major; rows past the last are zeros.
-template <int BM, int BN>
-__global__ void __launch_bounds__(512, 2) ffn_dw_kernel(const FfnDwArgs a) {
-  const int2 mn = dense_tile(blockIdx.x, gridDim.x, tiles_of(a.Md, BM), tiles_of(a.Nd, BN));
-  if (mn.x < 0) return;
-  const int m0 = mn.x * BM, n0 = mn.y * BN;
-  const int rows = min(BM, a.Md - m0), cols = min(BN, a.Nd - n0);
-  Tile8<Bf16, BM, BN, true, true> w;
-  w.begin();
-  w.a_cols(a.L + m0, 2 * a.Md, 2u * a.T * a.Md, rows);
-  w.b_cols(a.R + n0, 2 * a.Nd, 2u * a.T * a.Nd, cols);
-  w.run((a.T + 63) / 64);
-  const int c0 = w.wn * w.NB * 16;
-  if (c0 >= cols) return;
-#pragma unroll
-  for (int mb = 0; mb < w.MB; ++mb) {
-    const int m = w.row_of(mb);
-    const size_t at = (size_t)(m0 + m) * a.Nd + n0 + c0;
+struct Dw {
+  using Args = FfnDwArgs;
+  static constexpr bool kAKM = true, kBKM = true, kGated = false;
+  MOE_BOTH long long m(const Args& a) { return a.Md; }
+  MOE_BOTH long long n(const Args& a) { return a.Nd; }
+  MOE_BOTH int steps(const Args& a) { return (a.T + 63) / 64; }
+  template <class W>
+  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int cols, int) {
+    w.a_cols(a.L + row0, 2 * a.Md, 2u * a.T * a.Md, rows);
+    w.b_cols(a.R + n0, 2 * a.Nd, 2u * a.T * a.Nd, cols);
+  }
+  template <class W>
+  static MOE_DEV void store(const Args& a, const W& w, int row0, int rows, int n0, int cols) {
     if (a.bf16_dw) {
-      store_blocks<w.NB>(static_cast<uint16_t*>(a.dw) + at, w.acc[mb], w.lane, m < rows, a.acc);
-    } else if (m < rows) {
-      float* p = static_cast<float*>(a.dw) + at + 4 * (w.lane / 16);
+      store_rows(static_cast<uint16_t*>(a.dw), a.Nd, a.acc, w, row0, rows, n0, cols);
+      return;
+    }
+    const int c0 = w.wn * W::NB * 16;
+    if (c0 >= cols) return;
 #pragma unroll
-      for (int nb = 0; nb < w.NB; ++nb) {
+    for (int mb = 0; mb < W::MB; ++mb) {
+      const int m = w.row_of(mb);
+      if (m >= rows) continue;
+      float* p = static_cast<float*>(a.dw) + (size_t)(row0 + m) * a.Nd + n0 + c0 +
+                 4 * (w.lane / 16);
+#pragma unroll
+      for (int nb = 0; nb < W::NB; ++nb) {
         if (a.acc) store_dw4<true>(p + nb * 16, w.acc[mb][nb]);
         else store_dw4<false>(p + nb * 16, w.acc[mb][nb]);
       }
     }
   }
+};
+
+// ------------------------------------------------------------------------------------------
+// Where tile lt of P lies
+struct Place {
+  int row0, rows, n0, cols;
+};
+template <class P, int BM, int BN>
+MOE_DEV Place place_of(const typename P::Args& a, int lt) {
+  const int m = (int)P::m(a), n = (int)P::n(a);
+  const int2 mn = big_order(lt, (m + BM - 1) / BM, (n + BN - 1) / BN);
+  return {mn.x * BM, min(m - mn.x * BM, BM), mn.y * (P::kGated ? BN / 2 : BN),
+          min(n - mn.y * BN, BN)};
+}
+template <class P, int BM, int BN>
+MOE_BOTH long long tiles_of(const typename P::Args& a) {
+  return (P::m(a) + BM - 1) / BM * ((P::n(a) + BN - 1) / BN);
+}
+
+// A tile a workgroup, an XCD's share contiguous.
+template <class P, int BM, int BN>
+__global__ void __launch_bounds__(512, 2) ffn_kernel(const typename P::Args a) {
+  const int lt = xcd_contiguous(blockIdx.x, gridDim.x);
+  if (lt >= tiles_of<P, BM, BN>(a)) return;
+  const Place t = place_of<P, BM, BN>(a, lt);
+  Tile8<Bf16, BM, BN, P::kAKM, P::kBKM, P::kGated> w;
+  w.begin();
+  P::setup(a, w, t.row0, t.rows, t.n0, t.cols, 0);
+  w.run(P::steps(a));
+  P::store(a, w, t.row0, t.rows, t.n0, t.cols);
+}
+
+// Few tiles: the steps of K in S shares, as even as they come, and a workgroup for each share of
+// each 128 x 128 tile. Its sums go to memory as the lanes hold them (a.part), and
+// a second kernel, a wave for 16 rows of a wave's columns, adds the shares in order and stores.
+template <class P>
+__global__ void __launch_bounds__(512, 2) ffn_split_kernel(const typename P::Args a) {
+  const int S = a.shares, tiles = (int)tiles_of<P, 128, 128>(a);
+  const int j = xcd_contiguous(blockIdx.x, gridDim.x);
+  if (j >= tiles * S) return;
+  // one share of every tile, then the next: an XCD's tiles share their steps of K
+  const int share = j / tiles, lt = j % tiles;
+  const Place t = place_of<P, 128, 128>(a, lt);
+  const int nk = P::steps(a), k0 = (int)((long long)nk * share / S);
+  const int k1 = (int)((long long)nk * (share + 1) / S);
+  using W = Tile8<Bf16, 128, 128, P::kAKM, P::kBKM, P::kGated>;
+  W w;
+  w.begin();
+  P::setup(a, w, t.row0, t.rows, t.n0, t.cols, k0);
+  w.run(k1 - k0);
+  f32x4* p = reinterpret_cast<f32x4*>(a.part) +
+             ((size_t)(lt * S + share) * 8 + w.wave) * (W::MB * W::NB * kWave) + w.lane;
+#pragma unroll
+  for (int mb = 0; mb < W::MB; ++mb) {
+    if ((w.wm * W::MB + mb) * 16 >= t.rows) continue;
+#pragma unroll
+    for (int nb = 0; nb < W::NB; ++nb) p[(mb * W::NB + nb) * kWave] = w.acc[mb][nb];
+  }
+}
+template <class T>
+struct JoinedRows {  // one row block of a wave of tile T
+  static constexpr int MB = 1, NB = T::NB, BN = T::BN;
+  int lane, wn, row0;
+  f32x4 acc[1][NB];
+  MOE_DEV int row_of(int) const { return row0 + lane % 16; }
+};
+template <class P>
+__global__ void __launch_bounds__(256) ffn_join_kernel(const typename P::Args a) {
+  using T = Tile8<Bf16, 128, 128, P::kAKM, P::kBKM, P::kGated>;
+  const int S = a.shares, lt = blockIdx.x / (2 * T::MB);
+  const int b = blockIdx.x % (2 * T::MB) * 4 + threadIdx.x / kWave;  // row block of the tile's waves
+  const int wave = b / T::MB, mb = b % T::MB;
+  const Place t = place_of<P, 128, 128>(a, lt);
+  JoinedRows<T> w;
+  w.lane = threadIdx.x % kWave;
+  w.wn = wave % T::WN;
+  w.row0 = (wave / T::WN * T::MB + mb) * 16;
+  if (w.row0 >= t.rows) return;  // a whole wave
+  const f32x4* p = reinterpret_cast<const f32x4*>(a.part) +
+                   ((size_t)lt * S * 8 + wave) * (T::MB * T::NB * kWave) + mb * T::NB * kWave +
+                   w.lane;
+#pragma unroll
+  for (int nb = 0; nb < T::NB; ++nb) w.acc[0][nb] = p[nb * kWave];
+#pragma unroll 8
+  for (int s = 1; s < S; ++s) {
+    p += 8 * T::MB * T::NB * kWave;
+#pragma unroll
+    for (int nb = 0; nb < T::NB; ++nb) w.acc[0][nb] += p[nb * kWave];
+  }
+  P::store(a, w, t.row0, t.rows, t.n0, t.cols);
+}
+
+// A handful of tokens: up to 16, a workgroup for 8 columns of A.
+__global__ void __launch_bounds__(512, 4) ffn_skinny_gate_up_kernel(const FfnArgs a) {
+  __shared__ f32x4 red[8 * kWave];
+  const int n0 = blockIdx.x * 8, I = a.I;
+  SkinnyProduct<Bf16, 1, 1, 4> w;
+  w.begin();
+  w.a_rows(a.x, 2 * a.d, a.T);
+  w.b_rows(a.w1, 2 * a.d, [&](int i) { return n0 + (i < 8 ? i : I + i - 8); });
+  w.run(a.d / 64, red);
+  if (w.wave > 0) return;
+  // lanes 0..31 hold four gate columns of a row, lanes 32..63 the matching ups
+  const int m = w.lane % 16, c = n0 + 4 * (w.lane / 16 % 2);
+  const f32x4 v = w.acc[0][0];
+  f32x4 u;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) u[r] = __shfl_xor(v[r], 32);
+  if (m >= a.T) return;
+  if (a.H)
+    *reinterpret_cast<uint2*>(a.H + (size_t)m * 2 * I + (w.lane < 32 ? 0 : I) + c) =
+        make_uint2(to_bf2(v[0], v[1]), to_bf2(v[2], v[3]));
+  if (w.lane >= 32) return;
+  with_act(a.act, [&](auto tag) {
+    constexpr int A = decltype(tag)::value;
+    *reinterpret_cast<uint2*>(a.A + (size_t)m * I + c) =
+        make_uint2(to_bf2(act_of<A>(v[0]) * u[0], act_of<A>(v[1]) * u[1]),
+                   to_bf2(act_of<A>(v[2]) * u[2], act_of<A>(v[3]) * u[3]));
+  });
+}
+// Up to 16 NMB, a workgroup for 32 columns of y.
+template <int NMB, int U>
+__global__ void __launch_bounds__(512, 2) ffn_skinny_down_kernel(const FfnArgs a) {
+  __shared__ f32x4 red[8 * NMB * 2 * kWave];
+  const int n0 = blockIdx.x * 32;
+  SkinnyProduct<Bf16, NMB, 2, U> w;
+  w.begin();
+  w.a_rows(a.A, 2 * a.I, a.T);
+  w.b_rows(a.w2, 2 * a.I, [&](int i) { return n0 + i; });
+  w.run(a.I / 64, red);
+  if (w.wave >= NMB * 2) return;
+  const int m = w.wave / 2 * 16 + w.lane % 16;
+  const f32x4 v[1] = {w.acc[0][0]};
+  store_blocks<1>(a.y + (size_t)m * a.d + n0 + w.wave % 2 * 16, v, w.lane, m < a.T, a.acc_y);
 }
 
 long long ceil_div(long long n, int t) { return (n + t - 1) / t; }
@@ -205,44 +358,75 @@ Shape tile_shape(long long m, long long n) {
   return (Shape)best;
 }
 
+// Shares of K for up to half a card of 128 x 128 tiles: as many as fill it, of 12 steps at least (a
+// step is about 0.5 us, the second kernel 4 to 9). Unsplit and split, both kernels, in us: [g | u] of
+// 128 x 7168 x 2048 73 and 24, of 512 tokens 74 and 49; its dH 60 and 19, 61 and 30 (1024 tokens 64 and
+// 47); dx of 128 tokens 36 and 22. Shares of 8 steps where 16 was all: 18 for 12 (y of 333 x 4096 x
+// 1024).
+int shares_of(long long tiles, int steps) {
+  if (tiles > kCus / 2) return 1;
+  return (int)std::max(1LL, std::min((long long)kCus / tiles, (long long)steps / 12));
+}
+
 template <class K, class A>
-hipError_t launch_tiles(const char* name, K kernel, const A& a, long long tiles, hipStream_t s) {
+hipError_t launch_kernel(const char* name, K kernel, const A& a, long long grid, int threads,
+                         hipStream_t s) {
   {
     TraceScope trace(name, s);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((tiles + kXcds - 1) / kXcds * kXcds)), dim3(512), 0,
-                       s, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), 0, s, a);
   }
   return hipGetLastError();
 }
-// Kernel K<BM, BN> of the shape that fits m rows and n columns.
-#define MOE_LAUNCH_SHAPE(name, K, a, m, n, s)                                                   \
-  switch (tile_shape(m, n)) {                                                                   \
-    case kBig:                                                                                  \
-      return launch_tiles(name, K<256, 256>, a, ceil_div(m, 256) * ceil_div(n, 256), s);         \
-    case kTall:                                                                                 \
-      return launch_tiles(name, K<256, 128>, a, ceil_div(m, 256) * ceil_div(n, 128), s);         \
-    case kWide:                                                                                 \
-      return launch_tiles(name, K<128, 256>, a, ceil_div(m, 128) * ceil_div(n, 256), s);         \
-    default:                                                                                    \
-      return launch_tiles(name, K<128, 128>, a, ceil_div(m, 128) * ceil_div(n, 128), s);         \
+long long grid8(long long tiles) { return (tiles + kXcds - 1) / kXcds * kXcds; }
+
+template <class P>
+hipError_t launch_whole(const char* name, const typename P::Args& a, hipStream_t s) {
+  switch (tile_shape(P::m(a), P::n(a))) {
+    case kBig:
+      return launch_kernel(name, ffn_kernel<P, 256, 256>, a, grid8(tiles_of<P, 256, 256>(a)), 512, s);
+    case kTall:
+      return launch_kernel(name, ffn_kernel<P, 256, 128>, a, grid8(tiles_of<P, 256, 128>(a)), 512, s);
+    case kWide:
+      return launch_kernel(name, ffn_kernel<P, 128, 256>, a, grid8(tiles_of<P, 128, 256>(a)), 512, s);
+    default:
+      return launch_kernel(name, ffn_kernel<P, 128, 128>, a, grid8(tiles_of<P, 128, 128>(a)), 512, s);
   }
+}
+template <class P>
+hipError_t launch_product(FfnArgs a, hipStream_t s) {
+  const long long tiles = tiles_of<P, 128, 128>(a);
+  a.shares = shares_of(tiles, P::steps(a));
+  if (a.shares == 1) return launch_whole<P>(P::kName, a, s);
+  const hipError_t e =
+      launch_kernel(P::kName, ffn_split_kernel<P>, a, grid8(tiles * a.shares), 512, s);
+  if (e != hipSuccess) return e;
+  return launch_kernel(P::kName, ffn_join_kernel<P>, a, tiles * 8, 256, s);
+}
 
 }  // namespace
 
+// Up to 16 tokens (64 for y, whose K is the shorter) each weight is read once by a workgroup of its
+// own: [g | u] of 16 x 7168 x 2048 20 us (split along K 19 in two kernels, in whole tiles 53), its y
+// 9.5 (16, 18), y of 64 tokens 15.8 (17, 20). [g | u] of 64 would take 37 (22).
 hipError_t launch_ffn_gate_up(const FfnArgs& a, hipStream_t s) {
-  MOE_LAUNCH_SHAPE("ffn_gate_up", ffn_gate_up_kernel, a, a.T, 2LL * a.I, s)
+  if (a.T > 16) return launch_product<GateUp>(a, s);
+  return launch_kernel("ffn_gate_up", ffn_skinny_gate_up_kernel, a, a.I / 8, 512, s);
 }
 hipError_t launch_ffn_down(const FfnArgs& a, hipStream_t s) {
-  MOE_LAUNCH_SHAPE("ffn_down", ffn_down_kernel, a, a.T, a.d, s)
+  if (a.T > 64) return launch_product<Down>(a, s);
+  const auto kernel = a.T <= 16   ? ffn_skinny_down_kernel<1, 4>
+                      : a.T <= 32 ? ffn_skinny_down_kernel<2, 4>
+                                  : ffn_skinny_down_kernel<4, 2>;
+  return launch_kernel("ffn_down", kernel, a, a.d / 32, 512, s);
 }
 hipError_t launch_ffn_dh(const FfnArgs& a, hipStream_t s) {
-  MOE_LAUNCH_SHAPE("ffn_dh", ffn_dh_kernel, a, a.T, a.I, s)
+  return launch_product<Dh>(a, s);
 }
 hipError_t launch_ffn_dx(const FfnArgs& a, hipStream_t s) {
-  MOE_LAUNCH_SHAPE("ffn_dx", ffn_dx_kernel, a, a.T, a.d, s)
+  return launch_product<Dx>(a, s);
 }
 hipError_t launch_ffn_dw(const FfnDwArgs& a, hipStream_t s) {
-  MOE_LAUNCH_SHAPE(a.name, ffn_dw_kernel, a, a.Md, a.Nd, s)
+  return launch_whole<Dw>(a.name, a, s);
 }
 
 }  // namespace moe

@@ -99,8 +99,10 @@ struct FfnArgs {
   const uint16_t* dy;  // [T, d]
   uint16_t* dH;        // [T, 2I]
   uint16_t* dx;        // [T, d]
-  int T, d, I, act, acc_y, acc_dx;
+  float* part;         // partial sums of products split along K, kFfnPartBytes
+  int T, d, I, act, acc_y, acc_dx, shares;
 };
+constexpr size_t kFfnPartBytes = size_t(256) * 128 * 128 * 4;  // a 128 x 128 tile a CU
 struct FfnDwArgs {
   const uint16_t* L;  // [T, Md]
   const uint16_t* R;  // [T, Nd]

@@ -497,6 +497,112 @@ struct StreamProduct {
   MOE_DEV int row_of(int mb) const { return mb * 16 + lane % 16; }
 };
 
+// A handful of rows and few tiles: a product that reads its weights once, with every CU at it. A
+// workgroup takes 16 NNB of the weights' rows and up to 64 rows; its eight waves take the steps of
+// K in turn, each straight from memory into registers, U steps on their way, and add up their sums
+// through LDS in the waves' order. (One wave a tile, the other kernels' chain of steps, leaves a
+// CU with little on its way.) A gated tile's blocks hold 8 gate rows and the 8 up rows that match.
+template <class El, int NMB, int NNB, int U>
+struct SkinnyProduct {
+  using Acc = typename El::Acc;
+  __amdgpu_buffer_rsrc_t ra, rb;
+  uint32_t ao[NMB], bo[NNB];
+  int lane, wave;
+  i32x4 a[U][NMB][2], b[U][NNB][2];
+  Acc acc[NMB][NNB];
+
+  MOE_DEV void begin() {
+    lane = threadIdx.x % kWave;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  }
+  MOE_DEV void a_rows(const void* base, uint32_t pitch, int rows) {
+    ra = buf_rsrc(base);
+#pragma unroll
+    for (int mb = 0; mb < NMB; ++mb)  // rows past the count read the last one again
+      ao[mb] = (uint32_t)min(mb * 16 + lane % 16, rows - 1) * pitch + 16 * (lane / 16);
+  }
+  // row(i): where the tile's i-th weight row lies
+  template <class Row>
+  MOE_DEV void b_rows(const void* base, uint32_t pitch, Row row) {
+    rb = buf_rsrc(base);
+#pragma unroll
+    for (int nb = 0; nb < NNB; ++nb)
+      bo[nb] = (uint32_t)row(nb * 16 + lane % 16) * pitch + 16 * (lane / 16);
+  }
+  template <int AUX>
+  static MOE_DEV i32x4 load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, AUX));
+  }
+  template <int S>
+  MOE_DEV void fetch(int step) {
+    const uint32_t at = (uint32_t)step * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int nb = 0; nb < NNB; ++nb)
+        b[S][nb][h] = load<2>(rb, bo[nb] + 64 * h, at);  // read once: past the caches
+#pragma unroll
+      for (int mb = 0; mb < NMB; ++mb) a[S][mb][h] = load<0>(ra, ao[mb] + 64 * h, at);
+    }
+  }
+  template <int S>
+  MOE_DEV void multiply() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int mb = 0; mb < NMB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < NNB; ++nb) acc[mb][nb] = El::mma(b[S][nb][h], a[S][mb][h], acc[mb][nb]);
+  }
+  // The sums over nK steps: block (mb, nb)'s in wave mb NNB + nb's acc[0][0], for the waves that have
+  // one. red: 8 NMB NNB KB.
+  MOE_DEV void run(int nK, Acc* red) {
+#pragma unroll
+    for (int mb = 0; mb < NMB; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < NNB; ++nb) acc[mb][nb] = El::zero();
+    const int n = (nK - wave + 7) / 8;  // steps wave, wave + 8, ..
+    if (n > 0) {
+      each<U>([&](auto s) {
+        constexpr int S = decltype(s)::value;
+        fetch<S>(wave + 8 * min(S, n - 1));
+      });
+      int i = 0;
+      for (; i + 2 * U <= n; i += U)
+        each<U>([&](auto s) {
+          constexpr int S = decltype(s)::value;
+          multiply<S>();
+          fetch<S>(wave + 8 * (i + U + S));
+        });
+      if (i + U <= n) {
+        each<U>([&](auto s) {
+          constexpr int S = decltype(s)::value;
+          multiply<S>();
+          if (i + U + S < n) fetch<S>(wave + 8 * (i + U + S));
+        });
+        i += U;
+      }
+      each<U - 1>([&](auto s) {
+        constexpr int S = decltype(s)::value;
+        if (i + S < n) multiply<S>();
+      });
+    }
+    constexpr int NB = NMB * NNB;
+    static_assert(NB <= 8, "a wave for each block");
+#pragma unroll
+    for (int mb = 0; mb < NMB; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < NNB; ++nb)
+        red[(wave * NB + mb * NNB + nb) * kWave + lane] = acc[mb][nb];
+    __syncthreads();
+    if (wave < NB) {
+      acc[0][0] = red[wave * kWave + lane];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) acc[0][0] += red[(w * NB + wave) * kWave + lane];
+    }
+  }
+};
+
 // Two side-by-side 16 x 16 blocks of bf16 results stored (with add, added in fp32 to what is
 // there): lanes l and l ^ 16 swap halves, so that each stores eight consecutive columns and a row's
 // 64 bytes leave together. row: this lane's row at the blocks' first column.
