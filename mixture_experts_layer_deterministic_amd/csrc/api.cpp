@@ -988,16 +988,10 @@ int moe_ffn_backward(const moe_ffn* ffn, const void* x, const void* w1, const vo
   a.act = ffn->act;
   a.acc_dx = acc_dx != 0;
   Launches L;
-  L(launch_ffn_dh(a, s));
+  L(launch_ffn_dh_dw2(a, {a.dy, static_cast<const uint16_t*>(A), dw2, a.T, a.d, a.I, acc, bdw}, s));
   if (!L.err)
-    L(launch_ffn_dw({a.dy, static_cast<const uint16_t*>(A), dw2, a.T, a.d, a.I, acc, bdw,
-                     "ffn_dw2"},
-                    s));
-  if (!L.err) L(launch_ffn_dx(a, s));
-  if (!L.err)
-    L(launch_ffn_dw({a.dH, static_cast<const uint16_t*>(x), dw1, a.T, 2 * a.I, a.d, acc, bdw,
-                     "ffn_dw1"},
-                    s));
+    L(launch_ffn_dx_dw1(
+        a, {a.dH, static_cast<const uint16_t*>(x), dw1, a.T, 2 * a.I, a.d, acc, bdw}, s));
   return L.status();
 }
 

@@ -212,11 +212,8 @@ MOE_BOTH long long tiles_of(const typename P::Args& a) {
   return (P::m(a) + BM - 1) / BM * ((P::n(a) + BN - 1) / BN);
 }
 
-// A tile a workgroup, an XCD's share contiguous.
 template <class P, int BM, int BN>
-__global__ void __launch_bounds__(512, 2) ffn_kernel(const typename P::Args a) {
-  const int lt = xcd_contiguous(blockIdx.x, gridDim.x);
-  if (lt >= tiles_of<P, BM, BN>(a)) return;
+MOE_DEV void whole_tile(const typename P::Args& a, int lt) {
   const Place t = place_of<P, BM, BN>(a, lt);
   Tile8<Bf16, BM, BN, P::kAKM, P::kBKM, P::kGated> w;
   w.begin();
@@ -224,15 +221,19 @@ __global__ void __launch_bounds__(512, 2) ffn_kernel(const typename P::Args a) {
   w.run(P::steps(a));
   P::store(a, w, t.row0, t.rows, t.n0, t.cols);
 }
+// A tile a workgroup, an XCD's share contiguous.
+template <class P, int BM, int BN>
+__global__ void __launch_bounds__(512, 2) ffn_kernel(const typename P::Args a) {
+  const int lt = xcd_contiguous(blockIdx.x, gridDim.x);
+  if (lt < tiles_of<P, BM, BN>(a)) whole_tile<P, BM, BN>(a, lt);
+}
 
 // Few tiles: the steps of K in S shares, as even as they come, and a workgroup for each share of
 // each 128 x 128 tile. Its sums go to memory as the lanes hold them (a.part), and
 // a second kernel, a wave for 16 rows of a wave's columns, adds the shares in order and stores.
 template <class P>
-__global__ void __launch_bounds__(512, 2) ffn_split_kernel(const typename P::Args a) {
+MOE_DEV void share_of_tile(const typename P::Args& a, int j) {
   const int S = a.shares, tiles = (int)tiles_of<P, 128, 128>(a);
-  const int j = xcd_contiguous(blockIdx.x, gridDim.x);
-  if (j >= tiles * S) return;
   // one share of every tile, then the next: an XCD's tiles share their steps of K
   const int share = j / tiles, lt = j % tiles;
   const Place t = place_of<P, 128, 128>(a, lt);
@@ -252,6 +253,61 @@ __global__ void __launch_bounds__(512, 2) ffn_split_kernel(const typename P::Arg
     for (int nb = 0; nb < W::NB; ++nb) p[(mb * W::NB + nb) * kWave] = w.acc[mb][nb];
   }
 }
+template <class P>
+__global__ void __launch_bounds__(512, 2) ffn_split_kernel(const typename P::Args a) {
+  const int j = xcd_contiguous(blockIdx.x, gridDim.x);
+  if (j < tiles_of<P, 128, 128>(a) * a.shares) share_of_tile<P>(a, j);
+}
+
+// A gradient of rows and one of weights that do not wait for each other, in one launch: the
+// rows' tiles (or shares) first, `first` workgroups, then the weights'. One's last round runs beside
+// the other's first.
+enum Shape { kBig, kTall, kWide, kSmall, kShares };
+template <class P>
+struct Pair {
+  typename P::Args rows;
+  FfnDwArgs dw;
+  int rows_shape, dw_shape, first;
+};
+template <class P>
+__global__ void __launch_bounds__(512, 2) ffn_pair_kernel(const Pair<P> p) {
+  const int b = blockIdx.x;
+  if (b < p.first) {
+    const int lt = xcd_contiguous(b, p.first);
+    switch (p.rows_shape) {
+      case kBig:
+        if (lt < tiles_of<P, 256, 256>(p.rows)) whole_tile<P, 256, 256>(p.rows, lt);
+        break;
+      case kTall:
+        if (lt < tiles_of<P, 256, 128>(p.rows)) whole_tile<P, 256, 128>(p.rows, lt);
+        break;
+      case kWide:
+        if (lt < tiles_of<P, 128, 256>(p.rows)) whole_tile<P, 128, 256>(p.rows, lt);
+        break;
+      case kSmall:
+        if (lt < tiles_of<P, 128, 128>(p.rows)) whole_tile<P, 128, 128>(p.rows, lt);
+        break;
+      default:
+        if (lt < tiles_of<P, 128, 128>(p.rows) * p.rows.shares) share_of_tile<P>(p.rows, lt);
+    }
+    return;
+  }
+  const int lt = xcd_contiguous(b - p.first, gridDim.x - p.first);
+  switch (p.dw_shape) {
+    case kBig:
+      if (lt < tiles_of<Dw, 256, 256>(p.dw)) whole_tile<Dw, 256, 256>(p.dw, lt);
+      break;
+    case kTall:
+      if (lt < tiles_of<Dw, 256, 128>(p.dw)) whole_tile<Dw, 256, 128>(p.dw, lt);
+      break;
+    case kWide:
+      if (lt < tiles_of<Dw, 128, 256>(p.dw)) whole_tile<Dw, 128, 256>(p.dw, lt);
+      break;
+    default:
+      if (lt < tiles_of<Dw, 128, 128>(p.dw)) whole_tile<Dw, 128, 128>(p.dw, lt);
+  }
+}
+
 template <class T>
 struct JoinedRows {  // one row block of a wave of tile T
   static constexpr int MB = 1, NB = T::NB, BN = T::BN;
@@ -331,24 +387,27 @@ __global__ void __launch_bounds__(512, 2) ffn_skinny_down_kernel(const FfnArgs a
 
 long long ceil_div(long long n, int t) { return (n + t - 1) / t; }
 
-// The tile shape for a product of m rows and n columns: that of the fewest rounds of one tile a CU,
-// each at what a step of it takes when the card is full, in us: 256 x 256 1.35, 256 x 128 0.95,
-// 128 x 128 0.67 (bytes a step 64, 48 and 32 KB). Measured, the whole call in us, 256 x 256 / 256 x
-// 128 / 128 x 128: [g | u] of 2048 x 7168 x 2048 141 / 107 / 142 (128, 256, 512 tiles), its y
-// 51 / 64 / 88 (224, 448, 896), dH 155 / 107 / 80 (64, 128, 256); [g | u] of 1777 x 4096 x 1408
-// 80 / 53 / 72 (77, 154, 308).
-enum Shape { kBig, kTall, kWide, kSmall };
-Shape tile_shape(long long m, long long n) {
-  static const struct {
-    int bm, bn;
-    float us;
-  } shapes[4] = {{256, 256, 1.35f}, {256, 128, 0.95f}, {128, 256, 0.95f}, {128, 128, 0.67f}};
+// Tile shapes, and what a step takes when the card is full of them, in us (bytes a step 64, 48 and
+// 32 KB). Measured, the whole call in us, 256 x 256 / 256 x 128 / 128 x 128: [g | u] of 2048 x 7168 x
+// 2048 141 / 107 / 142 (128, 256, 512 tiles), its y 51 / 64 / 88 (224, 448, 896), dH 155 / 107 / 80 (64,
+// 128, 256); [g | u] of 1777 x 4096 x 1408 80 / 53 / 72 (77, 154, 308).
+constexpr struct {
+  int bm, bn;
+  float us;
+} kShapes[4] = {{256, 256, 1.35f}, {256, 128, 0.95f}, {128, 256, 0.95f}, {128, 128, 0.67f}};
+template <class P>
+long long shape_tiles(const typename P::Args& a, int shape) {
+  return ceil_div(P::m(a), kShapes[shape].bm) * ceil_div(P::n(a), kShapes[shape].bn);
+}
+// The shape of the fewest rounds of one tile a CU, each at its step's time.
+template <class P>
+Shape tile_shape(const typename P::Args& a) {
   int best = 0;
   float least = 0.f;
   long long fewest = 0;
   for (int i = 0; i < 4; ++i) {
-    const long long tiles = ceil_div(m, shapes[i].bm) * ceil_div(n, shapes[i].bn);
-    const float us = (float)ceil_div(tiles, kCus) * shapes[i].us;
+    const long long tiles = shape_tiles<P>(a, i);
+    const float us = (float)ceil_div(tiles, kCus) * kShapes[i].us;
     if (i == 0 || us < least || (us == least && tiles < fewest)) {
       best = i;
       least = us;
@@ -356,6 +415,22 @@ Shape tile_shape(long long m, long long n) {
     }
   }
   return (Shape)best;
+}
+// When the last of n1 tiles of t1 us and then n2 of t2 is done, each taken by the CU that is free
+// first.
+float time_of(long long n1, float t1, long long n2, float t2) {
+  // whole rounds of the first, and its last round on some of the CUs
+  const long long r = n1 / kCus, some = n1 % kCus;
+  float at[2] = {r * t1, (r + (some ? 1 : 0)) * t1};  // when the others and those are free
+  const long long n[2] = {kCus - some, some};
+  float done = n1 ? at[some ? 1 : 0] : 0.f;
+  while (n2 > 0) {
+    const int g = n[1] && at[1] < at[0] ? 1 : 0;
+    at[g] += t2;
+    done = std::max(done, at[g]);
+    n2 -= n[g];
+  }
+  return done;
 }
 
 // Shares of K for up to half a card of 128 x 128 tiles: as many as fill it, of 12 steps at least (a
@@ -381,7 +456,7 @@ long long grid8(long long tiles) { return (tiles + kXcds - 1) / kXcds * kXcds; }
 
 template <class P>
 hipError_t launch_whole(const char* name, const typename P::Args& a, hipStream_t s) {
-  switch (tile_shape(P::m(a), P::n(a))) {
+  switch (tile_shape<P>(a)) {
     case kBig:
       return launch_kernel(name, ffn_kernel<P, 256, 256>, a, grid8(tiles_of<P, 256, 256>(a)), 512, s);
     case kTall:
@@ -391,6 +466,35 @@ hipError_t launch_whole(const char* name, const typename P::Args& a, hipStream_t
     default:
       return launch_kernel(name, ffn_kernel<P, 128, 128>, a, grid8(tiles_of<P, 128, 128>(a)), 512, s);
   }
+}
+template <class P>
+hipError_t launch_pair(const char* name, const FfnArgs& rows, const FfnDwArgs& dw, hipStream_t s) {
+  Pair<P> p{rows, dw, 0, tile_shape<Dw>(dw), 0};
+  const long long small = tiles_of<P, 128, 128>(rows);
+  p.rows.shares = shares_of(small, P::steps(rows));
+  long long first = small * p.rows.shares;
+  if (p.rows.shares > 1) {
+    p.rows_shape = kShares;
+  } else {
+    float least = 0.f;
+    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < 4; ++j) {
+        const float us =
+            time_of(shape_tiles<P>(rows, i), kShapes[i].us * P::steps(rows),
+                    shape_tiles<Dw>(dw, j), kShapes[j].us * Dw::steps(dw));
+        if ((i == 0 && j == 0) || us < least) {
+          least = us;
+          p.rows_shape = i;
+          p.dw_shape = j;
+        }
+      }
+    first = shape_tiles<P>(rows, p.rows_shape);
+  }
+  p.first = (int)grid8(first);
+  const hipError_t e = launch_kernel(name, ffn_pair_kernel<P>, p,
+                                     p.first + grid8(shape_tiles<Dw>(dw, p.dw_shape)), 512, s);
+  if (e != hipSuccess || p.rows.shares == 1) return e;
+  return launch_kernel(P::kName, ffn_join_kernel<P>, p.rows, small * 8, 256, s);
 }
 template <class P>
 hipError_t launch_product(FfnArgs a, hipStream_t s) {
@@ -419,14 +523,11 @@ hipError_t launch_ffn_down(const FfnArgs& a, hipStream_t s) {
                                   : ffn_skinny_down_kernel<4, 2>;
   return launch_kernel("ffn_down", kernel, a, a.d / 32, 512, s);
 }
-hipError_t launch_ffn_dh(const FfnArgs& a, hipStream_t s) {
-  return launch_product<Dh>(a, s);
+hipError_t launch_ffn_dh_dw2(const FfnArgs& a, const FfnDwArgs& dw, hipStream_t s) {
+  return launch_pair<Dh>("ffn_dh_dw2", a, dw, s);
 }
-hipError_t launch_ffn_dx(const FfnArgs& a, hipStream_t s) {
-  return launch_product<Dx>(a, s);
-}
-hipError_t launch_ffn_dw(const FfnDwArgs& a, hipStream_t s) {
-  return launch_whole<Dw>(a.name, a, s);
+hipError_t launch_ffn_dx_dw1(const FfnArgs& a, const FfnDwArgs& dw, hipStream_t s) {
+  return launch_pair<Dx>("ffn_dx_dw1", a, dw, s);
 }
 
 }  // namespace moe

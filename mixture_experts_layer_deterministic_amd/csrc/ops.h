@@ -108,12 +108,11 @@ struct FfnDwArgs {
   const uint16_t* R;  // [T, Nd]
   void* dw;           // [Md, Nd] fp32, or (bf16_dw) bf16
   int T, Md, Nd, acc, bf16_dw;
-  const char* name;
 };
 hipError_t launch_ffn_gate_up(const FfnArgs& a, hipStream_t s);
 hipError_t launch_ffn_down(const FfnArgs& a, hipStream_t s);
-hipError_t launch_ffn_dh(const FfnArgs& a, hipStream_t s);
-hipError_t launch_ffn_dx(const FfnArgs& a, hipStream_t s);
-hipError_t launch_ffn_dw(const FfnDwArgs& a, hipStream_t s);
+// Each: a gradient of rows and one of weights
+hipError_t launch_ffn_dh_dw2(const FfnArgs& a, const FfnDwArgs& dw, hipStream_t s);
+hipError_t launch_ffn_dx_dw1(const FfnArgs& a, const FfnDwArgs& dw, hipStream_t s);
 
 }  // namespace moe
