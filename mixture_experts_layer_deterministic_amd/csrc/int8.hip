@@ -264,6 +264,55 @@ __global__ void __launch_bounds__(256, BM == 128 ? 2 : 4) i8_stream_kernel(const
   else i8_stream<8, SB, GATED>(a, t, n0, L);
 }
 
+// A handful of experts with a handful of rows: a workgroup for 16 NNB rows of an expert's weights
+// (gated: 8 NNB columns) and 16 NMB rows.
+template <int NMB, int NNB, int U, bool GATED>
+__global__ void __launch_bounds__(512, NMB * NNB == 1 ? 4 : 2) i8_skinny_kernel(
+    const I8GemmArgs a) {
+  __shared__ i32x4 red[8 * NMB * NNB * kWave];
+  const int nN = a.N / (16 * NNB), I = a.N / 2;
+  const RowTile t = find_rows<16 * NMB>(a.offsets, a.M, a.E, blockIdx.x / nN);
+  if (t.rows <= 0) return;  // whole workgroup
+  const int n0 = blockIdx.x % nN * (GATED ? 8 : 16) * NNB;
+  SkinnyProduct<Int8, NMB, NNB, U> w;
+  w.begin();
+  w.a_rows(a.a + (size_t)t.row0 * a.K, a.K, t.rows);
+  w.b_rows(a.b + (size_t)t.e * a.N * a.K, a.K, [&](int i) {
+    return !GATED ? n0 + i : n0 + i / 16 * 8 + (i % 16 < 8 ? i % 16 : I + i % 16 - 8);
+  });
+  w.run(a.K / 128, red);
+  if (w.wave >= NMB * NNB) return;
+  const int m = w.wave / NNB * 16 + w.lane % 16;
+  const float s = a.sa[t.row0 + min(m, t.rows - 1)];
+  const float* sb = a.sb + (size_t)t.e * a.N;
+  const size_t row = t.row0 + m;
+  if constexpr (!GATED) {
+    const int c = n0 + w.wave % NNB * 16;
+    const f32x4 sc = col_scales(sb + c + 4 * (w.lane / 16));
+    f32x4 v[1];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[0][r] = (float)w.acc[0][0][r] * s * sc[r];
+    store_blocks<1>(a.out + row * a.N + c, v, w.lane, m < t.rows, false);
+  } else {
+    // lanes 0..31 hold four gate columns of a row, lanes 32..63 the matching ups
+    const int c = n0 + w.wave % NNB * 8 + 4 * (w.lane / 16 % 2);
+    const f32x4 sc = col_scales(sb + (w.lane < 32 ? 0 : I) + c);
+    f32x4 g, u;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      g[r] = (float)w.acc[0][0][r] * s * sc[r];
+      u[r] = __shfl_xor(g[r], 32);
+    }
+    if (m >= t.rows || w.lane >= 32) return;
+    with_act(a.act, [&](auto tag) {
+      constexpr int A = decltype(tag)::value;
+      *reinterpret_cast<uint2*>(a.out + row * I + c) =
+          make_uint2(to_bf2(act_of<A>(g[0]) * u[0], act_of<A>(g[1]) * u[1]),
+                     to_bf2(act_of<A>(g[2]) * u[2], act_of<A>(g[3]) * u[3]));
+    });
+  }
+}
+
 }  // namespace
 
 hipError_t launch_i8_quant_rows(const uint16_t* src, long long rows, int cols, uint8_t* codes,
@@ -283,6 +332,14 @@ hipError_t launch_i8_quant_rows(const uint16_t* src, long long rows, int cols, u
   return hipGetLastError();
 }
 
+template <int NMB, int NNB>
+static void launch_skinny(const I8GemmArgs& a, bool gated, hipStream_t s) {
+  const dim3 grid((unsigned)(a.M / (16 * NMB) + a.E) * (a.N / (16 * NNB)));
+  if (gated)
+    hipLaunchKernelGGL((i8_skinny_kernel<NMB, NNB, 4, true>), grid, dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((i8_skinny_kernel<NMB, NNB, 4, false>), grid, dim3(512), 0, s, a);
+}
 hipError_t launch_i8_gemm(const I8GemmArgs& a, bool gated, hipStream_t s) {
   auto grid = [&](int bm, int bn) {
     const unsigned n = (unsigned)(a.M / bm + a.E) * (unsigned)((a.N + bn - 1) / bn);
@@ -290,6 +347,12 @@ hipError_t launch_i8_gemm(const I8GemmArgs& a, bool gated, hipStream_t s) {
   };
   TraceScope trace(gated ? "i8_gemm_gated" : "i8_gemm", s);
   const long long M = a.M, E = a.E, tiles = E * (a.N / 128);
+  if (tiles <= kCus / 4 && (M <= 32 * E || M <= 64)) {
+    if (M <= 16 * E) launch_skinny<1, 1>(a, gated, s);
+    else if (M <= 32 * E) launch_skinny<2, 1>(a, gated, s);
+    else launch_skinny<2, 2>(a, gated, s);
+    return hipGetLastError();
+  }
   const double busy = (double)tiles * -std::expm1(-(double)M / (double)E);
   if (busy > 2 * kCus && busy <= 2.75 * kCus && M <= 16 * E) {
     if (gated) hipLaunchKernelGGL((i8_stream_kernel<32, true>), grid(32, 128), dim3(256), 0, s, a);

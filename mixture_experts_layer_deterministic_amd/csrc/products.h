@@ -554,6 +554,34 @@ struct SkinnyProduct {
 #pragma unroll
         for (int nb = 0; nb < NNB; ++nb) acc[mb][nb] = El::mma(b[S][nb][h], a[S][mb][h], acc[mb][nb]);
   }
+  template <int V>
+  MOE_DEV void sum(int nK) {
+    const int n = (nK - wave + 7) / 8;  // steps wave, wave + 8, ..
+    if (n <= 0) return;
+    each<V>([&](auto s) {
+      constexpr int S = decltype(s)::value;
+      fetch<S>(wave + 8 * min(S, n - 1));
+    });
+    int i = 0;
+    for (; i + 2 * V <= n; i += V)
+      each<V>([&](auto s) {
+        constexpr int S = decltype(s)::value;
+        multiply<S>();
+        fetch<S>(wave + 8 * (i + V + S));
+      });
+    if (i + V <= n) {
+      each<V>([&](auto s) {
+        constexpr int S = decltype(s)::value;
+        multiply<S>();
+        if (i + V + S < n) fetch<S>(wave + 8 * (i + V + S));
+      });
+      i += V;
+    }
+    each<V - 1>([&](auto s) {
+      constexpr int S = decltype(s)::value;
+      if (i + S < n) multiply<S>();
+    });
+  }
   // The sums over nK steps: block (mb, nb)'s in wave mb NNB + nb's acc[0][0], for the waves that have
   // one. red: 8 NMB NNB KB.
   MOE_DEV void run(int nK, Acc* red) {
@@ -561,32 +589,8 @@ struct SkinnyProduct {
     for (int mb = 0; mb < NMB; ++mb)
 #pragma unroll
       for (int nb = 0; nb < NNB; ++nb) acc[mb][nb] = El::zero();
-    const int n = (nK - wave + 7) / 8;  // steps wave, wave + 8, ..
-    if (n > 0) {
-      each<U>([&](auto s) {
-        constexpr int S = decltype(s)::value;
-        fetch<S>(wave + 8 * min(S, n - 1));
-      });
-      int i = 0;
-      for (; i + 2 * U <= n; i += U)
-        each<U>([&](auto s) {
-          constexpr int S = decltype(s)::value;
-          multiply<S>();
-          fetch<S>(wave + 8 * (i + U + S));
-        });
-      if (i + U <= n) {
-        each<U>([&](auto s) {
-          constexpr int S = decltype(s)::value;
-          multiply<S>();
-          if (i + U + S < n) fetch<S>(wave + 8 * (i + U + S));
-        });
-        i += U;
-      }
-      each<U - 1>([&](auto s) {
-        constexpr int S = decltype(s)::value;
-        if (i + S < n) multiply<S>();
-      });
-    }
+    if (U > 2 && nK < 8 * U) sum<2>(nK);  // a wave has fewer steps than U
+    else sum<U>(nK);
     constexpr int NB = NMB * NNB;
     static_assert(NB <= 8, "a wave for each block");
 #pragma unroll
