@@ -17,7 +17,7 @@ namespace moe {
 namespace {
 
 // The five products. Each has rows m x columns n (a gated one: of its weights) over steps of K, the
-// layouts of its operands, how a tile reads them from step k0 on, and what becomes of its sums:
+// layouts of its operands, where a tile reads them from step k0 on, and what becomes of its sums:
 // store(w) for the rows row0 .. row0 + rows - 1 and columns n0 .. of the result, `cols` of the tile's
 // columns being there. w.acc holds the sums, for rows w.row_of(mb) and column blocks of wave w.wn.
 
@@ -30,11 +30,12 @@ struct GateUp {
   MOE_BOTH long long n(const Args& a) { return 2LL * a.I; }
   MOE_BOTH int steps(const Args& a) { return a.d / 64; }
   template <class W>
-  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int, int k0) {
-    w.a_rows(a.x + (size_t)row0 * a.d + 64 * k0, 2 * a.d, rows);
+  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int k0) {
+    w.a_rows(2 * a.d);
     const int I = a.I;
-    w.b_rows(a.w1 + 64 * k0, 2 * a.d,
-             [&](int i) { return i < W::BN / 2 ? n0 + i : I + n0 + i - W::BN / 2; });
+    w.b_rows(2 * a.d, [&](int i) { return i < W::BN / 2 ? i : I + i - W::BN / 2; });
+    w.next(a.x + (size_t)row0 * a.d + 64 * k0, 2u * rows * a.d - 128 * k0,
+           a.w1 + (size_t)n0 * a.d + 64 * k0, 2u * (2 * I - n0) * a.d - 128 * k0);
   }
   template <class W>
   static MOE_DEV void store(const Args& a, const W& w, int row0, int rows, int n0, int) {
@@ -85,9 +86,11 @@ struct Down {
   MOE_BOTH long long n(const Args& a) { return a.d; }
   MOE_BOTH int steps(const Args& a) { return a.I / 64; }
   template <class W>
-  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int cols, int k0) {
-    w.a_rows(a.A + (size_t)row0 * a.I + 64 * k0, 2 * a.I, rows);
-    w.b_rows(a.w2 + (size_t)n0 * a.I + 64 * k0, 2 * a.I, [&](int i) { return min(i, cols - 1); });
+  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int k0) {
+    w.a_rows(2 * a.I);
+    w.b_rows(2 * a.I, [](int i) { return i; });
+    w.next(a.A + (size_t)row0 * a.I + 64 * k0, 2u * rows * a.I - 128 * k0,
+           a.w2 + (size_t)n0 * a.I + 64 * k0, 2u * (a.d - n0) * a.I - 128 * k0);
   }
   template <class W>
   static MOE_DEV void store(const Args& a, const W& w, int row0, int rows, int n0, int cols) {
@@ -104,9 +107,11 @@ struct Dh {
   MOE_BOTH long long n(const Args& a) { return a.I; }
   MOE_BOTH int steps(const Args& a) { return a.d / 64; }
   template <class W>
-  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int cols, int k0) {
-    w.a_rows(a.dy + (size_t)row0 * a.d + 64 * k0, 2 * a.d, rows);
-    w.b_cols(a.w2 + (size_t)64 * k0 * a.I + n0, 2 * a.I, 2u * (a.d - 64 * k0) * a.I, cols);
+  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int k0) {
+    w.a_rows(2 * a.d);
+    w.b_cols(2 * a.I);
+    w.next(a.dy + (size_t)row0 * a.d + 64 * k0, 2u * rows * a.d - 128 * k0,
+           a.w2 + (size_t)64 * k0 * a.I + n0, 2u * (a.d - 64 * k0) * a.I - 2 * n0);
   }
   template <class W>
   static MOE_DEV void store(const Args& a, const W& w, int row0, int rows, int n0, int cols) {
@@ -150,9 +155,11 @@ struct Dx {
   MOE_BOTH long long n(const Args& a) { return a.d; }
   MOE_BOTH int steps(const Args& a) { return 2 * a.I / 64; }
   template <class W>
-  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int cols, int k0) {
-    w.a_rows(a.dH + (size_t)row0 * 2 * a.I + 64 * k0, 4 * a.I, rows);
-    w.b_cols(a.w1 + (size_t)64 * k0 * a.d + n0, 2 * a.d, 2u * (2 * a.I - 64 * k0) * a.d, cols);
+  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int k0) {
+    w.a_rows(4 * a.I);
+    w.b_cols(2 * a.d);
+    w.next(a.dH + (size_t)row0 * 2 * a.I + 64 * k0, 4u * rows * a.I - 128 * k0,
+           a.w1 + (size_t)64 * k0 * a.d + n0, 2u * (2 * a.I - 64 * k0) * a.d - 2 * n0);
   }
   template <class W>
   static MOE_DEV void store(const Args& a, const W& w, int row0, int rows, int n0, int cols) {
@@ -168,9 +175,10 @@ struct Dw {
   MOE_BOTH long long n(const Args& a) { return a.Nd; }
   MOE_BOTH int steps(const Args& a) { return (a.T + 63) / 64; }
   template <class W>
-  static MOE_DEV void setup(const Args& a, W& w, int row0, int rows, int n0, int cols, int) {
-    w.a_cols(a.L + row0, 2 * a.Md, 2u * a.T * a.Md, rows);
-    w.b_cols(a.R + n0, 2 * a.Nd, 2u * a.T * a.Nd, cols);
+  static MOE_DEV void setup(const Args& a, W& w, int row0, int, int n0, int) {
+    w.a_cols(2 * a.Md);
+    w.b_cols(2 * a.Nd);
+    w.next(a.L + row0, 2u * a.T * a.Md - 2 * row0, a.R + n0, 2u * a.T * a.Nd - 2 * n0);
   }
   template <class W>
   static MOE_DEV void store(const Args& a, const W& w, int row0, int rows, int n0, int cols) {
@@ -217,7 +225,7 @@ MOE_DEV void whole_tile(const typename P::Args& a, int lt) {
   const Place t = place_of<P, BM, BN>(a, lt);
   Tile8<Bf16, BM, BN, P::kAKM, P::kBKM, P::kGated> w;
   w.begin();
-  P::setup(a, w, t.row0, t.rows, t.n0, t.cols, 0);
+  P::setup(a, w, t.row0, t.rows, t.n0, 0);
   w.run(P::steps(a));
   P::store(a, w, t.row0, t.rows, t.n0, t.cols);
 }
@@ -242,7 +250,7 @@ MOE_DEV void share_of_tile(const typename P::Args& a, int j) {
   using W = Tile8<Bf16, 128, 128, P::kAKM, P::kBKM, P::kGated>;
   W w;
   w.begin();
-  P::setup(a, w, t.row0, t.rows, t.n0, t.cols, k0);
+  P::setup(a, w, t.row0, t.rows, t.n0, k0);
   w.run(k1 - k0);
   f32x4* p = reinterpret_cast<f32x4*>(a.part) +
              ((size_t)(lt * S + share) * 8 + w.wave) * (W::MB * W::NB * kWave) + w.lane;

@@ -175,61 +175,105 @@ MOE_DEV void i8_epilogue(const I8GemmArgs& a, const T& w, int e, int row0, int r
   }
 }
 
-template <int BM, int BN, bool GATED>
-MOE_DEV void i8_tile(const I8GemmArgs& a, int e, int row0, int rows, int n0) {
-  Tile8<Int8, BM, BN, false, false, GATED> w;
+struct I8Place {
+  int e, row0, rows, n0;  // rows <= 0: none
+};
+template <bool GATED, class T>
+MOE_DEV int i8_cols(const I8GemmArgs& a, const I8Place& t) {  // a plain tile's: its width, or 128
+  return GATED ? T::BN : min(T::BN, a.N - t.n0);
+}
+template <bool GATED, class T>
+MOE_DEV void i8_layout(const I8GemmArgs& a, T& w) {
   w.begin();
-  w.a_rows(a.a + (size_t)row0 * a.K, a.K, rows);
-  const uint8_t* b = a.b + (size_t)e * a.N * a.K;
-  int cols = BN;
-  if constexpr (GATED) {
-    const int I = a.N / 2;
-    w.b_rows(b, a.K, [&](int i) { return i < BN / 2 ? n0 + i : I + n0 + i - BN / 2; });
-  } else {
-    cols = min(BN, a.N - n0);  // BN, or 128 at an odd end
-    w.b_rows(b + (size_t)n0 * a.K, a.K, [&](int i) { return min(i, cols - 1); });
-  }
+  w.a_rows(a.K);
+  const int I = a.N / 2;
+  w.b_rows(a.K, [&](int i) { return !GATED || i < T::BN / 2 ? i : I + i - T::BN / 2; });
+}
+template <class T>
+MOE_DEV void i8_next(const I8GemmArgs& a, T& w, const I8Place& t) {
+  w.next(a.a + (size_t)t.row0 * a.K, (uint32_t)t.rows * a.K,
+         a.b + ((size_t)t.e * a.N + t.n0) * a.K, (uint32_t)(a.N - t.n0) * a.K);
+}
+template <int BM, int BN, bool GATED>
+MOE_DEV void i8_tile(const I8GemmArgs& a, const I8Place& t) {
+  using T = Tile8<Int8, BM, BN, false, false, GATED>;
+  T w;
+  i8_layout<GATED>(a, w);
+  i8_next(a, w, t);
   w.run(a.K / 128);
-  i8_epilogue<GATED>(a, w, e, row0, rows, n0, cols);
+  i8_epilogue<GATED>(a, w, t.e, t.row0, t.rows, t.n0, i8_cols<GATED, T>(a, t));
 }
 
 // Many rows an expert: 256 x 256 tiles, whole rounds of one a CU and then what is left, cut in two
-// (256 x 128) or four (128 x 128) where the parts still fit one round.
-template <bool GATED>
+// (256 x 128) or four (128 x 128) where the parts still fit one round. A workgroup stays for all its
+// tiles; where K has an even number of steps the next tile's first loads go out in the last steps of
+// the one before, so that they arrive under its epilogue.
+// FLOW: so; otherwise each tile starts anew.
+template <bool GATED, bool FLOW>
 __global__ void __launch_bounds__(512, 2) i8_big_kernel(const I8GemmArgs a) {
+  constexpr int kCols = GATED ? kBigT / 2 : kBigT;  // output columns
   const int nN = (a.N + kBigT - 1) / kBigT;
   const int nm = big_count(a), tiles = nm * nN;
-  const int whole = tiles / kCus * kCus, left = tiles - whole;
+  const int left = tiles % kCus, whole = tiles - left;
   const int cut = left * 4 <= kCus ? 4 : left * 2 <= kCus ? 2 : 1;
-  const int b = blockIdx.x;
-  int lt, part = 0;
-  if (b < whole) {
-    lt = xcd_contiguous(b, whole);
-  } else {
-    const int n8 = (left * cut + kXcds - 1) / kXcds * kXcds;
-    if (b - whole >= n8) return;  // whole workgroups leave
-    const int j = xcd_contiguous(b - whole, n8);
-    if (j >= left * cut) return;
-    lt = whole + j / cut;
-    part = j % cut;
+  const auto place = [&](int lt) {
+    const int2 mn = big_order(lt, nm, nN);
+    const RowTile t = big_rows(a, mn.x);
+    return I8Place{t.e, t.row0, t.rows, mn.y * kCols};
+  };
+  // An XCD's tiles are contiguous; the round after the whole ones takes those that are left.
+  int b = blockIdx.x;
+  if constexpr (!FLOW) {
+    if (b < whole) {
+      i8_tile<256, 256, GATED>(a, place(xcd_contiguous(b, whole)));
+      return;
+    }
+    b -= whole;
   }
-  const int2 mn = big_order(lt, nm, nN);
-  const RowTile t = big_rows(a, mn.x);
-  if (t.rows <= 0) return;
-  constexpr int kCols = GATED ? kBigT / 2 : kBigT;  // output columns
-  const int n0 = mn.y * kCols;
-  if (b < whole || cut == 1) {
-    i8_tile<256, 256, GATED>(a, t.e, t.row0, t.rows, n0);
+  const int n8 = (left * cut + kXcds - 1) / kXcds * kXcds, j = xcd_contiguous(b, n8);
+  const bool part = b < n8 && j < left * cut;
+  if constexpr (FLOW) {
+    const int rounds = whole / kCus + (cut == 1 && part ? 1 : 0);
+    const auto at_round = [&](int r) {
+      return place(r * kCus < whole ? xcd_contiguous(r * kCus + b, whole) : whole + j);
+    };
+    if (rounds > 0) {
+      using T = Tile8<Int8, 256, 256, false, false, GATED>;
+      T w;
+      i8_layout<GATED>(a, w);
+      I8Place t = at_round(0);
+      i8_next(a, w, t);
+      w.start(a.K / 128);
+      for (int r = 0;; ++r) {
+        I8Place n = t;
+        if (r + 1 < rounds) n = at_round(r + 1);
+        i8_next(a, w, n);
+        w.template sum<true>();
+        i8_epilogue<GATED>(a, w, t.e, t.row0, t.rows, t.n0, i8_cols<GATED, T>(a, t));
+        if (r + 1 == rounds) break;
+        t = n;
+      }
+      // the loads of a tile that does not come land before their places are given to another
+      __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
+      w.phase_end();
+    }
+  }
+  if (!part || (FLOW && cut == 1)) return;
+  I8Place t = place(whole + j / cut);
+  if (!FLOW && cut == 1) {
+    i8_tile<256, 256, GATED>(a, t);
     return;
   }
-  const int c = n0 + part % 2 * (kCols / 2);
-  if (c >= (GATED ? a.N / 2 : a.N)) return;
+  t.n0 += j % cut % 2 * (kCols / 2);
+  if (t.n0 >= (GATED ? a.N / 2 : a.N)) return;
   if (cut == 2) {
-    i8_tile<256, 128, GATED>(a, t.e, t.row0, t.rows, c);
+    i8_tile<256, 128, GATED>(a, t);
   } else {
-    const int r = part / 2 * 128;
+    const int r = j % cut / 2 * 128;
     if (r >= t.rows) return;
-    i8_tile<128, 128, GATED>(a, t.e, t.row0 + r, min(t.rows - r, 128), c);
+    t.row0 += r;
+    t.rows = min(t.rows - r, 128);
+    i8_tile<128, 128, GATED>(a, t);
   }
 }
 
@@ -364,10 +408,11 @@ hipError_t launch_i8_gemm(const I8GemmArgs& a, bool gated, hipStream_t s) {
     else hipLaunchKernelGGL((i8_stream_kernel<128, false>), grid(128, 128), dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  // room for every tile, and for a last round's parts
-  const dim3 big(grid(kBigT, kBigT).x + kCus);
-  if (gated) hipLaunchKernelGGL(i8_big_kernel<true>, big, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL(i8_big_kernel<false>, big, dim3(512), 0, s, a);
+  const bool flow = a.K / 128 % 2 == 0;  // two stages
+  const auto kernel = gated ? (flow ? i8_big_kernel<true, true> : i8_big_kernel<true, false>)
+                            : (flow ? i8_big_kernel<false, true> : i8_big_kernel<false, false>);
+  // a workgroup a CU, or room for every tile and for a last round's parts
+  hipLaunchKernelGGL(kernel, flow ? dim3(kCus) : dim3(grid(kBigT, kBigT).x + kCus), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 

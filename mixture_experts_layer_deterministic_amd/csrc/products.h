@@ -136,8 +136,11 @@ struct Tile8 {
   static_assert(El::kStepK == 64 || (!AKM && !BKM), "transposing reads are 16-bit");
   static_assert(!AKM || BKM, "parts by K need both K-major");
 
-  __amdgpu_buffer_rsrc_t ra, rb;
-  uint32_t ao[AJ], bo[BJ], astep, bstep;
+  struct Src {  // a tile's operands, from its first row (column) on
+    __amdgpu_buffer_rsrc_t a, b;
+  };
+  Src cur, nxt;
+  uint32_t ao[AJ], bo[BJ], astep, bstep;  // a lane's places in any tile, and a step's bytes
   int nK, lane, wave, wm, wn;
   FragAt f;
   Acc acc[MB][NB];
@@ -157,19 +160,18 @@ struct Tile8 {
   static MOE_DEV int tile_row(int L) {
     return U == 1 ? L : L % 128 / (B * 8) * (B * 16) + L / 128 * (B * 8) + L % (B * 8);
   }
-  // A's rows 0 .. rows - 1, `pitch` bytes apart; those past the end read the last one again
-  MOE_DEV void a_rows(const void* base, uint32_t pitch, int rows) {
-    ra = buf_rsrc(base);
+  // Where a tile's rows lie, `pitch` bytes apart; B's (columns of the product) i-th in row row(i)
+  // behind the first. K-major: `pitch` bytes from one row of K to the next. What lies past the end of
+  // an operand reads as zeros, and what lies past a tile's own rows or columns goes into sums that are
+  // not stored.
+  MOE_DEV void a_rows(uint32_t pitch) {
     astep = 128;
 #pragma unroll
     for (int j = 0; j < AJ; ++j)
-      ao[j] = (uint32_t)min(tile_row<AU, MB>(kb_of(j) * 8 + lane / 8), rows - 1) * pitch +
-              lds_piece(lane);
+      ao[j] = (uint32_t)tile_row<AU, MB>(kb_of(j) * 8 + lane / 8) * pitch + lds_piece(lane);
   }
-  // B's rows (columns of the product): row(i) is where the tile's i-th lies
   template <class Row>
-  MOE_DEV void b_rows(const void* base, uint32_t pitch, Row row) {
-    rb = buf_rsrc(base);
+  MOE_DEV void b_rows(uint32_t pitch, Row row) {
     bstep = 128;
 #pragma unroll
     for (int j = 0; j < BJ; ++j) {
@@ -177,34 +179,38 @@ struct Tile8 {
       bo[j] = (uint32_t)row(GATED ? L : tile_row<BU, NB>(L)) * pitch + lds_piece(lane);
     }
   }
-  // K-major: `bytes` from base on hold every row of K; what lies behind reads as zeros. Of the
-  // tile's W columns `width` are there (W, or 128 of 256); the others read those again.
   template <int W, int J>
-  MOE_DEV void k_major(uint32_t (&off)[J], uint32_t pitch, int width) {
+  MOE_DEV void k_major(uint32_t (&off)[J], uint32_t pitch) {
     constexpr int R = 512 / W;  // rows of K a load
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int kr = kb_of(j) * R + lane / (W / 8);
-      int c = (lane % (W / 8) * 8) ^ kmajor_swz(kr);
-      c = c < width ? c : c - 128;
-      off[j] = (uint32_t)kr * pitch + 2u * c;
+      off[j] = (uint32_t)kr * pitch + 2u * ((lane % (W / 8) * 8) ^ kmajor_swz(kr));
     }
   }
-  MOE_DEV void a_cols(const void* base, uint32_t pitch, uint32_t bytes, int width) {
-    ra = raw_rsrc(base, bytes);
+  MOE_DEV void a_cols(uint32_t pitch) {
     astep = 64 * pitch;
-    k_major<BM>(ao, pitch, width);
+    k_major<BM>(ao, pitch);
   }
-  MOE_DEV void b_cols(const void* base, uint32_t pitch, uint32_t bytes, int width) {
-    rb = raw_rsrc(base, bytes);
+  MOE_DEV void b_cols(uint32_t pitch) {
     bstep = 64 * pitch;
-    k_major<BN>(bo, pitch, width);
+    k_major<BN>(bo, pitch);
+  }
+  // The next tile: its first row and column, and the bytes of each operand from there on that may be
+  // read (rows of A past the last one's end are another tile's, or nobody's).
+  MOE_DEV void next(const void* a, uint32_t a_bytes, const void* b, uint32_t b_bytes) {
+    nxt = {raw_rsrc(a, a_bytes), raw_rsrc(b, b_bytes)};
   }
 
-  // Part P of step kb into stage S (P = 2: all of it)
-  template <int S, int P>
+  // Part P of step kb into stage S (P = 2: all of it). Past the tile's end FLOW goes on with the
+  // next tile's steps; else the last one is read again, into a place that nobody reads.
+  template <bool FLOW, int S, int P>
   MOE_DEV void issue(int kb) {
-    kb = min(kb, nK - 1);
+    if (!FLOW || kb < nK) issue_from<S, P>(cur, min(kb, nK - 1));
+    else issue_from<S, P>(nxt, kb - nK);
+  }
+  template <int S, int P>
+  MOE_DEV void issue_from(const Src& o, int kb) {
     // the range of a resource is checked against the lane's offset alone
     const uint32_t sa = AKM ? 0u : (uint32_t)kb * 128, va = AKM ? (uint32_t)kb * astep : 0u;
     const uint32_t sb = BKM ? 0u : (uint32_t)kb * 128, vb = BKM ? (uint32_t)kb * bstep : 0u;
@@ -212,12 +218,12 @@ struct Tile8 {
     auto load_a = [&](auto j) {
       constexpr int J = decltype(j)::value;
       if constexpr (P == 2 || P == J / 2)
-        load_lds16(ra, ao[J] + va, sa, prod_unit<U + J / 2>() + (2 * wave + J % 2) * 1024);
+        load_lds16(o.a, ao[J] + va, sa, prod_unit<U + J / 2>() + (2 * wave + J % 2) * 1024);
     };
     auto load_b = [&](auto j) {
       constexpr int J = decltype(j)::value;
       if constexpr (P == 2 || (kByK ? P == J / 2 : P == 0))
-        load_lds16(rb, bo[J] + vb, sb, prod_unit<U + AU + J / 2>() + (2 * wave + J % 2) * 1024);
+        load_lds16(o.b, bo[J] + vb, sb, prod_unit<U + AU + J / 2>() + (2 * wave + J % 2) * 1024);
     };
     load_b(Int<0>());
     load_b(Int<1>());
@@ -299,79 +305,93 @@ struct Tile8 {
     __builtin_amdgcn_s_setprio(0);
     phase_end();
   }
-  template <int S>
+  template <bool FLOW, int S>
   MOE_DEV void step(int kb) {
     if constexpr (!kTwo) {
       i32x4 bf[2][NB], af[2][MB];
-      issue<(S + NS - 1) % NS, 2>(kb + NS - 1);
+      issue<FLOW, (S + NS - 1) % NS, 2>(kb + NS - 1);
       read_b<S, 0, 2>(bf);
       read_a<S, 0, MB, 0, 2>(af);
       multiply<0, MB, 2>(bf, af);
     } else if constexpr (kByK) {
       i32x4 bf[1][NB], af[1][MB];
-      issue<S ^ 1, 1>(kb + 1);
+      issue<FLOW, S ^ 1, 1>(kb + 1);
       read_b<S, 0, 1>(bf);
       read_a<S, 0, MB, 0, 1>(af);
       multiply<0, MB, 1>(bf, af);
-      issue<S, 0>(kb + 2);
+      issue<FLOW, S, 0>(kb + 2);
       read_b<S, 1, 1>(bf);
       read_a<S, 0, MB, 1, 1>(af);
       multiply<0, MB, 1>(bf, af);
     } else {
       i32x4 bf[2][NB], af[2][MB / 2];
-      issue<S ^ 1, 1>(kb + 1);
+      issue<FLOW, S ^ 1, 1>(kb + 1);
       read_b<S, 0, 2>(bf);
       read_a<S, 0, MB / 2, 0, 2>(af);
       multiply<0, MB / 2, 2>(bf, af);
-      issue<S, 0>(kb + 2);
+      issue<FLOW, S, 0>(kb + 2);
       read_a<S, MB / 2, MB / 2, 0, 2>(af);
       multiply<MB / 2, MB / 2, 2>(bf, af);
     }
   }
-  template <int S, int C>  // steps kb + S, .. while fewer than C and n
+  template <bool FLOW, int S, int C>  // steps kb + S, .. while fewer than C and n
   MOE_DEV void steps(int kb, int n) {
     if constexpr (S < C) {
       if (S < n) {
-        step<S>(kb + S);
-        steps<S + 1, C>(kb, n);
+        step<FLOW, S>(kb + S);
+        steps<FLOW, S + 1, C>(kb, n);
       }
     }
   }
   template <int S>
   MOE_DEV void fill() {
     if constexpr (S < NS - 1) {
-      issue<S, 2>(S);
+      issue<false, S, 2>(S);
       loads_in_order();
       fill<S + 1>();
     }
   }
-  // The sums over `steps_of_k` steps (one at least) of what the operands were set to.
-  MOE_DEV void run(int steps_of_k) {
+  // The next tile becomes the current one, and its first loads go out.
+  MOE_DEV void start(int steps_of_k) {
     nK = steps_of_k;
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = El::zero();
+    cur = nxt;
     if constexpr (kTwo) {
-      issue<0, 0>(0);
+      issue<false, 0, 0>(0);
       loads_in_order();
-      issue<0, 1>(0);
+      issue<false, 0, 1>(0);
       loads_in_order();
-      issue<1, 0>(1);
+      issue<false, 1, 0>(1);
     } else {
       fill<0>();
     }
     __builtin_amdgcn_s_waitcnt(kWait);  // what step 0 reads first
     phase_end();
+  }
+  // The sums over the current tile's steps (one at least). FLOW, for numbers of steps that are a
+  // multiple of NS: the next tile's first loads are on their way at the end, as start leaves them.
+  template <bool FLOW>
+  MOE_DEV void sum() {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = El::zero();
     const bool late = wave >= 4;
     if (late) phase_end();
     int kb = 0;
-    for (; kb + NS <= nK; kb += NS) steps<0, NS>(kb, NS);
-    steps<0, NS - 1>(kb, nK - kb);
+    for (; kb + NS <= nK; kb += NS) steps<FLOW, 0, NS>(kb, NS);
+    if constexpr (!FLOW) steps<false, 0, NS - 1>(kb, nK - kb);
     if (!late) phase_end();  // as many barriers for the early waves as for the late ones
-    // the loads past the end land before the units are filled again or given back
-    __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
-    phase_end();
+    if constexpr (!FLOW) {
+      // the loads past the end land before the units are filled again or given back
+      __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
+      phase_end();
+    } else {
+      cur = nxt;
+    }
+  }
+  MOE_DEV void run(int steps_of_k) {
+    start(steps_of_k);
+    sum<false>();
   }
 
   MOE_DEV int row_of(int mb) const { return (wm * MB + mb) * 16 + lane % 16; }
