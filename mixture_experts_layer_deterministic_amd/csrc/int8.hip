@@ -116,50 +116,75 @@ __global__ void __launch_bounds__(256) i8_quant_rows_kernel(const uint16_t* __re
 // ------------------------------------------------------------------------------------------
 // The products
 
-// The scales of four consecutive columns (any multiple of 4 bytes).
-MOE_DEV f32x4 col_scales(const float* p) {
-  return f32x4{p[0], p[1], p[2], p[3]};
-}
+// Where an epilogue finds its scales: in memory, at any multiple of 4 bytes, or in LDS. row(m): of
+// the tile's row m; col(c): of four consecutive columns, c counting from the tile's first (a gated
+// tile's up columns from up on).
+MOE_DEV f32x4 col_scales(const float* p) { return f32x4{p[0], p[1], p[2], p[3]}; }
+struct I8ScalesMem {
+  const float *sa, *sb;
+  int rows, up;
+  MOE_DEV I8ScalesMem(const I8GemmArgs& a, int e, int row0, int rows_, int n0)
+      : sa(a.sa + row0), sb(a.sb + (size_t)e * a.N + n0), rows(rows_), up(a.N / 2) {}
+  MOE_DEV float row(int m) const { return sa[min(m, rows - 1)]; }
+  MOE_DEV f32x4 col(int c) const { return col_scales(sb + c); }
+};
+// 256 rows' and 256 columns' scales of a 256 x 256 tile, in a KB each behind the tiles' units; waves
+// 0..3 fetch the rows', waves 4..7 the columns' (gated: 128 of the gate, then the up projection's).
+struct I8ScalesLds {
+  static constexpr int up = 128;
+  const float* st;
+  template <bool GATED>
+  static MOE_DEV void fetch(const I8GemmArgs& a, int e, int row0, int rows, int n0, uint8_t* to) {
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), i = wave % 4 * 64 + lane;
+    const bool of_rows = wave < 4;
+    const float* p = of_rows ? a.sa + row0 : a.sb + (size_t)e * a.N + n0;
+    const int n = of_rows ? i : GATED && i >= 128 ? a.N / 2 + i - 128 : i;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        raw_rsrc(p, 4u * (of_rows ? rows : a.N - n0)),
+        (__attribute__((address_space(3))) void*)(to + wave * 256), 4, 4u * n, 0, 0, 0);
+  }
+  MOE_DEV float row(int m) const { return st[m]; }
+  MOE_DEV f32x4 col(int c) const { return *reinterpret_cast<const f32x4*>(st + 256 + c); }
+};
 // Rows row0 .. of the tile and columns n0 .. of its weights; a gated tile's n0 counts gate columns.
-template <bool GATED, class T>
-MOE_DEV void i8_epilogue(const I8GemmArgs& a, const T& w, int e, int row0, int rows, int n0,
+template <bool GATED, class T, class S>
+MOE_DEV void i8_epilogue(const I8GemmArgs& a, const T& w, const S& sc, int row0, int rows, int n0,
                          int cols) {
-  const float* sb = a.sb + (size_t)e * a.N;
   const int out_n = GATED ? a.N / 2 : a.N;
   if constexpr (!GATED) {
     const int c0 = w.wn * T::NB * 16;
     if (c0 >= cols) return;  // a whole wave
-    f32x4 sc[T::NB];
+    f32x4 sb[T::NB];
 #pragma unroll
-    for (int nb = 0; nb < T::NB; ++nb)
-      sc[nb] = col_scales(sb + n0 + c0 + nb * 16 + 4 * (w.lane / 16));
+    for (int nb = 0; nb < T::NB; ++nb) sb[nb] = sc.col(c0 + nb * 16 + 4 * (w.lane / 16));
 #pragma unroll
     for (int mb = 0; mb < T::MB; ++mb) {
       const int m = w.row_of(mb);
       const bool on = m < rows;
-      const float s = a.sa[row0 + min(m, rows - 1)];
+      const float s = sc.row(m);
       f32x4 v[T::NB];
 #pragma unroll
       for (int nb = 0; nb < T::NB; ++nb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[nb][r] = (float)w.acc[mb][nb][r] * s * sc[nb][r];
+        for (int r = 0; r < 4; ++r) v[nb][r] = (float)w.acc[mb][nb][r] * s * sb[nb][r];
       store_blocks<T::NB>(a.out + (size_t)(row0 + m) * out_n + n0 + c0, v, w.lane, on, false);
     }
   } else {
     constexpr int NG = T::NB / 2;
-    const int c0 = n0 + w.wn * NG * 16;
+    const int c0 = w.wn * NG * 16;
     f32x4 sg[NG], su[NG];
 #pragma unroll
     for (int nb = 0; nb < NG; ++nb) {
-      sg[nb] = col_scales(sb + c0 + nb * 16 + 4 * (w.lane / 16));
-      su[nb] = col_scales(sb + out_n + c0 + nb * 16 + 4 * (w.lane / 16));
+      sg[nb] = sc.col(c0 + nb * 16 + 4 * (w.lane / 16));
+      su[nb] = sc.col(sc.up + c0 + nb * 16 + 4 * (w.lane / 16));
     }
     with_act(a.act, [&](auto tag) {
 #pragma unroll
       for (int mb = 0; mb < T::MB; ++mb) {
         const int m = w.row_of(mb);
         const bool on = m < rows;
-        const float s = a.sa[row0 + min(m, rows - 1)];
+        const float s = sc.row(m);
         f32x4 v[NG];
 #pragma unroll
         for (int nb = 0; nb < NG; ++nb)
@@ -169,7 +194,7 @@ MOE_DEV void i8_epilogue(const I8GemmArgs& a, const T& w, int e, int row0, int r
             const float u = (float)w.acc[mb][nb + NG][r] * s * su[nb][r];
             v[nb][r] = act_of<decltype(tag)::value>(g) * u;
           }
-        store_blocks<NG>(a.out + (size_t)(row0 + m) * out_n + c0, v, w.lane, on, false);
+        store_blocks<NG>(a.out + (size_t)(row0 + m) * out_n + n0 + c0, v, w.lane, on, false);
       }
     });
   }
@@ -201,7 +226,8 @@ MOE_DEV void i8_tile(const I8GemmArgs& a, const I8Place& t) {
   i8_layout<GATED>(a, w);
   i8_next(a, w, t);
   w.run(a.K / 128);
-  i8_epilogue<GATED>(a, w, t.e, t.row0, t.rows, t.n0, i8_cols<GATED, T>(a, t));
+  const I8ScalesMem sc(a, t.e, t.row0, t.rows, t.n0);
+  i8_epilogue<GATED>(a, w, sc, t.row0, t.rows, t.n0, i8_cols<GATED, T>(a, t));
 }
 
 // Many rows an expert: 256 x 256 tiles, whole rounds of one a CU and then what is left, cut in two
@@ -243,13 +269,18 @@ __global__ void __launch_bounds__(512, 2) i8_big_kernel(const I8GemmArgs a) {
       i8_layout<GATED>(a, w);
       I8Place t = at_round(0);
       i8_next(a, w, t);
+      uint8_t* const st = prod_unit<8>();  // the tile's scales, then the next one's
+      I8ScalesLds::fetch<GATED>(a, t.e, t.row0, t.rows, t.n0, st);
+      loads_in_order();
       w.start(a.K / 128);
       for (int r = 0;; ++r) {
         I8Place n = t;
         if (r + 1 < rounds) n = at_round(r + 1);
         i8_next(a, w, n);
         w.template sum<true>();
-        i8_epilogue<GATED>(a, w, t.e, t.row0, t.rows, t.n0, i8_cols<GATED, T>(a, t));
+        const I8ScalesLds sc{reinterpret_cast<const float*>(st + r % 2 * 2048)};
+        i8_epilogue<GATED>(a, w, sc, t.row0, t.rows, t.n0, i8_cols<GATED, T>(a, t));
+        I8ScalesLds::fetch<GATED>(a, n.e, n.row0, n.rows, n.n0, st + (r + 1) % 2 * 2048);
         if (r + 1 == rounds) break;
         t = n;
       }
@@ -287,7 +318,8 @@ MOE_DEV void i8_stream(const I8GemmArgs& a, const RowTile& t, int n0, const Stre
     return !GATED ? n0 + i : i < 64 ? n0 + i : I + n0 + i - 64;
   });
   w.run(L, a.K / 128);
-  i8_epilogue<GATED>(a, w, t.e, t.row0, t.rows, n0, 128);
+  const I8ScalesMem sc(a, t.e, t.row0, t.rows, n0);
+  i8_epilogue<GATED>(a, w, sc, t.row0, t.rows, n0, 128);
 }
 template <int BM, bool GATED>
 __global__ void __launch_bounds__(256, BM == 128 ? 2 : 4) i8_stream_kernel(const I8GemmArgs a) {

@@ -378,8 +378,15 @@ struct Tile8 {
     const bool late = wave >= 4;
     if (late) phase_end();
     int kb = 0;
-    for (; kb + NS <= nK; kb += NS) steps<FLOW, 0, NS>(kb, NS);
-    if constexpr (!FLOW) steps<false, 0, NS - 1>(kb, nK - kb);
+    if constexpr (FLOW) {
+      do {  // at least once: so the compiler knows that what went out before has landed
+        steps<true, 0, NS>(kb, NS);
+        kb += NS;
+      } while (kb < nK);
+    } else {
+      for (; kb + NS <= nK; kb += NS) steps<false, 0, NS>(kb, NS);
+      steps<false, 0, NS - 1>(kb, nK - kb);
+    }
     if (!late) phase_end();  // as many barriers for the early waves as for the late ones
     if constexpr (!FLOW) {
       // the loads past the end land before the units are filled again or given back
@@ -628,31 +635,42 @@ struct SkinnyProduct {
 };
 
 // Two side-by-side 16 x 16 blocks of bf16 results stored (with add, added in fp32 to what is
-// there): lanes l and l ^ 16 swap halves, so that each stores eight consecutive columns and a row's
-// 64 bytes leave together. row: this lane's row at the blocks' first column.
+// there). Lanes 16..31 of lo and 0..15 of hi change places, and 48..63 and 32..47, so that each lane
+// stores eight consecutive columns and a row's 64 bytes leave together. row: this lane's row at the
+// blocks' first column.
+MOE_DEV void swap16(uint32_t& lo, uint32_t& hi) {
+  const auto v = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
+  lo = v[0];
+  hi = v[1];
+}
 MOE_DEV void store_pair(uint16_t* row, const f32x4& lo, const f32x4& hi, int lane, bool on,
                         bool add) {
   const int g = lane / 16;
-  const bool even = (g & 1) == 0;
-  float o[8];
+  uint4* p = reinterpret_cast<uint4*>(row + ((g & 1) == 0 ? 4 * g : 12 + 4 * g));
+  if (!add) {
+    uint32_t l0 = to_bf2(lo[0], lo[1]), l1 = to_bf2(lo[2], lo[3]);
+    uint32_t h0 = to_bf2(hi[0], hi[1]), h1 = to_bf2(hi[2], hi[3]);
+    swap16(l0, h0);
+    swap16(l1, h1);
+    if (on) *p = make_uint4(l0, l1, h0, h1);
+    return;
+  }
+  uint32_t o[8];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const float r = __shfl_xor(even ? hi[q] : lo[q], 16);
-    o[q] = even ? lo[q] : r;
-    o[4 + q] = even ? r : hi[q];
+    o[q] = __float_as_uint(lo[q]);
+    o[4 + q] = __float_as_uint(hi[q]);
+    swap16(o[q], o[4 + q]);
   }
   if (!on) return;
-  uint4* p = reinterpret_cast<uint4*>(row + (even ? 4 * g : 12 + 4 * g));
-  if (add) {
-    const uint4 v = *p;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint4 v = *p;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t r[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      o[2 * q] += bf2f_lo(w[q]);
-      o[2 * q + 1] += bf2f_hi(w[q]);
-    }
-  }
-  *p = make_uint4(to_bf2(o[0], o[1]), to_bf2(o[2], o[3]), to_bf2(o[4], o[5]), to_bf2(o[6], o[7]));
+  for (int q = 0; q < 4; ++q)
+    r[q] = to_bf2(__uint_as_float(o[2 * q]) + bf2f_lo(w[q]),
+                  __uint_as_float(o[2 * q + 1]) + bf2f_hi(w[q]));
+  *p = make_uint4(r[0], r[1], r[2], r[3]);
 }
 // NB blocks of a row, 16 columns each
 template <int NB>
@@ -679,25 +697,28 @@ MOE_DEV void store_blocks(uint16_t* row, const f32x4 (&v)[NB], int lane, bool on
 // The activations of the gated products and their derivatives, in fp32.
 constexpr int kSilu = 0, kGelu = 1, kGeluTanh = 2, kRelu = 3;
 constexpr float kGeluC = 0.7978845608028654f, kGeluK = 0.044715f;  // sqrt(2 / pi), the cubic's
+// 1 / (1 + exp(-x)) by the reciprocal instruction, off by two half steps where a division is by one,
+// for a third of its instructions: the epilogue of a gated 256 x 256 tile is 64 of these a lane.
+MOE_DEV float fast_sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
 template <int ACT>
 MOE_DEV float act_of(float g) {
-  if constexpr (ACT == kSilu) return g * sigmoid(g);
+  if constexpr (ACT == kSilu) return g * fast_sigmoid(g);
   else if constexpr (ACT == kGelu) return 0.5f * g * erfcf(g * -0.70710678f);
   else if constexpr (ACT == kGeluTanh)  // 0.5 (1 + tanh z) = sigmoid(2 z)
-    return g * sigmoid(2.f * kGeluC * (g + kGeluK * g * g * g));
+    return g * fast_sigmoid(2.f * kGeluC * (g + kGeluK * g * g * g));
   else return g < 0.f ? 0.f : g;  // NaN stays
 }
 // act(g) and act'(g)
 template <int ACT>
 MOE_DEV float2 act_grad(float g) {
   if constexpr (ACT == kSilu) {
-    const float s = sigmoid(g);
+    const float s = fast_sigmoid(g);
     return make_float2(g * s, s * (1.f + g * (1.f - s)));
   } else if constexpr (ACT == kGelu) {
     const float p = 0.5f * erfcf(g * -0.70710678f);  // 1 + erf would cancel
     return make_float2(g * p, p + g * 0.3989422804f * __expf(-0.5f * g * g));
   } else if constexpr (ACT == kGeluTanh) {
-    const float s = sigmoid(2.f * kGeluC * (g + kGeluK * g * g * g));
+    const float s = fast_sigmoid(2.f * kGeluC * (g + kGeluK * g * g * g));
     return make_float2(g * s,
                        s + g * s * (1.f - s) * (2.f * kGeluC) * (1.f + 3.f * kGeluK * g * g));
   } else {
