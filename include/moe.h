@@ -50,7 +50,9 @@ typedef enum moe_status {
 } moe_status;
 
 /* 3 is not in use. */
-enum { MOE_PREC_BF16 = 0, MOE_PREC_MXFP8 = 1, MOE_PREC_MXFP4 = 2, MOE_PREC_FP8 = 4 };
+enum {
+    MOE_PREC_BF16 = 0, MOE_PREC_MXFP8 = 1, MOE_PREC_MXFP4 = 2, MOE_PREC_FP8 = 4, MOE_PREC_INT8 = 5
+};
 
 /* cfg.flags bits */
 enum {
@@ -72,8 +74,8 @@ enum {
  * I % 128 == 0 (128-wide tiles along I); T * k < 2^31; T * E < 2^31; and, because the kernels
  * address rows with 32-bit offsets: T * d < 2^31, T * k * d < 2^31, T * k * 2I < 2^31 (an
  * expert may receive all T * k rows) and 4 * I * d < 2^31 (the bytes of one expert's W1).
- * precision MOE_PREC_BF16, MOE_PREC_MXFP8, MOE_PREC_FP8 or MOE_PREC_MXFP4 (MXFP4 also needs
- * I % 256 == 0: its K steps along I are 256 deep).
+ * precision MOE_PREC_BF16, MOE_PREC_MXFP8, MOE_PREC_FP8, MOE_PREC_INT8 or MOE_PREC_MXFP4 (MXFP4
+ * also needs I % 256 == 0: its K steps along I are 256 deep).
  * Every entry point that enqueues work also checks that the current HIP device is a gfx950
  * (MOE_ERR_UNSUPPORTED otherwise, MOE_ERR_HIP when no device can be queried).
  *
@@ -110,6 +112,14 @@ enum {
  * moe_quantize_weights is needed as in the MX modes.
  * MOE_FLAG_PERSISTENT and MOE_FLAG_MXFP8_WGRAD are not accepted, moe_forward_fused not provided.
  *
+ * INT8 mode is for inference: the experts' products in the 8-bit integers of the moe_i8_ calls below,
+ * a scale for each token and output channel. The ring slot holds bf16 Xp as in BF16 mode;
+ * moe_forward quantises its rows, forms A (bf16) from the exact integer products of the gate and up
+ * projections, and quantises A's rows for the down product. H is not kept: `saved` holds A
+ * alone (moe_sizes.saved_H means nothing). moe_quantize_weights is needed, and writes the forward's
+ * two weights only. No flag is accepted; moe_backward and moe_forward_fused return
+ * MOE_ERR_UNSUPPORTED. Limits: d and I below 2^17; T * k, E * 2I and E * d below 2^24.
+ *
  * Weight-gradient precision. The pages do not say in which precision the weight gradients are
  * kept. By default dw1 and dw2 are fp32 (the caller's main gradient, which microbatches
  * accumulate into). With MOE_FLAG_BF16_DW (any precision) they are bf16: each element is
@@ -135,7 +145,7 @@ typedef struct moe_sizes {
     size_t ws_O;           /* offset of the expert outputs O, bf16 [T*k, d], valid after forward */
     size_t ws_dH;          /* offset of dH, bf16 [T*k, 2I], valid after backward */
     size_t ws_dXp;         /* offset of dXp, bf16 [T*k, d], valid after backward */
-    size_t wq;             /* MX and FP8 modes: bytes of the quantised-weight buffer (else 0) */
+    size_t wq;             /* MX, FP8 and INT8 modes: bytes of the quantised-weight buffer (else 0) */
 } moe_sizes;
 
 /* Sizes of every caller buffer for `cfg`. Host only; enqueues nothing. (Plumbing of this
@@ -147,13 +157,13 @@ typedef struct moe_sizes {
 int moe_query(const moe_cfg* cfg, moe_sizes* out);
 
 /*
- * moe_quantize_weights - MX and FP8 modes: the quantised expert weights every such forward and
+ * moe_quantize_weights - MX, FP8 and INT8 modes: the quantised expert weights every such forward and
  * backward reads. Call it once per weight update; the result serves any number of batches.
  *
  *   w1  bf16 [E, 2I, d]   in
  *   w2  bf16 [E, d, I]    in
- *   wq  bytes [wq_bytes]  out, wq_bytes >= moe_sizes.wq. It receives four quantised tensors, each
- *       with its scales (per 32 in the MX modes): W1 along d [E, 2I, d] and W2 along I [E, d, I]
+ *   wq  bytes [wq_bytes]  out, wq_bytes >= moe_sizes.wq. It receives four quantised tensors (in INT8
+ *       mode the forward's two), each with its scales (per 32 in the MX modes): W1 along d [E, 2I, d] and W2 along I [E, d, I]
  *       (forward), and W2 along d stored transposed [E, I, d] and W1 along 2I stored transposed
  *       [E, d, 2I] (dgrad), in the mode's element format. The layout inside wq is private to the
  *       library.
@@ -253,7 +263,7 @@ int moe_permute_static(const moe_cfg* cfg, const int32_t* topk_idx, const void* 
  *   topk_w   fp32 [T, k]     in
  *   w1       bf16 [E, 2I, d] in
  *   w2       bf16 [E, d, I]  in
- *   wq, wq_bytes             in: MX and FP8 modes, the buffer moe_quantize_weights filled
+ *   wq, wq_bytes             in: MX, FP8 and INT8 modes, the buffer moe_quantize_weights filled
  *                                (ignored in BF16 mode, may be NULL)
  *   y        bf16 [T, d]     out
  *   saved    bytes [saved_bytes]   out: H and A at the offsets moe_query reports

@@ -27,6 +27,7 @@ MOE_PREC_BF16 = 0
 MOE_PREC_MXFP8 = 1
 MOE_PREC_MXFP4 = 2
 MOE_PREC_FP8 = 4
+MOE_PREC_INT8 = 5
 MOE_FLAG_PERSISTENT = 1
 MOE_FLAG_MXFP8_WGRAD = 2
 MOE_FLAG_BF16_DW = 4

@@ -22,7 +22,7 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct Layout {
-  bool mx, f8;  // the MX modes; the block-scaled FP8 mode
+  bool mx, f8, i8;  // the MX modes; the block-scaled FP8 mode; the INT8 mode
   int fb;  // MX code bits: 8 (MXFP8) or 4 (MXFP4); 0 in BF16 mode
   // workspace
   size_t status, sched, blk_cnt, blk_flag, rank, O, dH, dXp, dyw, dwpart, dl_pos, wg_count,
@@ -35,6 +35,8 @@ struct Layout {
   int P;
   // workspace, FP8 mode only: the rows of one product quantised (Xp, A, dY or dH), and dA'
   size_t f8q, f8s, dAp;
+  // workspace, INT8 mode only: the rows of one product quantised (Xp or A)
+  size_t i8q, i8s;
   // saved
   size_t H, A, saved_total;
   // ring slot: bf16 Xp, or MX Xp codes at 0 and scales at slot_sc
@@ -137,9 +139,13 @@ Layout layout(const moe_cfg* c) {
   L.f8q = take(f8 * Tk * fcols);
   L.f8s = take(f8 * sizeof(float) * Tk * (fcols / 128));
   L.dAp = take(f8 * 2 * Tk * I);
+  L.i8 = c->precision == MOE_PREC_INT8;
+  const size_t i8 = L.i8 ? 1 : 0;
+  L.i8q = take(i8 * Tk * std::max(d, I));
+  L.i8s = take(i8 * sizeof(float) * Tk);
   L.total = o;
   o = 0;
-  L.H = take(2 * Tk * 2 * I);
+  L.H = take(L.i8 ? 0 : 2 * Tk * 2 * I);
   L.A = take(2 * Tk * I);
   L.saved_total = o;
   if (L.mx) {
@@ -174,6 +180,14 @@ Layout layout(const moe_cfg* c) {
     L.w1bs = take(sizeof(float) * (n1 / 16384));
     L.wq_total = o;
   }
+  if (L.i8) {  // the forward's weights, a scale per output channel
+    o = 0;
+    L.w1f = take(E * 2 * I * d);
+    L.w1fs = take(sizeof(float) * E * 2 * I);
+    L.w2f = take(E * d * I);
+    L.w2fs = take(sizeof(float) * E * d);
+    L.wq_total = o;
+  }
   return L;
 }
 
@@ -201,8 +215,15 @@ struct Launches {
 int check_mode(const moe_cfg* c) {
   if (!cfg_ok(c)) return MOE_ERR_INVALID_ARG;
   if (c->precision != MOE_PREC_BF16 && c->precision != MOE_PREC_MXFP8 &&
-      c->precision != MOE_PREC_MXFP4 && c->precision != MOE_PREC_FP8)
+      c->precision != MOE_PREC_MXFP4 && c->precision != MOE_PREC_FP8 &&
+      c->precision != MOE_PREC_INT8)
     return MOE_ERR_UNSUPPORTED;
+  if (c->precision == MOE_PREC_INT8) {
+    const long long top = 1LL << 24, E = c->E;  // rows of one quantisation
+    if (c->flags || c->d >= (1 << 17) || c->I >= (1 << 17) || (long long)c->T * c->k >= top ||
+        E * 2 * c->I >= top || E * c->d >= top)
+      return MOE_ERR_INVALID_ARG;
+  }
   if (c->precision == MOE_PREC_FP8 && (c->flags & MOE_FLAG_PERSISTENT)) return MOE_ERR_INVALID_ARG;
   if (c->precision == MOE_PREC_MXFP4 && c->I % 256 != 0) return MOE_ERR_INVALID_ARG;
   if (c->flags & ~(MOE_FLAG_PERSISTENT | MOE_FLAG_MXFP8_WGRAD | MOE_FLAG_BF16_DW))
@@ -220,7 +241,7 @@ int check_ring(const Layout& L, const void* ring, size_t ring_bytes, int32_t slo
 
 // The quantised weights of the MX modes, or an error code when they are missing.
 int check_wq(const Layout& Y, const void* wq, size_t wq_bytes) {
-  if (!Y.mx && !Y.f8) return MOE_OK;
+  if (!Y.mx && !Y.f8 && !Y.i8) return MOE_OK;
   if (!aligned16(wq)) return MOE_ERR_INVALID_ARG;
   if (wq_bytes < Y.wq_total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return MOE_OK;
@@ -363,7 +384,7 @@ int moe_query(const moe_cfg* cfg, moe_sizes* out) {
   out->ws_O = L.O;
   out->ws_dH = L.dH;
   out->ws_dXp = L.dXp;
-  out->wq = L.mx || L.f8 ? L.wq_total : 0;
+  out->wq = L.mx || L.f8 || L.i8 ? L.wq_total : 0;
   return MOE_OK;
 }
 
@@ -372,7 +393,7 @@ int moe_quantize_weights(const moe_cfg* cfg, const void* w1, const void* w2, voi
   int st = check_mode(cfg);
   if (st) return st;
   const Layout Y = layout(cfg);
-  if (!Y.mx && !Y.f8) return MOE_ERR_INVALID_ARG;
+  if (!Y.mx && !Y.f8 && !Y.i8) return MOE_ERR_INVALID_ARG;
   if (!aligned16(w1) || !aligned16(w2) || !aligned16(wq)) return MOE_ERR_INVALID_ARG;
   if (wq_bytes < Y.wq_total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if ((st = check_device())) return st;
@@ -381,6 +402,13 @@ int moe_quantize_weights(const moe_cfg* cfg, const void* w1, const void* w2, voi
   const uint16_t* a1 = static_cast<const uint16_t*>(w1);
   const uint16_t* a2 = static_cast<const uint16_t*>(w2);
   Launches L;
+  if (Y.i8) {
+    L(launch_i8_quant_rows(a1, 2LL * E * I, d, at<uint8_t>(wq, Y.w1f), at<float>(wq, Y.w1fs), s));
+    if (!L.err)
+      L(launch_i8_quant_rows(a2, (long long)E * d, I, at<uint8_t>(wq, Y.w2f),
+                             at<float>(wq, Y.w2fs), s));
+    return L.status();
+  }
   if (Y.f8) {
     L(launch_fp8_quant_weights(a1, E, 2 * I, d, at<uint8_t>(wq, Y.w1f), at<float>(wq, Y.w1fs),
                                at<uint8_t>(wq, Y.w1b), at<float>(wq, Y.w1bs), s));
@@ -534,6 +562,23 @@ int moe_forward(const moe_cfg* cfg, const void* ring, size_t ring_bytes, int32_t
       L(launch_combine(O, tk_row, topk_w, cfg->T, cfg->k, d, static_cast<uint16_t*>(y), s));
     return L.status();
   }
+  if (Y.i8) {
+    uint8_t* q = at<uint8_t>(workspace, Y.i8q);
+    float* qs = at<float>(workspace, Y.i8s);
+    L(launch_i8_quant_rows(reinterpret_cast<const uint16_t*>(slot_base), Tk, d, q, qs, s));
+    if (!L.err)
+      L(launch_i8_gemm({offsets, q, qs, at<uint8_t>(wq, Y.w1f), at<float>(wq, Y.w1fs), A, Tk, E,
+                        2 * I, d, MOE_ACT_SILU},
+                       true, s));
+    if (!L.err) L(launch_i8_quant_rows(A, Tk, I, q, qs, s));
+    if (!L.err)
+      L(launch_i8_gemm({offsets, q, qs, at<uint8_t>(wq, Y.w2f), at<float>(wq, Y.w2fs), O, Tk, E, d,
+                        I, 0},
+                       false, s));
+    if (!L.err)
+      L(launch_combine(O, tk_row, topk_w, cfg->T, cfg->k, d, static_cast<uint16_t*>(y), s));
+    return L.status();
+  }
   L(launch_sched_build(offsets, E, Tk, sched, s));
   if (Y.mx) {
     uint8_t* aq = at<uint8_t>(workspace, Y.aq);
@@ -628,6 +673,7 @@ int moe_backward(const moe_cfg* cfg, const void* ring, size_t ring_bytes, int32_
                  size_t ws_bytes, moe_stream_t stream) {
   int st = check_mode(cfg);
   if (st) return st;
+  if (cfg->precision == MOE_PREC_INT8) return MOE_ERR_UNSUPPORTED;
   const Layout Y = layout(cfg);
   const bool routed = w_router != nullptr;
   if (!aligned4(offsets) || !aligned4(row_src) || !aligned4(tk_row) || !aligned4(topk_idx) ||

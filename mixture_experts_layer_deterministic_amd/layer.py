@@ -6,10 +6,39 @@ from __future__ import annotations
 
 import torch
 
-from . import (MOE_FLAG_BF16_DW, MOE_FLAG_MXFP8_WGRAD, MOE_FLAG_PERSISTENT, MOE_PREC_BF16,
-               MOE_PREC_MXFP4, MOE_PREC_MXFP8, _dev, make_cfg, moe_backward, moe_forward,
-               moe_forward_fused, moe_gate_backward, moe_permute, moe_query, moe_quantize_weights,
-               moe_route, moe_route_gated, moe_router_backward)
+from . import (MOE_ACT_SILU, MOE_FLAG_BF16_DW, MOE_FLAG_MXFP8_WGRAD, MOE_FLAG_PERSISTENT,
+               MOE_PREC_BF16, MOE_PREC_INT8, MOE_PREC_MXFP4, MOE_PREC_MXFP8, _dev, make_cfg,
+               make_ffn, moe_backward, moe_ffn_backward, moe_ffn_forward, moe_ffn_query,
+               moe_forward, moe_forward_fused, moe_gate_backward, moe_permute, moe_query,
+               moe_quantize_weights, moe_route, moe_route_gated, moe_router_backward)
+
+
+class SharedExpert:
+    """Caller-owned buffers of the dense gated feed-forward block (``moe_ffn_forward``,
+    ``moe_ffn_backward``): the expert every token passes beside its routed ones, or a block of its
+    own. ``train`` keeps H = [g | u] for the backward and owns the gradients dw1 and dw2."""
+
+    def __init__(self, T, d, I, act=MOE_ACT_SILU, device="cuda", train=True, bf16_dw=False):
+        self.cfg = make_ffn(T, d, I, act, MOE_FLAG_BF16_DW if bf16_dw else 0)
+        dev, bf = torch.device(device), torch.bfloat16
+        self.workspace = torch.empty(moe_ffn_query(self.cfg).workspace, dtype=torch.uint8,
+                                     device=dev)
+        self.A = torch.empty(T, I, dtype=bf, device=dev)
+        self.H = torch.empty(T, 2 * I, dtype=bf, device=dev) if train else None
+        dwt = bf if bf16_dw else torch.float32
+        self.dw1 = torch.zeros(2 * I, d, dtype=dwt, device=dev) if train else None
+        self.dw2 = torch.zeros(d, I, dtype=dwt, device=dev) if train else None
+
+    def forward(self, x, w1, w2, y, accumulate=False, stream=None):
+        """y = block(x), or with ``accumulate`` y + block(x)."""
+        moe_ffn_forward(self.cfg, x, w1, w2, self.H, self.A, y, accumulate, self.workspace, stream)
+
+    def backward(self, x, w1, w2, dy, dx, accumulate_dx=False, accumulate=False, stream=None):
+        """dx (added to with ``accumulate_dx``), dw1 and dw2 (added to with ``accumulate``)."""
+        if self.H is None:
+            raise ValueError("a block made without train keeps nothing for a backward")
+        moe_ffn_backward(self.cfg, x, w1, w2, self.H, self.A, dy, dx, self.dw1, self.dw2,
+                         accumulate_dx, accumulate, self.workspace, stream)
 
 
 class MoeLayer:
@@ -20,7 +49,12 @@ class MoeLayer:
     or ``MOE_PREC_MXFP4`` the layer also owns the quantised-weight buffer ``wq``;
     ``quantize_weights`` fills it, and ``mx_wgrad`` (MXFP8 only) makes the weight gradients
     MXFP8 too. ``MOE_PREC_FP8`` owns and fills ``wq`` likewise; its ring slots hold bf16 tokens.
-    ``bf16_dw`` keeps dw1 and dw2 in bf16.
+    ``bf16_dw`` keeps dw1 and dw2 in bf16. ``MOE_PREC_INT8`` owns and fills ``wq`` too, and is for
+    inference: it has no gradients, and no H.
+
+    With ``shared`` (a ``SharedExpert`` of the same T and d) the forward adds the shared expert's
+    output to y and the backward its gradient to dx; both then need the tokens ``x`` and its weights
+    ``shared_w`` = (w1, w2).
 
     With ``gate`` (from ``make_gate``) the layer routes by that gate instead of the renormalised
     top-k softmax, with ``gate_bias`` (fp32 [E], or None) in its choice, and backward takes the
@@ -29,7 +63,8 @@ class MoeLayer:
     """
 
     def __init__(self, T, d, E, k, I, device="cuda", ring_slots=1, persistent=False,
-                 precision=MOE_PREC_BF16, mx_wgrad=False, bf16_dw=False, gate=None, gate_bias=None):
+                 precision=MOE_PREC_BF16, mx_wgrad=False, bf16_dw=False, gate=None, gate_bias=None,
+                 shared=None):
         self.T, self.d, self.E, self.k, self.I = T, d, E, k, I
         flags = ((MOE_FLAG_PERSISTENT if persistent else 0) |
                  (MOE_FLAG_MXFP8_WGRAD if mx_wgrad else 0) | (MOE_FLAG_BF16_DW if bf16_dw else 0))
@@ -53,9 +88,13 @@ class MoeLayer:
         self.dx = torch.empty(T, d, dtype=bf, device=dev)
         self.d_topk_w = torch.empty(T, k, dtype=f32, device=dev)
         dwt = bf if bf16_dw else f32
-        self.dw1 = torch.zeros(E, 2 * I, d, dtype=dwt, device=dev)
-        self.dw2 = torch.zeros(E, d, I, dtype=dwt, device=dev)
-        self.dwr = torch.zeros(E, d, dtype=f32, device=dev)
+        self.infer = precision == MOE_PREC_INT8
+        self.dw1 = None if self.infer else torch.zeros(E, 2 * I, d, dtype=dwt, device=dev)
+        self.dw2 = None if self.infer else torch.zeros(E, d, I, dtype=dwt, device=dev)
+        self.dwr = None if self.infer else torch.zeros(E, d, dtype=f32, device=dev)
+        if shared is not None and (shared.cfg.T, shared.cfg.d) != (T, d):
+            raise ValueError("the shared expert takes other tokens than the layer")
+        self.shared = shared
         self.mx = precision in (MOE_PREC_MXFP8, MOE_PREC_MXFP4)
         self.fbits = 8 if precision == MOE_PREC_MXFP8 else 4 if precision == MOE_PREC_MXFP4 else 16
         self.wq = torch.empty(s.wq, dtype=u8, device=dev) if s.wq else None
@@ -82,6 +121,8 @@ class MoeLayer:
         return codes, self.ring[sc0:sc0 + Tk * d // 32].view(Tk, d // 32)
 
     def H(self):
+        if self.infer:
+            raise ValueError("the INT8 mode keeps no H")
         return self._view(self.saved, self.sizes.saved_H, self.T * self.k, 2 * self.I)
 
     def A(self):
@@ -121,26 +162,51 @@ class MoeLayer:
     def quantize_weights(self, w1, w2, stream=None):
         moe_quantize_weights(self.cfg, w1, w2, self.wq, stream)
 
-    def forward(self, w1, w2, slot=0, saved=None, stream=None):
+    def _shared_operands(self, x, shared_w):
+        if x is None or shared_w is None:
+            raise ValueError("a layer with a shared expert needs x and shared_w")
+        return x, *shared_w
+
+    def forward(self, w1, w2, slot=0, saved=None, stream=None, x=None, shared_w=None):
+        if self.shared is not None:
+            ops = self._shared_operands(x, shared_w)
         moe_forward(self.cfg, self.ring, slot, self.offsets, self.tk_row, self.topk_w, w1, w2,
                     self.wq, self.y, self.saved if saved is None else saved, self.workspace,
                     stream)
+        if self.shared is not None:
+            self.shared.forward(*ops, self.y, True, stream)
 
-    def forward_fused(self, x, w_router, w1, w2, slot=0, saved=None, stream=None):
+    def forward_fused(self, x, w_router, w1, w2, slot=0, saved=None, stream=None, shared_w=None):
         """route + permute + forward in one kernel launch (moe_forward_fused), which has no gate."""
         if self.gate is not None:
             raise ValueError("the single-launch forward routes by the top-k softmax only")
+        if self.shared is not None:
+            ops = self._shared_operands(x, shared_w)
         self.given = False
         moe_forward_fused(self.cfg, x, w_router, self.logits, self.topk_idx, self.topk_w,
                           self.ring, slot, self.counts, self.offsets, self.row_src, self.tk_row,
                           w1, w2, self.y, self.saved if saved is None else saved, self.workspace,
                           stream)
+        if self.shared is not None:
+            self.shared.forward(*ops, self.y, True, stream)
 
     def backward(self, w_router, w1, w2, dy, slot=0, accumulate=False, saved=None, stream=None,
-                 x=None):
+                 x=None, shared_w=None):
         """With a gate and a ``w_router``, ``x`` (the tokens) is needed too: the experts' backward
-        runs as for a given routing, then the gate's and the router's add theirs to dx and dwr."""
-        if self.gate is not None and w_router is not None:
+        runs as for a given routing, then the gate's and the router's add theirs to dx and dwr.
+        With a shared expert its backward comes last and adds to dx."""
+        if self.infer:
+            raise ValueError("the INT8 mode has no backward")
+        if self.shared is not None:
+            ops = self._shared_operands(x, shared_w)
+            if self.shared.H is None:
+                raise ValueError("the shared expert was made without train")
+            # refused before the experts' gradients are written or added to
+            T, d, I, bf = self.T, self.d, self.shared.cfg.I, torch.bfloat16
+            _dev("MoeLayer.backward", stream, (x, bf, T * d), (ops[1], bf, 2 * I * d),
+                 (ops[2], bf, d * I), (dy, bf, T * d))
+        gated = self.gate is not None and w_router is not None
+        if gated:
             if self.given:
                 raise ValueError("a given routing has no logits to take a gate's gradients at")
             if x is None:
@@ -148,30 +214,32 @@ class MoeLayer:
             # refused before the experts' gradients are written or added to
             _dev("MoeLayer.backward", stream, (x, torch.bfloat16, self.T * self.d),
                  (w_router, torch.bfloat16, self.E * self.d))
-            self.backward(None, w1, w2, dy, slot, accumulate, saved, stream)
+        routed = w_router is not None and not gated
+        moe_backward(self.cfg, self.ring, slot, self.offsets, self.row_src, self.tk_row,
+                     self.topk_idx, self.topk_w, w_router if routed else None, w1, w2, self.wq,
+                     self.saved if saved is None else saved, dy, self.dx, self.dw1, self.dw2,
+                     self.dwr if routed else None, self.d_topk_w, accumulate,
+                     self.workspace, stream)
+        if gated:
             moe_gate_backward(self.cfg, self.gate, self.logits, self.topk_idx, self.d_topk_w,
                               self.dlogits, False, stream)
             moe_router_backward(self.cfg, x, w_router, self.dlogits, self.dx, self.dwr, True,
                                 accumulate, stream)
-            return
-        moe_backward(self.cfg, self.ring, slot, self.offsets, self.row_src, self.tk_row,
-                     self.topk_idx, self.topk_w, w_router, w1, w2, self.wq,
-                     self.saved if saved is None else saved, dy, self.dx, self.dw1, self.dw2,
-                     self.dwr if w_router is not None else None, self.d_topk_w, accumulate,
-                     self.workspace, stream)
+        if self.shared is not None:
+            self.shared.backward(*ops, dy, self.dx, True, accumulate, stream)
 
-    def step(self, x, w_router, w1, w2, dy, slot=0, stream=None, fused=False):
+    def step(self, x, w_router, w1, w2, dy, slot=0, stream=None, fused=False, shared_w=None):
         """One fwd+bwd pass: route (when w_router is given), permute, forward, backward. With
         ``fused`` the first three run as one launch (moe_forward_fused)."""
         if fused:
-            self.forward_fused(x, w_router, w1, w2, slot, stream=stream)
-            self.backward(w_router, w1, w2, dy, slot, stream=stream)
+            self.forward_fused(x, w_router, w1, w2, slot, stream=stream, shared_w=shared_w)
+            self.backward(w_router, w1, w2, dy, slot, stream=stream, x=x, shared_w=shared_w)
             return
         if w_router is not None:
             self.route(x, w_router, stream)
         self.permute(x, slot, stream)
-        self.forward(w1, w2, slot, stream=stream)
-        self.backward(w_router, w1, w2, dy, slot, stream=stream, x=x)
+        self.forward(w1, w2, slot, stream=stream, x=x, shared_w=shared_w)
+        self.backward(w_router, w1, w2, dy, slot, stream=stream, x=x, shared_w=shared_w)
 
 
 class Macrobatch:

@@ -156,3 +156,66 @@ def test_activations_are_torchs(a):
     y.sum().backward()
     np.testing.assert_allclose(P64.act(a, g), y.detach().numpy(), rtol=1e-12, atol=1e-14)
     np.testing.assert_allclose(P64.act_grad(a, g), t.grad.numpy(), rtol=1e-9, atol=1e-12)
+
+
+def test_int8_mode_sizes_and_refusals():
+    T, d, E, k, I = 300, 512, 16, 3, 256
+    c = m.make_cfg(T, d, E, k, I, m.MOE_PREC_INT8)
+    s8, s = m.moe_query(c), m.moe_query(m.make_cfg(T, d, E, k, I))
+    up = lambda v: (v + 255) // 256 * 256
+    Tk = T * k
+    assert s8.ring_slot == s.ring_slot and s8.saved == up(2 * Tk * I) and s8.saved_A == 0
+    assert s8.wq == up(E * 2 * I * d) + up(4 * E * 2 * I) + up(E * d * I) + up(4 * E * d)
+    assert s8.workspace - s.workspace == up(Tk * max(d, I)) + up(4 * Tk)
+    for flag in (m.MOE_FLAG_PERSISTENT, m.MOE_FLAG_MXFP8_WGRAD, m.MOE_FLAG_BF16_DW):
+        with pytest.raises(m.MoeError) as e:
+            m.moe_query(m.make_cfg(T, d, E, k, I, m.MOE_PREC_INT8, flag))
+        assert e.value.status == ARG
+    for bad in ((4, 1 << 17, 1, 1, 128), (4, 256, 1, 1, 1 << 17), (1 << 20, 256, 32, 16, 128),
+                (4, 256, 1024, 1, 1 << 14), (4, 1 << 14, 1024, 1, 128)):
+        with pytest.raises(m.MoeError) as e:
+            m.moe_query(m.make_cfg(*bad, m.MOE_PREC_INT8))
+        assert e.value.status == ARG, bad
+    L, r = m.lib(), ctypes.byref(c)
+    assert L.moe_quantize_weights(r, P, P, P, s8.wq - 1, None) == -5
+    fwd = lambda wq, n: L.moe_forward(r, P, s8.ring_slot, 0, P, P, P, P, P, wq, n, P, P, s8.saved,
+                                      P, s8.workspace, None)
+    assert fwd(None, 0) == ARG and fwd(P, s8.wq - 1) == -5
+    assert L.moe_backward(r, P, s8.ring_slot, 0, P, P, P, P, P, None, P, P, P, s8.wq, P, s8.saved,
+                          P, P, P, P, None, P, 0, P, s8.workspace, None) == -3
+    assert L.moe_forward_fused(r, P, P, P, P, P, P, s8.ring_slot, 0, P, P, P, P, P, P, P, P,
+                               s8.saved, P, s8.workspace, None) == -3
+
+
+def test_layer_refusals(monkeypatch):
+    from mixture_experts_layer_deterministic_amd import layer
+    calls = []
+    for name in ("moe_forward", "moe_backward", "moe_ffn_forward", "moe_ffn_backward"):
+        monkeypatch.setattr(layer, name, lambda *a, n=name: calls.append(n))
+    monkeypatch.setattr(layer, "_dev", lambda *a: calls.append("checks"))
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    L = layer.MoeLayer(4, 256, 8, 2, 128, device="cpu", precision=m.MOE_PREC_INT8)
+    assert L.dw1 is None and L.dw2 is None
+    with pytest.raises(ValueError, match="no backward"):
+        L.backward(None, x, x, x)
+    with pytest.raises(ValueError, match="no H"):
+        L.H()
+    with pytest.raises(ValueError, match="other tokens"):
+        layer.MoeLayer(4, 256, 8, 2, 128, device="cpu",
+                       shared=layer.SharedExpert(5, 256, 128, device="cpu"))
+    sh = layer.SharedExpert(4, 256, 128, device="cpu", train=False)
+    L = layer.MoeLayer(4, 256, 8, 2, 128, device="cpu", shared=sh)
+    for call in (lambda: L.forward(x, x), lambda: L.forward(x, x, x=x),
+                 lambda: L.forward_fused(x, x, x, x), lambda: L.backward(None, x, x, x, x=x)):
+        with pytest.raises(ValueError, match="needs x and shared_w"):
+            call()
+    with pytest.raises(ValueError, match="without train"):
+        L.backward(None, x, x, x, x=x, shared_w=(x, x))
+    with pytest.raises(ValueError, match="nothing for a backward"):
+        sh.backward(x, x, x, x, x)
+    assert not calls
+    L.forward(x, x, x=x, shared_w=(x, x))
+    assert calls == ["moe_forward", "moe_ffn_forward"]
+    sh.H = x
+    L.backward(None, x, x, x, x=x, shared_w=(x, x))
+    assert calls[2:] == ["checks", "moe_backward", "moe_ffn_backward"]
