@@ -441,14 +441,28 @@ float time_of(long long n1, float t1, long long n2, float t2) {
   return done;
 }
 
-// Shares of K for up to half a card of 128 x 128 tiles: as many as fill it, of 12 steps at least (a
-// step is about 0.5 us, the second kernel 4 to 9). Unsplit and split, both kernels, in us: [g | u] of
-// 128 x 7168 x 2048 73 and 24, of 512 tokens 74 and 49; its dH 60 and 19, 61 and 30 (1024 tokens 64 and
-// 47); dx of 128 tokens 36 and 22. Shares of 8 steps where 16 was all: 18 for 12 (y of 333 x 4096 x
-// 1024).
+// What else a tile costs: its start, its first loads and its epilogue.
+constexpr float kTileUs = 4.f;
+// What shares of K cost beyond their steps: the second kernel, up to 9 us for a card full of sums.
+float shares_us(long long shares, long long tiles) {
+  return shares > 1 ? 4.f + 5.f * (float)(shares * tiles) / kCus : 0.f;
+}
+// Shares of K for few 128 x 128 tiles, of four steps at least: where the steps that are left and the
+// second kernel cost the least, a step of a card that is not full 0.6 us. Unsplit and split, both
+// kernels, in us: [g | u] of 128 x 7168 x 2048 73 and 24 (8 shares), of 512 tokens 74 and 49 (2); its
+// dH 60 and 19 (16), 61 and 30 (4); y of 333 x 4096 x 1024, 96 tiles of 16 steps, 12 and 18.
 int shares_of(long long tiles, int steps) {
-  if (tiles > kCus / 2) return 1;
-  return (int)std::max(1LL, std::min((long long)kCus / tiles, (long long)steps / 12));
+  const int most = (int)std::min((long long)kCus / std::max(tiles, 1LL), (long long)steps / 4);
+  int best = 1;
+  float least = 0.6f * steps;
+  for (int n = 2; n <= most; ++n) {
+    const float us = 0.6f * steps / n + shares_us(n, tiles);
+    if (us < least) {
+      least = us;
+      best = n;
+    }
+  }
+  return best;
 }
 
 template <class K, class A>
@@ -477,27 +491,29 @@ hipError_t launch_whole(const char* name, const typename P::Args& a, hipStream_t
 }
 template <class P>
 hipError_t launch_pair(const char* name, const FfnArgs& rows, const FfnDwArgs& dw, hipStream_t s) {
-  Pair<P> p{rows, dw, 0, tile_shape<Dw>(dw), 0};
+  // the rows' tiles in each shape, or in shares, with the weights' in each: the pair that is done first
+  Pair<P> p{rows, dw, 0, 0, 0};
   const long long small = tiles_of<P, 128, 128>(rows);
-  p.rows.shares = shares_of(small, P::steps(rows));
-  long long first = small * p.rows.shares;
-  if (p.rows.shares > 1) {
-    p.rows_shape = kShares;
-  } else {
-    float least = 0.f;
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const float us =
-            time_of(shape_tiles<P>(rows, i), kShapes[i].us * P::steps(rows),
-                    shape_tiles<Dw>(dw, j), kShapes[j].us * Dw::steps(dw));
-        if ((i == 0 && j == 0) || us < least) {
-          least = us;
-          p.rows_shape = i;
-          p.dw_shape = j;
-        }
+  const int shares = shares_of(small, P::steps(rows));
+  float least = 0.f;
+  for (int i = 0; i < (shares > 1 ? 5 : 4); ++i) {
+    const bool split = i == kShares;
+    const long long n = split ? small * shares : shape_tiles<P>(rows, i);
+    const float step = split ? kShapes[kSmall].us / shares : kShapes[i].us;
+    for (int j = 0; j < 4; ++j) {
+      const float us = time_of(n, kTileUs + step * P::steps(rows), shape_tiles<Dw>(dw, j),
+                               kTileUs + kShapes[j].us * Dw::steps(dw)) +
+                       (split ? shares_us(shares, small) : 0.f);
+      if ((i == 0 && j == 0) || us < least) {
+        least = us;
+        p.rows_shape = i;
+        p.dw_shape = j;
       }
-    first = shape_tiles<P>(rows, p.rows_shape);
+    }
   }
+  p.rows.shares = p.rows_shape == kShares ? shares : 1;
+  const long long first =
+      p.rows_shape == kShares ? small * shares : shape_tiles<P>(rows, p.rows_shape);
   p.first = (int)grid8(first);
   const hipError_t e = launch_kernel(name, ffn_pair_kernel<P>, p,
                                      p.first + grid8(shape_tiles<Dw>(dw, p.dw_shape)), 512, s);
