@@ -301,12 +301,13 @@ int check_ffn(const moe_ffn* f) {
   return MOE_OK;
 }
 struct FfnLayout {
-  size_t dH, part, total;
+  size_t dH, part, part_dw, total;
 };
 FfnLayout ffn_layout(const moe_ffn* f) {
   FfnLayout L{};
   L.part = align_up(2 * (size_t)f->T * 2 * f->I);
-  L.total = L.part + kFfnPartBytes;
+  L.part_dw = L.part + kFfnPartBytes;
+  L.total = L.part_dw + kFfnPartBytes;
   return L;
 }
 
@@ -1034,10 +1035,12 @@ int moe_ffn_backward(const moe_ffn* ffn, const void* x, const void* w1, const vo
   a.act = ffn->act;
   a.acc_dx = acc_dx != 0;
   Launches L;
-  L(launch_ffn_dh_dw2(a, {a.dy, static_cast<const uint16_t*>(A), dw2, a.T, a.d, a.I, acc, bdw}, s));
+  float* part = at<float>(workspace, Y.part_dw);
+  L(launch_ffn_dh_dw2(
+      a, {a.dy, static_cast<const uint16_t*>(A), dw2, part, a.T, a.d, a.I, acc, bdw, 1}, s));
   if (!L.err)
     L(launch_ffn_dx_dw1(
-        a, {a.dH, static_cast<const uint16_t*>(x), dw1, a.T, 2 * a.I, a.d, acc, bdw}, s));
+        a, {a.dH, static_cast<const uint16_t*>(x), dw1, part, a.T, 2 * a.I, a.d, acc, bdw, 1}, s));
   return L.status();
 }
 

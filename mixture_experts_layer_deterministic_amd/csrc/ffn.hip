@@ -102,7 +102,6 @@ struct Down {
 struct Dh {
   using Args = FfnArgs;
   static constexpr bool kAKM = false, kBKM = true, kGated = false;
-  static constexpr const char* kName = "ffn_dh";
   MOE_BOTH long long m(const Args& a) { return a.T; }
   MOE_BOTH long long n(const Args& a) { return a.I; }
   MOE_BOTH int steps(const Args& a) { return a.d / 64; }
@@ -150,7 +149,6 @@ struct Dh {
 struct Dx {
   using Args = FfnArgs;
   static constexpr bool kAKM = false, kBKM = true, kGated = false;
-  static constexpr const char* kName = "ffn_dx";
   MOE_BOTH long long m(const Args& a) { return a.T; }
   MOE_BOTH long long n(const Args& a) { return a.d; }
   MOE_BOTH int steps(const Args& a) { return 2 * a.I / 64; }
@@ -175,10 +173,11 @@ struct Dw {
   MOE_BOTH long long n(const Args& a) { return a.Nd; }
   MOE_BOTH int steps(const Args& a) { return (a.T + 63) / 64; }
   template <class W>
-  static MOE_DEV void setup(const Args& a, W& w, int row0, int, int n0, int) {
+  static MOE_DEV void setup(const Args& a, W& w, int row0, int, int n0, int k0) {
     w.a_cols(2 * a.Md);
     w.b_cols(2 * a.Nd);
-    w.next(a.L + row0, 2u * a.T * a.Md - 2 * row0, a.R + n0, 2u * a.T * a.Nd - 2 * n0);
+    w.next(a.L + (size_t)64 * k0 * a.Md + row0, 2u * (a.T - 64 * k0) * a.Md - 2 * row0,
+           a.R + (size_t)64 * k0 * a.Nd + n0, 2u * (a.T - 64 * k0) * a.Nd - 2 * n0);
   }
   template <class W>
   static MOE_DEV void store(const Args& a, const W& w, int row0, int rows, int n0, int cols) {
@@ -311,8 +310,11 @@ __global__ void __launch_bounds__(512, 2) ffn_pair_kernel(const Pair<P> p) {
     case kWide:
       if (lt < tiles_of<Dw, 128, 256>(p.dw)) whole_tile<Dw, 128, 256>(p.dw, lt);
       break;
-    default:
+    case kSmall:
       if (lt < tiles_of<Dw, 128, 128>(p.dw)) whole_tile<Dw, 128, 128>(p.dw, lt);
+      break;
+    default:
+      if (lt < tiles_of<Dw, 128, 128>(p.dw) * p.dw.shares) share_of_tile<Dw>(p.dw, lt);
   }
 }
 
@@ -323,11 +325,12 @@ struct JoinedRows {  // one row block of a wave of tile T
   f32x4 acc[1][NB];
   MOE_DEV int row_of(int) const { return row0 + lane % 16; }
 };
+// Workgroup b of eight a tile.
 template <class P>
-__global__ void __launch_bounds__(256) ffn_join_kernel(const typename P::Args a) {
+MOE_DEV void join_rows(const typename P::Args& a, int block) {
   using T = Tile8<Bf16, 128, 128, P::kAKM, P::kBKM, P::kGated>;
-  const int S = a.shares, lt = blockIdx.x / (2 * T::MB);
-  const int b = blockIdx.x % (2 * T::MB) * 4 + threadIdx.x / kWave;  // row block of the tile's waves
+  const int S = a.shares, lt = block / (2 * T::MB);
+  const int b = block % (2 * T::MB) * 4 + threadIdx.x / kWave;  // row block of the tile's waves
   const int wave = b / T::MB, mb = b % T::MB;
   const Place t = place_of<P, 128, 128>(a, lt);
   JoinedRows<T> w;
@@ -347,6 +350,17 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(const typename P::Args a)
     for (int nb = 0; nb < T::NB; ++nb) w.acc[0][nb] += p[nb * kWave];
   }
   P::store(a, w, t.row0, t.rows, t.n0, t.cols);
+}
+template <class P>
+__global__ void __launch_bounds__(256) ffn_join_kernel(const typename P::Args a) {
+  join_rows<P>(a, blockIdx.x);
+}
+// Of a pair: the first `rows` workgroups for the rows' gradient, the others for the weights'.
+template <class P>
+__global__ void __launch_bounds__(256) ffn_join_pair_kernel(const Pair<P> p, int rows) {
+  const int b = blockIdx.x;
+  if (b < rows) join_rows<P>(p.rows, b);
+  else join_rows<Dw>(p.dw, b - rows);
 }
 
 // A handful of tokens: up to 16, a workgroup for 8 columns of A.
@@ -377,20 +391,20 @@ __global__ void __launch_bounds__(512, 4) ffn_skinny_gate_up_kernel(const FfnArg
                    to_bf2(act_of<A>(v[2]) * u[2], act_of<A>(v[3]) * u[3]));
   });
 }
-// Up to 16 NMB, a workgroup for 32 columns of y.
-template <int NMB, int U>
+// Up to 16 NMB, a workgroup for 16 NNB columns of y.
+template <int NMB, int NNB, int U>
 __global__ void __launch_bounds__(512, 2) ffn_skinny_down_kernel(const FfnArgs a) {
-  __shared__ f32x4 red[8 * NMB * 2 * kWave];
-  const int n0 = blockIdx.x * 32;
-  SkinnyProduct<Bf16, NMB, 2, U> w;
+  __shared__ f32x4 red[8 * NMB * NNB * kWave];
+  const int n0 = blockIdx.x * 16 * NNB;
+  SkinnyProduct<Bf16, NMB, NNB, U> w;
   w.begin();
   w.a_rows(a.A, 2 * a.I, a.T);
   w.b_rows(a.w2, 2 * a.I, [&](int i) { return n0 + i; });
   w.run(a.I / 64, red);
-  if (w.wave >= NMB * 2) return;
-  const int m = w.wave / 2 * 16 + w.lane % 16;
+  if (w.wave >= NMB * NNB) return;
+  const int m = w.wave / NNB * 16 + w.lane % 16;
   const f32x4 v[1] = {w.acc[0][0]};
-  store_blocks<1>(a.y + (size_t)m * a.d + n0 + w.wave % 2 * 16, v, w.lane, m < a.T, a.acc_y);
+  store_blocks<1>(a.y + (size_t)m * a.d + n0 + w.wave % NNB * 16, v, w.lane, m < a.T, a.acc_y);
 }
 
 long long ceil_div(long long n, int t) { return (n + t - 1) / t; }
@@ -491,19 +505,22 @@ hipError_t launch_whole(const char* name, const typename P::Args& a, hipStream_t
 }
 template <class P>
 hipError_t launch_pair(const char* name, const FfnArgs& rows, const FfnDwArgs& dw, hipStream_t s) {
-  // the rows' tiles in each shape, or in shares, with the weights' in each: the pair that is done first
+  // the rows' tiles in each shape, or in shares, with the weights' likewise: the pair that is done
+  // first
   Pair<P> p{rows, dw, 0, 0, 0};
-  const long long small = tiles_of<P, 128, 128>(rows);
-  const int shares = shares_of(small, P::steps(rows));
+  const long long nr = tiles_of<P, 128, 128>(rows), nw = tiles_of<Dw, 128, 128>(dw);
+  const int sr = shares_of(nr, P::steps(rows)), sw = shares_of(nw, Dw::steps(dw));
   float least = 0.f;
-  for (int i = 0; i < (shares > 1 ? 5 : 4); ++i) {
-    const bool split = i == kShares;
-    const long long n = split ? small * shares : shape_tiles<P>(rows, i);
-    const float step = split ? kShapes[kSmall].us / shares : kShapes[i].us;
-    for (int j = 0; j < 4; ++j) {
-      const float us = time_of(n, kTileUs + step * P::steps(rows), shape_tiles<Dw>(dw, j),
-                               kTileUs + kShapes[j].us * Dw::steps(dw)) +
-                       (split ? shares_us(shares, small) : 0.f);
+  for (int i = 0; i < (sr > 1 ? 5 : 4); ++i) {
+    const bool si = i == kShares;
+    const long long n1 = si ? nr * sr : shape_tiles<P>(rows, i);
+    const float t1 = (si ? kShapes[kSmall].us / sr : kShapes[i].us) * P::steps(rows);
+    for (int j = 0; j < (sw > 1 ? 5 : 4); ++j) {
+      const bool sj = j == kShares;
+      const long long n2 = sj ? nw * sw : shape_tiles<Dw>(dw, j);
+      const float t2 = (sj ? kShapes[kSmall].us / sw : kShapes[j].us) * Dw::steps(dw);
+      const float join = std::max(si ? shares_us(sr, nr) : 0.f, sj ? shares_us(sw, nw) : 0.f);
+      const float us = time_of(n1, kTileUs + t1, n2, kTileUs + t2) + join;
       if ((i == 0 && j == 0) || us < least) {
         least = us;
         p.rows_shape = i;
@@ -511,14 +528,20 @@ hipError_t launch_pair(const char* name, const FfnArgs& rows, const FfnDwArgs& d
       }
     }
   }
-  p.rows.shares = p.rows_shape == kShares ? shares : 1;
-  const long long first =
-      p.rows_shape == kShares ? small * shares : shape_tiles<P>(rows, p.rows_shape);
-  p.first = (int)grid8(first);
-  const hipError_t e = launch_kernel(name, ffn_pair_kernel<P>, p,
-                                     p.first + grid8(shape_tiles<Dw>(dw, p.dw_shape)), 512, s);
-  if (e != hipSuccess || p.rows.shares == 1) return e;
-  return launch_kernel(P::kName, ffn_join_kernel<P>, p.rows, small * 8, 256, s);
+  const bool split_rows = p.rows_shape == kShares, split_dw = p.dw_shape == kShares;
+  p.rows.shares = split_rows ? sr : 1;
+  p.dw.shares = split_dw ? sw : 1;
+  p.first = (int)grid8(split_rows ? nr * sr : shape_tiles<P>(rows, p.rows_shape));
+  const long long second = grid8(split_dw ? nw * sw : shape_tiles<Dw>(dw, p.dw_shape));
+  hipError_t e = launch_kernel(name, ffn_pair_kernel<P>, p, p.first + second, 512, s);
+  if (e != hipSuccess || (!split_rows && !split_dw)) return e;
+  const long long jr = split_rows ? 8 * nr : 0, jw = split_dw ? 8 * nw : 0;
+  {
+    TraceScope trace(name, s);
+    hipLaunchKernelGGL(ffn_join_pair_kernel<P>, dim3((unsigned)(jr + jw)), dim3(256), 0, s, p,
+                       (int)jr);
+  }
+  return hipGetLastError();
 }
 template <class P>
 hipError_t launch_product(FfnArgs a, hipStream_t s) {
@@ -541,10 +564,13 @@ hipError_t launch_ffn_gate_up(const FfnArgs& a, hipStream_t s) {
   return launch_kernel("ffn_gate_up", ffn_skinny_gate_up_kernel, a, a.I / 8, 512, s);
 }
 hipError_t launch_ffn_down(const FfnArgs& a, hipStream_t s) {
-  if (a.T > 64) return launch_product<Down>(a, s);
-  const auto kernel = a.T <= 16   ? ffn_skinny_down_kernel<1, 4>
-                      : a.T <= 32 ? ffn_skinny_down_kernel<2, 4>
-                                  : ffn_skinny_down_kernel<4, 2>;
+  const bool wide = a.d / 32 >= kCus / 2;  // its 32 columns a workgroup on half the CUs at least
+  if (a.T > 64 || (a.T > 16 && !wide)) return launch_product<Down>(a, s);
+  if (!wide)
+    return launch_kernel("ffn_down", ffn_skinny_down_kernel<1, 1, 4>, a, a.d / 16, 512, s);
+  const auto kernel = a.T <= 16   ? ffn_skinny_down_kernel<1, 2, 4>
+                      : a.T <= 32 ? ffn_skinny_down_kernel<2, 2, 4>
+                                  : ffn_skinny_down_kernel<4, 2, 2>;
   return launch_kernel("ffn_down", kernel, a, a.d / 32, 512, s);
 }
 hipError_t launch_ffn_dh_dw2(const FfnArgs& a, const FfnDwArgs& dw, hipStream_t s) {

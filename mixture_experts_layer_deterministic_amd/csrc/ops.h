@@ -99,7 +99,7 @@ struct FfnArgs {
   const uint16_t* dy;  // [T, d]
   uint16_t* dH;        // [T, 2I]
   uint16_t* dx;        // [T, d]
-  float* part;         // partial sums of products split along K, kFfnPartBytes
+  float* part;         // sums of products split along K, kFfnPartBytes
   int T, d, I, act, acc_y, acc_dx, shares;
 };
 constexpr size_t kFfnPartBytes = size_t(256) * 128 * 128 * 4;  // a 128 x 128 tile a CU
@@ -107,7 +107,8 @@ struct FfnDwArgs {
   const uint16_t* L;  // [T, Md]
   const uint16_t* R;  // [T, Nd]
   void* dw;           // [Md, Nd] fp32, or (bf16_dw) bf16
-  int T, Md, Nd, acc, bf16_dw;
+  float* part;        // as in FfnArgs
+  int T, Md, Nd, acc, bf16_dw, shares;
 };
 hipError_t launch_ffn_gate_up(const FfnArgs& a, hipStream_t s);
 hipError_t launch_ffn_down(const FfnArgs& a, hipStream_t s);

@@ -112,7 +112,7 @@ def _check_backward(c, v, H, A, dx, dw1, dw2, acc):
 SHAPES = [(1, 128, 128), (2, 256, 128), (5, 384, 256), (15, 128, 384), (16, 512, 128),
           (17, 256, 640), (33, 640, 128), (63, 256, 256), (64, 384, 384), (65, 128, 128),
           (100, 512, 256), (129, 384, 128), (200, 256, 896), (256, 256, 256), (257, 640, 384),
-          (333, 1024, 256), (513, 384, 512), (777, 256, 128)]
+          (333, 1024, 256), (513, 384, 512), (777, 256, 128), (3001, 128, 128), (2500, 384, 256)]
 
 
 @pytest.mark.parametrize("T,d,I", SHAPES, ids=str)
@@ -164,6 +164,62 @@ def test_large_shapes_by_norm(T, d, I):
     got = dict(zip(("dx", "dw1", "dw2"), _backward(c, v, H, A)), H=H, A=A, y=y)
     for k, w in want.items():
         assert (got[k].float() - w).norm() <= 2 * P64.BF16 * w.norm(), k
+
+
+ACT64 = {P64.SILU: torch.nn.functional.silu, P64.GELU: torch.nn.functional.gelu,
+         P64.GELU_TANH: lambda g: torch.nn.functional.gelu(g, approximate="tanh"),
+         P64.RELU: torch.nn.functional.relu}
+
+
+# sizes at which the products take their other tile shapes, whole rounds and the odd ends of both
+@pytest.mark.parametrize("T,d,I,act", [(4096, 256, 2048, 0), (2100, 4096, 2048, 1),
+                                       (4000, 4096, 256, 2), (1777, 1024, 1408, 3),
+                                       (1000, 2304, 1920, 0), (300, 4096, 4096, 2)], ids=str)
+def test_large_shapes_element_by_element(T, d, I, act):
+    """The bounds of _check_forward and _check_backward, in 64 bits on the GPU."""
+    _announce(f"[ffn] elements of {T} x {d} x {I} act {act}")
+    c = m.make_ffn(T, d, I, act)
+    v = _inputs(T, d, I, 11)
+    H, A, y = _forward(c, v, acc=True)
+    dx, dw1, dw2 = _backward(c, v, H, A, acc=True)
+    x, w1, w2, dy, y0, dx0, dw10, dw20 = (v[k].double() for k in (
+        "x", "w1", "w2", "dy", "y0", "dx0", "dw10", "dw20"))
+    mm = lambda a, b: a @ b.contiguous()
+    F32, HALF = P64.F32, P64.BF16
+
+    def near(got, want, err, bf16=True):
+        e = err + (HALF * (want.abs() + err) if bf16 else 0.0) + 1e-37
+        r = ((got.double() - want).abs() / e).max().item()
+        assert r <= 1.0, r
+
+    def gate(g, u):
+        g, u = g.clone().requires_grad_(True), u.clone().requires_grad_(True)
+        f = ACT64[act](g)
+        df, = torch.autograd.grad(f.sum(), g)
+        return f.detach(), df
+
+    h, eh = mm(x, w1.t()), F32 * d * mm(x.abs(), w1.abs().t())
+    near(H, h, eh)
+    (g, u), (eg, eu) = h.split(I, dim=1), eh.split(I, dim=1)
+    ea = 1.2 * eg * u.abs() + g.abs() * eu + 1.2 * eg * eu + F32 * (24 + 8 * g.abs()) * (g * u).abs()
+    near(A, gate(g, u)[0] * u, ea)
+    As = A.double()
+    yw, ey = mm(As, w2.t()) + y0, F32 * I * mm(As.abs(), w2.abs().t())
+    near(y, yw, ey + F32 * (yw.abs() + ey))
+    g, u = H.double().split(I, dim=1)
+    f, df = gate(g, u)
+    da, eda = mm(dy, w2), F32 * d * mm(dy.abs(), w2.abs())
+    ea = F32 * (24 + 8 * g.abs()) * g.abs().clamp(min=1.2)
+    dh = torch.cat([da * u * df, da * f], dim=1)
+    edh = torch.cat([u.abs() * (eda * (df.abs() + ea) + da.abs() * ea),
+                     eda * (f.abs() + ea) + da.abs() * ea], dim=1)
+    edh = edh + (HALF + 4 * F32) * (dh.abs() + edh)
+    top = dh.abs() + edh
+    for got, want, err in (
+            (dx, mm(dh, w1) + dx0, mm(edh, w1.abs()) + F32 * 2 * I * mm(top, w1.abs())),
+            (dw1, mm(dh.t(), x) + dw10, mm(edh.t(), x.abs()) + F32 * T * mm(top.t(), x.abs())),
+            (dw2, mm(dy.t(), As) + dw20, F32 * T * mm(dy.abs().t(), As.abs()))):
+        near(got, want, err + F32 * (want.abs() + err), got.dtype == BF16)
 
 
 def test_values_that_are_not_finite_stay_in_their_rows():
