@@ -137,6 +137,73 @@ def test_products(counts, first, tail, N, K, act):
     _check(_run(off, a, sa, b, sb, act), off, a, sa, b, sb, act)
 
 
+# whole rounds of 256 x 256 tiles, and a last one uncut, in halves and in quarters; an even and an odd
+# number of steps of K
+@pytest.mark.parametrize("N", [3584, 4352, 4480, 4608])
+@pytest.mark.parametrize("K", [256, 384, 1024])
+@pytest.mark.parametrize("act", [None, P64.SILU, P64.GELU])
+def test_many_rows_an_expert(N, K, act):
+    counts, first, tail = [2100, 0, 3000, 5], 3, 9
+    _announce(f"[i8] {counts} rows, {N} x {K} act {act}")
+    E, M = len(counts), first + sum(counts) + tail
+    N = N if act is None else N // 256 * 256
+    a, sa, b, sb = _case(M, E, N, K, N + K)
+    if act is not None:
+        sb[:, :N // 2] *= 3.0 / (74.0 * 74.0 * K ** 0.5)
+    off = _offsets(counts, first)
+    out = _run(off, a, sa, b, sb, act)
+    at = off.tolist()
+    assert (out[:first] == 77).all() and (out[at[-1]:] == 77).all()
+    for e in range(E):
+        lo, hi = at[e], at[e + 1]
+        # the sums are whole numbers below 2^53
+        v = a[lo:hi].double() @ b[e].double().t().contiguous()
+        v = v * sa[lo:hi, None].double() * sb[e].double()
+        err = 3 * P64.F32 * v.abs()
+        if act is not None:
+            (g, u), (eg, eu) = v.split(N // 2, dim=1), err.split(N // 2, dim=1)
+            F = torch.nn.functional
+            v = (F.silu(g) if act == P64.SILU else F.gelu(g)) * u
+            err = (1.2 * eg * u.abs() + g.abs() * eu + 1.2 * eg * eu
+                   + P64.F32 * (24 + 8 * g.abs()) * (g * u).abs())  # P64.gated_error
+        tol = P64.BF16 * (v.abs() + err) + err + 1e-37
+        assert ((out[lo:hi].double() - v).abs() <= tol).all()
+
+
+# a handful of experts and rows (every CU at the weights), and the two streaming tiles
+@pytest.mark.parametrize("counts,N", [([1], 1024), ([16], 8192), ([9, 5], 4096), ([31], 2048),
+                                      ([20, 33, 2], 1024), ([64], 8192), ([40], 128),
+                                      ([16] * 18, 4096), ([3, 0, 14] * 7, 4096),
+                                      ([100, 60, 128, 96] * 3, 1024)], ids=str)
+@pytest.mark.parametrize("K", [128, 2048, 3968, 7168])
+@pytest.mark.parametrize("act", [None, P64.GELU_TANH])
+def test_few_rows_an_expert(counts, N, K, act):
+    E, M = len(counts), sum(counts)
+    if E * N * K > 3e8:
+        K = 640
+    if act is not None:
+        N = max(N, 256)  # I = N / 2 is a multiple of 128 too
+    _announce(f"[i8] {counts} rows, {N} x {K} act {act}")
+    a, sa, b, sb = _case(M, E, N, K, N + K + E)
+    if act is not None:
+        sb[:, :N // 2] *= 3.0 / (74.0 * 74.0 * K ** 0.5)
+    off = _offsets(counts)
+    out = _run(off, a, sa, b, sb, act)
+    at = off.tolist()
+    for e in range(E):
+        lo, hi = at[e], at[e + 1]
+        v = a[lo:hi].double() @ b[e].double().t().contiguous()
+        v = v * sa[lo:hi, None].double() * sb[e].double()
+        err = 3 * P64.F32 * v.abs()
+        if act is not None:
+            (g, u), (eg, eu) = v.split(N // 2, dim=1), err.split(N // 2, dim=1)
+            v = torch.nn.functional.gelu(g, approximate="tanh") * u
+            err = (1.2 * eg * u.abs() + g.abs() * eu + 1.2 * eg * eu
+                   + P64.F32 * (24 + 8 * g.abs()) * (g * u).abs())  # P64.gated_error
+        tol = P64.BF16 * (v.abs() + err) + err + 1e-37
+        assert ((out[lo:hi].double() - v).abs() <= tol).all()
+
+
 def test_sums_reach_the_ends_of_32_bits():
     K = (1 << 17) - 128
     a = torch.full((3, K), -128, dtype=torch.int8, device=DEV)
