@@ -530,7 +530,8 @@ int moe_i8_quantize_rows(const void* src, int32_t rows, int32_t cols, void* code
  *   b_scales fp32 [E, N]       in
  *   out      bf16 [M, N]       out
  * Shapes: 0 <= M < 2^31 (0 enqueues nothing; a, a_scales and out may then be NULL),
- * 1 <= E <= 1024, N and K multiples of 128, K < 2^17, N * K < 2^31. Errors: MOE_ERR_INVALID_ARG.
+ * 1 <= E <= 1024, N and K multiples of 128, K < 2^17, N * K < 2^31, and (M / 128 + 2 E) * (N / 128)
+ * below 2^24. Errors: MOE_ERR_INVALID_ARG.
  */
 int moe_i8_gemm(const int32_t* offsets, int32_t M, int32_t E, int32_t N, int32_t K, const void* a,
                 const float* a_scales, const void* b, const float* b_scales, void* out,

@@ -282,7 +282,8 @@ int i8_gemm(const int32_t* offsets, int32_t M, int32_t E, int32_t N, int32_t K, 
     return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;  // empty buffers have no address to check
   if (!aligned16(a) || !aligned4(a_scales) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
-  if ((M / 16LL + E) * (N / 128) >= (1LL << 31)) return MOE_ERR_INVALID_ARG;  // the grid
+  // every kernel's grid has fewer than 2^32 threads
+  if ((M / 128LL + 2 * E) * (N / 128) >= (1LL << 24)) return MOE_ERR_INVALID_ARG;
   if (const int st = check_device()) return st;
   I8GemmArgs g{offsets, static_cast<const uint8_t*>(a), a_scales, static_cast<const uint8_t*>(b),
                b_scales, static_cast<uint16_t*>(out), M, E, N, K, act};

@@ -54,10 +54,10 @@ def test_products_refuse(gated):
     big = list(good)
     big[3], big[4] = 1 << 17, 1 << 14  # N K = 2^31
     assert fn(*big) == ARG
-    big = list(good)
-    big[1], big[3] = 2 ** 31 - 1, 1 << 21  # more tiles than a grid has
-    big[4] = 128
-    assert fn(*big) == ARG
+    for M, E in ((2 ** 31 - 1, 1), (2 ** 24, 1), (1, 1024)):  # more threads than a grid has
+        big = list(good)
+        big[1], big[2], big[3], big[4] = M, E, 1 << 20, 128
+        assert fn(*big) == ARG
     empty = list(good)
     empty[1] = 0
     empty[ptr] = empty[ptr + 1] = empty[ptr + 4] = None
