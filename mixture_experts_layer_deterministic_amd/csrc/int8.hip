@@ -65,8 +65,9 @@ MOE_DEV uint32_t amax_bits8(const uint4& x) {
   return max((uint32_t)m[0], (uint32_t)m[1]);
 }
 
-// W waves take a row, U pieces of eight values a lane, all in registers: one read. U = 0: rows too
-// long for that are read twice.
+// W waves take a row, U pieces of eight values a lane, all in registers: one read, past the caches.
+// U = 0: rows too long for that are read twice. HBM bounds it, two thirds of it reads: 16384 x 7168 in
+// 55 us, 6.4 TB/s, and 57344 x 2048 in 55.
 template <int W, int U>
 __global__ void __launch_bounds__(256) i8_quant_rows_kernel(const uint16_t* __restrict__ src,
                                                             long long rows, int cols,
@@ -231,10 +232,14 @@ MOE_DEV void i8_tile(const I8GemmArgs& a, const I8Place& t) {
 }
 
 // Many rows an expert: 256 x 256 tiles, whole rounds of one a CU and then what is left, cut in two
-// (256 x 128) or four (128 x 128) where the parts still fit one round. A workgroup stays for all its
-// tiles; where K has an even number of steps the next tile's first loads go out in the last steps of
-// the one before, so that they arrive under its epilogue.
-// FLOW: so; otherwise each tile starts anew.
+// (256 x 128) or four (128 x 128) where the parts still fit one round. FLOW, where K has an even number
+// of steps: a workgroup stays for all its tiles, and the next tile's first loads go out in the last
+// steps of the one before, so that they arrive under its epilogue; otherwise each tile is a workgroup's.
+//
+// 16384 rows over 5 of 8 experts, gated 4096 x 7168: 369 us, 2.6e15 operations a second; 7168 x 2048:
+// 230 us, 2.1e15 (a library product of one expert's 16384 rows, int32 results and no scales, takes 436
+// and 257 us; this kernel 359 and 206 there). What bounds a step stands in
+// products.h. With each tile a workgroup of its own the second took 238.
 template <bool GATED, bool FLOW>
 __global__ void __launch_bounds__(512, 2) i8_big_kernel(const I8GemmArgs a) {
   constexpr int kCols = GATED ? kBigT / 2 : kBigT;  // output columns
@@ -308,6 +313,8 @@ __global__ void __launch_bounds__(512, 2) i8_big_kernel(const I8GemmArgs a) {
   }
 }
 
+// Few rows an expert: HBM bounds it. 256 experts of 64 rows, gated 4096 x 7168, in 1.33 ms, 5.8 TB/s; 24
+// rows over 11 of 16 experts, 7168 x 2048, in 29 to 31 us, 5.2 to 5.6 TB/s.
 template <int NMB, int SB, bool GATED>
 MOE_DEV void i8_stream(const I8GemmArgs& a, const RowTile& t, int n0, const StreamStages<SB>& L) {
   StreamProduct<Int8, NMB, SB, GATED> w;
@@ -341,7 +348,8 @@ __global__ void __launch_bounds__(256, BM == 128 ? 2 : 4) i8_stream_kernel(const
 }
 
 // A handful of experts with a handful of rows: a workgroup for 16 NNB rows of an expert's weights
-// (gated: 8 NNB columns) and 16 NMB rows.
+// (gated: 8 NNB columns) and 16 NMB rows. One expert of 16 rows, gated 4096 x 7168: 11 us, 2.7 TB/s of
+// weights.
 template <int NMB, int NNB, int U, bool GATED>
 __global__ void __launch_bounds__(512, NMB * NNB == 1 ? 4 : 2) i8_skinny_kernel(
     const I8GemmArgs a) {
@@ -416,6 +424,22 @@ static void launch_skinny(const I8GemmArgs& a, bool gated, hipStream_t s) {
   else
     hipLaunchKernelGGL((i8_skinny_kernel<NMB, NNB, 4, false>), grid, dim3(512), 0, s, a);
 }
+
+// Which kernel, by the rows an expert has on average and the 128-row tiles of the weights there are
+// (M, E and N are all the host knows of the load; every kernel is right for every load, and every
+// kernel's results are the same). Measured in us a call, rows spread evenly, experts x rows, gated
+// with N x K = 4096 x 7168 where not said:
+//  * up to 64 tiles and few rows: every CU at the weights. 1 x 1 9 (128-row streaming 26), 1 x 16 11
+//    (26), 1 x 64 18.5 (31), 2 x 16 19 (27). 2 x 64 34 (32), and 128 tiles, 4 x 16, 42 (29).
+//  * 513 to 665 tiles with rows in them, up to 16 rows: 32-row streaming, whose second round is then
+//    not nearly empty as that of two 128-row tiles a CU: 17 x 8 85 (94), 20 x 16 93 (112); 22 x 8 121
+//    (113), 28 x 8 135 (125). The host counts the experts that have rows as if M rows were dealt at
+//    random.
+//  * up to 112 rows: 128-row streaming. 64 x 96 362 (256 x 256 tiles 401), 16 x 96 93 (103), 32 x 128
+//    198 (210); from 129 rows on an expert's weights are read twice, 32 x 144 342 (214), and of experts
+//    with 128 on average half have more. But 193 to 256 tiles (192 from 64 rows on) in quarters of
+//    256 x 256 tiles fill the card just once: 7 x 64 50 (61), 8 x 48 52 (58), 6 x 96 50 (69), 7168 x
+//    4096 not gated 4 x 64 34 (38); 6 x 64 48 (37), 9 x 64 79 (64).
 hipError_t launch_i8_gemm(const I8GemmArgs& a, bool gated, hipStream_t s) {
   auto grid = [&](int bm, int bn) {
     const unsigned n = (unsigned)(a.M / bm + a.E) * (unsigned)((a.N + bn - 1) / bn);
@@ -430,21 +454,22 @@ hipError_t launch_i8_gemm(const I8GemmArgs& a, bool gated, hipStream_t s) {
     return hipGetLastError();
   }
   const double busy = (double)tiles * -std::expm1(-(double)M / (double)E);
-  if (busy > 2 * kCus && busy <= 2.75 * kCus && M <= 16 * E) {
-    if (gated) hipLaunchKernelGGL((i8_stream_kernel<32, true>), grid(32, 128), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((i8_stream_kernel<32, false>), grid(32, 128), dim3(256), 0, s, a);
-    return hipGetLastError();
+  constexpr int kMost = 3 * kCus / 4;
+  const bool once = tiles >= kMost && tiles <= kCus && M > (tiles > kMost ? 32 : 64) * E;
+  if (busy > 2 * kCus && busy <= 2.6 * kCus && M <= 16 * E) {
+    const auto kernel = gated ? i8_stream_kernel<32, true> : i8_stream_kernel<32, false>;
+    hipLaunchKernelGGL(kernel, grid(32, 128), dim3(256), 0, s, a);
+  } else if (M <= 112 * E && !once) {
+    const auto kernel = gated ? i8_stream_kernel<128, true> : i8_stream_kernel<128, false>;
+    hipLaunchKernelGGL(kernel, grid(128, 128), dim3(256), 0, s, a);
+  } else {
+    const bool flow = a.K / 128 % 2 == 0;  // two stages
+    const auto kernel = gated ? (flow ? i8_big_kernel<true, true> : i8_big_kernel<true, false>)
+                              : (flow ? i8_big_kernel<false, true> : i8_big_kernel<false, false>);
+    // a workgroup a CU, or room for every tile and for a last round's parts
+    const dim3 g = flow ? dim3(kCus) : dim3(grid(kBigT, kBigT).x + kCus);
+    hipLaunchKernelGGL(kernel, g, dim3(512), 0, s, a);
   }
-  if (M <= 112 * E) {
-    if (gated) hipLaunchKernelGGL((i8_stream_kernel<128, true>), grid(128, 128), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((i8_stream_kernel<128, false>), grid(128, 128), dim3(256), 0, s, a);
-    return hipGetLastError();
-  }
-  const bool flow = a.K / 128 % 2 == 0;  // two stages
-  const auto kernel = gated ? (flow ? i8_big_kernel<true, true> : i8_big_kernel<true, false>)
-                            : (flow ? i8_big_kernel<false, true> : i8_big_kernel<false, false>);
-  // a workgroup a CU, or room for every tile and for a last round's parts
-  hipLaunchKernelGGL(kernel, flow ? dim3(kCus) : dim3(grid(kBigT, kBigT).x + kCus), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 

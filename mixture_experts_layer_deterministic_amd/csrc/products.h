@@ -16,8 +16,8 @@
 //     phase        4k        4k + 1    4k + 2    4k + 3    4k + 4
 //     waves 0..3   read k.0  mfma k.0  read k.1  mfma k.1  read (k+1).0
 //     waves 4..7   mfma ..   read k.0  mfma k.0  read k.1  mfma k.1
-// What a tile waits for is its loads (without the MFMAs, or without the LDS reads, the time is the
-// same; without the loads two thirds), so they go out as early as their place is free:
+// Loads go out as early as their place is free; half stages refilled one by one instead of whole stages
+// took the forward of 2048 x 7168 x 2048 from 223 us to 157:
 //  * With NS = 3 stages and more, step k - 1's stage is read for the last time in phase 2k - 1, and a
 //    wave fills it with step k + NS - 1 in its phase read k.
 //  * The 256 x 256 tiles have two stages, each in two parts. Part 0 is what read k.0 reads: all of the
@@ -32,6 +32,12 @@
 // takes two: K-contiguous, the first half of each wave's blocks and the second; K-major, the halves
 // of the step. The units are distinct arrays and the loop is unrolled over the stages, so that the
 // compiler sees which loads and reads meet, and does not wait for every load before each read.
+//
+// A step takes 1.35 us in 256 x 256 tiles, 0.95 in 256 x 128 and 0.67 in 128 x 128 with the card full
+// of them, each some 12.5 TB/s of loads. In the first the MFMAs are busy 86% of the time at 1.77 GHz,
+// which is what the card's power allows: four waves of 128 x 128, which read a third less from LDS,
+// took 1.34 us, panels that all lie in L2 1.32, and a step without its loads, at a higher clock, 0.9 to
+// 0.98. No change: K begun elsewhere in each tile, a later start of every second CU.
 #pragma once
 
 #include "dma.h"
