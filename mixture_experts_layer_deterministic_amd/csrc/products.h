@@ -725,8 +725,9 @@ MOE_DEV float2 act_grad(float g) {
     return make_float2(g * p, p + g * 0.3989422804f * __expf(-0.5f * g * g));
   } else if constexpr (ACT == kGeluTanh) {
     const float s = fast_sigmoid(2.f * kGeluC * (g + kGeluK * g * g * g));
+    const float t = fminf(g * g, 256.f);  // from there on s (1 - s) is 0, and 0 inf would be NaN
     return make_float2(g * s,
-                       s + g * s * (1.f - s) * (2.f * kGeluC) * (1.f + 3.f * kGeluK * g * g));
+                       s + g * s * (1.f - s) * (2.f * kGeluC) * (1.f + 3.f * kGeluK * t));
   } else {
     return g < 0.f ? make_float2(0.f, 0.f) : make_float2(g, g > 0.f ? 1.f : g);
   }

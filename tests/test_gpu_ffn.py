@@ -241,6 +241,24 @@ def test_values_that_are_not_finite_stay_in_their_rows():
     assert torch.equal(dx[keep], clean[0][keep])
 
 
+@pytest.mark.parametrize("act", P64.ACTS)
+@pytest.mark.parametrize("T", [3, 150])
+def test_gates_of_any_magnitude_have_a_derivative(T, act):
+    """act' is 0 or 1 to the last bit from |g| = 200 on, also where g * g is past fp32's range."""
+    d, I = 256, 256
+    c = m.make_ffn(T, d, I, act)
+    v = _inputs(T, d, I, 6)
+    v["w1"][I:] = 0  # dx from the gate's gradients alone
+    H, A, _ = _forward(c, v)
+    H[:, :I:2], H[:, 1:I:2], H[:, I:] = 200.0, -200.0, 0.5
+    dx, dw1, _ = _backward(c, v, H, A)
+    assert torch.isfinite(dx.float()).all() and (dx != 0).any()
+    for far in (1e5, 1e13, 1e20, 1e30):
+        H[:, :I:2], H[:, 1:I:2] = far, -far
+        dx2, dw12, _ = _backward(c, v, H, A)
+        assert torch.equal(dx, dx2) and torch.equal(dw1[:I], dw12[:I]), far
+
+
 def test_what_lies_behind_the_last_token_is_left():
     """Buffers longer than T rows: rows behind stay, and are not read (they hold NaN)."""
     T, d, I, more = 70, 256, 384, 40
