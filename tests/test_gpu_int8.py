@@ -204,6 +204,16 @@ def test_few_rows_an_expert(counts, N, K, act):
         assert ((out[lo:hi].double() - v).abs() <= tol).all()
 
 
+# quarters of 256 x 256 tiles that fill the card just once: 192, 224 and 256 tiles of 128 rows of weights
+@pytest.mark.parametrize("counts,N", [([70, 0, 120, 3, 200, 7], 4096), ([33] * 7, 4096),
+                                      ([0, 300, 1, 128], 7168), ([50, 40, 0, 60, 35, 45, 129, 1], 4096)],
+                         ids=str)
+@pytest.mark.parametrize("K", [128, 256, 1664])
+@pytest.mark.parametrize("act", [None, P64.GELU_TANH])
+def test_few_large_tiles(counts, N, K, act):
+    test_few_rows_an_expert(counts, N, K, act)
+
+
 def test_sums_reach_the_ends_of_32_bits():
     K = (1 << 17) - 128
     a = torch.full((3, K), -128, dtype=torch.int8, device=DEV)
