@@ -16,29 +16,39 @@ from . import (MOE_ACT_SILU, MOE_FLAG_BF16_DW, MOE_FLAG_MXFP8_WGRAD, MOE_FLAG_PE
 class SharedExpert:
     """Caller-owned buffers of the dense gated feed-forward block (``moe_ffn_forward``,
     ``moe_ffn_backward``): the expert every token passes beside its routed ones, or a block of its
-    own. ``train`` keeps H = [g | u] for the backward and owns the gradients dw1 and dw2."""
+    own. ``train`` keeps H = [g | u] for the backward and owns the gradients dw1 and dw2. A caller
+    with several batches on their way gives each its own ``saved``, from ``new_saved``."""
 
     def __init__(self, T, d, I, act=MOE_ACT_SILU, device="cuda", train=True, bf16_dw=False):
         self.cfg = make_ffn(T, d, I, act, MOE_FLAG_BF16_DW if bf16_dw else 0)
         dev, bf = torch.device(device), torch.bfloat16
         self.workspace = torch.empty(moe_ffn_query(self.cfg).workspace, dtype=torch.uint8,
                                      device=dev)
-        self.A = torch.empty(T, I, dtype=bf, device=dev)
-        self.H = torch.empty(T, 2 * I, dtype=bf, device=dev) if train else None
+        self.train = train
+        self.H, self.A = self.new_saved()
         dwt = bf if bf16_dw else torch.float32
         self.dw1 = torch.zeros(2 * I, d, dtype=dwt, device=dev) if train else None
         self.dw2 = torch.zeros(d, I, dtype=dwt, device=dev) if train else None
 
-    def forward(self, x, w1, w2, y, accumulate=False, stream=None):
-        """y = block(x), or with ``accumulate`` y + block(x)."""
-        moe_ffn_forward(self.cfg, x, w1, w2, self.H, self.A, y, accumulate, self.workspace, stream)
+    def new_saved(self):
+        """(H, A): what one batch's forward stores for its backward."""
+        T, I, bf, dev = self.cfg.T, self.cfg.I, torch.bfloat16, self.workspace.device
+        return (torch.empty(T, 2 * I, dtype=bf, device=dev) if self.train else None,
+                torch.empty(T, I, dtype=bf, device=dev))
 
-    def backward(self, x, w1, w2, dy, dx, accumulate_dx=False, accumulate=False, stream=None):
+    def forward(self, x, w1, w2, y, accumulate=False, stream=None, saved=None):
+        """y = block(x), or with ``accumulate`` y + block(x)."""
+        H, A = (self.H, self.A) if saved is None else saved
+        moe_ffn_forward(self.cfg, x, w1, w2, H, A, y, accumulate, self.workspace, stream)
+
+    def backward(self, x, w1, w2, dy, dx, accumulate_dx=False, accumulate=False, stream=None,
+                 saved=None):
         """dx (added to with ``accumulate_dx``), dw1 and dw2 (added to with ``accumulate``)."""
-        if self.H is None:
+        H, A = (self.H, self.A) if saved is None else saved
+        if H is None:
             raise ValueError("a block made without train keeps nothing for a backward")
-        moe_ffn_backward(self.cfg, x, w1, w2, self.H, self.A, dy, dx, self.dw1, self.dw2,
-                         accumulate_dx, accumulate, self.workspace, stream)
+        moe_ffn_backward(self.cfg, x, w1, w2, H, A, dy, dx, self.dw1, self.dw2, accumulate_dx,
+                         accumulate, self.workspace, stream)
 
 
 class MoeLayer:
@@ -54,7 +64,8 @@ class MoeLayer:
 
     With ``shared`` (a ``SharedExpert`` of the same T and d) the forward adds the shared expert's
     output to y and the backward its gradient to dx; both then need the tokens ``x`` and its weights
-    ``shared_w`` = (w1, w2).
+    ``shared_w`` = (w1, w2), and a batch with a ``saved`` of its own also a ``shared_saved``
+    (``SharedExpert.new_saved``).
 
     With ``gate`` (from ``make_gate``) the layer routes by that gate instead of the renormalised
     top-k softmax, with ``gate_bias`` (fp32 [E], or None) in its choice, and backward takes the
@@ -162,44 +173,48 @@ class MoeLayer:
     def quantize_weights(self, w1, w2, stream=None):
         moe_quantize_weights(self.cfg, w1, w2, self.wq, stream)
 
-    def _shared_operands(self, x, shared_w):
+    def _shared_operands(self, x, shared_w, saved, shared_saved):
         if x is None or shared_w is None:
             raise ValueError("a layer with a shared expert needs x and shared_w")
+        if (saved is None) != (shared_saved is None):
+            raise ValueError("a batch's saved and shared_saved are given together")
         return x, *shared_w
 
-    def forward(self, w1, w2, slot=0, saved=None, stream=None, x=None, shared_w=None):
+    def forward(self, w1, w2, slot=0, saved=None, stream=None, x=None, shared_w=None,
+                shared_saved=None):
         if self.shared is not None:
-            ops = self._shared_operands(x, shared_w)
+            ops = self._shared_operands(x, shared_w, saved, shared_saved)
         moe_forward(self.cfg, self.ring, slot, self.offsets, self.tk_row, self.topk_w, w1, w2,
                     self.wq, self.y, self.saved if saved is None else saved, self.workspace,
                     stream)
         if self.shared is not None:
-            self.shared.forward(*ops, self.y, True, stream)
+            self.shared.forward(*ops, self.y, True, stream, shared_saved)
 
-    def forward_fused(self, x, w_router, w1, w2, slot=0, saved=None, stream=None, shared_w=None):
+    def forward_fused(self, x, w_router, w1, w2, slot=0, saved=None, stream=None, shared_w=None,
+                      shared_saved=None):
         """route + permute + forward in one kernel launch (moe_forward_fused), which has no gate."""
         if self.gate is not None:
             raise ValueError("the single-launch forward routes by the top-k softmax only")
         if self.shared is not None:
-            ops = self._shared_operands(x, shared_w)
+            ops = self._shared_operands(x, shared_w, saved, shared_saved)
         self.given = False
         moe_forward_fused(self.cfg, x, w_router, self.logits, self.topk_idx, self.topk_w,
                           self.ring, slot, self.counts, self.offsets, self.row_src, self.tk_row,
                           w1, w2, self.y, self.saved if saved is None else saved, self.workspace,
                           stream)
         if self.shared is not None:
-            self.shared.forward(*ops, self.y, True, stream)
+            self.shared.forward(*ops, self.y, True, stream, shared_saved)
 
     def backward(self, w_router, w1, w2, dy, slot=0, accumulate=False, saved=None, stream=None,
-                 x=None, shared_w=None):
+                 x=None, shared_w=None, shared_saved=None):
         """With a gate and a ``w_router``, ``x`` (the tokens) is needed too: the experts' backward
         runs as for a given routing, then the gate's and the router's add theirs to dx and dwr.
         With a shared expert its backward comes last and adds to dx."""
         if self.infer:
             raise ValueError("the INT8 mode has no backward")
         if self.shared is not None:
-            ops = self._shared_operands(x, shared_w)
-            if self.shared.H is None:
+            ops = self._shared_operands(x, shared_w, saved, shared_saved)
+            if (self.shared.H if shared_saved is None else shared_saved[0]) is None:
                 raise ValueError("the shared expert was made without train")
             # refused before the experts' gradients are written or added to
             T, d, I, bf = self.T, self.d, self.shared.cfg.I, torch.bfloat16
@@ -226,7 +241,7 @@ class MoeLayer:
             moe_router_backward(self.cfg, x, w_router, self.dlogits, self.dx, self.dwr, True,
                                 accumulate, stream)
         if self.shared is not None:
-            self.shared.backward(*ops, dy, self.dx, True, accumulate, stream)
+            self.shared.backward(*ops, dy, self.dx, True, accumulate, stream, shared_saved)
 
     def step(self, x, w_router, w1, w2, dy, slot=0, stream=None, fused=False, shared_w=None):
         """One fwd+bwd pass: route (when w_router is given), permute, forward, backward. With

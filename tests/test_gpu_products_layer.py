@@ -157,6 +157,43 @@ def test_training_step_with_a_shared_expert(shape, mode):
         assert torch.equal(a, b)
 
 
+def test_two_batches_on_their_way_with_a_shared_expert():
+    """Two forwards, then their backwards in reverse, each with its own saved: what each batch gives
+    alone, and the sums of both batches' weight gradients."""
+    inp, s = _inputs("tiny"), SHAPES["tiny"]
+    T, d, I = s["T"], s["d"], 384
+    block = lambda: SharedExpert(T, d, I, device=DEV)
+    sw = _shared_weights(d, I, 5)
+    X = [inp["X"], inp["X"].flip(0).contiguous()]
+    dY = [inp["dY"], inp["dY"].flip(1).contiguous()]
+    one = [_layer("tiny", shared=block()) for _ in X]
+    for L, x, dy in zip(one, X, dY):
+        L.step(x, inp["Wr"], inp["W1"], inp["W2"], dy, shared_w=sw)
+    both = _layer("tiny", shared=block(), ring_slots=2)
+    saved = [(torch.empty_like(both.saved), both.shared.new_saved()) for _ in X]
+    for i, x in enumerate(X):
+        both.route(x, inp["Wr"])
+        both.permute(x, i)
+        both.forward(inp["W1"], inp["W2"], i, saved[i][0], x=x, shared_w=sw,
+                     shared_saved=saved[i][1])
+        assert torch.equal(both.y, one[i].y)
+    for i in (1, 0):
+        both.route(X[i], inp["Wr"])
+        both.permute(X[i], i)
+        both.backward(inp["Wr"], inp["W1"], inp["W2"], dY[i], i, i == 0, saved[i][0], x=X[i],
+                      shared_w=sw, shared_saved=saved[i][1])
+        assert torch.equal(both.dx, one[i].dx)
+        if i == 1:
+            for k in ("dw1", "dw2"):
+                assert torch.equal(getattr(both.shared, k), getattr(one[1].shared, k))
+    # the same T products in fp32 on both sides, off by T half steps of their magnitudes at most on
+    # each, and one addition
+    A, dy = saved[0][1][1], _np(dY[0])
+    mag = np.abs(dy).T @ np.abs(_np(A)) + np.abs(_np(one[1].shared.dw2))
+    want = _np(one[0].shared.dw2) + _np(one[1].shared.dw2)
+    assert (np.abs(_np(both.shared.dw2) - want) <= 2 * (T + 1) * P64.F32 * mag).all()
+
+
 def test_int8_layer_with_a_shared_expert_captured_and_replayed():
     """A serving step in one graph: route, permute, int8 experts and the shared expert, replayed with
     other tokens between eager calls."""

@@ -219,3 +219,36 @@ def test_layer_refusals(monkeypatch):
     sh.H = x
     L.backward(None, x, x, x, x=x, shared_w=(x, x))
     assert calls[2:] == ["checks", "moe_backward", "moe_ffn_backward"]
+
+
+def test_a_shared_expert_keeps_a_batch_of_its_own_saved(monkeypatch):
+    """Batches with a saved of their own: the shared expert's H and A go with it, or it is refused."""
+    from mixture_experts_layer_deterministic_amd import layer
+    seen = []
+    for name in ("moe_forward", "moe_forward_fused", "moe_backward", "_dev"):
+        monkeypatch.setattr(layer, name, lambda *a, n=name: seen.append(n))
+    monkeypatch.setattr(layer, "moe_ffn_forward", lambda c, x, w1, w2, H, A, *a: seen.append((H, A)))
+    monkeypatch.setattr(layer, "moe_ffn_backward", lambda c, x, w1, w2, H, A, *a: seen.append((H, A)))
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    sh = layer.SharedExpert(4, 256, 128, device="cpu")
+    L = layer.MoeLayer(4, 256, 8, 2, 128, device="cpu", shared=sh)
+    w, saved, own = (x, x), torch.empty_like(L.saved), sh.new_saved()
+    assert own[0].shape == sh.H.shape and own[1].shape == sh.A.shape and own[0] is not sh.H
+    calls = (lambda **k: L.forward(x, x, x=x, shared_w=w, **k),
+             lambda **k: L.forward_fused(x, x, x, x, shared_w=w, **k),
+             lambda **k: L.backward(None, x, x, x, x=x, shared_w=w, **k))
+    for call in calls:
+        for half in (dict(saved=saved), dict(shared_saved=own)):
+            with pytest.raises(ValueError, match="given together"):
+                call(**half)
+    assert not seen
+    for call in calls:
+        call()
+        assert seen[-1][0] is sh.H and seen[-1][1] is sh.A
+        call(saved=saved, shared_saved=own)
+        assert seen[-1][0] is own[0] and seen[-1][1] is own[1]
+    bare = layer.SharedExpert(4, 256, 128, device="cpu", train=False)
+    assert bare.new_saved()[0] is None
+    L = layer.MoeLayer(4, 256, 8, 2, 128, device="cpu", shared=bare)
+    with pytest.raises(ValueError, match="without train"):
+        L.backward(None, x, x, x, x=x, shared_w=w, saved=saved, shared_saved=bare.new_saved())
