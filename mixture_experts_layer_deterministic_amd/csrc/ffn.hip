@@ -368,19 +368,20 @@ __global__ void __launch_bounds__(256) ffn_join_pair_kernel(const Pair<P> p, int
   else join_rows<Dw>(p.dw, b - rows);
 }
 
-// A handful of tokens: up to 16, a workgroup for 8 columns of A. 16 x 7168 x 2048 in 20 us, 3.0 TB/s
-// of weights.
-__global__ void __launch_bounds__(512, 4) ffn_skinny_gate_up_kernel(const FfnArgs a) {
-  __shared__ f32x4 red[8 * kWave];
+// A handful of tokens, up to 16 NMB: a workgroup for 8 columns of A. Its 34 MB of weights
+// for 8 x 4096 x 2048, and y's 17, take 15.5 us.
+template <int NMB, int U>
+__global__ void __launch_bounds__(512, NMB == 1 ? 4 : 2) ffn_skinny_gate_up_kernel(const FfnArgs a) {
+  __shared__ f32x4 red[8 * NMB * kWave];
   const int n0 = blockIdx.x * 8, I = a.I;
-  SkinnyProduct<Bf16, 1, 1, 4> w;
+  SkinnyProduct<Bf16, NMB, 1, U> w;
   w.begin();
   w.a_rows(a.x, 2 * a.d, a.T);
   w.b_rows(a.w1, 2 * a.d, [&](int i) { return n0 + (i < 8 ? i : I + i - 8); });
   w.run(a.d / 64, red);
-  if (w.wave > 0) return;
+  if (w.wave >= NMB) return;
   // lanes 0..31 hold four gate columns of a row, lanes 32..63 the matching ups
-  const int m = w.lane % 16, c = n0 + 4 * (w.lane / 16 % 2);
+  const int m = w.wave * 16 + w.lane % 16, c = n0 + 4 * (w.lane / 16 % 2);
   const f32x4 v = w.acc[0][0];
   f32x4 u;
 #pragma unroll
@@ -562,24 +563,41 @@ hipError_t launch_product(FfnArgs a, hipStream_t s) {
 
 }  // namespace
 
-// Up to 16 tokens (64 for y where it has 4096 columns and more) each weight is read once by a
-// workgroup of its own: [g | u] of 16 x 7168 x 2048 20 us (split along K 19 in two kernels, in whole
-// tiles 53), its y 9.5 (16, 18), y of 64 tokens 15.8 (17, 20). [g | u] of 64 would take 37 (22).
-// y of fewer columns would leave half the CUs idle: the forward of 64 x 1024 x 4096 in 26 us, so 37, of
-// 64 x 2048 x 8192 36 (74), of 64 x 2048 x 1024 25 (23).
-hipError_t launch_ffn_gate_up(const FfnArgs& a, hipStream_t s) {
-  if (a.T > 16) return launch_product<GateUp>(a, s);
-  return launch_kernel("ffn_gate_up", ffn_skinny_gate_up_kernel, a, a.I / 8, 512, s);
+// Few tokens: each weight read once by a workgroup that has nothing else to wait for. It also reads
+// the tokens, which come from L2 at the rate that the weights do, so this pays up to some 320 KB of
+// both a CU; more is split along K. Both kernels of the forward in us, with [g | u] so (split):
+// 2048 x 2048, 1 token 12 (16), 16 13 (17), 32, 192 KB, 19 (24), 64, 320 KB, 26 (28); 2048 x 4096, 24
+// tokens, 320 KB, 24.6 (25.7), 32 26 (25); 7168 x 2048, 16 tokens, 448 KB, 28.6 (26.5); 4096 x 8192,
+// 1 MB, 69 (56). Up to 4 tokens their part is small and large weights go faster so: 1 x 8192 x 16384
+// 150 (178), but 4096 x 8192 51 (48).
+// y so (split): 4096 x 2048, 16 tokens, 128 KB, 18 (22); 2048 x 4096, 16 tokens, 256 KB, 21 (21.5);
+// 4096 x 8192, 512 KB, 59 (57); 64 tokens, 32 columns a workgroup, 1.5 MB, 84 (49).
+constexpr long long kFewBytes = 320 << 10;
+long long bytes_a_cu(const FfnArgs& a, int cols, long long groups, int K) {
+  return 2LL * (cols + a.T) * K * ceil_div(groups, kCus);
 }
+hipError_t launch_ffn_gate_up(const FfnArgs& a, hipStream_t s) {
+  if (a.T > 64 || (a.T > 4 && bytes_a_cu(a, 16, a.I / 8, a.d) > kFewBytes))
+    return launch_product<GateUp>(a, s);
+  const auto kernel = a.T <= 16   ? ffn_skinny_gate_up_kernel<1, 4>
+                      : a.T <= 32 ? ffn_skinny_gate_up_kernel<2, 4>
+                                  : ffn_skinny_gate_up_kernel<4, 2>;
+  return launch_kernel("ffn_gate_up", kernel, a, a.I / 8, 512, s);
+}
+// 32 columns a workgroup where that leaves 192 of them, for half the reads of A: 7168 x 2048 28.6 us
+// against 29.6; 4096 columns, 128 workgroups, 20.6 against 17.8.
 hipError_t launch_ffn_down(const FfnArgs& a, hipStream_t s) {
-  const bool wide = a.d / 32 >= kCus / 2;  // its 32 columns a workgroup on half the CUs at least
-  if (a.T > 64 || (a.T > 16 && !wide)) return launch_product<Down>(a, s);
-  if (!wide)
-    return launch_kernel("ffn_down", ffn_skinny_down_kernel<1, 1, 4>, a, a.d / 16, 512, s);
-  const auto kernel = a.T <= 16   ? ffn_skinny_down_kernel<1, 2, 4>
-                      : a.T <= 32 ? ffn_skinny_down_kernel<2, 2, 4>
-                                  : ffn_skinny_down_kernel<4, 2, 2>;
-  return launch_kernel("ffn_down", kernel, a, a.d / 32, 512, s);
+  const bool wide = a.d / 32 >= kCus * 3 / 4;
+  const int cols = wide ? 32 : 16;
+  if (a.T > 64 || bytes_a_cu(a, cols, a.d / cols, a.I) > kFewBytes)
+    return launch_product<Down>(a, s);
+  const auto narrow = a.T <= 16   ? ffn_skinny_down_kernel<1, 1, 4>
+                      : a.T <= 32 ? ffn_skinny_down_kernel<2, 1, 4>
+                                  : ffn_skinny_down_kernel<4, 1, 2>;
+  const auto broad = a.T <= 16   ? ffn_skinny_down_kernel<1, 2, 4>
+                     : a.T <= 32 ? ffn_skinny_down_kernel<2, 2, 4>
+                                 : ffn_skinny_down_kernel<4, 2, 2>;
+  return launch_kernel("ffn_down", wide ? broad : narrow, a, a.d / cols, 512, s);
 }
 hipError_t launch_ffn_dh_dw2(const FfnArgs& a, const FfnDwArgs& dw, hipStream_t s) {
   return launch_pair<Dh>("ffn_dh_dw2", a, dw, s);

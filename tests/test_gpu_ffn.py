@@ -130,6 +130,14 @@ def test_forward(T, d, I, act):
     _check_forward(c, v, H, A3, y3, True)
 
 
+# few tokens: 16 and 32 columns of y a workgroup, 16 to 64 tokens, and either product too long for it
+@pytest.mark.parametrize("T", [1, 4, 5, 16, 17, 31, 32, 33, 50, 64])
+@pytest.mark.parametrize("d,I", [(6144, 128), (6272, 384), (1024, 1920), (128, 4096), (128, 8320),
+                                 (2048, 4224)])
+def test_few_tokens(T, d, I):
+    test_forward(T, d, I, P64.ACTS[(T + I) % len(P64.ACTS)])
+
+
 @pytest.mark.parametrize("T,d,I", SHAPES, ids=str)
 @pytest.mark.parametrize("act,bf16_dw,acc", [(0, 0, False), (1, 4, True), (2, 0, True),
                                              (3, 4, False)])
