@@ -464,9 +464,11 @@ float time_of(long long n1, float t1, long long n2, float t2) {
 
 // What else a tile costs: its start, its first loads and its epilogue.
 constexpr float kTileUs = 4.f;
-// What shares of K cost beyond their steps: the second kernel, up to 9 us for a card full of sums.
+// What shares of K cost beyond their steps: the second kernel, and up to 10 us for a card full of sums
+// to be written and read (17 MB). With 5 us for those 384 x 2048 x 1408 took 39 us forward, 31 as it is;
+// 256 x 4096 x 1408 36.5 and 31, backward 52 and 46; 512 x 4096 x 4096 backward 124 and 113.
 float shares_us(long long shares, long long tiles) {
-  return shares > 1 ? 4.f + 5.f * (float)(shares * tiles) / kCus : 0.f;
+  return shares > 1 ? 4.f + 10.f * (float)(shares * tiles) / kCus : 0.f;
 }
 // Shares of K for few 128 x 128 tiles, of four steps at least: where the steps that are left and the
 // second kernel cost the least, a step of a card that is not full 0.6 us. Unsplit and split, both
