@@ -265,10 +265,11 @@ _PLAIN = {"i8_rows": _i8_rows_plain, "i8_gemm": _i8_gemm_plain, "i8_gated": _i8_
 # The framework's calls
 
 
-@functools.lru_cache(maxsize=None)
-def _ffn(T, d, I, act):
-    """The block's shape and its workspace, which a program keeps as long as it keeps the shape.
-    Weight gradients are bf16, as dx is."""
+@functools.lru_cache(maxsize=16)
+def _ffn(T, d, I, act, device, stream):
+    """The block's shape and its workspace, which a program keeps as long as it keeps the shape, one
+    for each device and stream: calls that share a workspace follow each other. Weight gradients
+    are bf16, as dx is."""
     import mixture_experts_layer_deterministic_amd as m
     cfg = m.make_ffn(T, d, I, act, m.MOE_FLAG_BF16_DW)
     return cfg, torch.empty(m.moe_ffn_query(cfg).workspace, dtype=torch.uint8, device="cuda")
@@ -291,7 +292,8 @@ def _run_own(s):
                             s["sa"], s["b"], s["sb"], s["out"])
         return {"out": s["out"]}
     T, d, I = s["T"], s["d"], s["I"]
-    cfg, ws = _ffn(T, d, I, s["act"])
+    cfg, ws = _ffn(T, d, I, s["act"], torch.cuda.current_device(),
+                   torch.cuda.current_stream().cuda_stream)
     bf = dict(dtype=torch.bfloat16, device="cuda")
     if op == "ffn":
         y = s["y0"].clone() if s["acc"] else torch.empty(T, d, **bf)
