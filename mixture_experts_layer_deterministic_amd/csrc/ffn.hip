@@ -8,9 +8,8 @@
 //
 // Sums are fp32 in a fixed order. A is formed from the fp32 g and u, dH from the bf16 H that the
 // forward stored, and both are rounded once, as the next product reads them.
-#include <algorithm>
-
 #include "common.h"
+#include "ffn_plan.h"
 #include "kernels.h"
 #include "ops.h"
 #include "products.h"
@@ -274,7 +273,12 @@ __global__ void __launch_bounds__(512, 2) ffn_split_kernel(const typename P::Arg
 // A gradient of rows and one of weights that do not wait for each other, in one launch: the
 // rows' tiles (or shares) first, `first` workgroups, then the weights'. One's last round runs beside
 // the other's first: 333 x 4096 x 1024 73 -> 66 us.
-enum Shape { kBig, kTall, kWide, kSmall, kShares };
+using ffn::Shape;
+using ffn::kBig;
+using ffn::kTall;
+using ffn::kWide;
+using ffn::kSmall;
+using ffn::kShares;
 template <class P>
 struct Pair {
   typename P::Args rows;
@@ -414,78 +418,10 @@ __global__ void __launch_bounds__(512, 2) ffn_skinny_down_kernel(const FfnArgs a
   store_blocks<1>(a.y + (size_t)m * a.d + n0 + w.wave % NNB * 16, v, w.lane, m < a.T, a.acc_y);
 }
 
-long long ceil_div(long long n, int t) { return (n + t - 1) / t; }
-
-// Tile shapes, and what a step takes when the card is full of them, in us (bytes a step 64, 48 and
-// 32 KB). Measured, the whole call in us, 256 x 256 / 256 x 128 / 128 x 128: [g | u] of 2048 x 7168 x
-// 2048 141 / 107 / 142 (128, 256, 512 tiles), its y 51 / 64 / 88 (224, 448, 896), dH 155 / 107 / 80 (64,
-// 128, 256); [g | u] of 1777 x 4096 x 1408 80 / 53 / 72 (77, 154, 308).
-constexpr struct {
-  int bm, bn;
-  float us;
-} kShapes[4] = {{256, 256, 1.35f}, {256, 128, 0.95f}, {128, 256, 0.95f}, {128, 128, 0.67f}};
+static_assert(ffn::kPlanCus == kCus, "one card");
 template <class P>
-long long shape_tiles(const typename P::Args& a, int shape) {
-  return ceil_div(P::m(a), kShapes[shape].bm) * ceil_div(P::n(a), kShapes[shape].bn);
-}
-// The shape of the fewest rounds of one tile a CU, each at its step's time.
-template <class P>
-Shape tile_shape(const typename P::Args& a) {
-  int best = 0;
-  float least = 0.f;
-  long long fewest = 0;
-  for (int i = 0; i < 4; ++i) {
-    const long long tiles = shape_tiles<P>(a, i);
-    const float us = (float)ceil_div(tiles, kCus) * kShapes[i].us;
-    if (i == 0 || us < least || (us == least && tiles < fewest)) {
-      best = i;
-      least = us;
-      fewest = tiles;
-    }
-  }
-  return (Shape)best;
-}
-// When the last of n1 tiles of t1 us and then n2 of t2 is done, each taken by the CU that is free
-// first.
-float time_of(long long n1, float t1, long long n2, float t2) {
-  // whole rounds of the first, and its last round on some of the CUs
-  const long long r = n1 / kCus, some = n1 % kCus;
-  float at[2] = {r * t1, (r + (some ? 1 : 0)) * t1};  // when the others and those are free
-  const long long n[2] = {kCus - some, some};
-  float done = n1 ? at[some ? 1 : 0] : 0.f;
-  while (n2 > 0) {
-    const int g = n[1] && at[1] < at[0] ? 1 : 0;
-    at[g] += t2;
-    done = std::max(done, at[g]);
-    n2 -= n[g];
-  }
-  return done;
-}
-
-// What else a tile costs: its start, its first loads and its epilogue.
-constexpr float kTileUs = 4.f;
-// What shares of K cost beyond their steps: the second kernel, and up to 10 us for a card full of sums
-// to be written and read (17 MB). With 5 us for those 384 x 2048 x 1408 took 39 us forward, 31 as it is;
-// 256 x 4096 x 1408 36.5 and 31, backward 52 and 46; 512 x 4096 x 4096 backward 124 and 113.
-float shares_us(long long shares, long long tiles) {
-  return shares > 1 ? 4.f + 10.f * (float)(shares * tiles) / kCus : 0.f;
-}
-// Shares of K for few 128 x 128 tiles, of four steps at least: where the steps that are left and the
-// second kernel cost the least, a step of a card that is not full 0.6 us. Unsplit and split, both
-// kernels, in us: [g | u] of 128 x 7168 x 2048 73 and 24 (8 shares), of 512 tokens 74 and 49 (2); its
-// dH 60 and 19 (16), 61 and 30 (4); y of 333 x 4096 x 1024, 96 tiles of 16 steps, 12 and 18.
-int shares_of(long long tiles, int steps) {
-  const int most = (int)std::min((long long)kCus / std::max(tiles, 1LL), (long long)steps / 4);
-  int best = 1;
-  float least = 0.6f * steps;
-  for (int n = 2; n <= most; ++n) {
-    const float us = 0.6f * steps / n + shares_us(n, tiles);
-    if (us < least) {
-      least = us;
-      best = n;
-    }
-  }
-  return best;
+ffn::Size size_of(const typename P::Args& a) {
+  return {P::m(a), P::n(a), P::steps(a)};
 }
 
 template <class K, class A>
@@ -500,8 +436,8 @@ hipError_t launch_kernel(const char* name, K kernel, const A& a, long long grid,
 long long grid8(long long tiles) { return (tiles + kXcds - 1) / kXcds * kXcds; }
 
 template <class P>
-hipError_t launch_whole(const char* name, const typename P::Args& a, hipStream_t s) {
-  switch (tile_shape<P>(a)) {
+hipError_t launch_whole(Shape shape, const char* name, const typename P::Args& a, hipStream_t s) {
+  switch (shape) {
     case kBig:
       return launch_kernel(name, ffn_kernel<P, 256, 256>, a, grid8(tiles_of<P, 256, 256>(a)), 512, s);
     case kTall:
@@ -514,35 +450,16 @@ hipError_t launch_whole(const char* name, const typename P::Args& a, hipStream_t
 }
 template <class P>
 hipError_t launch_pair(const char* name, const FfnArgs& rows, const FfnDwArgs& dw, hipStream_t s) {
-  // the rows' tiles in each shape, or in shares, with the weights' likewise: the pair that is done
-  // first
-  Pair<P> p{rows, dw, 0, 0, 0};
-  const long long nr = tiles_of<P, 128, 128>(rows), nw = tiles_of<Dw, 128, 128>(dw);
-  const int sr = shares_of(nr, P::steps(rows)), sw = shares_of(nw, Dw::steps(dw));
-  float least = 0.f;
-  for (int i = 0; i < (sr > 1 ? 5 : 4); ++i) {
-    const bool si = i == kShares;
-    const long long n1 = si ? nr * sr : shape_tiles<P>(rows, i);
-    const float t1 = (si ? kShapes[kSmall].us / sr : kShapes[i].us) * P::steps(rows);
-    for (int j = 0; j < (sw > 1 ? 5 : 4); ++j) {
-      const bool sj = j == kShares;
-      const long long n2 = sj ? nw * sw : shape_tiles<Dw>(dw, j);
-      const float t2 = (sj ? kShapes[kSmall].us / sw : kShapes[j].us) * Dw::steps(dw);
-      const float join = std::max(si ? shares_us(sr, nr) : 0.f, sj ? shares_us(sw, nw) : 0.f);
-      const float us = time_of(n1, kTileUs + t1, n2, kTileUs + t2) + join;
-      if ((i == 0 && j == 0) || us < least) {
-        least = us;
-        p.rows_shape = i;
-        p.dw_shape = j;
-      }
-    }
-  }
-  const bool split_rows = p.rows_shape == kShares, split_dw = p.dw_shape == kShares;
-  p.rows.shares = split_rows ? sr : 1;
-  p.dw.shares = split_dw ? sw : 1;
-  p.first = (int)grid8(split_rows ? nr * sr : shape_tiles<P>(rows, p.rows_shape));
-  const long long second = grid8(split_dw ? nw * sw : shape_tiles<Dw>(dw, p.dw_shape));
-  hipError_t e = launch_kernel(name, ffn_pair_kernel<P>, p, p.first + second, 512, s);
+  const ffn::Size szr = size_of<P>(rows), szw = size_of<Dw>(dw);
+  const ffn::PairPlan plan = ffn::plan_of_pair(szr, szw);
+  Pair<P> p{rows, dw, plan.rows.shape, plan.dw.shape, 0};
+  p.rows.shares = plan.rows.shares;
+  p.dw.shares = plan.dw.shares;
+  const bool split_rows = plan.rows.shape == kShares, split_dw = plan.dw.shape == kShares;
+  const long long nr = ffn::shape_tiles(szr, split_rows ? kSmall : plan.rows.shape);
+  const long long nw = ffn::shape_tiles(szw, split_dw ? kSmall : plan.dw.shape);
+  p.first = (int)grid8(nr * p.rows.shares);
+  hipError_t e = launch_kernel(name, ffn_pair_kernel<P>, p, p.first + grid8(nw * p.dw.shares), 512, s);
   if (e != hipSuccess || (!split_rows && !split_dw)) return e;
   const long long jr = split_rows ? 8 * nr : 0, jw = split_dw ? 8 * nw : 0;
   {
@@ -554,9 +471,10 @@ hipError_t launch_pair(const char* name, const FfnArgs& rows, const FfnDwArgs& d
 }
 template <class P>
 hipError_t launch_product(FfnArgs a, hipStream_t s) {
+  const ffn::Plan plan = ffn::plan_of(size_of<P>(a));
+  a.shares = plan.shares;
+  if (plan.shape != kShares) return launch_whole<P>(plan.shape, P::kName, a, s);
   const long long tiles = tiles_of<P, 128, 128>(a);
-  a.shares = shares_of(tiles, P::steps(a));
-  if (a.shares == 1) return launch_whole<P>(P::kName, a, s);
   const hipError_t e =
       launch_kernel(P::kName, ffn_split_kernel<P>, a, grid8(tiles * a.shares), 512, s);
   if (e != hipSuccess) return e;
@@ -565,41 +483,23 @@ hipError_t launch_product(FfnArgs a, hipStream_t s) {
 
 }  // namespace
 
-// Few tokens: each weight read once by a workgroup that has nothing else to wait for. It also reads
-// the tokens, which come from L2 at the rate that the weights do, so this pays up to some 320 KB of
-// both a CU; more is split along K. Both kernels of the forward in us, with [g | u] so (split):
-// 2048 x 2048, 1 token 12 (16), 16 13 (17), 32, 192 KB, 19 (24), 64, 320 KB, 26 (28); 2048 x 4096, 24
-// tokens, 320 KB, 24.6 (25.7), 32 26 (25); 7168 x 2048, 16 tokens, 448 KB, 28.6 (26.5); 4096 x 8192,
-// 1 MB, 69 (56). Up to 4 tokens their part is small and large weights go faster so: 1 x 8192 x 16384
-// 150 (178), but 4096 x 8192 51 (48).
-// y so (split): 4096 x 2048, 16 tokens, 128 KB, 18 (22); 2048 x 4096, 16 tokens, 256 KB, 21 (21.5);
-// 4096 x 8192, 512 KB, 59 (57); 64 tokens, 32 columns a workgroup, 1.5 MB, 84 (49).
-constexpr long long kFewBytes = 320 << 10;
-long long bytes_a_cu(const FfnArgs& a, int cols, long long groups, int K) {
-  return 2LL * (cols + a.T) * K * ceil_div(groups, kCus);
-}
 hipError_t launch_ffn_gate_up(const FfnArgs& a, hipStream_t s) {
-  if (a.T > 64 || (a.T > 4 && bytes_a_cu(a, 16, a.I / 8, a.d) > kFewBytes))
-    return launch_product<GateUp>(a, s);
+  if (!ffn::few_gate_up(a.T, a.d, a.I)) return launch_product<GateUp>(a, s);
   const auto kernel = a.T <= 16   ? ffn_skinny_gate_up_kernel<1, 4>
                       : a.T <= 32 ? ffn_skinny_gate_up_kernel<2, 4>
                                   : ffn_skinny_gate_up_kernel<4, 2>;
   return launch_kernel("ffn_gate_up", kernel, a, a.I / 8, 512, s);
 }
-// 32 columns a workgroup where that leaves 192 of them, for half the reads of A: 7168 x 2048 28.6 us
-// against 29.6; 4096 columns, 128 workgroups, 20.6 against 17.8.
 hipError_t launch_ffn_down(const FfnArgs& a, hipStream_t s) {
-  const bool wide = a.d / 32 >= kCus * 3 / 4;
-  const int cols = wide ? 32 : 16;
-  if (a.T > 64 || bytes_a_cu(a, cols, a.d / cols, a.I) > kFewBytes)
-    return launch_product<Down>(a, s);
+  if (!ffn::few_down(a.T, a.d, a.I)) return launch_product<Down>(a, s);
+  const int cols = ffn::few_down_cols(a.d);
   const auto narrow = a.T <= 16   ? ffn_skinny_down_kernel<1, 1, 4>
                       : a.T <= 32 ? ffn_skinny_down_kernel<2, 1, 4>
                                   : ffn_skinny_down_kernel<4, 1, 2>;
   const auto broad = a.T <= 16   ? ffn_skinny_down_kernel<1, 2, 4>
                      : a.T <= 32 ? ffn_skinny_down_kernel<2, 2, 4>
                                  : ffn_skinny_down_kernel<4, 2, 2>;
-  return launch_kernel("ffn_down", wide ? broad : narrow, a, a.d / cols, 512, s);
+  return launch_kernel("ffn_down", cols == 32 ? broad : narrow, a, a.d / cols, 512, s);
 }
 hipError_t launch_ffn_dh_dw2(const FfnArgs& a, const FfnDwArgs& dw, hipStream_t s) {
   return launch_pair<Dh>("ffn_dh_dw2", a, dw, s);
