@@ -6,11 +6,12 @@ from __future__ import annotations
 
 import torch
 
-from . import (MOE_ACT_SILU, MOE_FLAG_BF16_DW, MOE_FLAG_MXFP8_WGRAD, MOE_FLAG_PERSISTENT,
-               MOE_PREC_BF16, MOE_PREC_INT8, MOE_PREC_MXFP4, MOE_PREC_MXFP8, _dev, make_cfg,
-               make_ffn, moe_backward, moe_ffn_backward, moe_ffn_forward, moe_ffn_query,
-               moe_forward, moe_forward_fused, moe_gate_backward, moe_permute, moe_query,
-               moe_quantize_weights, moe_route, moe_route_gated, moe_router_backward)
+from . import (MOE_ACT_SILU, MOE_ERR_INVALID_ARG, MOE_FLAG_BF16_DW, MOE_FLAG_MXFP8_WGRAD,
+               MOE_FLAG_PERSISTENT, MOE_PREC_BF16, MOE_PREC_INT8, MOE_PREC_MXFP4, MOE_PREC_MXFP8,
+               MoeError, _dev, make_cfg, make_ffn, moe_backward, moe_ffn_backward,
+               moe_ffn_forward, moe_ffn_query, moe_forward, moe_forward_fused,
+               moe_gate_backward, moe_permute, moe_query, moe_quantize_weights, moe_route,
+               moe_route_gated, moe_router_backward)
 
 
 class SharedExpert:
@@ -174,7 +175,7 @@ class MoeLayer:
         moe_quantize_weights(self.cfg, w1, w2, self.wq, stream)
 
     def _shared_operands(self, x, shared_w, saved, shared_saved):
-        if x is None or shared_w is None:
+        if x is None or shared_w is None or any(w is None for w in shared_w):
             raise ValueError("a layer with a shared expert needs x and shared_w")
         if (saved is None) != (shared_saved is None):
             raise ValueError("a batch's saved and shared_saved are given together")
@@ -182,6 +183,8 @@ class MoeLayer:
 
     def forward(self, w1, w2, slot=0, saved=None, stream=None, x=None, shared_w=None,
                 shared_saved=None):
+        """A shared expert's x, weights or buffers that ``moe_ffn_forward`` refuses are refused behind
+        the routed experts' forward: y then holds their output alone until a call that goes through."""
         if self.shared is not None:
             ops = self._shared_operands(x, shared_w, saved, shared_saved)
         moe_forward(self.cfg, self.ring, slot, self.offsets, self.tk_row, self.topk_w, w1, w2,
@@ -205,6 +208,18 @@ class MoeLayer:
         if self.shared is not None:
             self.shared.forward(*ops, self.y, True, stream, shared_saved)
 
+    # What a call behind moe_backward would refuse is refused before the experts' gradients are
+    # written or added to: a corrected call would add a batch's a second time.
+    def _before_gradients(self, stream, *args):
+        _dev("MoeLayer.backward", stream, *args)
+        if any(t is not None and t.data_ptr() % 16 for t, _, _ in args):
+            raise MoeError(MOE_ERR_INVALID_ARG, "MoeLayer.backward: a tensor that starts at a "
+                           "multiple of 16 bytes expected")
+
+    def _not_dx(self, *args):
+        if any(t is not None and t.data_ptr() == self.dx.data_ptr() for t in args):
+            raise MoeError(MOE_ERR_INVALID_ARG, "MoeLayer.backward: dx is neither x nor dy")
+
     def backward(self, w_router, w1, w2, dy, slot=0, accumulate=False, saved=None, stream=None,
                  x=None, shared_w=None, shared_saved=None):
         """With a gate and a ``w_router``, ``x`` (the tokens) is needed too: the experts' backward
@@ -212,23 +227,27 @@ class MoeLayer:
         With a shared expert its backward comes last and adds to dx."""
         if self.infer:
             raise ValueError("the INT8 mode has no backward")
+        T, d, bf = self.T, self.d, torch.bfloat16
         if self.shared is not None:
             ops = self._shared_operands(x, shared_w, saved, shared_saved)
-            if (self.shared.H if shared_saved is None else shared_saved[0]) is None:
-                raise ValueError("the shared expert was made without train")
-            # refused before the experts' gradients are written or added to
-            T, d, I, bf = self.T, self.d, self.shared.cfg.I, torch.bfloat16
-            _dev("MoeLayer.backward", stream, (x, bf, T * d), (ops[1], bf, 2 * I * d),
-                 (ops[2], bf, d * I), (dy, bf, T * d))
+            sh, I = self.shared, self.shared.cfg.I
+            H, A = (sh.H, sh.A) if shared_saved is None else shared_saved
+            if sh.H is None or H is None or A is None:
+                raise ValueError("the shared expert was made without train, or the batch's saved was")
+            dw = bf if sh.cfg.flags & MOE_FLAG_BF16_DW else torch.float32
+            self._before_gradients(stream, (x, bf, T * d), (ops[1], bf, 2 * I * d),
+                                   (ops[2], bf, d * I), (dy, bf, T * d), (H, bf, T * 2 * I),
+                                   (A, bf, T * I), (sh.dw1, dw, 2 * I * d), (sh.dw2, dw, d * I),
+                                   (sh.workspace, torch.uint8, 0), (self.dx, bf, T * d))
+            self._not_dx(x, dy)
         gated = self.gate is not None and w_router is not None
         if gated:
             if self.given:
                 raise ValueError("a given routing has no logits to take a gate's gradients at")
             if x is None:
                 raise ValueError("a gated layer's router gradients need x")
-            # refused before the experts' gradients are written or added to
-            _dev("MoeLayer.backward", stream, (x, torch.bfloat16, self.T * self.d),
-                 (w_router, torch.bfloat16, self.E * self.d))
+            self._before_gradients(stream, (x, bf, T * d), (w_router, bf, self.E * d))
+            self._not_dx(x)
         routed = w_router is not None and not gated
         moe_backward(self.cfg, self.ring, slot, self.offsets, self.row_src, self.tk_row,
                      self.topk_idx, self.topk_w, w_router if routed else None, w1, w2, self.wq,

@@ -225,3 +225,32 @@ def test_int8_layer_with_a_shared_expert_captured_and_replayed():
         step(R, X.clone())
         torch.cuda.synchronize()
         assert torch.equal(L.y, R.y) and torch.isfinite(L.y.float()).all()
+
+
+def test_a_refused_batch_leaves_every_gradient():
+    """A second microbatch whose shared_saved is another size's: nothing is added to any gradient, and
+    the corrected call gives what it gives without the refused one."""
+    inp, s = _inputs("ragged"), SHAPES["ragged"]
+    T, d, I = s["T"], s["d"], 384
+    sw, outs = _shared_weights(d, I, 7), []
+    for refuse in (False, True):
+        L = _layer("ragged", shared=SharedExpert(T, d, I, device=DEV))
+        L.step(inp["X"], inp["Wr"], inp["W1"], inp["W2"], inp["dY"], shared_w=sw)
+        back = lambda x, w, own=None: L.backward(
+            inp["Wr"], inp["W1"], inp["W2"], inp["dY"], 0, True, None if own is None else L.saved,
+            x=x, shared_w=w, shared_saved=own)
+        grads = (L.dw1, L.dw2, L.dwr, L.dx, L.shared.dw1, L.shared.dw2)
+        before = [t.clone() for t in grads]
+        if refuse:
+            H, A = L.shared.new_saved()
+            shifted = torch.empty(T * d + 8, dtype=BF16, device=DEV)[1:T * d + 1].view(T, d)
+            for args in ((inp["X"], sw, (H[:-1], A)), (inp["X"], sw, (H, A[:, :256])),
+                         (shifted, sw), (inp["X"], (sw[0], sw[1].t()))):
+                with pytest.raises(m.MoeError):
+                    back(*args)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(grads, before))
+        back(inp["X"], sw)
+        torch.cuda.synchronize()
+        outs.append([t.clone() for t in grads])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
