@@ -208,6 +208,10 @@ class MoeLayer:
         if self.shared is not None:
             self.shared.forward(*ops, self.y, True, stream, shared_saved)
 
+    def _trains(self):
+        if self.infer:
+            raise ValueError("the INT8 mode has no backward")
+
     # What a call behind moe_backward would refuse is refused before the experts' gradients are
     # written or added to: a corrected call would add a batch's a second time.
     def _before_gradients(self, stream, *args):
@@ -225,8 +229,7 @@ class MoeLayer:
         """With a gate and a ``w_router``, ``x`` (the tokens) is needed too: the experts' backward
         runs as for a given routing, then the gate's and the router's add theirs to dx and dwr.
         With a shared expert its backward comes last and adds to dx."""
-        if self.infer:
-            raise ValueError("the INT8 mode has no backward")
+        self._trains()
         T, d, bf = self.T, self.d, torch.bfloat16
         if self.shared is not None:
             ops = self._shared_operands(x, shared_w, saved, shared_saved)
@@ -265,6 +268,11 @@ class MoeLayer:
     def step(self, x, w_router, w1, w2, dy, slot=0, stream=None, fused=False, shared_w=None):
         """One fwd+bwd pass: route (when w_router is given), permute, forward, backward. With
         ``fused`` the first three run as one launch (moe_forward_fused)."""
+        self._trains()  # before anything runs
+        if self.shared is not None:
+            self._shared_operands(x, shared_w, None, None)
+            if self.shared.H is None:
+                raise ValueError("the shared expert was made without train")
         if fused:
             self.forward_fused(x, w_router, w1, w2, slot, stream=stream, shared_w=shared_w)
             self.backward(w_router, w1, w2, dy, slot, stream=stream, x=x, shared_w=shared_w)

@@ -1,5 +1,6 @@
 """MoeLayer.backward with a shared expert or a gate: what a later call would refuse is refused before
-the experts' gradients are written or added to, so that a corrected call counts a batch once."""
+the experts' gradients are written or added to, so that a corrected call counts a batch once. And
+MoeLayer.step, where there is no backward, before it does anything."""
 import pytest
 import torch
 
@@ -112,3 +113,26 @@ def test_a_gated_layers_tokens_are_refused_before_any_gradient(calls):
         assert not calls
     _backward(L, wr=wr)
     assert calls == ["moe_backward", "moe_gate_backward", "moe_router_backward"]
+
+
+@pytest.mark.parametrize("fused", [False, True])
+def test_a_step_without_a_backward_does_nothing(calls, fused):
+    """step is a forward and a backward: a layer for inference, or one whose shared expert was made
+    without train, refuses it before it routes or permutes."""
+    from mixture_experts_layer_deterministic_amd import layer
+    x, wr, w1, w2 = _bf(T, d), _bf(E, d), _bf(E, 2 * I, d), _bf(E, d, I)
+    L = layer.MoeLayer(T, d, E, k, I, device="cpu", precision=m.MOE_PREC_INT8)
+    with pytest.raises(ValueError, match="no backward"):
+        L.step(x, wr, w1, w2, x, fused=fused)
+    sw = (_bf(2 * S, d), _bf(d, S))
+    L, _ = _layer(train=False)
+    with pytest.raises(ValueError, match="without train"):
+        L.step(x, wr, w1, w2, x, fused=fused, shared_w=sw)
+    L, _ = _layer()
+    with pytest.raises(ValueError, match="needs x and shared_w"):
+        L.step(x, wr, w1, w2, x, fused=fused)
+    assert not calls
+    L.step(x, wr, w1, w2, _bf(T, d), fused=fused, shared_w=sw)
+    assert calls == (["moe_forward_fused"] if fused else
+                     ["moe_route", "moe_permute", "moe_forward"]) + [
+        "moe_ffn_forward", "moe_backward", "moe_ffn_backward"]
