@@ -117,7 +117,7 @@ enum {
  * moe_forward quantises its rows, forms A (bf16) from the exact integer products of the gate and up
  * projections, and quantises A's rows for the down product. H is not kept: `saved` holds A
  * alone (moe_sizes.saved_H means nothing). moe_quantize_weights is needed, and writes the forward's
- * two weights only. No flag is accepted; moe_backward and moe_forward_fused return
+ * two weights only; the bf16 weights are not needed behind it. No flag is accepted; moe_backward and moe_forward_fused return
  * MOE_ERR_UNSUPPORTED. Limits: d and I below 2^17; T * k, E * 2I and E * d below 2^24.
  *
  * Weight-gradient precision. The pages do not say in which precision the weight gradients are
@@ -261,8 +261,8 @@ int moe_permute_static(const moe_cfg* cfg, const int32_t* topk_idx, const void* 
  *   ring, ring_bytes, slot   in: the slot written by moe_permute
  *   offsets, tk_row          in: from moe_permute
  *   topk_w   fp32 [T, k]     in
- *   w1       bf16 [E, 2I, d] in
- *   w2       bf16 [E, d, I]  in
+ *   w1       bf16 [E, 2I, d] in (not read in INT8 mode, may be NULL)
+ *   w2       bf16 [E, d, I]  in (likewise)
  *   wq, wq_bytes             in: MX, FP8 and INT8 modes, the buffer moe_quantize_weights filled
  *                                (ignored in BF16 mode, may be NULL)
  *   y        bf16 [T, d]     out

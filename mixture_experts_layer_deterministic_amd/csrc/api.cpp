@@ -530,8 +530,10 @@ int moe_forward(const moe_cfg* cfg, const void* ring, size_t ring_bytes, int32_t
   int st = check_mode(cfg);
   if (st) return st;
   const Layout Y = layout(cfg);
-  if (!aligned4(offsets) || !aligned4(tk_row) || !aligned4(topk_w) || !aligned16(w1) ||
-      !aligned16(w2) || !aligned16(y) || !aligned16(saved) || !aligned16(workspace))
+  // INT8 mode reads wq alone
+  const auto weight_ok = [&](const void* w) { return (Y.i8 && !w) || aligned16(w); };
+  if (!aligned4(offsets) || !aligned4(tk_row) || !aligned4(topk_w) || !weight_ok(w1) ||
+      !weight_ok(w2) || !aligned16(y) || !aligned16(saved) || !aligned16(workspace))
     return MOE_ERR_INVALID_ARG;
   if ((st = check_ring(Y, ring, ring_bytes, slot))) return st;
   if ((st = check_wq(Y, wq, wq_bytes))) return st;

@@ -61,7 +61,7 @@ class MoeLayer:
     ``quantize_weights`` fills it, and ``mx_wgrad`` (MXFP8 only) makes the weight gradients
     MXFP8 too. ``MOE_PREC_FP8`` owns and fills ``wq`` likewise; its ring slots hold bf16 tokens.
     ``bf16_dw`` keeps dw1 and dw2 in bf16. ``MOE_PREC_INT8`` owns and fills ``wq`` too, and is for
-    inference: it has no gradients, and no H.
+    inference: it has no gradients, and no H, and its forward takes None for w1 and w2.
 
     With ``shared`` (a ``SharedExpert`` of the same T and d) the forward adds the shared expert's
     output to y and the backward its gradient to dx; both then need the tokens ``x`` and its weights

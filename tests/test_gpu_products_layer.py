@@ -254,3 +254,14 @@ def test_a_refused_batch_leaves_every_gradient():
         torch.cuda.synchronize()
         outs.append([t.clone() for t in grads])
     assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_int8_layer_serves_without_the_bf16_weights():
+    inp = _inputs("ragged")
+    L = _layer("ragged", precision=m.MOE_PREC_INT8)
+    L.quantize_weights(inp["W1"], inp["W2"])
+    _forward(L, inp)
+    want = L.y.clone()
+    L.y.zero_()
+    _forward(L, dict(inp, W1=None, W2=None))
+    assert torch.equal(L.y, want)
