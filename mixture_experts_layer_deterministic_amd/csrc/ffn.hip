@@ -105,6 +105,7 @@ struct Down {
 struct Dh {
   using Args = FfnArgs;
   static constexpr bool kAKM = false, kBKM = true, kGated = false;
+  static constexpr bool kWideDw = true;  // whether its dW is ever in 128 x 256 tiles
   MOE_BOTH long long m(const Args& a) { return a.T; }
   MOE_BOTH long long n(const Args& a) { return a.I; }
   MOE_BOTH int steps(const Args& a) { return a.d / 64; }
@@ -152,6 +153,8 @@ struct Dh {
 struct Dx {
   using Args = FfnArgs;
   static constexpr bool kAKM = false, kBKM = true, kGated = false;
+  // dW1 has 2I rows, whole 256s: 256 x 128 tiles are as few as 128 x 256 ones, and come first
+  static constexpr bool kWideDw = false;
   MOE_BOTH long long m(const Args& a) { return a.T; }
   MOE_BOTH long long n(const Args& a) { return a.d; }
   MOE_BOTH int steps(const Args& a) { return 2 * a.I / 64; }
@@ -317,7 +320,8 @@ __global__ void __launch_bounds__(512, 2) ffn_pair_kernel(const Pair<P> p) {
       if (lt < tiles_of<Dw, 256, 128>(p.dw)) whole_tile<Dw, 256, 128>(p.dw, lt);
       break;
     case kWide:
-      if (lt < tiles_of<Dw, 128, 256>(p.dw)) whole_tile<Dw, 128, 256>(p.dw, lt);
+      if constexpr (P::kWideDw)
+        if (lt < tiles_of<Dw, 128, 256>(p.dw)) whole_tile<Dw, 128, 256>(p.dw, lt);
       break;
     case kSmall:
       if (lt < tiles_of<Dw, 128, 128>(p.dw)) whole_tile<Dw, 128, 128>(p.dw, lt);
@@ -452,6 +456,7 @@ template <class P>
 hipError_t launch_pair(const char* name, const FfnArgs& rows, const FfnDwArgs& dw, hipStream_t s) {
   const ffn::Size szr = size_of<P>(rows), szw = size_of<Dw>(dw);
   const ffn::PairPlan plan = ffn::plan_of_pair(szr, szw);
+  if (!P::kWideDw && plan.dw.shape == kWide) return hipErrorInvalidValue;  // has no such tiles
   Pair<P> p{rows, dw, plan.rows.shape, plan.dw.shape, 0};
   p.rows.shares = plan.rows.shares;
   p.dw.shares = plan.dw.shares;
