@@ -2,9 +2,12 @@
 //   [g | u] = x W1^T    A = act(g) u    y (+)= A W2^T
 //   dA = dy W2    dH = bf16([dA u act'(g) | dA act(g)])
 //   dx (+)= dH W1    dW1 (+)= dH^T x    dW2 (+)= dy^T A
-// 2048 tokens x 7168 x 2048: forward 109 + 51 us (1.12e15 operations a second; library products of
-// these sizes, without activation or H, take 114 + 55), backward 123 + 204 us in two launches. What
-// bounds the tiles stands in products.h.
+// 2048 tokens x 7168 x 2048: forward 108 + 50 us (1.14e15 operations a second; library products of
+// these sizes, without activation or H, take 111 to 114 + 54), backward 121 to 124 + 198 to 200 us in
+// two launches, with fp32 gradients up to 9% more. What bounds the tiles stands in products.h.
+// Adding to what is there: y of 1777 x 4096 x 1408 22.7 -> 24.8 us, the backward's kernels of 333 x
+// 4096 x 1024 46 -> 50 us with bf16 gradients, 51 -> 70 with fp32 ones (50 MB more to read; each lane
+// loads, adds and stores in turn).
 //
 // Sums are fp32 in a fixed order. A is formed from the fp32 g and u, dH from the bf16 H that the
 // forward stored, and both are rounded once, as the next product reads them.

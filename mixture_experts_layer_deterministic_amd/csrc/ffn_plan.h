@@ -19,7 +19,9 @@ enum Shape { kBig, kTall, kWide, kSmall, kShares };
 // Tile shapes, and what a step takes when the card is full of them, in us (bytes a step 64, 48 and
 // 32 KB). Measured, the whole call in us, 256 x 256 / 256 x 128 / 128 x 128: [g | u] of 2048 x 7168 x
 // 2048 141 / 107 / 142 (128, 256, 512 tiles), its y 51 / 64 / 88 (224, 448, 896), dH 155 / 107 / 80 (64,
-// 128, 256); [g | u] of 1777 x 4096 x 1408 80 / 53 / 72 (77, 154, 308).
+// 128, 256); [g | u] of 1777 x 4096 x 1408 80 / 53 / 72 (77, 154, 308). 128 x 256 as 256 x 128: y of
+// 1920 x 4352 in the one and of 4352 x 1920 in the other, 255 tiles each, 31 and 31 us at I = 2048, 126
+// and 124 at 8192.
 constexpr struct {
   int bm, bn;
   float us;

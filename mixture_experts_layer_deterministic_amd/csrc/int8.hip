@@ -236,9 +236,9 @@ MOE_DEV void i8_tile(const I8GemmArgs& a, const I8Place& t) {
 // of steps: a workgroup stays for all its tiles, and the next tile's first loads go out in the last
 // steps of the one before, so that they arrive under its epilogue; otherwise each tile is a workgroup's.
 //
-// 16384 rows over 5 of 8 experts, gated 4096 x 7168: 369 us, 2.6e15 operations a second; 7168 x 2048:
-// 230 us, 2.1e15 (a library product of one expert's 16384 rows, int32 results and no scales, takes 436
-// and 257 us; this kernel 359 and 206 there). What bounds a step stands in
+// 16384 rows over 5 of 8 experts, gated 4096 x 7168: 360 us, 2.7e15 operations a second; 7168 x 2048:
+// 230 us, 2.1e15 (a library product of one expert's 16384 rows, int32 results and no scales, takes 426
+// and 247 us; this kernel 335 and 196 there). What bounds a step stands in
 // products.h. With each tile a workgroup of its own the second took 238.
 template <bool GATED, bool FLOW>
 __global__ void __launch_bounds__(512, 2) i8_big_kernel(const I8GemmArgs a) {
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(512, 2) i8_big_kernel(const I8GemmArgs a) {
 }
 
 // Few rows an expert: HBM bounds it. 256 experts of 64 rows, gated 4096 x 7168, in 1.33 ms, 5.8 TB/s; 24
-// rows over 11 of 16 experts, 7168 x 2048, in 29 to 31 us, 5.2 to 5.6 TB/s.
+// rows over 11 of 16 experts, 7168 x 2048, in 32 to 33 us, 5.0 TB/s.
 template <int NMB, int SB, bool GATED>
 MOE_DEV void i8_stream(const I8GemmArgs& a, const RowTile& t, int n0, const StreamStages<SB>& L) {
   StreamProduct<Int8, NMB, SB, GATED> w;
@@ -437,7 +437,7 @@ static void launch_skinny(const I8GemmArgs& a, bool gated, hipStream_t s) {
 //    random.
 //  * up to 112 rows: 128-row streaming. 64 x 96 362 (256 x 256 tiles 401), 16 x 96 93 (103), 32 x 128
 //    198 (210); from 129 rows on an expert's weights are read twice, 32 x 144 342 (214), and of experts
-//    with 128 on average half have more. But 193 to 256 tiles (192 from 64 rows on) in quarters of
+//    with 128 on average half have more. But 193 to 256 tiles (192 from 64 rows on) in halves of
 //    256 x 256 tiles fill the card just once: 7 x 64 50 (61), 8 x 48 52 (58), 6 x 96 50 (69), 7168 x
 //    4096 not gated 4 x 64 34 (38); 6 x 64 48 (37), 9 x 64 79 (64).
 hipError_t launch_i8_gemm(const I8GemmArgs& a, bool gated, hipStream_t s) {

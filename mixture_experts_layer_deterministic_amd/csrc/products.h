@@ -34,10 +34,11 @@
 // compiler sees which loads and reads meet, and does not wait for every load before each read.
 //
 // A step takes 1.35 us in 256 x 256 tiles, 0.95 in 256 x 128 and 0.67 in 128 x 128 with the card full
-// of them, each some 12.5 TB/s of loads. In the first the MFMAs are busy 86% of the time at 1.77 GHz,
-// which is what the card's power allows: four waves of 128 x 128, which read a third less from LDS,
-// took 1.34 us, panels that all lie in L2 1.32, and a step without its loads, at a higher clock, 0.9 to
-// 0.98. No change: K begun elsewhere in each tile, a later start of every second CU.
+// of them, each some 12.5 TB/s of loads. Over 128 steps and more of the first the MFMAs are busy 86 to
+// 91% of the time, and the clock, 2.4 GHz at first, falls as the card's power allows: 2.0 GHz after 0.1
+// ms of 256 int8 tiles, 1.8 after 0.2, 1.45 after 0.45. Four waves of 128 x 128, which read a third less
+// from LDS, took 1.34 us, panels that all lie in L2 1.32, and a step without its loads, at a higher
+// clock, 0.9 to 0.98. No change: K begun elsewhere in each tile, a later start of every second CU.
 #pragma once
 
 #include "dma.h"
