@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(256) i8_quant_rows_kernel(const uint16_t* __re
 #pragma unroll
     for (int i = 0; i < U; ++i) amax = max(amax, amax_bits8(x[i]));
   } else {
-    for (int c = c0; c < cols; c += kStep)
+    // unsigned: a row may end less than a step below 2^31
+    for (uint32_t c = c0; c < (uint32_t)cols; c += kStep)
       amax = max(amax, amax_bits8(*reinterpret_cast<const uint4*>(p + c)));
   }
 #pragma unroll
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(256) i8_quant_rows_kernel(const uint16_t* __re
       if (c0 + i * kStep < cols)
         *reinterpret_cast<uint2*>(q + c0 + i * kStep) = i8_codes8(x[i], s);
   } else {
-    for (int c = c0; c < cols; c += kStep)
+    for (uint32_t c = c0; c < (uint32_t)cols; c += kStep)
       *reinterpret_cast<uint2*>(q + c) = i8_codes8(*reinterpret_cast<const uint4*>(p + c), s);
   }
 }
