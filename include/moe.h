@@ -585,6 +585,7 @@ int moe_ffn_query(const moe_ffn* ffn, moe_ffn_sizes* out);
  *   A   bf16 [T, I]     out
  *   y   bf16 [T, d]     out (or added to); not x
  *   workspace bytes [ws_bytes]   scratch: calls that share one follow each other
+ * H, A and y overlap neither one another nor an input.
  */
 int moe_ffn_forward(const moe_ffn* ffn, const void* x, const void* w1, const void* w2, void* H,
                     void* A, void* y, int32_t acc_y, void* workspace, size_t ws_bytes,
@@ -603,6 +604,7 @@ int moe_ffn_forward(const moe_ffn* ffn, const void* x, const void* w1, const voi
  *   dw1 [2I, d]         out (or added to)
  *   dw2 [d, I]          out (or added to)
  *   workspace bytes [ws_bytes]   scratch
+ * dx, dw1 and dw2 overlap neither one another nor an input.
  */
 int moe_ffn_backward(const moe_ffn* ffn, const void* x, const void* w1, const void* w2,
                      const void* H, const void* A, const void* dy, void* dx, void* dw1, void* dw2,
